@@ -43,8 +43,10 @@ typedef enum {
     FA_ERR_UNSUPPORTED = 2,      /* head dimension D not in {32, 64, 128}; device not sm_103 */
     FA_ERR_CUDA = 3,             /* a CUDA runtime/driver call failed (launch, attribute, tensor map) */
     FA_ERR_TIMEOUT = 4,          /* a kernel wait ran past its time limit (read with fa_read_device_status) */
-    FA_ERR_DEBUG_CHECK = 5       /* debug builds: a device-side bounds or schedule check failed
+    FA_ERR_DEBUG_CHECK = 5,      /* debug builds: a device-side bounds or schedule check failed
                                     (read with fa_read_device_status; details: fa_debug_report) */
+    FA_ERR_INDEX = 6             /* a page number, length or position in device memory was out of range
+                                    (read with fa_read_device_status) */
 } fa_status;
 
 /*
@@ -253,10 +255,160 @@ FA_API int fa_fwd_split_noalloc(const void* q, const void* k, const void* v, con
                          float* lse, int B, int H, int Nq, int Nk, int D, float scale,
                          int num_splits, void* stream);
 
+/* A strided tensor [B, H, N, D]: strides in elements, the last axis contiguous.
+ * A stride is >= 0 (0 broadcasts an input); strides of axes of size 1 are not used. */
+typedef struct fa_tensor {
+    void* data;
+    long long stride_b, stride_h, stride_n;
+} fa_tensor;
+
+/* Element types of fa_rope. */
+typedef enum { FA_DTYPE_BF16 = 0, FA_DTYPE_FP16 = 1, FA_DTYPE_FP32 = 2 } fa_dtype;
+
+/* Which elements of a row form the pairs that turn. */
+typedef enum {
+    FA_ROPE_ADJACENT = 0, /* (2i, 2i + 1) */
+    FA_ROPE_HALVES = 1    /* (i, i + D/2) */
+} fa_rope_pairing;
+
+#define FA_ROPE_MAX_AXES 4
+
+/* The axes of fa_rope: dims[a] (even, >= 2) of the row's D elements belong to
+ * axis a, in order, and sum to D; theta[a] > 0; scale[a] multiplies the
+ * positions (1 for none). */
+typedef struct fa_rope_axes {
+    int count;
+    int dims[FA_ROPE_MAX_AXES];
+    double theta[FA_ROPE_MAX_AXES];
+    double scale[FA_ROPE_MAX_AXES];
+} fa_rope_axes;
+
+/*
+ * fa_rope — rotary positions over several axes (time, height, width) on q and
+ * k, ahead of the attention.
+ *
+ * The D/2 pairs of a row are dealt to the axes in order, dims[a]/2 each; pair j
+ * of axis a of token n turns by pos[b][n][a] * scale[a] * theta[a]^(-2j/dims[a]):
+ * (x0, x1) -> (x0 cos - x1 sin, x0 sin + x1 cos).  A token at position 0 on
+ * every axis is unchanged.  inverse != 0 turns the other way, which is also
+ * the gradient: dx = fa_rope(dy, inverse).  (For a broadcast input the caller
+ * sums the gradient over the broadcast axis.)
+ *
+ *   pos       device int32 [B, N, count], batch stride pos_stride_b elements
+ *             (0: one set of positions for every batch entry); any int32
+ *             value: the angle is reduced exactly
+ *   q, q_out  [B, Hq, N, D] of `dtype`; k, k_out [B, Hk, N, D], or both NULL.
+ *             Inputs may have any strides (slices of a token-major projection
+ *             among them); outputs too, as long as no element is written
+ *             twice.  An output may be exactly its input (in place); else the
+ *             outputs share no element with the inputs or each other.
+ *   D in {32, 64, 128}.  Speed, not results, depends on alignment: rows that
+ *   start 16-byte aligned are read and written 16 bytes at a time.
+ *
+ * One kernel is enqueued on `stream`.  Arithmetic is fp32, rounded once to
+ * `dtype`.  Errors as fa_fwd; pointers aligned to their element.
+ */
+FA_API int fa_rope(const fa_rope_axes* axes, const int* pos, long long pos_stride_b, const fa_tensor* q,
+                   const fa_tensor* q_out, int Hq, const fa_tensor* k, const fa_tensor* k_out, int Hk, int B,
+                   int N, int D, int dtype, int pairing, int inverse, void* stream);
+
+/*
+ * A paged key/value cache in 8 bits.  A page holds page_tokens consecutive
+ * tokens of a sequence for every head; which pages a sequence owns, in order,
+ * is the caller's int32 table [B, table_width].
+ *
+ *   k, v              device, e4m3 codes [num_pages, H, page_tokens, D], 16-byte aligned
+ *   k_scale, v_scale  device fp32 [num_pages, H]: an element is code * scale.
+ *                     The scale is the least power of two s in [2^-117, 2^119]
+ *                     with max |x| <= 448 s over the page's tokens of the head.
+ *   page_tokens in {32, 64, 128};  D in {32, 64, 128}
+ *
+ * Nothing needs clearing: a page's scale and codes are read only where tokens
+ * have been written.
+ */
+typedef struct fa_cache {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int num_pages, H, page_tokens, D;
+} fa_cache;
+
+/*
+ * fa_cache_write — quantise new tokens and append them to the cache.
+ *
+ * Token i < count[b] of sequence b goes to position start[b] + i, i.e. to page
+ * table[b][position / page_tokens].  start[b] is the number of tokens the
+ * sequence holds: positions before it in the first page written are kept
+ * (multiplied by the ratio of the scales, a power of two, and rounded again
+ * where the page's scale has to grow), positions after the last token written
+ * are left as they were and hold nothing.  Non-finite elements are stored as
+ * NaN and take no part in the scale.
+ *
+ *   k, v   bf16 [B, H, N, D], any strides
+ *   table  device int32 [B, table_width]
+ *   start  device int32 [B];  count  device int32 [B], 0 <= count[b] <= N, or
+ *          NULL for N each
+ *
+ * The pages written must be distinct: a page listed for two sequences of the
+ * call may be read by the attention but not written by both (its contents are
+ * then undefined).  A page number outside [0, num_pages), a start or count
+ * below 0, a count above N and a position past the table record FA_ERR_INDEX
+ * in the device status word; tokens that have no valid place are not written.
+ * One kernel is enqueued on `stream`.
+ */
+FA_API int fa_cache_write(const fa_cache* cache, const fa_tensor* k, const fa_tensor* v, const int* table,
+                          int table_width, const int* start, const int* count, int B, int N, void* stream);
+
+/*
+ * fa_cache_read — read tokens first[b] .. first[b] + N - 1 of each sequence back
+ * as bf16 (exact: code * scale is a bf16 number); positions from lens[b] on
+ * give zeros.
+ *
+ *   lens   device int32 [B]: tokens the sequence holds
+ *   first  device int32 [B], or NULL for 0
+ *   k_out, v_out  device bf16 [B, H, N, D], contiguous, 16-byte aligned
+ *
+ * An index out of range records FA_ERR_INDEX in the device status word (a page
+ * outside the cache is read as page 0, a length or position is clamped).  One
+ * kernel is enqueued on `stream`.
+ */
+FA_API int fa_cache_read(const fa_cache* cache, const int* table, int table_width, const int* lens,
+                         const int* first, void* k_out, void* v_out, int B, int N, void* stream);
+
+/*
+ * fa_fwd_cache — attention of new queries to the cache, prompts, chunks and
+ * single tokens alike.
+ *
+ * As fa_fwd (scale, O, LSE), with K and V read from the cache: sequence b has
+ * the keys 0 .. lens[b] - 1.  causal != 0: query row i sees the keys
+ * j <= q_start[b] + i only; q_start NULL means lens[b] - Nq (the queries are
+ * the last Nq tokens).  Hq is a multiple of the cache's H: query head h reads
+ * key head h / (Hq / H).  A row that sees no key (an empty sequence, a row
+ * before the first key) gives O = 0, LSE = -inf.
+ *
+ *   q, out   device bf16 [B, Hq, Nq, D], lse fp32 [B, Hq, Nq], as fa_fwd's
+ *   table, lens, q_start  as above; pages may be shared between sequences.
+ *            Table entries past a sequence's length are not read.
+ *   workspace  device scratch, 16-byte aligned, at least
+ *            fa_cache_workspace_bytes(...) bytes (may be NULL when that is 0),
+ *            not shared with a concurrent call.
+ *
+ * An index out of range records FA_ERR_INDEX (see fa_cache_read).
+ */
+FA_API int fa_fwd_cache(const void* q, const fa_cache* cache, const int* table, int table_width,
+                        const int* lens, const int* q_start, int causal, void* out, float* lse, int B, int Hq,
+                        int Nq, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes fa_fwd_cache needs (0 for none, and for invalid sizes). */
+FA_API size_t fa_cache_workspace_bytes(int B, int Hq, int Hk, int Nq, int D, int table_width, int page_tokens);
+
 /*
  * fa_read_device_status — read, and reset to FA_OK, the status word that
- * kernels on the current device write when an internal wait times out.
- * Synchronises `stream` first.  Writes FA_OK or FA_ERR_TIMEOUT to *status.
+ * kernels on the current device write when an internal wait times out or an
+ * index in device memory is out of range.  Synchronises `stream` first.
+ * Writes FA_OK or the first error recorded (FA_ERR_TIMEOUT, FA_ERR_INDEX;
+ * FA_ERR_DEBUG_CHECK in debug builds) to *status.
  * Returns FA_OK, FA_ERR_INVALID_ARGUMENT (status NULL) or FA_ERR_CUDA.
  */
 FA_API int fa_read_device_status(void* stream, int* status);

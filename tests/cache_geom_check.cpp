@@ -1,0 +1,107 @@
+// Index arithmetic of the paged e4m3 cache (fa_cache_geom.h) against its
+// definitions: the scale rule, the checks of numbers that come from device
+// memory, and the split of the attention's tiles over a grid.  Prints "ok" or
+// the first mismatch.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+#include <cstring>
+#include <random>
+#include <vector>
+
+#include "fa_cache_geom.h"
+
+static int scales() {
+  for (uint32_t bits = 0; bits < 0x7f80u; ++bits) {  // every finite bf16 >= 0
+    const uint32_t w = bits << 16;
+    float a;
+    std::memcpy(&a, &w, 4);
+    int e = fa::kCacheExpMin;
+    while (e < fa::kCacheExpMax && (double)a > std::ldexp(448.0, e)) ++e;
+    if (fa::cache_scale_exp(w) != e) {
+      std::printf("scale of %g: %d != %d\n", a, fa::cache_scale_exp(w), e);
+      return 1;
+    }
+  }
+  return 0;
+}
+
+static int checks() {
+  const int n[] = {INT_MIN, -1, 0, 1, 99, 100, 101, INT_MAX};
+  for (int x : n) {
+    bool bad = false;
+    const int got = fa::cache_clamp(x, 100, bad);
+    if (got < 0 || got > 100 || bad != (x < 0 || x > 100) || (!bad && got != x)) {
+      std::printf("clamp %d: %d %d\n", x, got, bad);
+      return 1;
+    }
+    bad = false;
+    const int id = fa::cache_page(x, 100, bad);
+    if (id < 0 || id >= 100 || bad != (x < 0 || x >= 100) || (!bad && id != x)) {
+      std::printf("page %d: %d %d\n", x, id, bad);
+      return 1;
+    }
+  }
+  return 0;
+}
+
+// Every tile of every unit is walked once, by one CTA, in order; a CTA has at
+// most two stretches that are not whole units, in different slots; the CTAs
+// of a unit are those between the owners of its first and last tile.
+static int walk(const std::vector<int>& lens, int units, int max_len, int grid) {
+  const int B = (int)lens.size();
+  std::vector<long long> base(B + 1, 0);
+  std::vector<int> nt(B);
+  for (int b = 0; b < B; ++b) {
+    const long long len = lens[b] < 0 ? 0 : (lens[b] > max_len ? max_len : lens[b]);
+    nt[b] = len == 0 ? 1 : (int)((len + 127) / 128);
+    base[b + 1] = base[b] + (long long)nt[b] * units;
+  }
+  const long long total = base[B];
+  long long seen = 0;
+  for (int c = 0; c < grid; ++c) {
+    const long long t0 = fa::cache_range_begin(total, grid, c), t1 = fa::cache_range_begin(total, grid, c + 1);
+    if (t0 != seen || t1 < t0) return std::printf("range %d\n", c), 1;
+    int b0 = 0;
+    while (b0 + 1 < B && base[b0 + 1] <= t0) ++b0;
+    fa::CacheWalk w;
+    w.start(lens.data(), B, units, max_len, t0, t1, b0, base[b0]);
+    fa::CacheSegment s;
+    int used = 0;
+    while (w.next(s)) {
+      if (s.b < 0 || s.b >= B || s.unit < 0 || s.unit >= units || s.ntiles < 1 || s.total != nt[s.b] ||
+          s.tile0 < 0 || s.tile0 + s.ntiles > s.total)
+        return std::printf("segment outside\n"), 1;
+      const long long first = base[s.b] + (long long)s.unit * s.total;
+      if (first + s.tile0 != seen) return std::printf("order\n"), 1;
+      for (long long t = seen; t < seen + s.ntiles; ++t)
+        if (fa::cache_range_owner(total, grid, t) != c) return std::printf("owner\n"), 1;
+      seen += s.ntiles;
+      if (s.ntiles < s.total) {
+        const int slot = fa::cache_slot(total, grid, c, first) - 2 * c;
+        if (slot != (first > t0 ? 1 : 0) || (used >> slot) & 1)
+          return std::printf("slot\n"), 1;
+        used |= 1 << slot;
+      }
+    }
+    if (seen != t1) return std::printf("end\n"), 1;
+  }
+  return seen == total ? 0 : (std::printf("total\n"), 1);
+}
+
+int main() {
+  if (scales() || checks()) return 1;
+  std::mt19937 r(7);
+  for (int i = 0; i < 3000; ++i) {
+    const int B = 1 + r() % 9, units = 1 + r() % 12, max_len = 1 + r() % 4000;
+    std::vector<int> lens(B);
+    for (int& n : lens) n = r() % 10 == 0 ? (r() % 2 ? -5 : INT_MAX) : (int)(r() % (max_len + 1));
+    if (walk(lens, units, max_len, 1 + r() % 400)) return 1;
+  }
+  // 2^31 tokens a sequence, many heads: the tile count needs 64 bits
+  if (fa::cache_range_begin(1LL << 45, 304, 304) != 1LL << 45) return std::printf("wide\n"), 1;
+  if (walk({INT_MAX - 127, 5, 0}, 3, INT_MAX - 127, 37) == 1) return 1;
+  std::printf("ok\n");
+  return 0;
+}

@@ -21,6 +21,7 @@ FA_ERR_UNSUPPORTED = 2
 FA_ERR_CUDA = 3
 FA_ERR_TIMEOUT = 4
 FA_ERR_DEBUG_CHECK = 5
+FA_ERR_INDEX = 6
 
 FA_MASK_NONE = 0
 FA_MASK_KEY_PADDING = 1
@@ -34,6 +35,25 @@ _lock = threading.Lock()
 class FaMask(ctypes.Structure):
     """The C struct fa_mask."""
     _fields_ = [("kind", ctypes.c_int), ("data", ctypes.c_void_p), ("heads", ctypes.c_int)]
+
+
+class FaTensor(ctypes.Structure):
+    """The C struct fa_tensor."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
+                ("stride_h", ctypes.c_longlong), ("stride_n", ctypes.c_longlong)]
+
+
+class FaRopeAxes(ctypes.Structure):
+    """The C struct fa_rope_axes."""
+    _fields_ = [("count", ctypes.c_int), ("dims", ctypes.c_int * 4), ("theta", ctypes.c_double * 4),
+                ("scale", ctypes.c_double * 4)]
+
+
+class FaCache(ctypes.Structure):
+    """The C struct fa_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("H", ctypes.c_int),
+                ("page_tokens", ctypes.c_int), ("D", ctypes.c_int)]
 
 
 def library_path() -> str:
@@ -76,6 +96,19 @@ def load_library() -> ctypes.CDLL:
             lib.fa_split_workspace_bytes.restype = sz
             lib.fa_split_count.argtypes = [i32, i32, i32, i32, i32]
             lib.fa_split_count.restype = i32
+            tp = ctypes.POINTER(FaTensor)
+            lib.fa_rope.argtypes = [ctypes.POINTER(FaRopeAxes), vp, ctypes.c_longlong, tp, tp, i32, tp,
+                                    tp, i32, i32, i32, i32, i32, i32, i32, vp]
+            lib.fa_rope.restype = i32
+            cp = ctypes.POINTER(FaCache)
+            lib.fa_cache_write.argtypes = [cp, tp, tp, vp, i32, vp, vp, i32, i32, vp]
+            lib.fa_cache_write.restype = i32
+            lib.fa_cache_read.argtypes = [cp, vp, i32, vp, vp, vp, vp, i32, i32, vp]
+            lib.fa_cache_read.restype = i32
+            lib.fa_fwd_cache.argtypes = [vp, cp, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32, f32, vp, sz, vp]
+            lib.fa_fwd_cache.restype = i32
+            lib.fa_cache_workspace_bytes.argtypes = [i32] * 7
+            lib.fa_cache_workspace_bytes.restype = sz
             lib.fa_read_device_status.argtypes = [vp, ctypes.POINTER(i32)]
             lib.fa_read_device_status.restype = i32
             lib.fa_measure_ex2_rate.argtypes = [vp, ctypes.POINTER(ctypes.c_double)]
@@ -352,7 +385,8 @@ def measure_ex2_rate(stream=None) -> float:
 
 
 def read_device_status(stream=None) -> int:
-    """Synchronise and return (then reset) the device status word: FA_OK or FA_ERR_TIMEOUT."""
+    """Synchronise and return (then reset) the device status word: FA_OK, FA_ERR_TIMEOUT, or
+    FA_ERR_INDEX (a page number, length or position out of range in device memory)."""
     st = ctypes.c_int(0)
     rc = load_library().fa_read_device_status(_stream_handle(stream), ctypes.byref(st))
     if rc != FA_OK:

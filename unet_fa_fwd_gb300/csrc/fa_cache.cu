@@ -1,0 +1,446 @@
+// fa_cache.cu — C ABI of the operators around a cached attention (declared in
+// include/fa.h): rotary positions, the paged e4m3 key/value cache, and the
+// attention that reads it.  Arguments are validated before any CUDA call.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "fa.h"
+#include "fa_cache_attn.cuh"
+#include "fa_cache_quant.cuh"
+#include "fa_host.h"
+#include "fa_log.h"
+#include "fa_rope.cuh"
+
+namespace {
+
+using fa::aligned16;
+using fa::ranges_overlap;
+
+bool head_dim_ok(int D) { return D == 32 || D == 64 || D == 128; }
+
+// ---- strided [B][H][N][D] tensors (the last axis contiguous) ----
+
+// Elements from the first to one past the last; 0 when that (or an offset)
+// does not fit 62 bits or a stride is negative.
+int64_t extent(const fa_tensor& t, int B, int H, int N, int D) {
+  const long long strides[3] = {t.stride_b, t.stride_h, t.stride_n};
+  const int sizes[3] = {B, H, N};
+  __int128 e = D;
+  for (int i = 0; i < 3; ++i) {
+    if (strides[i] < 0) return 0;
+    e += (__int128)strides[i] * (sizes[i] - 1);
+  }
+  return e > ((__int128)1 << 58) ? 0 : (int64_t)e;
+}
+
+// No element is written twice: ordered by stride, each axis steps over all
+// that the smaller ones span.
+bool writes_once(const fa_tensor& t, int B, int H, int N, int D) {
+  long long st[3] = {t.stride_b, t.stride_h, t.stride_n};
+  int n[3] = {B, H, N};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (st[j] < st[i]) {
+        const long long s = st[i]; st[i] = st[j]; st[j] = s;
+        const int m = n[i]; n[i] = n[j]; n[j] = m;
+      }
+  int64_t span = D;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) continue;
+    if (st[i] < span) return false;
+    span += st[i] * (n[i] - 1);
+  }
+  return true;
+}
+
+// Two tensors share no element: their ranges are apart, or both are slices of
+// one token-major buffer (same strides) whose head blocks do not meet.
+bool apart(const fa_tensor& a, int Ha, const fa_tensor& b, int Hb, int B, int N, int D, int size) {
+  if (!ranges_overlap(a.data, (size_t)extent(a, B, Ha, N, D) * size, b.data,
+                      (size_t)extent(b, B, Hb, N, D) * size))
+    return true;
+  if (a.stride_b != b.stride_b || a.stride_h != b.stride_h || a.stride_n != b.stride_n) return false;
+  const bool a_first = a.data < b.data;
+  const int64_t bytes = a_first ? static_cast<char*>(b.data) - static_cast<char*>(a.data)
+                                : static_cast<char*>(a.data) - static_cast<char*>(b.data);
+  if (bytes % size) return false;
+  const int64_t d = bytes / size;
+  const int Hlo = a_first ? Ha : Hb, Hhi = a_first ? Hb : Ha;
+  const int64_t lo = a.stride_h * (Hlo - 1) + D, hi = d + a.stride_h * (Hhi - 1) + D;  // head blocks of a token
+  if (d < lo) return false;
+  if (N > 1 && a.stride_n < hi) return false;
+  const int64_t span = hi + (N > 1 ? a.stride_n * (N - 1) : 0);
+  return B == 1 || a.stride_b >= span;
+}
+
+bool same(const fa_tensor& a, const fa_tensor& b) {
+  return a.data == b.data && a.stride_b == b.stride_b && a.stride_h == b.stride_h && a.stride_n == b.stride_n;
+}
+
+// Every row starts 16-byte aligned.
+bool rows16(const fa_tensor& t, int B, int H, int N, int size) {
+  const int e = 16 / size;
+  return aligned16(t.data) && (B == 1 || t.stride_b % e == 0) && (H == 1 || t.stride_h % e == 0) &&
+         (N == 1 || t.stride_n % e == 0);
+}
+
+// ---- rotary positions ----
+
+template <typename T, int D, int E, bool HALVES>
+int launch_rope(fa::RopeParams& p, int sm_count, cudaStream_t s) {
+  constexpr int CHUNKS = HALVES ? D / 2 / E : D / E;
+  const long long blocks = (p.tokens * CHUNKS + fa::kRopeThreads - 1) / fa::kRopeThreads;
+  if (blocks > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
+  // Heads are dealt to more blocks while the blocks do not fill the SMs'
+  // 8 x 256 threads twice; at least one batch of loads each.
+  const int batches = (p.heads + fa::kRopeBatch - 1) / fa::kRopeBatch;
+  long long groups = (16LL * sm_count + blocks - 1) / blocks;
+  if (groups > batches) groups = batches;
+  const int per = (int)((batches + groups - 1) / groups);
+  p.heads_per_block = per * fa::kRopeBatch;
+  const int gy = (batches + per - 1) / per;
+  fa::log_launch("fa_rope_kernel<D=%d,%d-byte elements,%d per access,%s> grid %lld x %d x %d threads, %lld tokens, "
+                 "%d heads%s", D, (int)sizeof(T), E, HALVES ? "halves" : "adjacent", blocks, gy, fa::kRopeThreads,
+                 p.tokens, p.heads, p.inverse ? ", inverse" : "");
+  fa::fa_rope_kernel<T, D, E, HALVES><<<dim3((unsigned)blocks, gy), fa::kRopeThreads, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <typename T, int D>
+int dispatch_rope(fa::RopeParams& p, bool vec, bool halves, int sm_count, cudaStream_t s) {
+  constexpr int E = 16 / sizeof(T);
+  if (halves)
+    return vec ? launch_rope<T, D, E, true>(p, sm_count, s) : launch_rope<T, D, 2, true>(p, sm_count, s);
+  return vec ? launch_rope<T, D, E, false>(p, sm_count, s) : launch_rope<T, D, 2, false>(p, sm_count, s);
+}
+
+template <typename T>
+int dispatch_rope(int D, fa::RopeParams& p, bool vec, bool halves, int sm_count, cudaStream_t s) {
+  switch (D) {
+    case 32: return dispatch_rope<T, 32>(p, vec, halves, sm_count, s);
+    case 64: return dispatch_rope<T, 64>(p, vec, halves, sm_count, s);
+    default: return dispatch_rope<T, 128>(p, vec, halves, sm_count, s);
+  }
+}
+
+// ---- the cache ----
+
+struct CacheBytes {
+  size_t code, scale;
+};
+
+int validate_cache(const fa_cache* c, const int* table, int width, int B, CacheBytes* bytes) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !table) return FA_ERR_INVALID_ARGUMENT;
+  if (c->num_pages < 1 || c->H < 1 || width < 1 || B < 1) return FA_ERR_INVALID_ARGUMENT;
+  if (!head_dim_ok(c->D)) return FA_ERR_UNSUPPORTED;
+  if (c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(c->k) || !aligned16(c->v) || (reinterpret_cast<uintptr_t>(c->k_scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(c->v_scale) & 3u) || (reinterpret_cast<uintptr_t>(table) & 3u))
+    return FA_ERR_INVALID_ARGUMENT;
+  // (page, head) pairs are a coordinate of the tensor maps; positions are 32-bit
+  if ((int64_t)c->num_pages * c->H > INT_MAX || (int64_t)width * c->page_tokens > INT_MAX)
+    return FA_ERR_INVALID_ARGUMENT;
+  const size_t heads = (size_t)c->num_pages * c->H;
+  bytes->code = heads * c->page_tokens * c->D;
+  bytes->scale = heads * sizeof(float);
+  const void* p[4] = {c->k, c->v, c->k_scale, c->v_scale};
+  const size_t n[4] = {bytes->code, bytes->code, bytes->scale, bytes->scale};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = i + 1; j < 4; ++j)
+      if (ranges_overlap(p[i], n[i], p[j], n[j])) return FA_ERR_INVALID_ARGUMENT;
+    if (ranges_overlap(p[i], n[i], table, (size_t)B * width * sizeof(int))) return FA_ERR_INVALID_ARGUMENT;
+  }
+  return FA_OK;
+}
+
+bool overlaps_cache(const fa_cache* c, const CacheBytes& n, const void* p, size_t bytes) {
+  return ranges_overlap(p, bytes, c->k, n.code) || ranges_overlap(p, bytes, c->v, n.code) ||
+         ranges_overlap(p, bytes, c->k_scale, n.scale) || ranges_overlap(p, bytes, c->v_scale, n.scale);
+}
+
+// A per-sequence array of ints (or NULL where it may be left out).
+bool ints_ok(const int* a, bool optional) {
+  return a ? (reinterpret_cast<uintptr_t>(a) & 3u) == 0 : optional;
+}
+
+fa::CacheView view(const fa_cache* c, const int* table, int width) {
+  fa::CacheView v;
+  v.code[0] = static_cast<uint8_t*>(c->k);
+  v.code[1] = static_cast<uint8_t*>(c->v);
+  v.scale[0] = c->k_scale;
+  v.scale[1] = c->v_scale;
+  v.table = table;
+  v.width = width;
+  v.num_pages = c->num_pages;
+  v.H = c->H;
+  v.page = c->page_tokens;
+  return v;
+}
+
+template <int D, int PAGE>
+void launch_write(const fa::CacheWriteParams& p, bool vec, unsigned blocks, cudaStream_t s) {
+  if (vec)
+    fa::fa_cache_write_kernel<D, PAGE, true><<<blocks, fa::kQuantThreads, 0, s>>>(p);
+  else
+    fa::fa_cache_write_kernel<D, PAGE, false><<<blocks, fa::kQuantThreads, 0, s>>>(p);
+}
+
+template <int D>
+void launch_write(const fa::CacheWriteParams& p, bool vec, unsigned blocks, cudaStream_t s) {
+  switch (p.c.page) {
+    case 32: launch_write<D, 32>(p, vec, blocks, s); break;
+    case 64: launch_write<D, 64>(p, vec, blocks, s); break;
+    default: launch_write<D, 128>(p, vec, blocks, s); break;
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_rope(const fa_rope_axes* axes, const int* pos, long long pos_stride_b, const fa_tensor* q,
+            const fa_tensor* q_out, int Hq, const fa_tensor* k, const fa_tensor* k_out, int Hk, int B,
+            int N, int D, int dtype, int pairing, int inverse, void* stream) {
+  // ---- validation: no CUDA call before this block passes ----
+  if (!axes || !pos || !q || !q_out || !q->data || !q_out->data) return FA_ERR_INVALID_ARGUMENT;
+  if ((k == nullptr) != (k_out == nullptr) || (k && (!k->data || !k_out->data || Hk < 1)))
+    return FA_ERR_INVALID_ARGUMENT;
+  if (B < 1 || N < 1 || Hq < 1 || pos_stride_b < 0) return FA_ERR_INVALID_ARGUMENT;
+  if (!head_dim_ok(D)) return FA_ERR_UNSUPPORTED;
+  if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP16 && dtype != FA_DTYPE_FP32) return FA_ERR_UNSUPPORTED;
+  if (pairing != FA_ROPE_ADJACENT && pairing != FA_ROPE_HALVES) return FA_ERR_INVALID_ARGUMENT;
+  if (axes->count < 1 || axes->count > FA_ROPE_MAX_AXES) return FA_ERR_INVALID_ARGUMENT;
+  int sum = 0;
+  for (int a = 0; a < axes->count; ++a) {
+    if (axes->dims[a] < 2 || axes->dims[a] % 2 || axes->dims[a] > D) return FA_ERR_INVALID_ARGUMENT;
+    if (!(axes->theta[a] > 0.0) || !std::isfinite(axes->theta[a]) || !std::isfinite(axes->scale[a]))
+      return FA_ERR_INVALID_ARGUMENT;
+    sum += axes->dims[a];
+  }
+  if (sum != D) return FA_ERR_INVALID_ARGUMENT;
+  const int size = dtype == FA_DTYPE_FP32 ? 4 : 2;
+  const int nt = k ? 2 : 1;
+  const fa_tensor in[2] = {*q, k ? *k : *q}, out[2] = {*q_out, k_out ? *k_out : *q_out};
+  const int H[2] = {Hq, k ? Hk : 0};
+  if ((int64_t)Hq + H[1] > INT_MAX - fa::kRopeBatch) return FA_ERR_INVALID_ARGUMENT;
+  if ((reinterpret_cast<uintptr_t>(pos) & 3u)) return FA_ERR_INVALID_ARGUMENT;
+  const __int128 pos_n = (__int128)pos_stride_b * (B - 1) + (__int128)N * axes->count;
+  if (pos_n > ((__int128)1 << 58)) return FA_ERR_INVALID_ARGUMENT;
+  bool vec = true;
+  for (int i = 0; i < nt; ++i) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(in[i].data) | reinterpret_cast<uintptr_t>(out[i].data);
+    if (a % size) return FA_ERR_INVALID_ARGUMENT;
+    const int64_t ei = extent(in[i], B, H[i], N, D), eo = extent(out[i], B, H[i], N, D);
+    if (!ei || !eo || !writes_once(out[i], B, H[i], N, D)) return FA_ERR_INVALID_ARGUMENT;
+    if (ranges_overlap(out[i].data, (size_t)eo * size, pos, (size_t)pos_n * sizeof(int)))
+      return FA_ERR_INVALID_ARGUMENT;
+    vec = vec && rows16(in[i], B, H[i], N, size) && rows16(out[i], B, H[i], N, size);
+  }
+  for (int i = 0; i < nt; ++i)
+    for (int j = 0; j < nt; ++j) {
+      if (!(i == j && same(out[i], in[j])) && !apart(out[i], H[i], in[j], H[j], B, N, D, size))
+        return FA_ERR_INVALID_ARGUMENT;
+      if (i < j && !apart(out[i], H[i], out[j], H[j], B, N, D, size)) return FA_ERR_INVALID_ARGUMENT;
+    }
+
+  fa::RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  for (int i = 0; i < nt; ++i)
+    p.t[i] = fa::RopeTensor{in[i].data, out[i].data, in[i].stride_b, in[i].stride_h, in[i].stride_n,
+                            out[i].stride_b, out[i].stride_h, out[i].stride_n, H[i]};
+  p.pos = pos;
+  p.pos_b = pos_stride_b;
+  p.A = axes->count;
+  p.N = N;
+  p.heads = Hq + H[1];
+  p.tokens = (long long)B * N;
+  p.inverse = inverse ? 1 : 0;
+  int pair = 0;
+  for (int a = 0; a < axes->count; ++a)
+    for (int j = 0; j < axes->dims[a] / 2; ++j, ++pair) {
+      // turns per unit of position, modulo one, as a 64-bit fraction
+      const double f = axes->scale[a] * std::pow(axes->theta[a], -2.0 * j / axes->dims[a]) * 0.15915494309189535;
+      if (!std::isfinite(f)) return FA_ERR_INVALID_ARGUMENT;
+      const double frac = f - std::floor(f);  // in [0, 1]; 1 only for a tiny negative f
+      p.freq[pair] = frac < 1.0 ? (unsigned long long)(frac * 18446744073709551616.0) : 0ull;
+      p.axis[pair] = (unsigned char)a;
+    }
+  fa::DeviceState* st = nullptr;
+  const int rc = fa::current_device(&st);
+  if (rc != FA_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool halves = pairing == FA_ROPE_HALVES;
+  switch (dtype) {
+    case FA_DTYPE_BF16: return dispatch_rope<__nv_bfloat16>(D, p, vec, halves, st->sm_count, s);
+    case FA_DTYPE_FP16: return dispatch_rope<__half>(D, p, vec, halves, st->sm_count, s);
+    default: return dispatch_rope<float>(D, p, vec, halves, st->sm_count, s);
+  }
+}
+
+int fa_cache_write(const fa_cache* cache, const fa_tensor* k, const fa_tensor* v, const int* table, int table_width,
+                   const int* start, const int* count, int B, int N, void* stream) {
+  CacheBytes bytes;
+  int rc = validate_cache(cache, table, table_width, B, &bytes);
+  if (rc != FA_OK) return rc;
+  if (!k || !v || !k->data || !v->data || N < 1 || !ints_ok(start, false) || !ints_ok(count, true))
+    return FA_ERR_INVALID_ARGUMENT;
+  const int D = cache->D, H = cache->H, page = cache->page_tokens;
+  if ((int64_t)table_width * page + N > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
+  bool vec = true;
+  const fa_tensor* in[2] = {k, v};
+  for (int i = 0; i < 2; ++i) {
+    const int64_t e = extent(*in[i], B, H, N, D);
+    if (!e || (reinterpret_cast<uintptr_t>(in[i]->data) & 1u)) return FA_ERR_INVALID_ARGUMENT;
+    if (overlaps_cache(cache, bytes, in[i]->data, (size_t)e * 2)) return FA_ERR_INVALID_ARGUMENT;
+    vec = vec && rows16(*in[i], B, H, N, 2);
+  }
+  if (overlaps_cache(cache, bytes, start, (size_t)B * sizeof(int)) ||
+      (count && overlaps_cache(cache, bytes, count, (size_t)B * sizeof(int))))
+    return FA_ERR_INVALID_ARGUMENT;
+  fa::CacheWriteParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = view(cache, table, table_width);
+  for (int i = 0; i < 2; ++i) {
+    p.x[i] = static_cast<const __nv_bfloat16*>(in[i]->data);
+    p.xb[i] = in[i]->stride_b;
+    p.xh[i] = in[i]->stride_h;
+    p.xn[i] = in[i]->stride_n;
+  }
+  p.start = start;
+  p.count = count;
+  p.B = B;
+  p.N = N;
+  p.slots = (N + page - 2) / page + 1;  // N tokens from anywhere in a page
+  const int64_t blocks = 2LL * B * H * p.slots;
+  if (blocks > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
+
+  fa::DeviceState* st = nullptr;
+  rc = fa::current_device(&st);
+  if (rc != FA_OK) return rc;
+  p.status = st->status;
+  fa::log_launch("fa_cache_write_kernel<D=%d,page %d,%s> grid %lld x %d threads (%d pages a sequence and head at most)",
+                 D, page, vec ? "16-byte loads" : "scalar loads", (long long)blocks, fa::kQuantThreads, p.slots);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (D) {
+    case 32: launch_write<32>(p, vec, (unsigned)blocks, s); break;
+    case 64: launch_write<64>(p, vec, (unsigned)blocks, s); break;
+    default: launch_write<128>(p, vec, (unsigned)blocks, s); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_cache_read(const fa_cache* cache, const int* table, int table_width, const int* lens, const int* first,
+                  void* k_out, void* v_out, int B, int N, void* stream) {
+  CacheBytes bytes;
+  int rc = validate_cache(cache, table, table_width, B, &bytes);
+  if (rc != FA_OK) return rc;
+  if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) || N < 1 || !ints_ok(lens, false) ||
+      !ints_ok(first, true))
+    return FA_ERR_INVALID_ARGUMENT;
+  const int D = cache->D, H = cache->H;
+  const size_t out = (size_t)B * H * N * D * 2, ints = (size_t)B * sizeof(int);
+  void* outs[2] = {k_out, v_out};
+  for (int i = 0; i < 2; ++i)
+    if (overlaps_cache(cache, bytes, outs[i], out) || ranges_overlap(outs[i], out, lens, ints) ||
+        ranges_overlap(outs[i], out, first, ints) ||
+        ranges_overlap(outs[i], out, table, (size_t)B * table_width * sizeof(int)))
+      return FA_ERR_INVALID_ARGUMENT;
+  if (ranges_overlap(k_out, out, v_out, out)) return FA_ERR_INVALID_ARGUMENT;
+  const int64_t per = ((int64_t)N * (D / 16) + fa::kQuantThreads - 1) / fa::kQuantThreads;
+  if (per * B * H * 2 > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
+  fa::CacheReadParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = view(cache, table, table_width);
+  p.out[0] = static_cast<__nv_bfloat16*>(k_out);
+  p.out[1] = static_cast<__nv_bfloat16*>(v_out);
+  p.lens = lens;
+  p.first = first;
+  p.B = B;
+  p.N = N;
+  p.blocks = (int)per;
+
+  fa::DeviceState* st = nullptr;
+  rc = fa::current_device(&st);
+  if (rc != FA_OK) return rc;
+  p.status = st->status;
+  const unsigned blocks = (unsigned)(per * B * H * 2);
+  fa::log_launch("fa_cache_read_kernel<D=%d> grid %u x %d threads", D, blocks, fa::kQuantThreads);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (D) {
+    case 32: fa::fa_cache_read_kernel<32><<<blocks, fa::kQuantThreads, 0, s>>>(p); break;
+    case 64: fa::fa_cache_read_kernel<64><<<blocks, fa::kQuantThreads, 0, s>>>(p); break;
+    default: fa::fa_cache_read_kernel<128><<<blocks, fa::kQuantThreads, 0, s>>>(p); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_cache_workspace_bytes(int B, int Hq, int Hk, int Nq, int D, int table_width, int page_tokens) {
+  (void)B; (void)Hq; (void)Hk; (void)Nq; (void)D; (void)table_width; (void)page_tokens;
+  return 0;
+}
+
+int fa_fwd_cache(const void* q, const fa_cache* cache, const int* table, int table_width, const int* lens,
+                 const int* q_start, int causal, void* out, float* lse, int B, int Hq, int Nq, float scale,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  CacheBytes bytes;
+  int rc = validate_cache(cache, table, table_width, B, &bytes);
+  if (rc != FA_OK) return rc;
+  if (!q || !out || !lse || !aligned16(q) || !aligned16(out) || !aligned16(lse) || !ints_ok(lens, false) ||
+      !ints_ok(q_start, true))
+    return FA_ERR_INVALID_ARGUMENT;
+  if (Nq < 1 || Hq < 1 || Hq % cache->H) return FA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(scale)) return FA_ERR_INVALID_ARGUMENT;
+  const int D = cache->D;
+  const int64_t rows = (int64_t)B * Hq * Nq;
+  if ((int64_t)B * Hq > INT_MAX || rows > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
+  const size_t qb = (size_t)rows * D * 2, lb = (size_t)rows * 4, ints = (size_t)B * sizeof(int);
+  if (ranges_overlap(out, qb, q, qb) || ranges_overlap(out, qb, lse, lb) || ranges_overlap(lse, lb, q, qb) ||
+      overlaps_cache(cache, bytes, out, qb) || overlaps_cache(cache, bytes, lse, lb) ||
+      ranges_overlap(out, qb, table, (size_t)B * table_width * sizeof(int)) ||
+      ranges_overlap(lse, lb, table, (size_t)B * table_width * sizeof(int)) || ranges_overlap(out, qb, lens, ints) ||
+      ranges_overlap(lse, lb, lens, ints) || ranges_overlap(out, qb, q_start, ints) ||
+      ranges_overlap(lse, lb, q_start, ints))
+    return FA_ERR_INVALID_ARGUMENT;
+  const size_t need = fa_cache_workspace_bytes(B, Hq, cache->H, Nq, D, table_width, cache->page_tokens);
+  if (need) {
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need) return FA_ERR_INVALID_ARGUMENT;
+    if (ranges_overlap(workspace, need, q, qb) || ranges_overlap(workspace, need, out, qb) ||
+        ranges_overlap(workspace, need, lse, lb) || overlaps_cache(cache, bytes, workspace, need) ||
+        ranges_overlap(workspace, need, table, (size_t)B * table_width * sizeof(int)) ||
+        ranges_overlap(workspace, need, lens, ints) || ranges_overlap(workspace, need, q_start, ints))
+      return FA_ERR_INVALID_ARGUMENT;
+  }
+
+  fa::DeviceState* st = nullptr;
+  rc = fa::current_device(&st);
+  if (rc != FA_OK) return rc;
+  fa::CacheAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = view(cache, table, table_width);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.lens = lens;
+  p.q_start = q_start;
+  p.B = B;
+  p.Hq = Hq;
+  p.Nq = Nq;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.status = st->status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  fa::log_launch("fa_cache_rows_kernel<D=%d> grid %lld x 128 threads", D, (long long)rows);
+  switch (D) {
+    case 32: fa::fa_cache_rows_kernel<32><<<(unsigned)rows, 128, 0, s>>>(p); break;
+    case 64: fa::fa_cache_rows_kernel<64><<<(unsigned)rows, 128, 0, s>>>(p); break;
+    default: fa::fa_cache_rows_kernel<128><<<(unsigned)rows, 128, 0, s>>>(p); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -22,6 +22,7 @@
 
 #include "fa.h"
 #include "fa_attn_launch.h"
+#include "fa_host.h"
 #include "fa_log.h"
 #include "fa_quant.cuh"
 #include "fa_window_geom.h"
@@ -38,38 +39,16 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceState {
-  bool ready = false;
-  bool supported = false;
-  int device = 0;
-  int sm_count = 0;
-  int* status = nullptr;  // device address of g_device_status
-  int* debug_record = nullptr;  // device address of g_debug_record
-};
+using fa::aligned16;
+using fa::DeviceState;
+using fa::ranges_overlap;
+using fa::timeout_ns_from_env;
 
 std::mutex g_mutex;
 DeviceState g_devices[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-bool ranges_overlap(const void* a, size_t abytes, const void* b, size_t bbytes) {
-  if (!a || !b || abytes == 0 || bbytes == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + bbytes && b0 < a0 + abytes;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-unsigned long long timeout_ns_from_env() {
-  const char* e = std::getenv("FA_WAIT_TIMEOUT_MS");
-  if (e && *e) {
-    char* end = nullptr;
-    unsigned long long ms = std::strtoull(e, &end, 10);
-    if (end != e && ms > 0) return ms * 1000000ull;
-  }
-  return 2000ull * 1000000ull;  // 2 s per wait; a healthy wait lasts microseconds
-}
 
 // Set-up per device: capability check, SM count, driver entry point.
 int device_setup(int dev, DeviceState** out) {
@@ -107,6 +86,44 @@ int device_setup(int dev, DeviceState** out) {
   *out = &st;
   return FA_OK;
 }
+
+}  // namespace
+
+namespace fa {
+
+int current_device(DeviceState** out) {
+  const char* inject = std::getenv("FA_FAULT_INJECT");
+  if (inject && std::strcmp(inject, "launch") == 0) return FA_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  const int rc = device_setup(dev, out);
+  if (rc != FA_OK) return rc;
+  return (*out)->supported ? FA_OK : FA_ERR_UNSUPPORTED;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return g_encode; }
+
+bool ranges_overlap(const void* a, size_t abytes, const void* b, size_t bbytes) {
+  if (!a || !b || abytes == 0 || bbytes == 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + bbytes && b0 < a0 + abytes;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+unsigned long long timeout_ns_from_env() {
+  const char* e = std::getenv("FA_WAIT_TIMEOUT_MS");
+  if (e && *e) {
+    char* end = nullptr;
+    unsigned long long ms = std::strtoull(e, &end, 10);
+    if (end != e && ms > 0) return ms * 1000000ull;
+  }
+  return 2000ull * 1000000ull;  // 2 s per wait; a healthy wait lasts microseconds
+}
+
+}  // namespace fa
+
+namespace {
 
 // 3-D tensor map over a contiguous bf16 [BH][N][D] tensor; box = one chunk of
 // 128 rows (inner extent = the swizzle span), swizzled to match the UMMA
@@ -208,13 +225,8 @@ bool workspace_overlaps(const void* ws, size_t ws_bytes, const void* q, const vo
 int setup(const void* q, const void* k, const void* v, const float* mask, void* out, float* lse,
           int H, int Nq, int Nk, int D, float scale, const Shape& sh, fa::Params* prm,
           DeviceState** st) {
-  const char* inject = std::getenv("FA_FAULT_INJECT");
-  if (inject && std::strcmp(inject, "launch") == 0) return FA_ERR_CUDA;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
-  int rc = device_setup(dev, st);
+  const int rc = fa::current_device(st);
   if (rc != FA_OK) return rc;
-  if (!(*st)->supported) return FA_ERR_UNSUPPORTED;
 
   std::memset(prm, 0, sizeof(*prm));
   if (encode_map(&prm->tm_q, q, (int)sh.BH, Nq, D) != FA_OK ||
@@ -248,6 +260,7 @@ int setup(const void* q, const void* k, const void* v, const float* mask, void* 
   const char* plant = std::getenv("FA_DEBUG_PLANT");
   prm->debug_plant = (plant && std::strcmp(plant, "store") == 0) ? 1 : 0;
 #endif
+  const char* inject = std::getenv("FA_FAULT_INJECT");
   prm->inject_stall = (inject && std::strcmp(inject, "stall") == 0) ? 1 : 0;
   return FA_OK;
 }
@@ -657,6 +670,7 @@ const char* fa_status_string(int status) {
     case FA_ERR_CUDA: return "FA_ERR_CUDA";
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT";
     case FA_ERR_DEBUG_CHECK: return "FA_ERR_DEBUG_CHECK";
+    case FA_ERR_INDEX: return "FA_ERR_INDEX";
     default: return "FA_ERR_UNKNOWN";
   }
 }
