@@ -49,7 +49,7 @@ static int checks() {
 // Every tile of every unit is walked once, by one CTA, in order; a CTA has at
 // most two stretches that are not whole units, in different slots; the CTAs
 // of a unit are those between the owners of its first and last tile.
-static int walk(const std::vector<int>& lens, int units, int max_len, int grid) {
+static int walk(const std::vector<int>& lens, int units, int max_len, int ctas) {
   const int B = (int)lens.size();
   std::vector<long long> base(B + 1, 0);
   std::vector<int> nt(B);
@@ -59,10 +59,11 @@ static int walk(const std::vector<int>& lens, int units, int max_len, int grid) 
     base[b + 1] = base[b] + (long long)nt[b] * units;
   }
   const long long total = base[B];
+  const int grid = fa::cache_active(total, ctas);
   long long seen = 0;
   for (int c = 0; c < grid; ++c) {
     const long long t0 = fa::cache_range_begin(total, grid, c), t1 = fa::cache_range_begin(total, grid, c + 1);
-    if (t0 != seen || t1 < t0) return std::printf("range %d\n", c), 1;
+    if (t0 != seen || t1 <= t0) return std::printf("range %d\n", c), 1;
     int b0 = 0;
     while (b0 + 1 < B && base[b0 + 1] <= t0) ++b0;
     fa::CacheWalk w;
@@ -75,7 +76,8 @@ static int walk(const std::vector<int>& lens, int units, int max_len, int grid) 
         return std::printf("segment outside\n"), 1;
       const long long first = base[s.b] + (long long)s.unit * s.total;
       if (first + s.tile0 != seen) return std::printf("order\n"), 1;
-      for (long long t = seen; t < seen + s.ntiles; ++t)
+      // (a long stretch: its two ends only)
+      for (long long t = seen; t < seen + s.ntiles; t += s.ntiles > 5000 ? s.ntiles - 1 : 1)
         if (fa::cache_range_owner(total, grid, t) != c) return std::printf("owner\n"), 1;
       seen += s.ntiles;
       if (s.ntiles < s.total) {
@@ -101,7 +103,7 @@ int main() {
   }
   // 2^31 tokens a sequence, many heads: the tile count needs 64 bits
   if (fa::cache_range_begin(1LL << 45, 304, 304) != 1LL << 45) return std::printf("wide\n"), 1;
-  if (walk({INT_MAX - 127, 5, 0}, 3, INT_MAX - 127, 37) == 1) return 1;
+  if (walk({INT_MAX, 5, 0}, 3, INT_MAX, 37)) return 1;
   std::printf("ok\n");
   return 0;
 }

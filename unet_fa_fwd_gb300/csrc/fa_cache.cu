@@ -7,7 +7,9 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
+#include <mutex>
 
 #include "fa.h"
 #include "fa_cache_attn.cuh"
@@ -199,6 +201,93 @@ void launch_write(const fa::CacheWriteParams& p, bool vec, unsigned blocks, cuda
   }
 }
 
+// The attention's row tiles and workspace.  RT rows of a key head share a pass
+// over its tiles: 4, 8 or 16, the least that holds them all (a row costs its
+// share of the softmax, a second pass the whole stream of codes again).
+struct CachePlan {
+  int R, rt, row_tiles;
+  int64_t units;        // per batch entry
+  int64_t tiles;        // at most, all units
+  size_t part_o, total; // workspace: partial O, and with their maxima and sums
+};
+
+CachePlan cache_plan(int B, int Hq, int Hk, int Nq, int D, int width, int page) {
+  CachePlan l{};
+  l.R = (int)((int64_t)Hq / Hk * Nq);
+  l.rt = l.R <= 4 ? 4 : (l.R <= 8 ? 8 : 16);
+  l.row_tiles = (l.R + l.rt - 1) / l.rt;
+  l.units = (int64_t)Hk * l.row_tiles;
+  const int64_t per = fa::cache_tiles(width * page);
+  l.tiles = per * l.units * B;
+  if (per > 1) {  // a unit of one tile is never cut
+    const size_t slots = 2 * (size_t)(l.tiles < fa::kCacheMaxGrid ? l.tiles : fa::kCacheMaxGrid);
+    l.part_o = (slots * l.rt * D * sizeof(float) + 255) & ~size_t(255);
+    l.total = l.part_o + slots * l.rt * 2 * sizeof(float);
+  }
+  return l;
+}
+
+// Tensor map over a cache's codes [num_pages * H][page][D] bytes: one box is a
+// page of a head, swizzled over its D-byte rows as the MMA operands are.
+int encode_cache_map(CUtensorMap* map, void* base, const fa_cache* c) {
+  cuuint64_t dims[3] = {(cuuint64_t)c->D, (cuuint64_t)c->page_tokens, (cuuint64_t)c->num_pages * c->H};
+  cuuint64_t strides[2] = {(cuuint64_t)c->D, (cuuint64_t)c->D * c->page_tokens};
+  cuuint32_t box[3] = {(cuuint32_t)c->D, (cuuint32_t)c->page_tokens, 1u};
+  cuuint32_t estride[3] = {1u, 1u, 1u};
+  const CUtensorMapSwizzle sw = c->D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                            : (c->D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+  const CUresult r = fa::tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box,
+                                              estride, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D, int RT>
+int launch_cache_attn(fa::CacheAttnParams& p, const CachePlan& plan, const fa::DeviceState& st, cudaStream_t s) {
+  using C = fa::CacheCfg<D, RT>;
+  static std::mutex mu;
+  static int resident[64] = {};  // CTAs an SM holds, per device
+  int per_sm = 0;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    int& r = resident[st.device];
+    if (!r) {
+      int n = 0;
+      if (cudaFuncSetAttribute(fa::fa_cache_attn_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               C::SMEM_BYTES) != cudaSuccess ||
+          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fa::fa_cache_attn_kernel<D, RT>, fa::kCacheThreads,
+                                                        C::SMEM_BYTES) != cudaSuccess || n < 1)
+        return FA_ERR_CUDA;
+      r = n < 512 / C::TMEM_COLS ? n : 512 / C::TMEM_COLS;
+    }
+    per_sm = r;
+  }
+  int64_t grid = (int64_t)per_sm * st.sm_count;
+  if (grid > fa::kCacheMaxGrid) grid = fa::kCacheMaxGrid;
+  if (grid > plan.tiles) grid = plan.tiles;
+  p.ctas = (int)grid;
+  fa::log_launch("fa_cache_attn_kernel<D=%d,%d rows> grid %d x %d threads (%d per SM) smem %d B tmem %d cols "
+                 "stages %d, %lld units a sequence, %lld tiles at most", D, RT, p.ctas, fa::kCacheThreads, per_sm,
+                 C::SMEM_BYTES, C::TMEM_COLS, C::STAGES, (long long)plan.units, (long long)plan.tiles);
+  fa::fa_cache_attn_kernel<D, RT><<<p.ctas, fa::kCacheThreads, C::SMEM_BYTES, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (!plan.total) return FA_OK;  // no unit can be cut
+  const unsigned blocks = (unsigned)(plan.units * p.B);
+  fa::log_launch("fa_cache_merge_kernel<D=%d,%d rows> grid %u x 128 threads", D, RT, blocks);
+  fa::fa_cache_merge_kernel<D, RT><<<blocks, 128, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D>
+int launch_cache_attn(fa::CacheAttnParams& p, const CachePlan& plan, const fa::DeviceState& st, cudaStream_t s) {
+  switch (plan.rt) {
+    case 4: return launch_cache_attn<D, 4>(p, plan, st, s);
+    case 8: return launch_cache_attn<D, 8>(p, plan, st, s);
+    default: return launch_cache_attn<D, 16>(p, plan, st, s);
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -380,8 +469,10 @@ int fa_cache_read(const fa_cache* cache, const int* table, int table_width, cons
 }
 
 size_t fa_cache_workspace_bytes(int B, int Hq, int Hk, int Nq, int D, int table_width, int page_tokens) {
-  (void)B; (void)Hq; (void)Hk; (void)Nq; (void)D; (void)table_width; (void)page_tokens;
-  return 0;
+  if (B < 1 || Hk < 1 || Hq < 1 || Hq % Hk || Nq < 1 || !head_dim_ok(D) || table_width < 1 || page_tokens < 1 ||
+      (int64_t)Hq / Hk * Nq > INT_MAX || (int64_t)table_width * page_tokens > INT_MAX)
+    return 0;
+  return cache_plan(B, Hq, Hk, Nq, D, table_width, page_tokens).total;
 }
 
 int fa_fwd_cache(const void* q, const fa_cache* cache, const int* table, int table_width, const int* lens,
@@ -406,7 +497,9 @@ int fa_fwd_cache(const void* q, const fa_cache* cache, const int* table, int tab
       ranges_overlap(lse, lb, lens, ints) || ranges_overlap(out, qb, q_start, ints) ||
       ranges_overlap(lse, lb, q_start, ints))
     return FA_ERR_INVALID_ARGUMENT;
-  const size_t need = fa_cache_workspace_bytes(B, Hq, cache->H, Nq, D, table_width, cache->page_tokens);
+  const CachePlan plan = cache_plan(B, Hq, cache->H, Nq, D, table_width, cache->page_tokens);
+  if (plan.units * B > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
+  const size_t need = plan.total;
   if (need) {
     if (!workspace || !aligned16(workspace) || workspace_bytes < need) return FA_ERR_INVALID_ARGUMENT;
     if (ranges_overlap(workspace, need, q, qb) || ranges_overlap(workspace, need, out, qb) ||
@@ -428,19 +521,28 @@ int fa_fwd_cache(const void* q, const fa_cache* cache, const int* table, int tab
   p.lens = lens;
   p.q_start = q_start;
   p.B = B;
-  p.Hq = Hq;
   p.Nq = Nq;
   p.causal = causal ? 1 : 0;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.status = st->status;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  fa::log_launch("fa_cache_rows_kernel<D=%d> grid %lld x 128 threads", D, (long long)rows);
-  switch (D) {
-    case 32: fa::fa_cache_rows_kernel<32><<<(unsigned)rows, 128, 0, s>>>(p); break;
-    case 64: fa::fa_cache_rows_kernel<64><<<(unsigned)rows, 128, 0, s>>>(p); break;
-    default: fa::fa_cache_rows_kernel<128><<<(unsigned)rows, 128, 0, s>>>(p); break;
+  p.R = plan.R;
+  p.row_tiles = plan.row_tiles;
+  p.max_len = table_width * cache->page_tokens;
+  if (need) {
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_o);
   }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  p.timeout_ns = fa::timeout_ns_from_env();
+  const char* inject = std::getenv("FA_FAULT_INJECT");
+  p.inject_stall = (inject && std::strcmp(inject, "stall") == 0) ? 1 : 0;
+  if (encode_cache_map(&p.tm_k, cache->k, cache) != FA_OK || encode_cache_map(&p.tm_v, cache->v, cache) != FA_OK)
+    return FA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (D) {
+    case 32: return launch_cache_attn<32>(p, plan, *st, s);
+    case 64: return launch_cache_attn<64>(p, plan, *st, s);
+    default: return launch_cache_attn<128>(p, plan, *st, s);
+  }
 }
 
 }  // extern "C"

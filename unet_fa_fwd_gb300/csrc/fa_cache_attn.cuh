@@ -2,10 +2,42 @@
 //   t_ij = scale * q_i . k_j,  O_i = sum_j softmax_j(t_ij) v_j,
 //   LSE_i = ln sum_j e^(t_ij),
 // over the keys j < len[b], with `causal` j <= q_start[b] + i too.  Query head
-// hq reads key head hq / (Hq / Hk).  A row that sees no key gives O = 0 and
+// hq reads key head hq / (Hq / H).  A row that sees no key gives O = 0 and
 // LSE = -inf.
+//
+// The rows of a key head's queries (its Hq / H query heads times Nq rows) are
+// few here, so the products are taken the other way round: the 128 keys of a
+// tile are the M side of the MMA and the rows the N side,
+//   S^T [128 keys, rows] = K Q^T,   O^T [D channels, rows] = V^T P^T,
+// and the codes go from HBM to the tensor cores as they are: TMA copies pages
+// into shared memory and kind::f8f6f4 reads them as its A operand (K with the
+// channels contiguous, V transposed).  No thread ever touches a code.
+//
+// What the e4m3 side cannot hold in one number is split over several N
+// columns, each the rounding of what the one before left, scaled up by 16:
+//   q = s (hi + lo / 16)               (s: a power of two a row; exact for
+//     elements above 2^-14 of the row's largest, bf16 having 8 bits and e4m3
+//     four; below, off by 2^-23 of it),
+//   p = hi + mid / 16 + lo / 256       (12 bits, or 2^-25 of the row's largest p).
+// The columns are extra work for the tensor cores only, which have time: the
+// kernel is HBM bound.  Sums are fp32 throughout; each tile's O^T is added to
+// fp32 registers (so a page's scale of V is applied outside the MMA, and O is
+// rescaled there when the running maximum moves).
+//
+// Within a tile pages may differ in their scale of V: p carries the ratio of
+// the page's scale to the tile's largest (a power of two <= 1), so the 2^-25
+// above is relative to the largest V of the 128 tokens.
+//
+// All units' tiles (fa_cache_geom.h) are cut into equal ranges, one per CTA, so
+// ragged lengths and few heads balance alike; a unit cut between CTAs leaves
+// fp32 partial results that fa_cache_merge_kernel joins in a fixed order.
+//
+// Warps: 0-3 softmax (thread = key of the tile, and channel of O), 4 producer
+// (page numbers, scales, TMA), 5 MMA issuer and owner of tensor memory.  Waits
+// are bounded as in the forward kernel.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <climits>
 #include <cstdint>
@@ -16,81 +48,623 @@
 
 namespace fa {
 
+constexpr int kCacheStatusTimeout = 4;  // == FA_ERR_TIMEOUT
+constexpr int kCacheMaxGrid = 1024;     // partial results are sized for this many CTAs
+constexpr int kCacheThreads = 192;
+constexpr int kCacheStagesMax = 8;
+
 struct CacheAttnParams {
+  CUtensorMap tm_k, tm_v;  // [num_pages * H][page][D] bytes
   CacheView c;
-  const __nv_bfloat16* q;  // [B][Hq][Nq][D]
+  const __nv_bfloat16* q;  // [B][Hq][Nq][D]: the rows of a key head are contiguous
   __nv_bfloat16* out;      // [B][Hq][Nq][D]
   float* lse;              // [B][Hq][Nq]
   const int* lens;         // [B]
   const int* q_start;      // [B] or nullptr: len - Nq
-  int B, Hq, Nq, causal;
+  float* part_o;           // [2 * ctas][RT][D]
+  float* part_ml;          // [2 * ctas][RT][2]: maximum (log2 domain), sum
+  int B, Nq, causal;
+  int R;                   // rows of a key head: Hq / H * Nq
+  int row_tiles;           // ceil(R / RT)
+  int max_len;             // width * page
+  int ctas;                // of the attention kernel's launch
   float scale_log2;
   int* status;
+  unsigned long long timeout_ns;
+  int inject_stall;        // test hook: CTA 0 withholds its second tile
 };
 
-// One block per query row: 128 keys at a time, one key per thread for the
-// scores, one channel per thread for the values.
-template <int D>
-__global__ void __launch_bounds__(128) fa_cache_rows_kernel(const __grid_constant__ CacheAttnParams p) {
-  __shared__ float q[D], prob[128], red[4];
-  __shared__ int ids[128];
-  const int tid = threadIdx.x;
-  const long long row = blockIdx.x;
-  const int i = (int)(row % p.Nq);
-  const int hq = (int)(row / p.Nq % p.Hq), b = (int)(row / p.Nq / p.Hq);
-  const int h = hq / (p.Hq / p.c.H);
-  bool bad = false;
-  const int most = (int)min((long long)p.c.width * p.c.page, (long long)INT32_MAX);
-  const int len = cache_clamp(p.lens[b], most, bad);
-  long long last = len;
-  if (p.causal) last = min(last, (long long)(p.q_start ? p.q_start[b] : len - p.Nq) + i + 1);
-  if (tid < D) q[tid] = __bfloat162float(p.q[row * D + tid]) * p.scale_log2;
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  auto block_max = [&](float x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    if ((tid & 31) == 0) red[tid >> 5] = x;
-    __syncthreads();
-    return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  };
-  for (long long k0 = 0; k0 < last; k0 += 128) {
-    __syncthreads();
-    const long long key = k0 + tid;
-    float t = -INFINITY;
-    if (key < last) {
-      const int index = (int)(key / p.c.page);
-      const int id = cache_page(p.c.table[(long long)b * p.c.width + index], p.c.num_pages, bad);
-      ids[tid] = id;
-      const long long base = (long long)id * p.c.H + h;
-      const uint8_t* kr = p.c.code[0] + (base * p.c.page + key % p.c.page) * D;
-      float dot = 0.f;
-      for (int d = 0; d < D; d += 2) {
-        const float2 f = e4m3x2_value(*reinterpret_cast<const uint16_t*>(kr + d));
-        dot = fmaf(q[d], f.x, fmaf(q[d + 1], f.y, dot));
-      }
-      t = dot * p.c.scale[0][base];
+template <int D, int RT>
+struct CacheCfg {
+  static constexpr int TILE_BYTES = kCacheTile * D;      // 128 tokens of K or V
+  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+  static constexpr int NS = (2 * RT + 15) / 16 * 16;     // N of S^T: hi and lo of each row
+  static constexpr int NO = (3 * RT + 15) / 16 * 16;     // N of O^T: hi, mid, lo
+  static constexpr uint32_t LAYOUT = D == 128 ? 2u : (D == 64 ? 4u : 6u);  // swizzle over a token's D bytes
+  static constexpr int SBO = 8 * D;
+  static constexpr int STAGES = D == 128 ? 3 : (D == 64 ? 4 : 6);
+  static constexpr int SMEM_Q = (NS * D + 1023) / 1024 * 1024;
+  static constexpr int SMEM_P = NO * kCacheTile;         // K-major: 128 keys of a column contiguous
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SMEM_Q + SMEM_P + 2048;
+  static constexpr int COL_S = 0, COL_O = 2 * NS;
+  static constexpr int TMEM_COLS = 2 * NS + NO <= 64 ? 64 : 128;
+  static_assert(2 * NS + NO <= 128, "tensor memory");
+  static_assert(STAGES <= kCacheStagesMax, "ring barriers");
+};
+
+struct CacheBars {
+  uint64_t kv_full[kCacheStagesMax], kv_empty[kCacheStagesMax];
+  uint64_t s_full[2], p_ready, pv_done, q_ready, drain;
+  long long total, t0, t1, base0;
+  int grid, b0;
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  int wg_fail;
+  float ks[kCacheStagesMax][4], vs[kCacheStagesMax][4];  // scales of a tile's pages
+  float c[16];     // row: multiplier of the raw product, times the page's scale of K
+  int lim[16];     // row: its last visible key
+  float red[4][16];
+};
+static_assert(sizeof(CacheBars) <= 2048, "barrier space");
+
+__device__ __forceinline__ uint64_t cache_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
+         (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)layout << 61;
+}
+
+// Byte (row, col) of a K-major operand of W-byte rows, swizzled over W bytes.
+template <int W>
+__device__ __forceinline__ uint32_t cache_swizzle(int row, int col) {
+  const int x = W == 128 ? (row & 7) : (W == 64 ? ((row >> 1) & 3) : ((row >> 2) & 1));
+  return (uint32_t)(row * W + ((((col >> 4) ^ x) << 4) | (col & 15)));
+}
+
+// Bounded wait of a whole warp; false once the CTA is giving up.
+__device__ __forceinline__ bool cache_wait(uint64_t* bar, uint32_t parity, CacheBars* bars,
+                                           const CacheAttnParams& p) {
+  const uint32_t a = ptx::smem_u32(bar);
+  if (__all_sync(0xffffffffu, ptx::mbar_try_wait(a, parity))) return true;
+  bool ok = false;
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (true) {
+    if (ptx::mbar_try_wait_sleep(a, parity, 20000u)) {
+      ok = true;
+      break;
     }
-    const float m_new = fmaxf(m, block_max(t));
-    const float e = t == -INFINITY ? 0.f : exp2f(t - m_new);
-    prob[tid] = e;
-    __syncthreads();
-    const float alpha = m == -INFINITY ? 0.f : exp2f(m - m_new);
-    m = m_new;
-    l *= alpha;
-    acc *= alpha;
-    const int n = (int)min(128LL, last - k0);
-    for (int j = 0; j < n; ++j) {
-      l += prob[j];
-      if (tid < D) {
-        const long long base = (long long)ids[j] * p.c.H + h;
-        const float v = e4m3x2_value(p.c.code[1][(base * p.c.page + (k0 + j) % p.c.page) * D + tid]).x;
-        acc = fmaf(prob[j] * p.c.scale[1][base], v, acc);
-      }
+    if (bars->abort_flag) break;
+    if (ptx::global_timer_ns() - t0 > p.timeout_ns) {
+      bars->abort_flag = 1;
+      atomicCAS(p.status, 0, kCacheStatusTimeout);
+      break;
     }
   }
-  if (tid < D) p.out[row * D + tid] = __float2bfloat16_rn(l > 0.f ? acc / l : l);
-  if (tid == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l);
-  if (bad) atomicCAS(p.status, 0, kStatusIndex);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Wait (bounded) for copies or MMAs in flight before the CTA ends.
+__device__ __forceinline__ void cache_drain(uint64_t* bar, uint32_t parity, const CacheAttnParams& p) {
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (!ptx::mbar_try_wait(ptx::smem_u32(bar), parity) && ptx::global_timer_ns() - t0 < p.timeout_ns) {
+  }
+}
+
+// OR of a predicate over the four softmax warps (also a barrier among them).
+__device__ __forceinline__ bool cache_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      ".reg .pred p, q;\n"
+      "setp.ne.u32 p, %1, 0;\n"
+      "barrier.cta.red.or.pred q, 2, 128, p;\n"
+      "selp.u32 %0, 1, 0, q;\n"
+      "}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+// The tile range of this CTA and the batch entry it starts in (one warp).
+__device__ __forceinline__ void cache_plan(const CacheAttnParams& p, int units, uint32_t lane, CacheBars* bars) {
+  bool bad = false;
+  long long total = 0;
+  for (int b = (int)lane; b < p.B; b += 32) total += cache_tiles(cache_clamp(p.lens[b], p.max_len, bad));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= units;
+  const int grid = cache_active(total, p.ctas), c = (int)blockIdx.x;
+  const long long t0 = c < grid ? cache_range_begin(total, grid, c) : total;
+  const long long t1 = c < grid ? cache_range_begin(total, grid, c + 1) : total;
+  long long base = 0, base0 = 0;
+  int b0 = 0;
+  for (int b = 0; b < p.B; b += 32) {
+    bool unused = false;
+    const int i = b + (int)lane;
+    const long long n = i < p.B ? (long long)cache_tiles(cache_clamp(p.lens[i], p.max_len, unused)) * units : 0;
+    long long incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if ((int)lane >= o) incl += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, i < p.B && base + incl > t0);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      b0 = b + src;
+      base0 = base + __shfl_sync(0xffffffffu, incl - n, src);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) atomicCAS(p.status, 0, kStatusIndex);
+  if (lane == 0) {
+    bars->total = total;
+    bars->grid = grid;
+    bars->t0 = t0;
+    bars->t1 = t1;
+    bars->b0 = b0;
+    bars->base0 = base0;
+  }
+}
+
+template <int D, int RT>
+__global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
+  using C = CacheCfg<D, RT>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sRing = smem;
+  uint8_t* sQ = sRing + C::STAGES * C::STAGE_BYTES;
+  uint8_t* sP = sQ + C::SMEM_Q;
+  CacheBars* bars = reinterpret_cast<CacheBars*>(sP + C::SMEM_P);
+  const int warp = threadIdx.x / 32, tid = threadIdx.x;
+  const uint32_t lane = threadIdx.x % 32;
+  const int units = p.c.H * p.row_tiles;
+
+  if (tid == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->kv_empty[s]), 1);
+    }
+    ptx::mbar_init(ptx::smem_u32(&bars->s_full[0]), 1);
+    ptx::mbar_init(ptx::smem_u32(&bars->s_full[1]), 1);
+    ptx::mbar_init(ptx::smem_u32(&bars->p_ready), 128);
+    ptx::mbar_init(ptx::smem_u32(&bars->q_ready), 128);
+    ptx::mbar_init(ptx::smem_u32(&bars->pv_done), 1);
+    ptx::mbar_init(ptx::smem_u32(&bars->drain), 1);
+    bars->abort_flag = 0;
+    bars->wg_fail = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 4) cache_plan(p, units, lane, bars);
+  if (warp == 5) {
+    ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), C::TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  CacheWalk walk;
+  walk.start(p.lens, p.B, units, p.max_len, bars->t0, bars->t1, bars->b0, bars->base0);
+  CacheSegment sg;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer --
+    if (lane == 0) {
+      ptx::tma_prefetch_desc(&p.tm_k);
+      ptx::tma_prefetch_desc(&p.tm_v);
+    }
+    const int page = p.c.page, ppt = kCacheTile / page;  // pages of a tile
+    const int batch = 32 / ppt;                          // tiles whose pages the lanes hold
+    uint32_t it = 0, skipped = 0xffffffffu;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const int h = sg.unit / p.row_tiles;
+      const int npages = sg.len == 0 ? 0 : (sg.len - 1) / page + 1;
+      const int* row = p.c.table + (long long)sg.b * p.c.width;
+      int id = 0;
+      float ks = 0.f, vs = 0.f;
+      for (int j = 0; j < sg.ntiles; ++j, ++it) {
+        const int in_batch = j % batch;
+        if (in_batch == 0) {  // the lanes fetch the next 32 pages' numbers and scales
+          const int idx = (sg.tile0 + j) * ppt + (int)lane;
+          bool bad = false;
+          id = 0;
+          ks = vs = 0.f;
+          if (idx < npages && idx < (sg.tile0 + sg.ntiles) * ppt) {
+            id = cache_page(row[idx], p.c.num_pages, bad);
+            const long long at = (long long)id * p.c.H + h;
+            ks = p.c.scale[0][at];
+            vs = p.c.scale[1][at];
+          }
+          if (bad) atomicCAS(p.status, 0, kStatusIndex);
+        }
+        const uint32_t s = it % C::STAGES;
+        ok = cache_wait(&bars->kv_empty[s], ((it / C::STAGES) & 1) ^ 1, bars, p);
+        if (!ok) break;
+        if (p.inject_stall && blockIdx.x == 0 && it == 1) {  // nothing arrives: consumers time out
+          skipped = it;
+          continue;
+        }
+        const int src = in_batch * ppt + (int)(lane % ppt);
+        const int my_id = __shfl_sync(0xffffffffu, id, src);
+        const float my_ks = __shfl_sync(0xffffffffu, ks, src), my_vs = __shfl_sync(0xffffffffu, vs, src);
+        const int first = (sg.tile0 + j) * ppt;
+        const int n = max(0, min(ppt, npages - first));  // pages of this tile that hold tokens
+        if ((int)lane < ppt) {
+          bars->ks[s][lane] = my_ks;
+          bars->vs[s][lane] = my_vs;
+        }
+        const uint32_t full = ptx::smem_u32(&bars->kv_full[s]);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full, (uint32_t)(2 * n * page * D));
+        __syncwarp();
+        if ((int)lane < n) {
+          const uint32_t dst = ptx::smem_u32(sRing + s * C::STAGE_BYTES) + lane * page * D;
+          const int at = my_id * p.c.H + h;
+          ptx::tma_load_3d(dst, &p.tm_k, full, 0, 0, at);
+          ptx::tma_load_3d(dst + C::TILE_BYTES, &p.tm_v, full, 0, 0, at);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) {
+      // Drain: every copy issued has landed once its stage's last phase is complete.
+      for (int s = 0; s < C::STAGES; ++s) {
+        uint32_t n = it > (uint32_t)s ? (it - 1 - s) / C::STAGES + 1 : 0;
+        if (skipped < it && skipped % C::STAGES == (uint32_t)s) --n;
+        if (n) cache_drain(&bars->kv_full[s], (n - 1) & 1, p);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ----------------------------------------------------------------- MMA --
+    constexpr uint32_t kIdesc = (1u << 4) | (8u << 24);  // e4m3 x e4m3, fp32 sums, M = 128
+    constexpr uint32_t IDESC_S = kIdesc | ((uint32_t)(C::NS >> 3) << 17);
+    constexpr uint32_t IDESC_O = kIdesc | ((uint32_t)(C::NO >> 3) << 17) | (1u << 15);  // A = V, transposed
+    const uint64_t dk = cache_desc(ptx::smem_u32(sRing), 16, C::SBO, C::LAYOUT);
+    // V as the transposed A: 8 tokens x D channels per swizzle atom.  M is 128
+    // whatever D is: with a leading offset of 0 the channels repeat (their
+    // lanes of O^T are not read).
+    const uint64_t dv = cache_desc(ptx::smem_u32(sRing) + C::TILE_BYTES, 0, C::SBO, C::LAYOUT);
+    const uint64_t dq = cache_desc(ptx::smem_u32(sQ), 16, C::SBO, C::LAYOUT);
+    const uint64_t dp = cache_desc(ptx::smem_u32(sP), 16, 1024, 2u);
+    auto issue_s = [&](uint32_t stage, uint32_t buf) {
+      const uint32_t a = (uint32_t)dk + stage * (C::STAGE_BYTES >> 4), d = tmem + C::COL_S + buf * C::NS;
+      if constexpr (D == 128)
+        ptx::mma_ss_f8_x4_el<2, 4, 6>(d, a, (uint32_t)(dk >> 32), (uint32_t)dq, (uint32_t)(dq >> 32), IDESC_S, 0);
+      else if constexpr (D == 64)
+        ptx::mma_ss_f8_x2_el<2>(d, a, (uint32_t)(dk >> 32), (uint32_t)dq, (uint32_t)(dq >> 32), IDESC_S, 0);
+      else
+        ptx::mma_ss_f8_x1_el(d, a, (uint32_t)(dk >> 32), (uint32_t)dq, (uint32_t)(dq >> 32), IDESC_S, 0);
+    };
+    auto issue_o = [&](uint32_t stage) {
+      const uint32_t a = (uint32_t)dv + stage * (C::STAGE_BYTES >> 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)  // 32 keys each
+        ptx::mma_ss_f8_x1_el(tmem + C::COL_O, a + k * (32 * D >> 4), (uint32_t)(dv >> 32), (uint32_t)dp + k * 2,
+                             (uint32_t)(dp >> 32), IDESC_O, k ? 1u : 0u);
+    };
+    uint32_t it = 0, seg = 0;  // tiles and segments so far
+    bool ok = true;
+    // P of tile n is ready: its product, which also frees its stage.
+    auto finish_tile = [&](uint32_t n) -> bool {
+      if (!cache_wait(&bars->p_ready, n & 1, bars, p)) return false;
+      ptx::tc_fence_after_sync();
+      issue_o(n % C::STAGES);
+      ptx::mma_commit_el(ptx::smem_u32(&bars->kv_empty[n % C::STAGES]));
+      ptx::mma_commit_el(ptx::smem_u32(&bars->pv_done));
+      return true;
+    };
+    while (ok && walk.next(sg)) {
+      ok = cache_wait(&bars->q_ready, seg & 1, bars, p);
+      ++seg;
+      if (!ok) break;
+      for (int j = 0; j < sg.ntiles; ++j, ++it) {
+        ok = cache_wait(&bars->kv_full[it % C::STAGES], (it / C::STAGES) & 1, bars, p);
+        if (!ok) break;
+        ptx::tc_fence_after_sync();
+        // The other S buffer was read before P of tile it - 2 was released.
+        issue_s(it % C::STAGES, it & 1);
+        ptx::mma_commit_el(ptx::smem_u32(&bars->s_full[it & 1]));
+        if (j > 0) ok = finish_tile(it - 1);
+        if (!ok) break;
+      }
+      if (ok) ok = finish_tile(it - 1);
+    }
+    ptx::mma_commit_el(ptx::smem_u32(&bars->drain));
+    cache_drain(&bars->drain, 0, p);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax --
+    // p is kept between 2^-25 and 2^8.75 (e4m3's largest is 448) by a running
+    // reference m: on the first tile, and whenever a score passes m + 8.75, m
+    // becomes the row's maximum less 7.
+    constexpr float kTop = 7.f, kLimit = 8.75f, kNone = -1e30f;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const uint32_t tS = tmem + lane_base + C::COL_S, tO = tmem + lane_base + C::COL_O;
+    uint32_t it = 0;
+    bool fail = false;
+    while (walk.next(sg)) {
+      const int h = sg.unit / p.row_tiles, rt = sg.unit - h * p.row_tiles;
+      const long long bh = (long long)sg.b * p.c.H + h;
+      const int rows = min(RT, p.R - rt * RT);
+      // Q: each warp splits rows warp, warp + 4, ... into hi and lo columns.
+      {
+        constexpr int PER = D / 32;
+        const long long start = p.q_start ? p.q_start[sg.b] : sg.len - p.Nq;
+        for (int r = warp; r < RT; r += 4) {
+          float x[PER];
+          uint32_t amax = 0;
+          const bool in = r < rows;
+          if (in) {
+            const __nv_bfloat16* src = p.q + (bh * p.R + rt * RT + r) * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+              x[e] = __bfloat162float(src[e]);
+              amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[e] = 0.f;
+          }
+          amax = __reduce_max_sync(0xffffffffu, amax);
+          // 2^e: the least power of two with amax <= 448 * 2^e (not below 2^-100)
+          const int e2 = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+          const float inv = __int_as_float((127 - e2) << 23);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            const float v = x[e] * inv;
+            const uint32_t hi = e4m3x2_bits(v, 0.f);
+            const float left = (v - e4m3x2_value(hi).x) * 16.f;
+            const uint32_t lo = e4m3x2_bits(left, 0.f);
+            sQ[cache_swizzle<D>(2 * r, (int)lane * PER + e)] = (uint8_t)hi;
+            sQ[cache_swizzle<D>(2 * r + 1, (int)lane * PER + e)] = (uint8_t)lo;
+          }
+          if (lane == 0) {
+            // a row that holds a number that is not finite gives NaN
+            bars->c[r] = amax >= 0x7f800000u ? __int_as_float(0x7fc00000)
+                                             : __int_as_float((e2 + 127) << 23) * p.scale_log2;
+            long long lim = sg.len - 1;
+            if (p.causal) lim = min(lim, start + (rt * RT + r) % p.Nq);
+            bars->lim[r] = (int)max(lim, -1LL);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready));
+        ptx::named_barrier_sync(3, 128);
+      }
+      float m[RT], l[RT], o[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        m[r] = kNone;
+        l[r] = o[r] = 0.f;
+      }
+      float v_scale = 0.f;   // of the tile whose O^T is still to be added
+      bool pending = false;
+      // Adds the last tile's O^T, in units of the current m, to o.
+      auto take_o = [&]() {
+        if (!cache_wait(&bars->pv_done, (it - 1) & 1, bars, p)) fail = true;
+        ptx::tc_fence_after_sync();
+        uint32_t r0[16];
+        if constexpr (RT == 4) {
+          ptx::tmem_ld32x32b_x16(tO, r0);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            o[r] += v_scale * (__uint_as_float(r0[3 * r]) + 0.0625f * __uint_as_float(r0[3 * r + 1]) +
+                               0.00390625f * __uint_as_float(r0[3 * r + 2]));
+        } else {
+          uint32_t r1[32];
+          float f[48];
+          ptx::tmem_ld32x32b_x32(tO, r1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r1[i]);
+          if constexpr (RT == 16) {
+            ptx::tmem_ld32x32b_x16(tO + 32, r0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[32 + i] = __uint_as_float(r0[i]);
+          }
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            o[r] += v_scale * (f[3 * r] + 0.0625f * f[3 * r + 1] + 0.00390625f * f[3 * r + 2]);
+        }
+        pending = false;
+      };
+
+      bool stop = false;
+      for (int j = 0; j < sg.ntiles; ++j) {
+        const uint32_t s = it % C::STAGES;
+        const int key = (sg.tile0 + j) * kCacheTile + tid;
+        const int in_page = tid / p.c.page;
+        if (!cache_wait(&bars->kv_full[s], (it / C::STAGES) & 1, bars, p)) fail = true;
+        const float ks = bars->ks[s][in_page], vs = bars->vs[s][in_page];
+        float vt = bars->vs[s][0];  // the tile's largest scale of V (pages without tokens have 0)
+        for (int i = 1; i < kCacheTile / p.c.page; ++i) vt = fmaxf(vt, bars->vs[s][i]);
+        if (!cache_wait(&bars->s_full[it & 1], (it >> 1) & 1, bars, p)) fail = true;
+        ptx::tc_fence_after_sync();
+        float t[RT];
+        bool need = false;
+        {
+          auto scores = [&](const uint32_t* sv) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              const float raw = fmaf(__uint_as_float(sv[2 * r + 1]), 0.0625f, __uint_as_float(sv[2 * r]));
+              t[r] = key <= bars->lim[r] ? raw * (bars->c[r] * ks) : -INFINITY;
+              need = need || t[r] - m[r] > kLimit;
+            }
+          };
+          if constexpr (C::NS == 16) {
+            uint32_t sv[16];
+            ptx::tmem_ld32x32b_x16(tS + (it & 1) * C::NS, sv);
+            scores(sv);
+          } else {
+            uint32_t sv[32];
+            ptx::tmem_ld32x32b_x32(tS + (it & 1) * C::NS, sv);
+            scores(sv);
+          }
+        }
+        if (cache_any(need || fail)) {
+          if (pending) take_o();
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            float x = t[r];
+#pragma unroll
+            for (int k = 16; k; k >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+            if (lane == 0) bars->red[warp][r] = x;
+          }
+          if (fail) bars->wg_fail = 1;
+          ptx::named_barrier_sync(3, 128);
+          if (bars->wg_fail) {
+            stop = true;
+            break;
+          }
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const float x = fmaxf(fmaxf(bars->red[0][r], bars->red[1][r]), fmaxf(bars->red[2][r], bars->red[3][r]));
+            if (x - m[r] > kLimit) {
+              const float alpha = ptx::ex2(m[r] - (x - kTop));
+              m[r] = x - kTop;
+              l[r] *= alpha;
+              o[r] *= alpha;
+            }
+          }
+        }
+        const float ratio = vt > 0.f ? vs / vt : 0.f;
+        float pr[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const float e = ptx::ex2(t[r] - m[r]);
+          l[r] += e;
+          pr[r] = e * ratio;
+        }
+        if (pending) take_o();  // P and O^T are free once the last tile's product is done
+#pragma unroll
+        for (int r = 0; r < RT; r += 2) {
+          const uint32_t hi = e4m3x2_bits(pr[r], pr[r + 1]);
+          const float2 h = e4m3x2_value(hi);
+          const float a0 = (pr[r] - h.x) * 16.f, a1 = (pr[r + 1] - h.y) * 16.f;
+          const uint32_t mid = e4m3x2_bits(a0, a1);
+          const float2 g = e4m3x2_value(mid);
+          const uint32_t lo = e4m3x2_bits((a0 - g.x) * 16.f, (a1 - g.y) * 16.f);
+          sP[cache_swizzle<128>(3 * r, tid)] = (uint8_t)hi;
+          sP[cache_swizzle<128>(3 * r + 1, tid)] = (uint8_t)mid;
+          sP[cache_swizzle<128>(3 * r + 2, tid)] = (uint8_t)lo;
+          sP[cache_swizzle<128>(3 * r + 3, tid)] = (uint8_t)(hi >> 8);
+          sP[cache_swizzle<128>(3 * r + 4, tid)] = (uint8_t)(mid >> 8);
+          sP[cache_swizzle<128>(3 * r + 5, tid)] = (uint8_t)(lo >> 8);
+        }
+        // Rows of V past the length may hold anything, NaN among it: zero them.
+        const int held = sg.len - (sg.tile0 + j) * kCacheTile;
+        if (held < kCacheTile) {
+          uint8_t* sV = sRing + s * C::STAGE_BYTES + C::TILE_BYTES;
+          for (int i = max(held, 0) * D + tid * 16; i < C::TILE_BYTES; i += 128 * 16)
+            *reinterpret_cast<uint4*>(sV + i) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        ptx::tc_fence_before_sync();
+        ptx::mbar_arrive(ptx::smem_u32(&bars->p_ready));
+        v_scale = vt;
+        pending = true;
+        ++it;
+      }
+      if (!stop && pending) take_o();
+      if (cache_any(fail || stop)) break;
+
+      // The row's sum over the 128 threads.
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float x = l[r];
+#pragma unroll
+        for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+        if (lane == 0) bars->red[warp][r] = x;
+      }
+      ptx::named_barrier_sync(3, 128);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) l[r] = bars->red[0][r] + bars->red[1][r] + bars->red[2][r] + bars->red[3][r];
+      if (sg.ntiles == sg.total) {
+        const long long row0 = bh * p.R + rt * RT;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          if (r >= rows) break;
+          if (tid < D) p.out[(row0 + r) * D + tid] = __float2bfloat16_rn(l[r] == 0.f ? 0.f : o[r] / l[r]);
+          if (tid == r) p.lse[row0 + r] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * 0.6931471805599453f;
+        }
+      } else {
+        const long long unit_t0 = walk.base + (long long)sg.unit * sg.total;
+        const long long slot = cache_slot(bars->total, bars->grid, (int)blockIdx.x, unit_t0);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          if (r >= rows) break;
+          if (tid < D) p.part_o[(slot * RT + r) * D + tid] = o[r];
+          if (tid == r) {
+            p.part_ml[(slot * RT + r) * 2] = m[r];
+            p.part_ml[(slot * RT + r) * 2 + 1] = l[r];
+          }
+        }
+      }
+    }
+    ptx::tc_fence_before_sync();
+  }
+  __syncthreads();
+  if (warp == 5) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Joins the partial results of the units that were cut between CTAs: for each
+// row, over its pieces s in order, m = max m_s, l = sum 2^(m_s - m) l_s,
+// O = sum 2^(m_s - m) O_s / l.  One block a unit, thread = channel.
+template <int D, int RT>
+__global__ void __launch_bounds__(128) fa_cache_merge_kernel(const __grid_constant__ CacheAttnParams p) {
+  const int tid = threadIdx.x;
+  const int units = p.c.H * p.row_tiles;
+  const int b = blockIdx.x / units, unit = blockIdx.x - b * units;
+  __shared__ long long sums[2][4];
+  long long before = 0, total = 0;
+  bool bad = false;
+  for (int i = tid; i < p.B; i += 128) {
+    const int n = cache_tiles(cache_clamp(p.lens[i], p.max_len, bad));
+    total += n;
+    if (i < b) before += n;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if ((tid & 31) == 0) {
+    sums[0][tid >> 5] = total;
+    sums[1][tid >> 5] = before;
+  }
+  __syncthreads();
+  total = (sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3]) * units;
+  before = (sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3]) * units;
+  const int nt = cache_tiles(cache_clamp(p.lens[b], p.max_len, bad));
+  const long long first = before + (long long)unit * nt;
+  const int grid = cache_active(total, p.ctas);
+  const int c0 = cache_range_owner(total, grid, first), c1 = cache_range_owner(total, grid, first + nt - 1);
+  if (c0 == c1) return;  // written by the attention kernel
+  const int h = unit / p.row_tiles, rt = unit - h * p.row_tiles;
+  const int rows = min(RT, p.R - rt * RT);
+  const long long row0 = ((long long)b * p.c.H + h) * p.R + rt * RT;
+  for (int r = 0; r < rows; ++r) {
+    float m = -INFINITY;
+    for (int c = c0; c <= c1; ++c) {
+      const float* ml = p.part_ml + ((long long)cache_slot(total, grid, c, first) * RT + r) * 2;
+      m = ml[1] == 0.f ? m : fmaxf(m, ml[0]);
+    }
+    float l = 0.f, o = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+      const long long at = (long long)cache_slot(total, grid, c, first) * RT + r;
+      const float lc = p.part_ml[at * 2 + 1];
+      if (lc == 0.f) continue;  // no key of this piece is visible
+      const float w = ptx::ex2(p.part_ml[at * 2] - m);
+      l = fmaf(w, lc, l);
+      if (tid < D) o = fmaf(w, p.part_o[at * D + tid], o);
+    }
+    if (tid < D) p.out[(row0 + r) * D + tid] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+    if (tid == 0) p.lse[row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
 }
 
 }  // namespace fa

@@ -49,11 +49,15 @@ FA_HD int cache_page(int id, int num_pages, bool& bad) {
 // A unit is one (batch entry, key head, row tile); it has as many 128-key
 // tiles as its batch entry's length (at least one, so that an empty sequence
 // still gets its outputs written).  The tiles of all units in order are cut
-// into G equal ranges, one per CTA.
+// into equal ranges, one per CTA; no range is empty, so with fewer tiles than
+// CTAs the last CTAs have none.
 constexpr int kCacheTile = 128;
 
-FA_HD int cache_tiles(int len) { return len <= 0 ? 1 : (len + kCacheTile - 1) / kCacheTile; }
+FA_HD int cache_tiles(int len) { return len <= 0 ? 1 : (len - 1) / kCacheTile + 1; }
 
+FA_HD int cache_active(long long total, int ctas) { return total < ctas ? (int)total : ctas; }
+
+// `grid` below is cache_active(total, ctas).
 FA_HD long long cache_range_begin(long long total, int grid, int cta) {
   return total / grid * cta + total % grid * cta / grid;  // floor(total * cta / grid)
 }
