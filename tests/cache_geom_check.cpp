@@ -47,43 +47,62 @@ static int checks() {
 }
 
 // Every tile of every unit is walked once, by one CTA, in order; a CTA has at
-// most two stretches that are not whole units, in different slots; the CTAs
-// of a unit are those between the owners of its first and last tile.
-static int walk(const std::vector<int>& lens, int units, int max_len, int ctas) {
+// most two stretches that are not whole units, in different slots; tiles past
+// a unit's last visible key are left out.
+static int walk(const std::vector<int>& lens, const std::vector<int>& starts, int H, int g, int Nq, int RT, int causal,
+                int max_len, int ctas) {
   const int B = (int)lens.size();
+  fa::CacheRows rows{lens.data(), starts.empty() ? nullptr : starts.data(), B, H, g, Nq, g * Nq, RT,
+                     (g * Nq + RT - 1) / RT, causal, max_len};
+  struct Unit { int b, h, rt; long long t0; int nt; };
+  std::vector<Unit> units;
   std::vector<long long> base(B + 1, 0);
-  std::vector<int> nt(B);
+  long long total = 0;
   for (int b = 0; b < B; ++b) {
     const long long len = lens[b] < 0 ? 0 : (lens[b] > max_len ? max_len : lens[b]);
-    nt[b] = len == 0 ? 1 : (int)((len + 127) / 128);
-    base[b + 1] = base[b] + (long long)nt[b] * units;
+    const long long first = starts.empty() ? len - Nq : starts[b];
+    for (int h = 0; h < H; ++h)
+      for (int rt = 0; rt < rows.row_tiles; ++rt) {
+        long long keys = len;
+        if (causal) {  // the largest count of keys that a row of the tile sees
+          keys = 0;
+          for (int r = rt * RT; r < (rt + 1) * RT && r < g * Nq; ++r) {
+            const long long n = first + r / g + 1;
+            if (n > keys) keys = n;
+          }
+          if (keys > len) keys = len;
+        }
+        const int nt = keys <= 0 ? 1 : (int)((keys + 127) / 128);
+        units.push_back({b, h, rt, total, nt});
+        total += nt;
+      }
+    base[b + 1] = total;
   }
-  const long long total = base[B];
   const int grid = fa::cache_active(total, ctas);
   long long seen = 0;
+  size_t u = 0;
   for (int c = 0; c < grid; ++c) {
     const long long t0 = fa::cache_range_begin(total, grid, c), t1 = fa::cache_range_begin(total, grid, c + 1);
     if (t0 != seen || t1 <= t0) return std::printf("range %d\n", c), 1;
     int b0 = 0;
     while (b0 + 1 < B && base[b0 + 1] <= t0) ++b0;
     fa::CacheWalk w;
-    w.start(lens.data(), B, units, max_len, t0, t1, b0, base[b0]);
+    w.start(rows, t0, t1, b0, base[b0]);
     fa::CacheSegment s;
     int used = 0;
     while (w.next(s)) {
-      if (s.b < 0 || s.b >= B || s.unit < 0 || s.unit >= units || s.ntiles < 1 || s.total != nt[s.b] ||
-          s.tile0 < 0 || s.tile0 + s.ntiles > s.total)
-        return std::printf("segment outside\n"), 1;
-      const long long first = base[s.b] + (long long)s.unit * s.total;
-      if (first + s.tile0 != seen) return std::printf("order\n"), 1;
+      while (seen >= units[u].t0 + units[u].nt) ++u;
+      const Unit& x = units[u];
+      if (s.b != x.b || s.h != x.h || s.rt != x.rt || s.unit_t0 != x.t0 || s.total != x.nt || s.ntiles < 1 ||
+          s.tile0 < 0 || s.tile0 + s.ntiles > s.total || s.unit_t0 + s.tile0 != seen)
+        return std::printf("segment\n"), 1;
       // (a long stretch: its two ends only)
       for (long long t = seen; t < seen + s.ntiles; t += s.ntiles > 5000 ? s.ntiles - 1 : 1)
         if (fa::cache_range_owner(total, grid, t) != c) return std::printf("owner\n"), 1;
       seen += s.ntiles;
       if (s.ntiles < s.total) {
-        const int slot = fa::cache_slot(total, grid, c, first) - 2 * c;
-        if (slot != (first > t0 ? 1 : 0) || (used >> slot) & 1)
-          return std::printf("slot\n"), 1;
+        const int slot = fa::cache_slot(c, t0, s.unit_t0) - 2 * c;
+        if (slot != (s.unit_t0 > t0 ? 1 : 0) || (used >> slot) & 1) return std::printf("slot\n"), 1;
         used |= 1 << slot;
       }
     }
@@ -96,14 +115,18 @@ int main() {
   if (scales() || checks()) return 1;
   std::mt19937 r(7);
   for (int i = 0; i < 3000; ++i) {
-    const int B = 1 + r() % 9, units = 1 + r() % 12, max_len = 1 + r() % 4000;
-    std::vector<int> lens(B);
+    const int B = 1 + r() % 9, H = 1 + r() % 5, g = 1 + r() % 5, max_len = 1 + r() % 4000;
+    const int Nq = r() % 3 ? 1 + r() % 8 : 1 + r() % 300, RT = 4 << r() % 7;
+    std::vector<int> lens(B), starts;
     for (int& n : lens) n = r() % 10 == 0 ? (r() % 2 ? -5 : INT_MAX) : (int)(r() % (max_len + 1));
-    if (walk(lens, units, max_len, 1 + r() % 400)) return 1;
+    if (r() % 3 == 0)
+      for (int b = 0; b < B; ++b)
+        starts.push_back(r() % 8 == 0 ? (r() % 2 ? INT_MIN : INT_MAX) : (int)(r() % (max_len + 1)) - 50);
+    if (walk(lens, starts, H, g, Nq, RT, r() % 2, max_len, 1 + r() % 400)) return 1;
   }
   // 2^31 tokens a sequence, many heads: the tile count needs 64 bits
   if (fa::cache_range_begin(1LL << 45, 304, 304) != 1LL << 45) return std::printf("wide\n"), 1;
-  if (walk({INT_MAX, 5, 0}, 3, INT_MAX, 37)) return 1;
+  if (walk({INT_MAX, 5, 0}, {}, 3, 2, 1, 4, 1, INT_MAX, 37)) return 1;
   std::printf("ok\n");
   return 0;
 }

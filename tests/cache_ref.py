@@ -70,7 +70,8 @@ def tile_weight(v, page):
 
 def attend(q, k, v, scale, causal=False, q_start=None):
     """One sequence: q [Hq, Nq, D], k, v [Hk, L, D] in 64 bits.  Returns O, LSE, the mean of |v|
-    under each row's probabilities, and the largest sum_d |q k| * |scale| over a row's keys."""
+    under each row's probabilities, and over a row's keys the largest sum_d |q k| |scale| and
+    max |q| sum_d |k| |scale|."""
     Hq, Nq, D = q.shape
     Hk, L = k.shape[:2]
     q = q.double()
@@ -81,9 +82,10 @@ def attend(q, k, v, scale, causal=False, q_start=None):
         seen = torch.arange(L, device=q.device) <= first + torch.arange(Nq, device=q.device)[:, None]
     if L == 0 or not seen.any():
         z = torch.zeros(Hq, Nq, D, dtype=torch.float64, device=q.device)
-        return z, torch.full((Hq, Nq), -math.inf, dtype=torch.float64, device=q.device), z, z[..., 0]
+        return z, torch.full((Hq, Nq), -math.inf, dtype=torch.float64, device=q.device), z, z[..., 0], z[..., 0]
     t = torch.where(seen, q @ k.transpose(1, 2) * scale, -math.inf)
     lse = torch.logsumexp(t, -1)
     p = torch.where(seen, torch.exp(t - lse[..., None]), 0.0).nan_to_num(0.0)
     size = (q.abs() @ k.abs().transpose(1, 2) * abs(scale) * seen).amax(-1)
-    return p @ v, lse, p @ v.abs(), size
+    spread = q.abs().amax(-1) * abs(scale) * k.abs().sum(-1).amax(-1)[:, None]
+    return p @ v, lse, p @ v.abs(), size, spread

@@ -1,13 +1,15 @@
 """The paged e4m3 cache and the attention to it on the GPU, against 64-bit
 definitions (tests/cache_ref.py).
 
-Attention tolerance.  With A = sum_j p_j |v_j| (a row's mean of |v|) and
-Q = max_j sum_d |scale q_d k_jd|:
-  * scores: the codes are exact and q is held to 2^-22 of its row's largest
-    element; the tensor cores' fp32 sums are within 2^-19 of the sum of
-    magnitudes: |dt| <= 2^-18 Q, plus 2^-22 |t| for the fp32 products and the
-    2^-22 of ex2: together dt <= 2^-17 Q + 2^-21 moves every p by that factor
-    and LSE by dt;
+Attention tolerance.  With A = sum_j p_j |v_j| (a row's mean of |v|),
+Q = max_j sum_d |scale q_d k_jd| and Q' = max_j |scale| max_d |q_d| sum_d |k_jd|:
+  * scores: the codes are exact.  q is held in two e4m3 numbers, the row's
+    largest element at 224 or more; the second's least step (2^-9 for many
+    rows, where it has the first's scale) leaves 2^-10 / 224 < 2^-17.8 of the
+    largest element: 2^-17.8 Q'.  The tensor cores' fp32 sums are within 2^-19
+    of the sum of magnitudes (2^-18 Q with the two parts), and 2^-22 |t| for the
+    fp32 products and 2^-22 for ex2: together
+    dt <= 2^-17 Q + 2^-17.8 Q' + 2^-21 moves every p by that factor and LSE by dt;
   * p is held in 12 bits, or rounded to bf16 for long chunks (half a step:
     2^-8), so sum p v moves by at most 2^-8 A;
   * 12 bits end at e4m3's subnormals: with the row's largest p at 2^7 or more,
@@ -80,9 +82,9 @@ def _filled(B, lens, H, page, D, seed, spread=0.0):
 
 
 def _close(out, lse, want, v, page, label=""):
-    o, l, a, size = want
+    o, l, a, size, spread = want
     n_keys = v.shape[1]
-    dt = size * 2.0 ** -17 + 2.0 ** -21
+    dt = size * 2.0 ** -17 + spread * 2.0 ** -17.8 + 2.0 ** -21
     tol = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2 * dt[..., None] + n_keys / 32 * 2.0 ** -24) * a
     if n_keys:
         floor = 2.0 ** -24 * ref.tile_weight(v.double(), page).sum(1)  # 2^-25, and the weight's factor of 2

@@ -13,6 +13,7 @@
 
 #include "fa.h"
 #include "fa_cache_attn.cuh"
+#include "fa_cache_chunk.cuh"
 #include "fa_cache_quant.cuh"
 #include "fa_host.h"
 #include "fa_log.h"
@@ -202,27 +203,32 @@ void launch_write(const fa::CacheWriteParams& p, bool vec, unsigned blocks, cuda
 }
 
 // The attention's row tiles and workspace.  RT rows of a key head share a pass
-// over its tiles: 4, 8 or 16, the least that holds them all (a row costs its
-// share of the softmax, a second pass the whole stream of codes again).
+// over its tiles: 4, 8 or 16, the least that holds them all, in the kernel for
+// few rows (a row costs its share of the softmax, a second pass the whole
+// stream of codes again); 256 in the one for many, from kCacheFewRows on.
+constexpr int kCacheFewRows = 32;
+
 struct CachePlan {
   int R, rt, row_tiles;
   int64_t units;        // per batch entry
   int64_t tiles;        // at most, all units
-  size_t part_o, total; // workspace: partial O, and with their maxima and sums
+  size_t part_o, cut, total;  // workspace: partial O; up to their maxima and sums; in all
 };
 
 CachePlan cache_plan(int B, int Hq, int Hk, int Nq, int D, int width, int page) {
   CachePlan l{};
   l.R = (int)((int64_t)Hq / Hk * Nq);
-  l.rt = l.R <= 4 ? 4 : (l.R <= 8 ? 8 : 16);
+  l.rt = l.R > kCacheFewRows ? fa::kChunkRows : (l.R <= 4 ? 4 : (l.R <= 8 ? 8 : 16));
   l.row_tiles = (l.R + l.rt - 1) / l.rt;
   l.units = (int64_t)Hk * l.row_tiles;
   const int64_t per = fa::cache_tiles(width * page);
   l.tiles = per * l.units * B;
   if (per > 1) {  // a unit of one tile is never cut
-    const size_t slots = 2 * (size_t)(l.tiles < fa::kCacheMaxGrid ? l.tiles : fa::kCacheMaxGrid);
+    const int64_t most = l.rt == fa::kChunkRows ? fa::kChunkMaxGrid : fa::kCacheMaxGrid;
+    const size_t slots = 2 * (size_t)(l.tiles < most ? l.tiles : most);
     l.part_o = (slots * l.rt * D * sizeof(float) + 255) & ~size_t(255);
-    l.total = l.part_o + slots * l.rt * 2 * sizeof(float);
+    l.cut = l.part_o + ((slots * l.rt * 2 * sizeof(float) + 255) & ~size_t(255));
+    l.total = l.cut + slots / 2 * sizeof(int4);
   }
   return l;
 }
@@ -241,6 +247,22 @@ int encode_cache_map(CUtensorMap* map, void* base, const fa_cache* c) {
                                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+// Launches a merge so that its blocks may start while the kernel before it on
+// the stream finishes (it waits for that kernel itself).
+int launch_after(void (*kernel)(const fa::CacheAttnParams), unsigned blocks, unsigned threads,
+                 const fa::CacheAttnParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D, int RT>
@@ -273,15 +295,43 @@ int launch_cache_attn(fa::CacheAttnParams& p, const CachePlan& plan, const fa::D
   fa::fa_cache_attn_kernel<D, RT><<<p.ctas, fa::kCacheThreads, C::SMEM_BYTES, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (!plan.total) return FA_OK;  // no unit can be cut
-  const unsigned blocks = (unsigned)(plan.units * p.B);
+  const unsigned blocks = (unsigned)p.ctas * RT;
   fa::log_launch("fa_cache_merge_kernel<D=%d,%d rows> grid %u x 128 threads", D, RT, blocks);
-  fa::fa_cache_merge_kernel<D, RT><<<blocks, 128, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_after(fa::fa_cache_merge_kernel<D, RT>, blocks, 128, p, s);
+}
+
+template <int D>
+int launch_cache_chunk(fa::CacheAttnParams& p, const CachePlan& plan, const fa::DeviceState& st, cudaStream_t s) {
+  using C = fa::ChunkCfg<D>;
+  static std::mutex mu;
+  static bool ready[64] = {};
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[st.device]) {
+      if (cudaFuncSetAttribute(fa::fa_cache_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               C::SMEM_BYTES) != cudaSuccess)
+        return FA_ERR_CUDA;
+      ready[st.device] = true;
+    }
+  }
+  int64_t grid = st.sm_count < fa::kChunkMaxGrid ? st.sm_count : fa::kChunkMaxGrid;
+  if (grid > plan.tiles) grid = plan.tiles;
+  p.ctas = (int)grid;
+  fa::log_launch("fa_cache_chunk_kernel<D=%d> grid %d x %d threads smem %d B tmem 512 cols stages %d + %d, %lld units "
+                 "a sequence, %lld tiles at most", D, p.ctas, fa::kChunkThreads, C::SMEM_BYTES, C::K_STAGES,
+                 C::V_STAGES, (long long)plan.units, (long long)plan.tiles);
+  fa::fa_cache_chunk_kernel<D><<<p.ctas, fa::kChunkThreads, C::SMEM_BYTES, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (!plan.total) return FA_OK;  // no unit can be cut
+  const unsigned blocks = (unsigned)p.ctas * (D / 16);
+  fa::log_launch("fa_cache_chunk_merge_kernel<D=%d> grid %u x %d threads", D, blocks, fa::kChunkRows);
+  return launch_after(fa::fa_cache_chunk_merge_kernel<D>, blocks, fa::kChunkRows, p, s);
 }
 
 template <int D>
 int launch_cache_attn(fa::CacheAttnParams& p, const CachePlan& plan, const fa::DeviceState& st, cudaStream_t s) {
   switch (plan.rt) {
+    case fa::kChunkRows: return launch_cache_chunk<D>(p, plan, st, s);
     case 4: return launch_cache_attn<D, 4>(p, plan, st, s);
     case 8: return launch_cache_attn<D, 8>(p, plan, st, s);
     default: return launch_cache_attn<D, 16>(p, plan, st, s);
@@ -518,19 +568,14 @@ int fa_fwd_cache(const void* q, const fa_cache* cache, const int* table, int tab
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  p.lens = lens;
-  p.q_start = q_start;
-  p.B = B;
-  p.Nq = Nq;
-  p.causal = causal ? 1 : 0;
+  p.rows = fa::CacheRows{lens, q_start, B, cache->H, Hq / cache->H, Nq, plan.R, plan.rt, plan.row_tiles,
+                         causal ? 1 : 0, table_width * cache->page_tokens};
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.status = st->status;
-  p.R = plan.R;
-  p.row_tiles = plan.row_tiles;
-  p.max_len = table_width * cache->page_tokens;
   if (need) {
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_o);
+    p.cut = reinterpret_cast<int4*>(static_cast<char*>(workspace) + plan.cut);
   }
   p.timeout_ns = fa::timeout_ns_from_env();
   const char* inject = std::getenv("FA_FAULT_INJECT");

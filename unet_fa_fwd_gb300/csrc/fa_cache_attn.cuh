@@ -53,25 +53,40 @@ constexpr int kCacheMaxGrid = 1024;     // partial results are sized for this ma
 constexpr int kCacheThreads = 192;
 constexpr int kCacheStagesMax = 8;
 
+// A CTA's range of tiles.
+struct CacheRange {
+  long long total, t0, t1, base0;  // tiles in all; the range; first tile of entry b0
+  int grid, b0;                    // CTAs with a range; the batch entry that holds t0
+};
+
 struct CacheAttnParams {
   CUtensorMap tm_k, tm_v;  // [num_pages * H][page][D] bytes
   CacheView c;
-  const __nv_bfloat16* q;  // [B][Hq][Nq][D]: the rows of a key head are contiguous
+  CacheRows rows;
+  const __nv_bfloat16* q;  // [B][Hq][Nq][D]
   __nv_bfloat16* out;      // [B][Hq][Nq][D]
   float* lse;              // [B][Hq][Nq]
-  const int* lens;         // [B]
-  const int* q_start;      // [B] or nullptr: len - Nq
   float* part_o;           // [2 * ctas][RT][D]
   float* part_ml;          // [2 * ctas][RT][2]: maximum (log2 domain), sum
-  int B, Nq, causal;
-  int R;                   // rows of a key head: Hq / H * Nq
-  int row_tiles;           // ceil(R / RT)
-  int max_len;             // width * page
+  int4* cut;               // [ctas]: the unit that starts in a CTA's range and goes on past it
   int ctas;                // of the attention kernel's launch
   float scale_log2;
   int* status;
   unsigned long long timeout_ns;
   int inject_stall;        // test hook: CTA 0 withholds its second tile
+
+  // cut[c]: batch entry (-1: no such unit), key head, row tile, and the CTA that
+  // holds its last tile times two, plus one if its first piece is in slot 1.
+  __device__ __forceinline__ void note_cut(const CacheSegment& s, const CacheRange& range) const {
+    if (s.tile0 != 0 || s.ntiles == s.total) return;
+    const int last = cache_range_owner(range.total, range.grid, s.unit_t0 + s.total - 1);
+    cut[blockIdx.x] = make_int4(s.b, s.h, s.rt, 2 * last + (s.unit_t0 > range.t0 ? 1 : 0));
+  }
+  // Row of q, out and lse of row r of a key head.
+  __device__ __forceinline__ long long row_at(int b, int h, int r) const {
+    const int i = r / rows.g;
+    return (((long long)b * rows.H + h) * rows.g + (r - i * rows.g)) * rows.Nq + i;
+  }
 };
 
 template <int D, int RT>
@@ -95,8 +110,7 @@ struct CacheCfg {
 struct CacheBars {
   uint64_t kv_full[kCacheStagesMax], kv_empty[kCacheStagesMax];
   uint64_t s_full[2], p_ready, pv_done, q_ready, drain;
-  long long total, t0, t1, base0;
-  int grid, b0;
+  CacheRange plan;
   uint32_t tmem_base;
   volatile int abort_flag;
   int wg_fail;
@@ -120,8 +134,8 @@ __device__ __forceinline__ uint32_t cache_swizzle(int row, int col) {
 }
 
 // Bounded wait of a whole warp; false once the CTA is giving up.
-__device__ __forceinline__ bool cache_wait(uint64_t* bar, uint32_t parity, CacheBars* bars,
-                                           const CacheAttnParams& p) {
+template <typename Bars>
+__device__ __forceinline__ bool cache_wait(uint64_t* bar, uint32_t parity, Bars* bars, const CacheAttnParams& p) {
   const uint32_t a = ptx::smem_u32(bar);
   if (__all_sync(0xffffffffu, ptx::mbar_try_wait(a, parity))) return true;
   bool ok = false;
@@ -165,29 +179,34 @@ __device__ __forceinline__ bool cache_any(bool x) {
 }
 
 // The tile range of this CTA and the batch entry it starts in (one warp).
-__device__ __forceinline__ void cache_plan(const CacheAttnParams& p, int units, uint32_t lane, CacheBars* bars) {
+__device__ __forceinline__ void cache_plan(const CacheRows& rows, int ctas, int* status, uint32_t lane,
+                                           CacheRange* out) {
   bool bad = false;
+  auto tiles = [&](int b) -> long long {
+    if (b >= rows.B) return 0;
+    const int len = rows.len(b, bad);
+    return rows.head_tiles(len, rows.first(b, len)) * rows.H;
+  };
   long long total = 0;
-  for (int b = (int)lane; b < p.B; b += 32) total += cache_tiles(cache_clamp(p.lens[b], p.max_len, bad));
+  const long long mine = tiles((int)lane);  // of the first 32 entries, used again below
+  for (int b = (int)lane; b < rows.B; b += 32) total += b < 32 ? mine : tiles(b);
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= units;
-  const int grid = cache_active(total, p.ctas), c = (int)blockIdx.x;
+  const int grid = cache_active(total, ctas), c = (int)blockIdx.x;
   const long long t0 = c < grid ? cache_range_begin(total, grid, c) : total;
   const long long t1 = c < grid ? cache_range_begin(total, grid, c + 1) : total;
   long long base = 0, base0 = 0;
   int b0 = 0;
-  for (int b = 0; b < p.B; b += 32) {
-    bool unused = false;
+  for (int b = 0; b < rows.B && t0 < total; b += 32) {
     const int i = b + (int)lane;
-    const long long n = i < p.B ? (long long)cache_tiles(cache_clamp(p.lens[i], p.max_len, unused)) * units : 0;
+    const long long n = b == 0 ? mine : tiles(i);
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
       if ((int)lane >= o) incl += v;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, i < p.B && base + incl > t0);
+    const uint32_t past = __ballot_sync(0xffffffffu, i < rows.B && base + incl > t0);
     if (past) {
       const int src = __ffs(past) - 1;
       b0 = b + src;
@@ -196,15 +215,8 @@ __device__ __forceinline__ void cache_plan(const CacheAttnParams& p, int units, 
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) atomicCAS(p.status, 0, kStatusIndex);
-  if (lane == 0) {
-    bars->total = total;
-    bars->grid = grid;
-    bars->t0 = t0;
-    bars->t1 = t1;
-    bars->b0 = b0;
-    bars->base0 = base0;
-  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) atomicCAS(status, 0, kStatusIndex);
+  if (lane == 0) *out = CacheRange{total, t0, t1, base0, grid, b0};
 }
 
 template <int D, int RT>
@@ -217,9 +229,9 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
   CacheBars* bars = reinterpret_cast<CacheBars*>(sP + C::SMEM_P);
   const int warp = threadIdx.x / 32, tid = threadIdx.x;
   const uint32_t lane = threadIdx.x % 32;
-  const int units = p.c.H * p.row_tiles;
 
   if (tid == 0) {
+    if (p.cut) p.cut[blockIdx.x].x = -1;
     for (int s = 0; s < C::STAGES; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&bars->kv_empty[s]), 1);
@@ -234,7 +246,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
     bars->wg_fail = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 4) cache_plan(p, units, lane, bars);
+  if (warp == 4) cache_plan(p.rows, p.ctas, p.status, lane, &bars->plan);
   if (warp == 5) {
     ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), C::TMEM_COLS);
     ptx::tmem_relinquish();
@@ -244,7 +256,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
   ptx::tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
   CacheWalk walk;
-  walk.start(p.lens, p.B, units, p.max_len, bars->t0, bars->t1, bars->b0, bars->base0);
+  walk.start(p.rows, bars->plan.t0, bars->plan.t1, bars->plan.b0, bars->plan.base0);
   CacheSegment sg;
 
   if (warp == 4) {
@@ -258,7 +270,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
     uint32_t it = 0, skipped = 0xffffffffu;
     bool ok = true;
     while (ok && walk.next(sg)) {
-      const int h = sg.unit / p.row_tiles;
+      const int h = sg.h;
       const int npages = sg.len == 0 ? 0 : (sg.len - 1) / page + 1;
       const int* row = p.c.table + (long long)sg.b * p.c.width;
       int id = 0;
@@ -385,19 +397,16 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
     uint32_t it = 0;
     bool fail = false;
     while (walk.next(sg)) {
-      const int h = sg.unit / p.row_tiles, rt = sg.unit - h * p.row_tiles;
-      const long long bh = (long long)sg.b * p.c.H + h;
-      const int rows = min(RT, p.R - rt * RT);
+      const int row0 = sg.rt * RT, rows = min(RT, p.rows.R - row0);
       // Q: each warp splits rows warp, warp + 4, ... into hi and lo columns.
       {
         constexpr int PER = D / 32;
-        const long long start = p.q_start ? p.q_start[sg.b] : sg.len - p.Nq;
         for (int r = warp; r < RT; r += 4) {
           float x[PER];
           uint32_t amax = 0;
           const bool in = r < rows;
           if (in) {
-            const __nv_bfloat16* src = p.q + (bh * p.R + rt * RT + r) * D + lane * PER;
+            const __nv_bfloat16* src = p.q + p.row_at(sg.b, sg.h, row0 + r) * D + lane * PER;
 #pragma unroll
             for (int e = 0; e < PER; ++e) {
               x[e] = __bfloat162float(src[e]);
@@ -424,9 +433,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
             // a row that holds a number that is not finite gives NaN
             bars->c[r] = amax >= 0x7f800000u ? __int_as_float(0x7fc00000)
                                              : __int_as_float((e2 + 127) << 23) * p.scale_log2;
-            long long lim = sg.len - 1;
-            if (p.causal) lim = min(lim, start + (rt * RT + r) % p.Nq);
-            bars->lim[r] = (int)max(lim, -1LL);
+            bars->lim[r] = p.rows.limit(sg.len, sg.first, (row0 + r) / p.rows.g);
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -581,16 +588,16 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
 #pragma unroll
       for (int r = 0; r < RT; ++r) l[r] = bars->red[0][r] + bars->red[1][r] + bars->red[2][r] + bars->red[3][r];
       if (sg.ntiles == sg.total) {
-        const long long row0 = bh * p.R + rt * RT;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           if (r >= rows) break;
-          if (tid < D) p.out[(row0 + r) * D + tid] = __float2bfloat16_rn(l[r] == 0.f ? 0.f : o[r] / l[r]);
-          if (tid == r) p.lse[row0 + r] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * 0.6931471805599453f;
+          const long long at = p.row_at(sg.b, sg.h, row0 + r);
+          if (tid < D) p.out[at * D + tid] = __float2bfloat16_rn(l[r] == 0.f ? 0.f : o[r] / l[r]);
+          if (tid == r) p.lse[at] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * 0.6931471805599453f;
         }
       } else {
-        const long long unit_t0 = walk.base + (long long)sg.unit * sg.total;
-        const long long slot = cache_slot(bars->total, bars->grid, (int)blockIdx.x, unit_t0);
+        const long long slot = cache_slot((int)blockIdx.x, bars->plan.t0, sg.unit_t0);
+        if (tid == 0) p.note_cut(sg, bars->plan);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           if (r >= rows) break;
@@ -613,58 +620,71 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
 
 // Joins the partial results of the units that were cut between CTAs: for each
 // row, over its pieces s in order, m = max m_s, l = sum 2^(m_s - m) l_s,
-// O = sum 2^(m_s - m) O_s / l.  One block a unit, thread = channel.
+// O = sum 2^(m_s - m) O_s / l.  One block for each row of the unit that is cut
+// at the end of a CTA's range: its threads first take a piece each (maxima,
+// sums, weights), then four channels of every G-th piece.
 template <int D, int RT>
 __global__ void __launch_bounds__(128) fa_cache_merge_kernel(const __grid_constant__ CacheAttnParams p) {
+  constexpr int LANES = D / 4, G = 128 / LANES;  // threads of a row of O; pieces read at a time
+  __shared__ float weight[kCacheMaxGrid], red[4], part[G][D];
   const int tid = threadIdx.x;
-  const int units = p.c.H * p.row_tiles;
-  const int b = blockIdx.x / units, unit = blockIdx.x - b * units;
-  __shared__ long long sums[2][4];
-  long long before = 0, total = 0;
-  bool bad = false;
-  for (int i = tid; i < p.B; i += 128) {
-    const int n = cache_tiles(cache_clamp(p.lens[i], p.max_len, bad));
-    total += n;
-    if (i < b) before += n;
-  }
+  const int c0 = blockIdx.x / RT, in_tile = blockIdx.x - c0 * RT;
+  // Launched while the attention kernel still runs (programmatic dependent
+  // launch): every block waits for it, those with nothing to join too, so that
+  // this kernel's end stands for both.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 cut = p.cut[c0];
+  const int r = cut.z * RT + in_tile, c1 = cut.w >> 1;
+  if (cut.x < 0 || r >= p.rows.R) return;
+  // The unit is the first stretch of every CTA but c0.
+  auto slot = [&](int c) { return (2LL * c + (c == c0 ? (cut.w & 1) : 0)) * RT + in_tile; };
+  const int pieces = c1 - c0 + 1;
+  auto block = [&](float x, bool max) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
+    for (int o = 16; o; o >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, x, o);
+      x = max ? fmaxf(x, y) : x + y;
+    }
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = x;
+    __syncthreads();
+    return max ? fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) : (red[0] + red[1]) + (red[2] + red[3]);
+  };
+  float m = -INFINITY, l = 0.f;
+  for (int i = tid; i < pieces; i += 128) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(c0 + i) * 2);
+    if (ml.y != 0.f) m = fmaxf(m, ml.x);  // a piece with no visible key has sum 0
   }
-  if ((tid & 31) == 0) {
-    sums[0][tid >> 5] = total;
-    sums[1][tid >> 5] = before;
+  m = block(m, true);
+  for (int i = tid; i < pieces; i += 128) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(c0 + i) * 2);
+    const float w = ml.y != 0.f ? ptx::ex2(ml.x - m) : 0.f;
+    weight[i] = w;
+    l = fmaf(w, ml.y, l);
   }
+  l = block(l, false);  // (its barriers also publish the weights)
+  const int lane = tid % LANES, g = tid / LANES;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = g; i < pieces; i += G) {
+    const float w = weight[i];
+    if (w == 0.f) continue;
+    const float4 x = *reinterpret_cast<const float4*>(p.part_o + slot(c0 + i) * D + lane * 4);
+    o.x = fmaf(w, x.x, o.x);
+    o.y = fmaf(w, x.y, o.y);
+    o.z = fmaf(w, x.z, o.z);
+    o.w = fmaf(w, x.w, o.w);
+  }
+  *reinterpret_cast<float4*>(&part[g][lane * 4]) = o;
   __syncthreads();
-  total = (sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3]) * units;
-  before = (sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3]) * units;
-  const int nt = cache_tiles(cache_clamp(p.lens[b], p.max_len, bad));
-  const long long first = before + (long long)unit * nt;
-  const int grid = cache_active(total, p.ctas);
-  const int c0 = cache_range_owner(total, grid, first), c1 = cache_range_owner(total, grid, first + nt - 1);
-  if (c0 == c1) return;  // written by the attention kernel
-  const int h = unit / p.row_tiles, rt = unit - h * p.row_tiles;
-  const int rows = min(RT, p.R - rt * RT);
-  const long long row0 = ((long long)b * p.c.H + h) * p.R + rt * RT;
-  for (int r = 0; r < rows; ++r) {
-    float m = -INFINITY;
-    for (int c = c0; c <= c1; ++c) {
-      const float* ml = p.part_ml + ((long long)cache_slot(total, grid, c, first) * RT + r) * 2;
-      m = ml[1] == 0.f ? m : fmaxf(m, ml[0]);
-    }
-    float l = 0.f, o = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const long long at = (long long)cache_slot(total, grid, c, first) * RT + r;
-      const float lc = p.part_ml[at * 2 + 1];
-      if (lc == 0.f) continue;  // no key of this piece is visible
-      const float w = ptx::ex2(p.part_ml[at * 2] - m);
-      l = fmaf(w, lc, l);
-      if (tid < D) o = fmaf(w, p.part_o[at * D + tid], o);
-    }
-    if (tid < D) p.out[(row0 + r) * D + tid] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
-    if (tid == 0) p.lse[row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  const long long at = p.row_at(cut.x, cut.y, r);
+  if (tid < D) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < G; ++i) x += part[i][tid];
+    p.out[at * D + tid] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
   }
+  if (tid == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace fa

@@ -1,0 +1,600 @@
+// fa_cache_chunk.cuh — the cached attention (see fa_cache_attn.cuh) for many
+// rows: prompts, chunks of video, and drafts of grouped heads.
+//
+// Here the tensor cores are the bound, so the products have the rows on the M
+// side, as in the forward kernel: 256 rows (two tiles of 128) a CTA, one thread
+// a row in the softmax, P over S in tensor memory, two softmax warpgroups that
+// ping-pong.
+//
+// S = Q K^T runs as e4m3 x e4m3 with K's codes as they are: a row of Q is
+// s (hi + lo), two e4m3 numbers (s a power of two that puts the row's largest
+// element in (224, 448]), and S accumulates both products.  Two e4m3 MMAs cost
+// what one bf16 MMA does, and K needs no conversion.  An element of q is exact
+// above 2^-10 of its row's largest, and off by 2^-18 of that below.  The scales
+// of q's row and of K's page go into the softmax's multiplier.
+//
+// P V runs in bf16: two warps turn each V page into bf16 (code * scale is a
+// bf16 number, so nothing is lost) in the layout that the MMA reads, one tile
+// ahead.  P is rounded to bf16 as in the forward kernel.
+//
+// Units' tiles are cut into equal ranges, one per CTA (1 CTA per SM), as in
+// fa_cache_attn.cuh: 192 units of 256 rows on 152 SMs would leave a third of
+// the second round idle.
+//
+// Warps: 0-3 and 4-7 softmax of the two row tiles, 8 producer, 9 MMA issuer,
+// 10-11 V conversion.
+#pragma once
+
+#include "fa_cache_attn.cuh"
+
+namespace fa {
+
+constexpr int kChunkRows = 256;
+constexpr int kChunkThreads = 384;
+constexpr int kChunkConvert = 64;  // threads that convert V
+constexpr int kChunkMaxGrid = 192;  // one CTA per SM; partial results are sized for this many
+constexpr int kChunkMeta = 8;  // tiles whose scales are kept: more than the pipeline's depth (5)
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int T8 = kCacheTile * D;              // 128 rows in e4m3
+  static constexpr int T16 = 2 * T8;                     // in bf16
+  static constexpr int SW = D >= 64 ? 128 : 64;          // swizzle span of the bf16 tile
+  static constexpr int CHUNK = kCacheTile * SW;          // its 128-row blocks of SW bytes
+  static constexpr uint32_t LAYOUT8 = D == 128 ? 2u : (D == 64 ? 4u : 6u);
+  static constexpr uint32_t LAYOUT16 = D >= 64 ? 2u : 4u;
+  static constexpr int K_STAGES = 3, V_STAGES = 2;       // K and V codes; V in bf16
+  static constexpr int SMEM_BYTES = 4 * T8 + 2 * K_STAGES * T8 + V_STAGES * T16 + 2048;
+  static constexpr int COL_S = 0, COL_O = 256;           // S and O of tile t: + 128 t, + D t
+};
+
+struct ChunkBars {
+  uint64_t k_full[3], k_empty[3], v8_full[3], v8_empty[3], v_full[2], v_empty[2];
+  uint64_t meta_full[kChunkMeta];
+  uint64_t q_ready[2], s_full[2], p_half[2], p_ready[2], o_full[2], drain;
+  CacheRange plan;
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  float ks[kChunkMeta][4], vs[kChunkMeta][4];  // scales of a tile's 32-token groups
+};
+static_assert(sizeof(ChunkBars) <= 2048, "barrier space");
+
+// 16 codes to bf16, times a power of two (exact).
+__device__ __forceinline__ void chunk_bf16(const uint4& v, float scale, uint4 (&out)[2]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float2 f = e4m3x2_value((w[k / 2] >> (16 * (k & 1))) & 0xffffu);
+    o[k] = ptx::pack_bf16x2(f.x * scale, f.y * scale);
+  }
+  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const __grid_constant__ CacheAttnParams p) {
+  using C = ChunkCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem;                              // tile t: hi at 2 t, lo at 2 t + 1
+  uint8_t* sK = sQ + 4 * C::T8;
+  uint8_t* sV8 = sK + C::K_STAGES * C::T8;
+  uint8_t* sV = sV8 + C::K_STAGES * C::T8;
+  ChunkBars* bars = reinterpret_cast<ChunkBars*>(sV + C::V_STAGES * C::T16);
+  const int warp = threadIdx.x / 32;
+  const uint32_t lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    if (p.cut) p.cut[blockIdx.x].x = -1;
+    for (int s = 0; s < C::K_STAGES; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&bars->k_full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->k_empty[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->v8_full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->v8_empty[s]), kChunkConvert);
+    }
+    for (int s = 0; s < C::V_STAGES; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&bars->v_full[s]), kChunkConvert);
+      ptx::mbar_init(ptx::smem_u32(&bars->v_empty[s]), 1);
+    }
+    for (int s = 0; s < kChunkMeta; ++s) ptx::mbar_init(ptx::smem_u32(&bars->meta_full[s]), 1);
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(ptx::smem_u32(&bars->q_ready[t]), 128);
+      ptx::mbar_init(ptx::smem_u32(&bars->s_full[t]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->p_half[t]), 128);
+      ptx::mbar_init(ptx::smem_u32(&bars->p_ready[t]), 128);
+      ptx::mbar_init(ptx::smem_u32(&bars->o_full[t]), 1);
+    }
+    ptx::mbar_init(ptx::smem_u32(&bars->drain), 1);
+    bars->abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 8) cache_plan(p.rows, p.ctas, p.status, lane, &bars->plan);
+  if (warp == 9) {
+    ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  CacheWalk walk;
+  walk.start(p.rows, bars->plan.t0, bars->plan.t1, bars->plan.b0, bars->plan.base0);
+  CacheSegment sg;
+  auto finish = [&]() {
+    ptx::named_barrier_sync(1, kChunkThreads);
+    if (warp == 9) {
+      ptx::tc_fence_after_sync();
+      ptx::tmem_dealloc(tmem, 512);
+    }
+  };
+
+  if (warp >= 10) {
+    // -------------------------------------------------------- V conversion --
+    // A warp's 32 lanes take 16-byte pieces so that eight lanes in a row read
+    // and write all banks: four pieces of a row and of the row 5 away in the
+    // swizzle pattern (D = 32: two pieces of four rows).
+    constexpr int CPR = D / 16, HALVES = D == 128 ? 2 : 1, RPI = D == 32 ? 16 : 8;
+    constexpr int STEPS = kCacheTile / RPI / 2 * HALVES;  // 32 pieces a warp each
+    static_assert(CPR * kCacheTile == kChunkConvert * STEPS, "pieces of a tile");
+    const int w = warp - 10;
+    const int q = (int)lane >> 2;
+    const int in_row = D == 32 ? (int)lane >> 1 : (q >> 1) ^ ((q & 1) * 5);
+    const int in_col = D == 32 ? (int)lane & 1 : (int)lane & 3;
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      for (int j = 0; j < sg.ntiles; ++j, ++it) {
+        const uint32_t s8 = it % C::K_STAGES, s16 = it % C::V_STAGES;
+        ok = cache_wait(&bars->v8_full[s8], (it / C::K_STAGES) & 1, bars, p) &&
+             cache_wait(&bars->v_empty[s16], ((it / C::V_STAGES) & 1) ^ 1, bars, p);
+        if (!ok) break;
+        const uint8_t* src = sV8 + s8 * C::T8;
+        uint8_t* dst = sV + s16 * C::T16;
+        const float* vs = bars->vs[it % kChunkMeta];
+        // Rows past the length may hold anything, NaN among it: zeros.
+        const int held = sg.len - (sg.tile0 + j) * kCacheTile;
+#pragma unroll 8
+        for (int k = 0; k < STEPS; ++k) {
+          const int row = ((k / HALVES) * 2 + w) * RPI + in_row;
+          const int c = (HALVES == 2 ? (k & 1) * 4 : 0) + in_col;
+          uint4 v = *reinterpret_cast<const uint4*>(src + cache_swizzle<D>(row, 16 * c));
+          if (row >= held) v = make_uint4(0u, 0u, 0u, 0u);
+          uint4 o[2];
+          chunk_bf16(v, row < held ? vs[row >> 5] : 0.f, o);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int piece = 2 * c + x;  // 16 bytes of the bf16 row
+            const uint32_t at = C::SW == 128
+                                    ? (uint32_t)((piece >> 3) * C::CHUNK + row * 128 + (((piece & 7) ^ (row & 7)) << 4))
+                                    : (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+            *reinterpret_cast<uint4*>(dst + at) = o[x];
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        ptx::mbar_arrive(ptx::smem_u32(&bars->v_full[s16]));
+        ptx::mbar_arrive(ptx::smem_u32(&bars->v8_empty[s8]));
+      }
+    }
+    __syncwarp();
+    finish();
+    return;
+  }
+  if (warp >= 8) {
+    if (warp == 8) {
+      // ---------------------------------------------------------- producer --
+      if (lane == 0) {
+        ptx::tma_prefetch_desc(&p.tm_k);
+        ptx::tma_prefetch_desc(&p.tm_v);
+      }
+      const int page = p.c.page, ppt = kCacheTile / page, batch = 32 / ppt;
+      uint32_t it = 0, skipped = 0xffffffffu;
+      bool ok = true;
+      while (ok && walk.next(sg)) {
+        const int npages = sg.len == 0 ? 0 : (sg.len - 1) / page + 1;
+        const int* row = p.c.table + (long long)sg.b * p.c.width;
+        int id = 0;
+        float ks = 0.f, vs = 0.f;
+        for (int j = 0; j < sg.ntiles; ++j, ++it) {
+          const int in_batch = j % batch;
+          if (in_batch == 0) {  // the lanes fetch the next 32 pages' numbers and scales
+            const int idx = (sg.tile0 + j) * ppt + (int)lane;
+            bool bad = false;
+            id = 0;
+            ks = vs = 0.f;
+            if (idx < npages && idx < (sg.tile0 + sg.ntiles) * ppt) {
+              id = cache_page(row[idx], p.c.num_pages, bad);
+              const long long at = (long long)id * p.c.H + sg.h;
+              ks = p.c.scale[0][at];
+              vs = p.c.scale[1][at];
+            }
+            if (bad) atomicCAS(p.status, 0, kStatusIndex);
+          }
+          const uint32_t s = it % C::K_STAGES, ph = ((it / C::K_STAGES) & 1) ^ 1, meta = it % kChunkMeta;
+          ok = cache_wait(&bars->k_empty[s], ph, bars, p) && cache_wait(&bars->v8_empty[s], ph, bars, p);
+          if (!ok) break;
+          if (p.inject_stall && blockIdx.x == 0 && it == 1) {  // nothing arrives: consumers time out
+            skipped = it;
+            continue;
+          }
+          const int src = in_batch * ppt + (int)(lane % ppt);
+          const int my_id = __shfl_sync(0xffffffffu, id, src);
+          const int g = in_batch * ppt + (int)(lane & 3) * 32 / page;  // page of this lane's 32 tokens
+          const float my_ks = __shfl_sync(0xffffffffu, ks, g), my_vs = __shfl_sync(0xffffffffu, vs, g);
+          const int n = max(0, min(ppt, npages - (sg.tile0 + j) * ppt));  // pages that hold tokens
+          // The scales' slot was last used eight tiles ago; the V slot that is
+          // free now means that tile it - 5 is through the softmax.
+          if (lane < 4) {
+            bars->ks[meta][lane] = my_ks;
+            bars->vs[meta][lane] = my_vs;
+          }
+          const uint32_t kf = ptx::smem_u32(&bars->k_full[s]), vf = ptx::smem_u32(&bars->v8_full[s]);
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(ptx::smem_u32(&bars->meta_full[meta]));
+            ptx::mbar_arrive_expect_tx(kf, (uint32_t)(n * page * D));
+            ptx::mbar_arrive_expect_tx(vf, (uint32_t)(n * page * D));
+          }
+          __syncwarp();
+          if ((int)lane < n) {
+            const uint32_t off = s * C::T8 + lane * page * D;
+            const int at = my_id * p.c.H + sg.h;
+            ptx::tma_load_3d(ptx::smem_u32(sK) + off, &p.tm_k, kf, 0, 0, at);
+            ptx::tma_load_3d(ptx::smem_u32(sV8) + off, &p.tm_v, vf, 0, 0, at);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok && lane == 0) {
+        // Drain: every copy issued has landed once its stage's last phase is complete.
+        for (int s = 0; s < C::K_STAGES; ++s) {
+          uint32_t n = it > (uint32_t)s ? (it - 1 - s) / C::K_STAGES + 1 : 0;
+          if (skipped < it && skipped % C::K_STAGES == (uint32_t)s) --n;
+          if (n) {
+            cache_drain(&bars->k_full[s], (n - 1) & 1, p);
+            cache_drain(&bars->v8_full[s], (n - 1) & 1, p);
+          }
+        }
+      }
+    } else if (warp == 9) {
+      // --------------------------------------------------------------- MMA --
+      constexpr uint32_t IDESC_S = (1u << 4) | (16u << 17) | (8u << 24);  // e4m3, 128 x 128
+      constexpr uint32_t IDESC_PV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                    (8u << 24);                           // bf16, 128 x D, B transposed
+      constexpr uint32_t kVStep = (16 * C::SW) >> 4;                      // 16 keys of V
+      const uint64_t dq = cache_desc(ptx::smem_u32(sQ), 16, 8 * D, C::LAYOUT8);
+      const uint64_t dk = cache_desc(ptx::smem_u32(sK), 16, 8 * D, C::LAYOUT8);
+      const uint64_t dv = cache_desc(ptx::smem_u32(sV), C::CHUNK, 8 * C::SW, C::LAYOUT16);
+      const uint32_t q_hi = (uint32_t)(dq >> 32), k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
+      auto issue_s = [&](int t, uint32_t stage) {
+        const uint32_t d = tmem + C::COL_S + t * 128, b = (uint32_t)dk + stage * (C::T8 >> 4);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {  // hi, then lo on top
+          const uint32_t a = (uint32_t)dq + (2 * t + part) * (C::T8 >> 4);
+          if constexpr (D == 128)
+            ptx::mma_ss_f8_x4_el<2, 4, 6>(d, a, q_hi, b, k_hi, IDESC_S, part);
+          else if constexpr (D == 64)
+            ptx::mma_ss_f8_x2_el<2>(d, a, q_hi, b, k_hi, IDESC_S, part);
+          else
+            ptx::mma_ss_f8_x1_el(d, a, q_hi, b, k_hi, IDESC_S, part);
+        }
+        ptx::mma_commit_el(ptx::smem_u32(&bars->s_full[t]));
+      };
+      uint32_t it = 0, pc[2] = {0, 0}, qc[2] = {0, 0};
+      // O_t += P_t V in two halves of 64 keys, each as soon as its P is there.
+      auto issue_pv = [&](int t, uint32_t stage, bool first, uint32_t parity) -> bool {
+        const uint32_t b = (uint32_t)dv + stage * (C::T16 >> 4), d = tmem + C::COL_O + t * D;
+        const uint32_t a = tmem + C::COL_S + t * 128;
+        if (!cache_wait(&bars->p_half[t], parity, bars, p)) return false;
+        ptx::tc_fence_after_sync();
+        ptx::mma_ts_x4_el<kVStep>(d, a, b, v_hi, IDESC_PV, first ? 0u : 1u);
+        if (!cache_wait(&bars->p_ready[t], parity, bars, p)) return false;
+        ptx::tc_fence_after_sync();
+        ptx::mma_ts_x4_el<kVStep>(d, a + 32, b + 4 * kVStep, v_hi, IDESC_PV, 1u);
+        return true;
+      };
+      auto take_k = [&](uint32_t n) -> bool {
+        const bool r = cache_wait(&bars->k_full[n % C::K_STAGES], (n / C::K_STAGES) & 1, bars, p);
+        ptx::tc_fence_after_sync();
+        return r;
+      };
+      bool ok = true;
+      while (ok && walk.next(sg)) {
+        const bool two = sg.rt * kChunkRows + 128 < p.rows.R;
+        ok = take_k(it) && cache_wait(&bars->q_ready[0], qc[0] & 1, bars, p);
+        if (!ok) break;
+        ++qc[0];
+        ptx::tc_fence_after_sync();
+        issue_s(0, it % C::K_STAGES);
+        if (two) {
+          ok = cache_wait(&bars->q_ready[1], qc[1] & 1, bars, p);
+          if (!ok) break;
+          ++qc[1];
+          ptx::tc_fence_after_sync();
+          issue_s(1, it % C::K_STAGES);
+        }
+        ptx::mma_commit_el(ptx::smem_u32(&bars->k_empty[it % C::K_STAGES]));
+        for (int j = 0; j < sg.ntiles; ++j, ++it) {
+          const bool more = j + 1 < sg.ntiles;
+          const uint32_t sv = it % C::V_STAGES, sk = (it + 1) % C::K_STAGES;
+          ok = cache_wait(&bars->v_full[sv], (it / C::V_STAGES) & 1, bars, p);
+          if (!ok) break;
+          ptx::tc_fence_after_sync();
+          ok = issue_pv(0, sv, j == 0, pc[0] & 1);
+          if (!ok) break;
+          ++pc[0];
+          if (more) {
+            ok = take_k(it + 1);
+            if (!ok) break;
+            issue_s(0, sk);
+          } else {
+            ptx::mma_commit_el(ptx::smem_u32(&bars->o_full[0]));
+          }
+          if (two) {
+            ok = issue_pv(1, sv, j == 0, pc[1] & 1);
+            if (!ok) break;
+            ++pc[1];
+            if (!more) ptx::mma_commit_el(ptx::smem_u32(&bars->o_full[1]));
+          }
+          ptx::mma_commit_el(ptx::smem_u32(&bars->v_empty[sv]));
+          if (more) {
+            if (two) issue_s(1, sk);
+            ptx::mma_commit_el(ptx::smem_u32(&bars->k_empty[sk]));
+          }
+        }
+      }
+      ptx::mma_commit_el(ptx::smem_u32(&bars->drain));
+      cache_drain(&bars->drain, 0, p);
+    }
+    __syncwarp();
+    finish();
+    return;
+  }
+
+  // ---------------------------------------------------------------- softmax --
+  const int t = warp / 4;
+  const int in_tile = (warp % 4) * 32 + (int)lane;  // row of the tile, lane of tensor memory
+  const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
+  const uint32_t tS = tmem + lane_base + C::COL_S + t * 128, tO = tmem + lane_base + C::COL_O + t * D;
+  uint8_t* q_hi = sQ + 2 * t * C::T8;
+  uint8_t* q_lo = q_hi + C::T8;
+  uint32_t it = 0, sc = 0, oc = 0;
+  bool ok = true;
+  while (ok && walk.next(sg)) {
+    const int row0 = sg.rt * kChunkRows + t * 128;
+    if (row0 >= p.rows.R) {  // (tile 1 of a short unit)
+      it += (uint32_t)sg.ntiles;
+      continue;
+    }
+    const int row = row0 + in_tile;
+    const bool valid = row < p.rows.R;
+    const long long at = p.row_at(sg.b, sg.h, valid ? row : row0);
+    // This thread's row of Q as s (hi + lo).  The MMAs that read the last
+    // unit's Q are done: their S has been read.
+    float c;
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + at * D);
+      uint32_t amax = 0;
+#pragma unroll 4
+      for (int k = 0; k < D / 8; ++k) {
+        const uint4 v = __ldg(src + k);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = max(amax, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
+      }
+      const int e2 = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+      // a negative scale turns the row round, so that the multiplier is positive
+      const float inv = __int_as_float((127 - e2) << 23) * (p.scale_log2 < 0.f ? -1.f : 1.f);
+#pragma unroll 2
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint4 v = __ldg(src + 2 * k + x);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h[4], l[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = __uint_as_float(w[e] << 16) * inv, b = __uint_as_float(w[e] & 0xffff0000u) * inv;
+            h[e] = e4m3x2_bits(a, b);
+            const float2 f = e4m3x2_value(h[e]);
+            l[e] = e4m3x2_bits(a - f.x, b - f.y);
+          }
+          hi[2 * x] = h[0] | (h[1] << 16);
+          hi[2 * x + 1] = h[2] | (h[3] << 16);
+          lo[2 * x] = l[0] | (l[1] << 16);
+          lo[2 * x + 1] = l[2] | (l[3] << 16);
+        }
+        const uint32_t off = cache_swizzle<D>(in_tile, 16 * k);
+        *reinterpret_cast<uint4*>(q_hi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(q_lo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      // a row that holds a number that is not finite gives NaN
+      c = amax >= 0x7f800000u ? __int_as_float(0x7fc00000) : __int_as_float((e2 + 127) << 23) * fabsf(p.scale_log2);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready[t]));
+    }
+    const int lim = p.rows.limit(sg.len, sg.first, (valid ? row : row0) / p.rows.g);
+    const int wlim = __reduce_min_sync(0xffffffffu, lim);
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < sg.ntiles; ++j, ++it) {
+      const int kbase = (sg.tile0 + j) * kCacheTile;
+      const uint32_t meta = it % kChunkMeta;
+      ok = cache_wait(&bars->meta_full[meta], (it / kChunkMeta) & 1, bars, p);
+      if (!ok) break;
+      float sl[4];  // multipliers of the raw scores of each 32 keys: positive, or NaN
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        sl[g] = c * bars->ks[meta][g];
+        if (sl[g] < 1.17549435e-38f) sl[g] = 1.17549435e-38f;
+      }
+      ok = cache_wait(&bars->s_full[t], sc & 1, bars, p);
+      if (!ok) break;
+      ++sc;
+      ptx::tc_fence_after_sync();
+      float s[128];
+      {
+        uint32_t r[128];
+        ptx::tmem_ld32x32b_x128(tS, r);
+#pragma unroll
+        for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(r[i]);
+      }
+      if (kbase + kCacheTile - 1 > wlim) {  // some row does not see every key
+        const int hi = lim - kbase;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) s[i] = i <= hi ? s[i] : -INFINITY;
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float a0 = s[32 * g], a1 = s[32 * g + 1];
+#pragma unroll
+        for (int i = 2; i < 32; i += 4) {
+          a0 = ptx::fmax3(a0, s[32 * g + i], s[32 * g + i + 1]);
+          if (i + 3 < 32) a1 = ptx::fmax3(a1, s[32 * g + i + 2], s[32 * g + i + 3]);
+        }
+        mx = fmaxf(mx, fmaxf(a0, a1) * sl[g]);
+      }
+      // The reference moves only when the maximum grew by more than 8 (exact:
+      // O, l and LSE use the same one).
+      const float m_new = fmaxf(m, mx);
+      const bool grow = m_new - m > 8.f;  // -inf - -inf: NaN, false
+      float alpha = 1.f;
+      if (grow) {
+        alpha = ptx::ex2(m - m_new);
+        m = m_new;
+      }
+      const float m_use = m == -INFINITY ? 0.f : m;
+      l *= alpha;
+      const bool rescale = j > 0 && __any_sync(0xffffffffu, grow);
+      auto release = [&](uint64_t* bar) {
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before_sync();
+        ptx::mbar_arrive(ptx::smem_u32(bar));
+      };
+      float2 lsum = make_float2(0.f, 0.f);
+      const float2 nm2 = make_float2(-m_use, -m_use);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float2 sl2 = make_float2(sl[g], sl[g]);
+        uint32_t packed[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 x = __ffma2_rn(make_float2(s[32 * g + i], s[32 * g + i + 1]), sl2, nm2);
+          const float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+          lsum = __fadd2_rn(lsum, e);
+          packed[i / 2] = ptx::pack_bf16x2(e.x, e.y);
+        }
+        ptx::tmem_st32x32b_x16(tS + 16 * g, packed);
+        if (g == 1 && !rescale) release(&bars->p_half[t]);
+      }
+      l += lsum.x + lsum.y;
+      if (rescale) {
+        // P V of the last tile is done: the S just read was issued after it.
+#pragma unroll
+        for (int cb = 0; cb < D; cb += 32) {
+          uint32_t r[32];
+          ptx::tmem_ld32x32b_x32(tO + cb, r);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+          ptx::tmem_st32x32b_x32(tO + cb, r);
+        }
+        release(&bars->p_half[t]);
+      }
+      release(&bars->p_ready[t]);
+    }
+    if (!ok) break;
+    ok = cache_wait(&bars->o_full[t], oc & 1, bars, p);
+    if (!ok) break;
+    ++oc;
+    ptx::tc_fence_after_sync();
+    if (sg.ntiles == sg.total) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int cb = 0; cb < D; cb += 32) {
+        uint32_t r[32];
+        ptx::tmem_ld32x32b_x32(tO + cb, r);
+        if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + cb);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = ptx::pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]) * inv, __uint_as_float(r[8 * k + 2 * e + 1]) * inv);
+            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (valid) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    } else {
+      // Partial O four channels at a time, the rows of a warp side by side.
+      const long long slot = cache_slot((int)blockIdx.x, bars->plan.t0, sg.unit_t0);
+      const int in_unit = t * 128 + in_tile;
+      if (threadIdx.x == 0) p.note_cut(sg, bars->plan);
+      float4* dst = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * kChunkRows + in_unit;
+#pragma unroll
+      for (int cb = 0; cb < D; cb += 32) {
+        uint32_t r[32];
+        ptx::tmem_ld32x32b_x32(tO + cb, r);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          dst[(cb / 4 + k) * kChunkRows] =
+              make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]), __uint_as_float(r[4 * k + 2]),
+                          __uint_as_float(r[4 * k + 3]));
+      }
+      reinterpret_cast<float2*>(p.part_ml)[slot * kChunkRows + in_unit] = make_float2(m, l);
+    }
+    ptx::tc_fence_before_sync();  // O has been read: the next unit's products may overwrite it
+  }
+  ptx::tc_fence_before_sync();
+  finish();
+}
+
+// Joins the pieces of the units cut between CTAs, as fa_cache_merge_kernel;
+// one block for 16 channels of a unit's 256 rows, thread = row.
+template <int D>
+__global__ void __launch_bounds__(kChunkRows) fa_cache_chunk_merge_kernel(const __grid_constant__ CacheAttnParams p) {
+  constexpr int PARTS = D / 16;
+  const int c0 = blockIdx.x / PARTS, part = blockIdx.x - c0 * PARTS;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // see fa_cache_merge_kernel
+  const int4 cut = p.cut[c0];
+  const int row = cut.z * kChunkRows + (int)threadIdx.x, c1 = cut.w >> 1;
+  if (cut.x < 0 || row >= p.rows.R) return;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + threadIdx.x;
+  auto slot = [&](int c) { return 2LL * c + (c == c0 ? (cut.w & 1) : 0); };
+  float m = -INFINITY, l = 0.f;
+  for (int c = c0; c <= c1; ++c) {
+    const float2 x = ml[slot(c) * kChunkRows];
+    if (x.y != 0.f) m = fmaxf(m, x.x);
+  }
+  float4 o[4] = {};
+  for (int c = c0; c <= c1; ++c) {
+    const float2 x = ml[slot(c) * kChunkRows];
+    if (x.y == 0.f) continue;
+    const float w = ptx::ex2(x.x - m);
+    l = fmaf(w, x.y, l);
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot(c) * (D / 4) + part * 4) * kChunkRows + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = src[k * kChunkRows];
+      o[k].x = fmaf(w, v.x, o[k].x);
+      o[k].y = fmaf(w, v.y, o[k].y);
+      o[k].z = fmaf(w, v.z, o[k].z);
+      o[k].w = fmaf(w, v.w, o[k].w);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const long long at = p.row_at(cut.x, cut.y, row);
+  uint32_t w[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    w[2 * k] = ptx::pack_bf16x2(o[k].x * inv, o[k].y * inv);
+    w[2 * k + 1] = ptx::pack_bf16x2(o[k].z * inv, o[k].w * inv);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + part * 16);
+  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (part == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+}  // namespace fa

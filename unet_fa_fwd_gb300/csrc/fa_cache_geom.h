@@ -46,14 +46,46 @@ FA_HD int cache_page(int id, int num_pages, bool& bad) {
 }
 
 // ---- the attention's work ----
-// A unit is one (batch entry, key head, row tile); it has as many 128-key
-// tiles as its batch entry's length (at least one, so that an empty sequence
-// still gets its outputs written).  The tiles of all units in order are cut
-// into equal ranges, one per CTA; no range is empty, so with fewer tiles than
-// CTAs the last CTAs have none.
+// The rows of a key head are its g = Hq / H query heads' Nq rows each, taken
+// position by position (row r: position r / g of query head r % g), so that a
+// tile of RT rows covers few positions.  A unit is one (batch entry, key head,
+// row tile); it has the 128-key tiles that some row of it sees, at least one
+// (so that an empty row still gets its outputs written).  The tiles of all
+// units in order are cut into equal ranges, one per CTA; no range is empty, so
+// with fewer tiles than CTAs the last CTAs have none.
 constexpr int kCacheTile = 128;
 
 FA_HD int cache_tiles(int len) { return len <= 0 ? 1 : (len - 1) / kCacheTile + 1; }
+
+// Lengths and positions may hold anything: lengths are kept inside
+// [0, max_len], positions are added in 64 bits.
+struct CacheRows {
+  const int* lens;     // [B]
+  const int* q_start;  // [B] or nullptr: len - Nq
+  int B, H, g, Nq, R, RT, row_tiles, causal, max_len;
+
+  FA_HD int len(int b, bool& bad) const { return cache_clamp(lens[b], max_len, bad); }
+  FA_HD long long first(int b, int len) const { return q_start ? (long long)q_start[b] : (long long)len - Nq; }
+  // Last key that the row at position i sees, -1 for none.
+  FA_HD int limit(int len, long long first, int i) const {
+    long long last = len - 1;
+    if (causal && first + i < last) last = first + i;
+    return last < -1 ? -1 : (int)last;
+  }
+  // Tiles of row tile rt of a batch entry of this length and first position.
+  FA_HD int tiles(int len, long long first, int rt) const {
+    if (!causal) return cache_tiles(len);
+    const int rows = (rt + 1) * (long long)RT < R ? (rt + 1) * RT : R;
+    return cache_tiles(limit(len, first, (rows - 1) / g) + 1);
+  }
+  // Tiles of all row tiles of a key head.
+  FA_HD long long head_tiles(int len, long long first) const {
+    if (!causal || row_tiles == 1) return (long long)tiles(len, first, 0) * row_tiles;
+    long long n = 0;
+    for (int rt = 0; rt < row_tiles; ++rt) n += tiles(len, first, rt);
+    return n;
+  }
+};
 
 FA_HD int cache_active(long long total, int ctas) { return total < ctas ? (int)total : ctas; }
 
@@ -73,50 +105,68 @@ FA_HD int cache_range_owner(long long total, int grid, long long t) {
 
 // One stretch of a unit's tiles inside a CTA's range.
 struct CacheSegment {
-  int b, unit;         // batch entry; (key head, row tile) within it
-  int len;             // its checked length
+  int b, h, rt;        // the unit
+  int len;             // its batch entry's checked length
+  long long first;     // position of the first query row
+  long long unit_t0;   // the unit's first tile
   int tile0, ntiles;   // this stretch
   int total;           // tiles of the unit
 };
 
-// Walks a CTA's range of tiles.  `lens` may hold anything; lengths are kept
-// inside [0, max_len].
+// Walks a CTA's range of tiles.
 struct CacheWalk {
-  const int* lens;
-  int B, units, max_len;     // batch entries; units per entry
-  long long t, end, base;    // next tile, end of the range, first tile of entry b
-  int b, len, nt;
+  const CacheRows* r;
+  long long t, end, base;    // next tile, end of the range, first tile of the current unit
+  long long first;
+  int b, h, rt, len, nt;
 
   // `b0`, `base0`: the batch entry that holds tile t0, and its first tile.
-  FA_HD void start(const int* l, int B_, int units_, int max_len_, long long t0, long long t1, int b0,
-                   long long base0) {
-    lens = l;
-    B = B_;
-    units = units_;
-    max_len = max_len_;
+  FA_HD void start(const CacheRows& rows, long long t0, long long t1, int b0, long long base0) {
+    r = &rows;
     t = t0;
     end = t1;
     base = base0;
     b = b0;
+    h = rt = 0;
     load();
+    if (t >= end) return;
+    const long long per_head = r->head_tiles(len, first);
+    h = (int)((t - base) / per_head);
+    base += h * per_head;
+    unit();
+    while (t >= base + nt) {
+      base += nt;
+      ++rt;
+      unit();
+    }
   }
   FA_HD void load() {
     bool bad = false;
-    len = b < B ? cache_clamp(lens[b], max_len, bad) : 0;
-    nt = cache_tiles(len);
+    len = b < r->B ? r->len(b, bad) : 0;
+    first = b < r->B ? r->first(b, len) : 0;
   }
+  FA_HD void unit() { nt = r->tiles(len, first, rt); }
   FA_HD bool next(CacheSegment& s) {
     if (t >= end) return false;
-    while (t >= base + (long long)nt * units) {
-      base += (long long)nt * units;
-      ++b;
-      load();
+    if (t >= base + nt) {  // the range goes on with the next unit
+      base += nt;
+      if (++rt == r->row_tiles) {
+        rt = 0;
+        if (++h == r->H) {
+          h = 0;
+          ++b;
+          load();
+        }
+      }
+      unit();
     }
-    const long long rel = t - base;
     s.b = b;
-    s.unit = (int)(rel / nt);
-    s.tile0 = (int)(rel - (long long)s.unit * nt);
+    s.h = h;
+    s.rt = rt;
     s.len = len;
+    s.first = first;
+    s.unit_t0 = base;
+    s.tile0 = (int)(t - base);
     s.total = nt;
     const long long left = end - t;
     s.ntiles = nt - s.tile0 < left ? nt - s.tile0 : (int)left;
@@ -126,10 +176,7 @@ struct CacheWalk {
 };
 
 // Partial results: a CTA has at most two stretches that are not whole units,
-// its first (slot 0) and its last (slot 1).  The slot that CTA c uses for the
-// unit whose first tile is unit_t0:
-FA_HD int cache_slot(long long total, int grid, int c, long long unit_t0) {
-  return 2 * c + (unit_t0 > cache_range_begin(total, grid, c) ? 1 : 0);
-}
+// its first (slot 0) and its last (slot 1 when the unit starts inside the range).
+FA_HD int cache_slot(int c, long long range_t0, long long unit_t0) { return 2 * c + (unit_t0 > range_t0 ? 1 : 0); }
 
 }  // namespace fa
