@@ -23,10 +23,17 @@ from .binding import (FA_OK, FaCache, FaRopeAxes, FaTensor, _stream_handle, load
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _PAIRINGS = {"adjacent": 0, "halves": 1}
 _MAX_AXES = 4
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+# A call's host time is most of a small call's, so the common case (tensors on the current device,
+# its current stream) takes no context manager and reads the stream's handle directly.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 @contextlib.contextmanager
 def _scope(device, stream):
+    """The device current, and the stream too, so that what a call allocates belongs to that stream."""
     with torch.cuda.device(device):
         if stream is None:
             yield
@@ -37,14 +44,15 @@ def _scope(device, stream):
                 yield
 
 
-def _on(t: torch.Tensor, stream):
-    """Where a call on ``t`` runs: its device current, and ``stream`` (the device's current
-    stream if None) current, so that what the call allocates belongs to that stream."""
-    if not t.is_cuda:
+def _run(t: torch.Tensor, stream, call, *args):
+    """call(*args, device index, stream handle) where a call on ``t`` and ``stream`` runs."""
+    device = t.get_device()
+    if device < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if stream is None and t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return _scope(t.device, stream)
+    if stream is None and device == torch.cuda.current_device():
+        return call(*args, device, _raw_stream(device))
+    with _scope(t.device, stream):
+        return call(*args, device, _raw_stream(device) if stream is None else _stream_handle(stream))
 
 
 def _raise(name: str, rc: int) -> None:
@@ -52,35 +60,32 @@ def _raise(name: str, rc: int) -> None:
         raise RuntimeError(f"{name} failed: {status_string(rc)}")
 
 
-def _same_device(t: torch.Tensor, name: str, other: torch.Tensor) -> None:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != other.device:
-        raise ValueError(f"{name} must be on {other.device}, got {t.device}")
-
-
-def _exact(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, like: torch.Tensor) -> int:
-    """A contiguous tensor's pointer, checked."""
+def _refuse(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> None:
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    _same_device(t, name, like)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _exact(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
+    """A contiguous tensor's pointer, checked."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, device)
     return t.data_ptr()
 
 
-def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, like: torch.Tensor) -> FaTensor:
+def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> FaTensor:
     """A [B, H, N, D] tensor of any strides, the last axis contiguous."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _refuse(t, name, dtype, shape, device)
     b, h, n, d = t.stride()
     if d != 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    _same_device(t, name, like)
     return FaTensor(t.data_ptr(), b, h, n)
 
 
@@ -98,6 +103,7 @@ class RopeAxes:
         self.scale = self._each(scale, n, "scale")
         vals = self.struct = FaRopeAxes(count=n)
         vals.dims[:n], vals.theta[:n], vals.scale[:n] = self.dims, self.theta, self.scale
+        self.ref = ctypes.byref(vals)
 
     @staticmethod
     def _each(x, n, name):
@@ -113,7 +119,52 @@ class RopeAxes:
 def _bhnd(t: torch.Tensor, name: str) -> tuple:
     if t.dim() != 4:
         raise ValueError(f"{name} must be [B, H, N, D]")
-    return tuple(t.shape)
+    return t.shape
+
+
+def _rope_new(shape, dtype, device, token_major) -> torch.Tensor:
+    B, H, N, D = shape
+    if token_major:
+        return torch.empty((B, N, H, D), dtype=dtype, device=device).transpose(1, 2)
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rope(q, k, pos, axes, q_out, k_out, new, token_major, pairing, inverse, device, handle):
+    B, Hq, N, D = shape = _bhnd(q, "q")
+    dtype = q.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"q must be bf16, fp16 or fp32, got {dtype}")
+    if pairing not in _PAIRINGS:
+        raise ValueError(f"pairing must be one of {tuple(_PAIRINGS)}, got {pairing!r}")
+    A = len(axes.dims)
+    if pos.dtype is not _I32:
+        raise TypeError(f"pos must be torch.int32, got {pos.dtype}")
+    if pos.shape != (B, N, A) and pos.shape != (N, A):
+        raise ValueError(f"pos must have shape {(B, N, A)} or {(N, A)}, got {tuple(pos.shape)}")
+    ps = pos.stride()
+    if (A > 1 and ps[-1] != 1) or (N > 1 and ps[-2] != A):
+        raise ValueError("pos must be contiguous along its tokens and axes")
+    if pos.get_device() != device:
+        raise ValueError(f"pos must be on cuda:{device}, got {pos.device}")
+    qt = _strided(q, "q", dtype, shape, device)
+    if k is not None:
+        Hk = _bhnd(k, "k")[1]
+        k_shape = (B, Hk, N, D)
+        kt = _strided(k, "k", dtype, k_shape, device)
+    if new:
+        q_out = _rope_new(shape, dtype, q.device, token_major)
+        k_out = None if k is None else _rope_new(k_shape, dtype, q.device, token_major)
+    qo = _strided(q_out, "q_out", dtype, shape, device)
+    lib = load_library()
+    if k is None:
+        rc = lib.fa_rope(axes.ref, pos.data_ptr(), ps[0] if len(ps) == 3 else 0, qt, qo, Hq, None, None, 0, B, N, D,
+                         _DTYPES[dtype], _PAIRINGS[pairing], inverse, handle)
+    else:
+        ko = _strided(k_out, "k_out", dtype, k_shape, device)
+        rc = lib.fa_rope(axes.ref, pos.data_ptr(), ps[0] if len(ps) == 3 else 0, qt, qo, Hq, kt, ko, Hk, B, N, D,
+                         _DTYPES[dtype], _PAIRINGS[pairing], inverse, handle)
+    _raise("fa_rope", rc)
+    return q_out, k_out
 
 
 def fa_rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, axes: RopeAxes, q_out: torch.Tensor,
@@ -121,39 +172,9 @@ def fa_rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, axes: Ro
     """Enqueue the rotation into caller-provided outputs (any strides; the inputs themselves for in
     place).  q [B, Hq, N, D] and k [B, Hk, N, D] (or None) of one dtype, bf16, fp16 or fp32; pos int32
     [B, N, A] or [N, A]."""
-    B, Hq, N, D = _bhnd(q, "q")
-    if q.dtype not in _DTYPES:
-        raise TypeError(f"q must be bf16, fp16 or fp32, got {q.dtype}")
-    if pairing not in _PAIRINGS:
-        raise ValueError(f"pairing must be one of {tuple(_PAIRINGS)}, got {pairing!r}")
     if (k is None) != (k_out is None):
         raise ValueError("pass k and k_out together, or neither")
-    A = len(axes.dims)
-    if pos.dtype != torch.int32:
-        raise TypeError(f"pos must be torch.int32, got {pos.dtype}")
-    if pos.shape != (B, N, A) and pos.shape != (N, A):
-        raise ValueError(f"pos must have shape {(B, N, A)} or {(N, A)}, got {tuple(pos.shape)}")
-    if (A > 1 and pos.stride(-1) != 1) or (N > 1 and pos.stride(-2) != A):
-        raise ValueError("pos must be contiguous along its tokens and axes")
-    _same_device(pos, "pos", q)
-    ts = [_strided(q, "q", q.dtype, (B, Hq, N, D), q), _strided(q_out, "q_out", q.dtype, (B, Hq, N, D), q)]
-    Hk = 0
-    if k is not None:
-        Hk = _bhnd(k, "k")[1]
-        ts += [_strided(k, "k", q.dtype, (B, Hk, N, D), q), _strided(k_out, "k_out", q.dtype, (B, Hk, N, D), q)]
-    refs = [ctypes.byref(t) for t in ts] + [None] * (4 - len(ts))
-    with _on(q, stream):
-        rc = load_library().fa_rope(ctypes.byref(axes.struct), pos.data_ptr(), pos.stride(0) if pos.dim() == 3 else 0,
-                                    refs[0], refs[1], Hq, refs[2], refs[3], Hk, B, N, D, _DTYPES[q.dtype],
-                                    _PAIRINGS[pairing], int(bool(inverse)), _stream_handle(stream))
-    _raise("fa_rope", rc)
-
-
-def _rope_new(t: torch.Tensor, token_major: bool) -> torch.Tensor:
-    B, H, N, D = t.shape
-    if token_major:
-        return torch.empty((B, N, H, D), dtype=t.dtype, device=t.device).transpose(1, 2)
-    return torch.empty((B, H, N, D), dtype=t.dtype, device=t.device)
+    _run(q, stream, _rope, q, k, pos, axes, q_out, k_out, False, False, pairing, bool(inverse))
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, axes: RopeAxes, pairing: str = "adjacent",
@@ -162,13 +183,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, axes: RopeA
     contiguous [B, H, N, D] as the attention takes them, or with ``token_major`` views of contiguous
     [B, N, H, D] tensors.  Inputs may have any strides (slices of a projection)."""
     _bhnd(q, "q")
-    if k is not None:
-        _bhnd(k, "k")
-    with _on(q, stream):
-        q_out = _rope_new(q, token_major)
-        k_out = None if k is None else _rope_new(k, token_major)
-    fa_rope(q, k, pos, axes, q_out, k_out, pairing=pairing, inverse=inverse, stream=stream)
-    return q_out, k_out
+    return _run(q, stream, _rope, q, k, pos, axes, None, None, True, token_major, pairing, bool(inverse))
 
 
 def rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, pos: torch.Tensor, axes: RopeAxes,
@@ -188,12 +203,17 @@ class KVCache8:
         if k.dim() != 4:
             raise ValueError("k must be [pages, H, page_tokens, D]")
         pages, H, page, D = k.shape
-        if k.dtype not in (torch.float8_e4m3fn, torch.uint8):
-            raise TypeError(f"k must be torch.float8_e4m3fn or torch.uint8, got {k.dtype}")
-        self.struct = FaCache(_exact(k, "k", k.dtype, k.shape, k), _exact(v, "v", k.dtype, k.shape, k),
-                              _exact(k_scale, "k_scale", torch.float32, (pages, H), k),
-                              _exact(v_scale, "v_scale", torch.float32, (pages, H), k), pages, H, page, D)
+        dtype, device = k.dtype, k.get_device()
+        if dtype is not torch.float8_e4m3fn and dtype is not torch.uint8:
+            raise TypeError(f"k must be torch.float8_e4m3fn or torch.uint8, got {dtype}")
+        if device < 0:
+            raise ValueError("k must be a CUDA tensor")
+        self.struct = FaCache(_exact(k, "k", dtype, k.shape, device), _exact(v, "v", dtype, k.shape, device),
+                              _exact(k_scale, "k_scale", _F32, (pages, H), device),
+                              _exact(v_scale, "v_scale", _F32, (pages, H), device), pages, H, page, D)
+        self.ref = ctypes.byref(self.struct)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.heads, self.page_tokens, self.head_dim = H, page, D
 
     @classmethod
     def empty(cls, num_pages: int, heads: int, page_tokens: int, head_dim: int, device="cuda") -> "KVCache8":
@@ -203,14 +223,29 @@ class KVCache8:
         return cls(*codes, *scales)
 
 
-def _table(table: torch.Tensor, B: int, cache: KVCache8) -> int:
+def _table(table: torch.Tensor, B: int, device: int) -> int:
     if table.dim() != 2:
         raise ValueError("table must be [B, pages of a sequence]")
-    return _exact(table, "table", torch.int32, (B, table.shape[1]), cache.k)
+    return _exact(table, "table", _I32, (B, table.shape[1]), device)
 
 
-def _ints(t: torch.Tensor | None, name: str, B: int, cache: KVCache8) -> int | None:
-    return None if t is None else _exact(t, name, torch.int32, (B,), cache.k)
+def _ints(t: torch.Tensor | None, name: str, B: int, device: int) -> int | None:
+    return None if t is None else _exact(t, name, _I32, (B,), device)
+
+
+def _same_heads(cache: KVCache8, name: str, H: int, D: int) -> None:
+    if H != cache.heads or D != cache.head_dim:
+        raise ValueError(f"{name} must have {cache.heads} heads of {cache.head_dim}, got {H} of {D}")
+
+
+def _write(cache, k, v, table, start, count, device, handle):
+    B, H, N, D = shape = _bhnd(k, "k")
+    _same_heads(cache, "k", H, D)
+    rc = load_library().fa_cache_write(cache.ref, _strided(k, "k", _BF16, shape, device),
+                                       _strided(v, "v", _BF16, shape, device), _table(table, B, device),
+                                       table.shape[1], _ints(start, "start", B, device),
+                                       _ints(count, "count", B, device), B, N, handle)
+    _raise("fa_cache_write", rc)
 
 
 def cache_write(cache: KVCache8, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, start: torch.Tensor,
@@ -218,49 +253,64 @@ def cache_write(cache: KVCache8, k: torch.Tensor, v: torch.Tensor, table: torch.
     """Quantise tokens and append them: token i < count[b] (N if None) of k, v (bf16 [B, H, N, D], any
     strides) goes to position start[b] + i of sequence b, page table[b, position // page_tokens].
     start int32 [B] is what each sequence holds already.  The pages written must be distinct."""
-    B, H, N, D = _bhnd(k, "k")
-    c = cache.struct
-    if (H, D) != (c.H, c.D):
-        raise ValueError(f"k must have {c.H} heads of {c.D}, got {H} of {D}")
-    kt = _strided(k, "k", torch.bfloat16, (B, H, N, D), cache.k)
-    vt = _strided(v, "v", torch.bfloat16, (B, H, N, D), cache.k)
-    tab, at, n = _table(table, B, cache), _ints(start, "start", B, cache), _ints(count, "count", B, cache)
-    with _on(cache.k, stream):
-        rc = load_library().fa_cache_write(ctypes.byref(c), ctypes.byref(kt), ctypes.byref(vt), tab, table.shape[1],
-                                           at, n, B, N, _stream_handle(stream))
-    _raise("fa_cache_write", rc)
+    _run(cache.k, stream, _write, cache, k, v, table, start, count)
+
+
+def _read(cache, table, lens, k_out, v_out, n, start, device, handle):
+    if k_out is None:
+        shape = (table.shape[0], cache.heads, n, cache.head_dim)
+        k_out = torch.empty(shape, dtype=_BF16, device=cache.k.device)
+        v_out = torch.empty(shape, dtype=_BF16, device=cache.k.device)
+    B, H, N, D = shape = _bhnd(k_out, "k_out")
+    _same_heads(cache, "k_out", H, D)
+    rc = load_library().fa_cache_read(cache.ref, _table(table, B, device), table.shape[1],
+                                      _ints(lens, "lens", B, device), _ints(start, "start", B, device),
+                                      _exact(k_out, "k_out", _BF16, shape, device),
+                                      _exact(v_out, "v_out", _BF16, shape, device), B, N, handle)
+    _raise("fa_cache_read", rc)
+    return k_out, v_out
 
 
 def fa_cache_read(cache: KVCache8, table: torch.Tensor, lens: torch.Tensor, k_out: torch.Tensor,
                   v_out: torch.Tensor, start: torch.Tensor | None = None, stream=None) -> None:
     """Read tokens start[b] (0 if None) .. start[b] + N - 1 of each sequence into caller-provided bf16
     [B, H, N, D]; positions from lens[b] on give zeros."""
-    B, H, N, D = _bhnd(k_out, "k_out")
-    c = cache.struct
-    if (H, D) != (c.H, c.D):
-        raise ValueError(f"k_out must have {c.H} heads of {c.D}, got {H} of {D}")
-    ko = _exact(k_out, "k_out", torch.bfloat16, (B, H, N, D), cache.k)
-    vo = _exact(v_out, "v_out", torch.bfloat16, (B, H, N, D), cache.k)
-    tab, n, at = _table(table, B, cache), _ints(lens, "lens", B, cache), _ints(start, "start", B, cache)
-    with _on(cache.k, stream):
-        rc = load_library().fa_cache_read(ctypes.byref(c), tab, table.shape[1], n, at, ko, vo, B, N,
-                                          _stream_handle(stream))
-    _raise("fa_cache_read", rc)
+    _run(cache.k, stream, _read, cache, table, lens, k_out, v_out, None, start)
 
 
 def cache_read(cache: KVCache8, table: torch.Tensor, lens: torch.Tensor, n: int,
                start: torch.Tensor | None = None, stream=None):
     """Allocate outputs and read ``n`` tokens of each sequence back; returns (k, v) bf16 [B, H, n, D]."""
-    c = cache.struct
-    with _on(cache.k, stream):
-        k, v = (torch.empty((table.shape[0], c.H, n, c.D), dtype=torch.bfloat16, device=cache.k.device)
-                for _ in range(2))
-    fa_cache_read(cache, table, lens, k, v, start=start, stream=stream)
-    return k, v
+    return _run(cache.k, stream, _read, cache, table, lens, None, None, n, start)
 
 
 def cache_workspace_bytes(B: int, Hq: int, Hk: int, Nq: int, D: int, table_width: int, page_tokens: int) -> int:
     return int(load_library().fa_cache_workspace_bytes(B, Hq, Hk, Nq, D, table_width, page_tokens))
+
+
+def _attend(q, cache, table, lens, out, lse, workspace, causal, q_start, scale, device, handle):
+    B, Hq, Nq, D = shape = _bhnd(q, "q")
+    if D != cache.head_dim:
+        raise ValueError(f"q must have heads of {cache.head_dim}, got {D}")
+    qp, tab = _exact(q, "q", _BF16, shape, device), _table(table, B, device)
+    lib = load_library()
+    if out is None:
+        need = lib.fa_cache_workspace_bytes(B, Hq, cache.heads, Nq, D, table.shape[1], cache.page_tokens)
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        lse = torch.empty((B, Hq, Nq), dtype=_F32, device=q.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.get_device() != device:
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    rc = lib.fa_fwd_cache(qp, cache.ref, tab, table.shape[1], _ints(lens, "lens", B, device),
+                          _ints(q_start, "q_start", B, device), causal, _exact(out, "out", _BF16, shape, device),
+                          _exact(lse, "lse", _F32, (B, Hq, Nq), device), B, Hq, Nq, scale, ws_ptr, ws_bytes, handle)
+    _raise("fa_fwd_cache", rc)
+    return out, lse
 
 
 def fa_fwd_cache(q: torch.Tensor, cache: KVCache8, table: torch.Tensor, lens: torch.Tensor, out: torch.Tensor,
@@ -268,26 +318,7 @@ def fa_fwd_cache(q: torch.Tensor, cache: KVCache8, table: torch.Tensor, lens: to
                  q_start: torch.Tensor | None = None, scale: float | None = None, stream=None) -> None:
     """Enqueue the attention to the cache into caller-provided ``out`` and ``lse``; ``workspace`` holds
     at least cache_workspace_bytes(...) bytes (None when that is 0)."""
-    B, Hq, Nq, D = _bhnd(q, "q")
-    c = cache.struct
-    if D != c.D:
-        raise ValueError(f"q must have heads of {c.D}, got {D}")
-    qp = _exact(q, "q", torch.bfloat16, (B, Hq, Nq, D), cache.k)
-    op = _exact(out, "out", torch.bfloat16, (B, Hq, Nq, D), cache.k)
-    lp = _exact(lse, "lse", torch.float32, (B, Hq, Nq), cache.k)
-    tab, n, at = _table(table, B, cache), _ints(lens, "lens", B, cache), _ints(q_start, "q_start", B, cache)
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        _same_device(workspace, "workspace", q)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with _on(q, stream):
-        rc = load_library().fa_fwd_cache(qp, ctypes.byref(c), tab, table.shape[1], n, at, int(bool(causal)), op, lp,
-                                         B, Hq, Nq, ctypes.c_float(scale), ws_ptr, ws_bytes, _stream_handle(stream))
-    _raise("fa_fwd_cache", rc)
+    _run(cache.k, stream, _attend, q, cache, table, lens, out, lse, workspace, bool(causal), q_start, scale)
 
 
 def fwd_cache(q: torch.Tensor, cache: KVCache8, table: torch.Tensor, lens: torch.Tensor, causal: bool = False,
@@ -295,12 +326,4 @@ def fwd_cache(q: torch.Tensor, cache: KVCache8, table: torch.Tensor, lens: torch
     """Allocate outputs and workspace and attend to the cache: q bf16 [B, Hq, Nq, D] against the keys
     0 .. lens[b] - 1 of each sequence (int32 [B]); with ``causal`` row i sees the keys up to
     q_start[b] + i (lens[b] - Nq + i if None).  Returns (O bf16 [B, Hq, Nq, D], LSE fp32 [B, Hq, Nq])."""
-    B, Hq, Nq, D = _bhnd(q, "q")
-    c = cache.struct
-    need = cache_workspace_bytes(B, Hq, c.H, Nq, D, table.shape[-1], c.page_tokens)
-    with _on(q, stream):
-        out = torch.empty((B, Hq, Nq, D), dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    fa_fwd_cache(q, cache, table, lens, out, lse, ws, causal=causal, q_start=q_start, scale=scale, stream=stream)
-    return out, lse
+    return _run(cache.k, stream, _attend, q, cache, table, lens, None, None, None, bool(causal), q_start, scale)
