@@ -59,17 +59,26 @@ struct ChunkBars {
 };
 static_assert(sizeof(ChunkBars) <= 2048, "barrier space");
 
-// 16 codes to bf16, times a power of two (exact).
-__device__ __forceinline__ void chunk_bf16(const uint4& v, float scale, uint4 (&out)[2]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float2 f = e4m3x2_value((w[k / 2] >> (16 * (k & 1))) & 0xffffu);
-    o[k] = ptx::pack_bf16x2(f.x * scale, f.y * scale);
-  }
-  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+// Four codes to bf16 times a scale, exact, as two words that hold channels
+// 0, 2 and 1, 3 (O's columns are put in order when they are written).
+//
+// The conversion instruction is slow (16 codes in some 280 cycles a warp with
+// it, under 100 this way), so the bits are moved: an e4m3 code's exponent and
+// mantissa put at bits 4-10 of a bf16 are its value times 2^-120 (exponent
+// bias 127 for 7), subnormals included, and `mul` = 2^120 scale brings it back.
+// That is right but for NaN (0x7f), which `seen` catches in the top bit of the
+// bytes, and needs 2^120 scale to be a bf16 number.
+__device__ __forceinline__ void chunk_four(uint32_t x, uint32_t mul, uint32_t& even, uint32_t& odd, uint32_t& seen) {
+  seen |= (x & 0x7f7f7f7fu) + 0x01010101u;
+  even = ((x << 4) & 0x07f007f0u) | ((x << 8) & 0x80008000u);
+  odd = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(even) : "r"(mul));
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(odd) : "r"(mul));
+}
+// The same by conversion, for NaN and for scales above 2^7.
+__device__ __noinline__ uint2 chunk_four_any(uint32_t x, float scale) {
+  const float2 a = e4m3x2_value(x & 0xffffu), b = e4m3x2_value(x >> 16);
+  return make_uint2(ptx::pack_bf16x2(a.x * scale, b.x * scale), ptx::pack_bf16x2(a.y * scale, b.y * scale));
 }
 
 template <int D>
@@ -159,8 +168,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
           const int c = (HALVES == 2 ? (k & 1) * 4 : 0) + in_col;
           uint4 v = *reinterpret_cast<const uint4*>(src + cache_swizzle<D>(row, 16 * c));
           if (row >= held) v = make_uint4(0u, 0u, 0u, 0u);
-          uint4 o[2];
-          chunk_bf16(v, row < held ? vs[row >> 5] : 0.f, o);
+          const float scale = vs[row >> 5];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t m1 = (__float_as_uint(fminf(scale, 128.f)) + (120u << 23)) >> 16, mul = m1 | (m1 << 16);
+          uint32_t f[8], seen = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) chunk_four(w[e], mul, f[2 * e], f[2 * e + 1], seen);
+          if ((seen & 0x80808080u) || scale > 128.f) {
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+              const uint2 y = chunk_four_any(w[e], scale);
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                if (z == e) {
+                  f[2 * z] = y.x;
+                  f[2 * z + 1] = y.y;
+                }
+            }
+          }
+          const uint4 o[2] = {make_uint4(f[0], f[1], f[2], f[3]), make_uint4(f[4], f[5], f[6], f[7])};
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int piece = 2 * c + x;  // 16 bytes of the bf16 row
@@ -519,8 +545,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
           for (int k = 0; k < 4; ++k) {
             uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = ptx::pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]) * inv, __uint_as_float(r[8 * k + 2 * e + 1]) * inv);
+            for (int e = 0; e < 4; ++e) {  // columns hold channels 0, 2, 1, 3 of every four
+              const int i = 8 * k + 4 * (e >> 1) + (e & 1);
+              w[e] = ptx::pack_bf16x2(__uint_as_float(r[i]) * inv, __uint_as_float(r[i + 2]) * inv);
+            }
             dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
@@ -539,7 +567,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           dst[(cb / 4 + k) * kChunkRows] =
-              make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]), __uint_as_float(r[4 * k + 2]),
+              make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 1]),
                           __uint_as_float(r[4 * k + 3]));
       }
       reinterpret_cast<float2*>(p.part_ml)[slot * kChunkRows + in_unit] = make_float2(m, l);
