@@ -13,9 +13,15 @@
 // above 2^-10 of its row's largest, and off by 2^-18 of that below.  The scales
 // of q's row and of K's page go into the softmax's multiplier.
 //
-// P V runs in bf16: two warps turn each V page into bf16 (code * scale is a
-// bf16 number, so nothing is lost) in the layout that the MMA reads, one tile
-// ahead.  P is rounded to bf16 as in the forward kernel.
+// P V runs in f16, which holds every e4m3 number: two warps turn V's codes into
+// f16 in the layout that the MMA reads, one tile ahead.  (One instruction for
+// two codes.  Code times scale in bf16 instead cost two to four times as many,
+// and those two warps became the bound: 394 us for 2048 rows of 24 heads on
+// 16896 keys of 128, 510 us by moving bits, for 290 us this way.)  P is rounded
+// to f16: 11 bits, or 2^-25 of the row's largest p.  It carries its page's
+// scale of V relative to the largest scale so far, v_ref, so that 2^-25 stands
+// for at most v_ref / scale times as much of p; O is in units of v_ref and
+// rescaled when that grows.
 //
 // Units' tiles are cut into equal ranges, one per CTA (1 CTA per SM), as in
 // fa_cache_attn.cuh: 192 units of 256 rows on 152 SMs would leave a third of
@@ -38,12 +44,12 @@ constexpr int kChunkMeta = 8;  // tiles whose scales are kept: more than the pip
 template <int D>
 struct ChunkCfg {
   static constexpr int T8 = kCacheTile * D;              // 128 rows in e4m3
-  static constexpr int T16 = 2 * T8;                     // in bf16
-  static constexpr int SW = D >= 64 ? 128 : 64;          // swizzle span of the bf16 tile
+  static constexpr int T16 = 2 * T8;                     // in f16
+  static constexpr int SW = D >= 64 ? 128 : 64;          // swizzle span of the f16 tile
   static constexpr int CHUNK = kCacheTile * SW;          // its 128-row blocks of SW bytes
   static constexpr uint32_t LAYOUT8 = D == 128 ? 2u : (D == 64 ? 4u : 6u);
   static constexpr uint32_t LAYOUT16 = D >= 64 ? 2u : 4u;
-  static constexpr int K_STAGES = 3, V_STAGES = 2;       // K and V codes; V in bf16
+  static constexpr int K_STAGES = 3, V_STAGES = 2;       // K and V codes; V in f16
   static constexpr int SMEM_BYTES = 4 * T8 + 2 * K_STAGES * T8 + V_STAGES * T16 + 2048;
   static constexpr int COL_S = 0, COL_O = 256;           // S and O of tile t: + 128 t, + D t
 };
@@ -55,30 +61,26 @@ struct ChunkBars {
   CacheRange plan;
   uint32_t tmem_base;
   volatile int abort_flag;
-  float ks[kChunkMeta][4], vs[kChunkMeta][4];  // scales of a tile's 32-token groups
+  alignas(16) float ks[kChunkMeta][4];
+  alignas(16) float vs[kChunkMeta][4];  // scales of a tile's 32-token groups
 };
 static_assert(sizeof(ChunkBars) <= 2048, "barrier space");
 
-// Four codes to bf16 times a scale, exact, as two words that hold channels
-// 0, 2 and 1, 3 (O's columns are put in order when they are written).
-//
-// The conversion instruction is slow (16 codes in some 280 cycles a warp with
-// it, under 100 this way), so the bits are moved: an e4m3 code's exponent and
-// mantissa put at bits 4-10 of a bf16 are its value times 2^-120 (exponent
-// bias 127 for 7), subnormals included, and `mul` = 2^120 scale brings it back.
-// That is right but for NaN (0x7f), which `seen` catches in the top bit of the
-// bytes, and needs 2^120 scale to be a bf16 number.
-__device__ __forceinline__ void chunk_four(uint32_t x, uint32_t mul, uint32_t& even, uint32_t& odd, uint32_t& seen) {
-  seen |= (x & 0x7f7f7f7fu) + 0x01010101u;
-  even = ((x << 4) & 0x07f007f0u) | ((x << 8) & 0x80008000u);
-  odd = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(even) : "r"(mul));
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(odd) : "r"(mul));
+// 16 codes as f16 (exact; NaN stays NaN).
+__device__ __forceinline__ void chunk_f16(const uint4& v, uint4 (&out)[2]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[k]) : "h"((uint16_t)(w[k / 2] >> (16 * (k & 1)))));
+  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
-// The same by conversion, for NaN and for scales above 2^7.
-__device__ __noinline__ uint2 chunk_four_any(uint32_t x, float scale) {
-  const float2 a = e4m3x2_value(x & 0xffffu), b = e4m3x2_value(x >> 16);
-  return make_uint2(ptx::pack_bf16x2(a.x * scale, b.x * scale), ptx::pack_bf16x2(a.y * scale, b.y * scale));
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 template <int D>
@@ -159,41 +161,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
         if (!ok) break;
         const uint8_t* src = sV8 + s8 * C::T8;
         uint8_t* dst = sV + s16 * C::T16;
-        const float* vs = bars->vs[it % kChunkMeta];
         // Rows past the length may hold anything, NaN among it: zeros.
         const int held = sg.len - (sg.tile0 + j) * kCacheTile;
-#pragma unroll 8
-        for (int k = 0; k < STEPS; ++k) {
-          const int row = ((k / HALVES) * 2 + w) * RPI + in_row;
-          const int c = (HALVES == 2 ? (k & 1) * 4 : 0) + in_col;
-          uint4 v = *reinterpret_cast<const uint4*>(src + cache_swizzle<D>(row, 16 * c));
-          if (row >= held) v = make_uint4(0u, 0u, 0u, 0u);
-          const float scale = vs[row >> 5];
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          const uint32_t m1 = (__float_as_uint(fminf(scale, 128.f)) + (120u << 23)) >> 16, mul = m1 | (m1 << 16);
-          uint32_t f[8], seen = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) chunk_four(w[e], mul, f[2 * e], f[2 * e + 1], seen);
-          if ((seen & 0x80808080u) || scale > 128.f) {
+        // Piece k of this lane: its row and 16-channel column, its 32 bytes of f16.
+        auto row_of = [&](int k) { return ((k / HALVES) * 2 + w) * RPI + in_row; };
+        auto col_of = [&](int k) { return (HALVES == 2 ? (k & 1) * 4 : 0) + in_col; };
+        constexpr int BATCH = STEPS < 8 ? STEPS : 8;  // loads in flight together
 #pragma unroll 1
-            for (int e = 0; e < 4; ++e) {
-              const uint2 y = chunk_four_any(w[e], scale);
+        for (int k0 = 0; k0 < STEPS; k0 += BATCH) {
+          uint4 v[BATCH];
 #pragma unroll
-              for (int z = 0; z < 4; ++z)
-                if (z == e) {
-                  f[2 * z] = y.x;
-                  f[2 * z + 1] = y.y;
-                }
-            }
+          for (int k = 0; k < BATCH; ++k) {
+            v[k] = *reinterpret_cast<const uint4*>(src + cache_swizzle<D>(row_of(k0 + k), 16 * col_of(k0 + k)));
+            if (row_of(k0 + k) >= held) v[k] = make_uint4(0u, 0u, 0u, 0u);
           }
-          const uint4 o[2] = {make_uint4(f[0], f[1], f[2], f[3]), make_uint4(f[4], f[5], f[6], f[7])};
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int piece = 2 * c + x;  // 16 bytes of the bf16 row
-            const uint32_t at = C::SW == 128
-                                    ? (uint32_t)((piece >> 3) * C::CHUNK + row * 128 + (((piece & 7) ^ (row & 7)) << 4))
-                                    : (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
-            *reinterpret_cast<uint4*>(dst + at) = o[x];
+          for (int k = 0; k < BATCH; ++k) {
+            uint4 o[2];
+            chunk_f16(v[k], o);
+            const int row = row_of(k0 + k);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int piece = 2 * col_of(k0 + k) + x;  // 16 bytes of the f16 row
+              const uint32_t at = C::SW == 128
+                                      ? (uint32_t)((piece >> 3) * C::CHUNK + row * 128 + (((piece & 7) ^ (row & 7)) << 4))
+                                      : (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+              *reinterpret_cast<uint4*>(dst + at) = o[x];
+            }
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -284,8 +278,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     } else if (warp == 9) {
       // --------------------------------------------------------------- MMA --
       constexpr uint32_t IDESC_S = (1u << 4) | (16u << 17) | (8u << 24);  // e4m3, 128 x 128
-      constexpr uint32_t IDESC_PV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
-                                    (8u << 24);                           // bf16, 128 x D, B transposed
+      constexpr uint32_t IDESC_PV = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                    (8u << 24);                           // f16, 128 x D, B transposed
       constexpr uint32_t kVStep = (16 * C::SW) >> 4;                      // 16 keys of V
       const uint64_t dq = cache_desc(ptx::smem_u32(sQ), 16, 8 * D, C::LAYOUT8);
       const uint64_t dk = cache_desc(ptx::smem_u32(sK), 16, 8 * D, C::LAYOUT8);
@@ -442,17 +436,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     const int lim = p.rows.limit(sg.len, sg.first, (valid ? row : row0) / p.rows.g);
     const int wlim = __reduce_min_sync(0xffffffffu, lim);
     float m = -INFINITY, l = 0.f;
+    float v_ref = 0.f;  // the largest scale of V so far: the unit of O
     for (int j = 0; j < sg.ntiles; ++j, ++it) {
       const int kbase = (sg.tile0 + j) * kCacheTile;
       const uint32_t meta = it % kChunkMeta;
       ok = cache_wait(&bars->meta_full[meta], (it / kChunkMeta) & 1, bars, p);
       if (!ok) break;
       float sl[4];  // multipliers of the raw scores of each 32 keys: positive, or NaN
+      int ve[4];    // exponents of their scales of V, less that of the unit (0 at most)
+      const float4 vs = *reinterpret_cast<const float4*>(bars->vs[meta]);
+      const float v_new = fmaxf(fmaxf(fmaxf(vs.x, vs.y), fmaxf(vs.z, vs.w)), v_ref);
+      const int v_down = max((__float_as_int(v_ref) >> 23) - (__float_as_int(v_new) >> 23), -100);
+      {
+        const float4 ks = *reinterpret_cast<const float4*>(bars->ks[meta]);
+        const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, v4[4] = {vs.x, vs.y, vs.z, vs.w};
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        sl[g] = c * bars->ks[meta][g];
-        if (sl[g] < 1.17549435e-38f) sl[g] = 1.17549435e-38f;
+        for (int g = 0; g < 4; ++g) {
+          sl[g] = c * k4[g];
+          if (sl[g] < 1.17549435e-38f) sl[g] = 1.17549435e-38f;
+          ve[g] = max((__float_as_int(v4[g]) >> 23) - (__float_as_int(v_new) >> 23), -100);
+        }
       }
+      v_ref = v_new;
       ok = cache_wait(&bars->s_full[t], sc & 1, bars, p);
       if (!ok) break;
       ++sc;
@@ -491,16 +496,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       }
       const float m_use = m == -INFINITY ? 0.f : m;
       l *= alpha;
-      const bool rescale = j > 0 && __any_sync(0xffffffffu, grow);
+      const bool rescale = j > 0 && (v_down < 0 || __any_sync(0xffffffffu, grow));
+      alpha *= __int_as_float((v_down + 127) << 23);  // for O, which is in units of v_ref
       auto release = [&](uint64_t* bar) {
         ptx::tmem_wait_st();
         ptx::tc_fence_before_sync();
         ptx::mbar_arrive(ptx::smem_u32(bar));
       };
-      float2 lsum = make_float2(0.f, 0.f);
-      const float2 nm2 = make_float2(-m_use, -m_use);
+      // p carries the ratio of its page's scale of V to v_ref: a shift of the
+      // exponent, taken back from the sum.
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
+        float2 lsum = make_float2(0.f, 0.f);
+        const float shift = (float)ve[g] - m_use;
+        const float2 nm2 = make_float2(shift, shift);
         const float2 sl2 = make_float2(sl[g], sl[g]);
         uint32_t packed[16];
 #pragma unroll
@@ -508,12 +517,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
           const float2 x = __ffma2_rn(make_float2(s[32 * g + i], s[32 * g + i + 1]), sl2, nm2);
           const float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
           lsum = __fadd2_rn(lsum, e);
-          packed[i / 2] = ptx::pack_bf16x2(e.x, e.y);
+          packed[i / 2] = pack_f16x2(e.x, e.y);
         }
         ptx::tmem_st32x32b_x16(tS + 16 * g, packed);
+        l = fmaf(lsum.x + lsum.y, __int_as_float((127 - ve[g]) << 23), l);
         if (g == 1 && !rescale) release(&bars->p_half[t]);
       }
-      l += lsum.x + lsum.y;
       if (rescale) {
         // P V of the last tile is done: the S just read was issued after it.
 #pragma unroll
@@ -534,7 +543,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     ++oc;
     ptx::tc_fence_after_sync();
     if (sg.ntiles == sg.total) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = l == 0.f ? 0.f : v_ref / l;
 #pragma unroll
       for (int cb = 0; cb < D; cb += 32) {
         uint32_t r[32];
@@ -545,10 +554,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
           for (int k = 0; k < 4; ++k) {
             uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {  // columns hold channels 0, 2, 1, 3 of every four
-              const int i = 8 * k + 4 * (e >> 1) + (e & 1);
-              w[e] = ptx::pack_bf16x2(__uint_as_float(r[i]) * inv, __uint_as_float(r[i + 2]) * inv);
-            }
+            for (int e = 0; e < 4; ++e)
+              w[e] = ptx::pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]) * inv, __uint_as_float(r[8 * k + 2 * e + 1]) * inv);
             dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
@@ -567,8 +574,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           dst[(cb / 4 + k) * kChunkRows] =
-              make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 1]),
-                          __uint_as_float(r[4 * k + 3]));
+              make_float4(__uint_as_float(r[4 * k]) * v_ref, __uint_as_float(r[4 * k + 1]) * v_ref,
+                          __uint_as_float(r[4 * k + 2]) * v_ref, __uint_as_float(r[4 * k + 3]) * v_ref);
       }
       reinterpret_cast<float2*>(p.part_ml)[slot * kChunkRows + in_unit] = make_float2(m, l);
     }
