@@ -300,7 +300,7 @@ int launch_cache_attn(fa::CacheAttnParams& p, const CachePlan& plan, const fa::D
   return launch_after(fa::fa_cache_merge_kernel<D, RT>, blocks, 128, p, s);
 }
 
-template <int D>
+template <int D, bool ONE>
 int launch_cache_chunk(fa::CacheAttnParams& p, const CachePlan& plan, const fa::DeviceState& st, cudaStream_t s) {
   using C = fa::ChunkCfg<D>;
   static std::mutex mu;
@@ -308,7 +308,7 @@ int launch_cache_chunk(fa::CacheAttnParams& p, const CachePlan& plan, const fa::
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[st.device]) {
-      if (cudaFuncSetAttribute(fa::fa_cache_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(fa::fa_cache_chunk_kernel<D, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                C::SMEM_BYTES) != cudaSuccess)
         return FA_ERR_CUDA;
       ready[st.device] = true;
@@ -317,10 +317,11 @@ int launch_cache_chunk(fa::CacheAttnParams& p, const CachePlan& plan, const fa::
   int64_t grid = st.sm_count < fa::kChunkMaxGrid ? st.sm_count : fa::kChunkMaxGrid;
   if (grid > plan.tiles) grid = plan.tiles;
   p.ctas = (int)grid;
-  fa::log_launch("fa_cache_chunk_kernel<D=%d> grid %d x %d threads smem %d B tmem 512 cols stages %d + %d, %lld units "
-                 "a sequence, %lld tiles at most", D, p.ctas, fa::kChunkThreads, C::SMEM_BYTES, C::K_STAGES,
-                 C::V_STAGES, (long long)plan.units, (long long)plan.tiles);
-  fa::fa_cache_chunk_kernel<D><<<p.ctas, fa::kChunkThreads, C::SMEM_BYTES, s>>>(p);
+  fa::log_launch("fa_cache_chunk_kernel<D=%d,%s> grid %d x %d threads smem %d B tmem 512 cols stages %d + %d, %lld units "
+                 "a sequence, %lld tiles at most", D, ONE ? "a page a tile" : "pages in tiles", p.ctas,
+                 fa::kChunkThreads, C::SMEM_BYTES, C::K_STAGES, C::V_STAGES, (long long)plan.units,
+                 (long long)plan.tiles);
+  fa::fa_cache_chunk_kernel<D, ONE><<<p.ctas, fa::kChunkThreads, C::SMEM_BYTES, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (!plan.total) return FA_OK;  // no unit can be cut
   const unsigned blocks = (unsigned)p.ctas * (D / 16);
@@ -331,7 +332,9 @@ int launch_cache_chunk(fa::CacheAttnParams& p, const CachePlan& plan, const fa::
 template <int D>
 int launch_cache_attn(fa::CacheAttnParams& p, const CachePlan& plan, const fa::DeviceState& st, cudaStream_t s) {
   switch (plan.rt) {
-    case fa::kChunkRows: return launch_cache_chunk<D>(p, plan, st, s);
+    case fa::kChunkRows:
+      return p.c.page == fa::kCacheTile ? launch_cache_chunk<D, true>(p, plan, st, s)
+                                        : launch_cache_chunk<D, false>(p, plan, st, s);
     case 4: return launch_cache_attn<D, 4>(p, plan, st, s);
     case 8: return launch_cache_attn<D, 8>(p, plan, st, s);
     default: return launch_cache_attn<D, 16>(p, plan, st, s);

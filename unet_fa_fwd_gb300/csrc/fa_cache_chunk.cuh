@@ -83,7 +83,8 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-template <int D>
+// ONE: a page is a whole tile (128 tokens), so a tile has one scale.
+template <int D, bool ONE>
 __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const __grid_constant__ CacheAttnParams p) {
   using C = ChunkCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -388,48 +389,45 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     const int row = row0 + in_tile;
     const bool valid = row < p.rows.R;
     const long long at = p.row_at(sg.b, sg.h, valid ? row : row0);
-    // This thread's row of Q as s (hi + lo).  The MMAs that read the last
-    // unit's Q are done: their S has been read.
-    float c;
+    // The warp's 32 rows of Q as s (hi + lo), D / 8 lanes to a row.  The MMAs
+    // that read the last unit's Q are done: their S has been read.
+    float c = 0.f;
     {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + at * D);
-      uint32_t amax = 0;
-#pragma unroll 4
-      for (int k = 0; k < D / 8; ++k) {
-        const uint4 v = __ldg(src + k);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      constexpr int LPR = D / 8, RPS = 32 / LPR;  // lanes of a row, rows of a step
+      uint4 v[LPR];
+#pragma unroll
+      for (int k = 0; k < LPR; ++k) {
+        const long long from = __shfl_sync(0xffffffffu, at, k * RPS + (int)lane / LPR);
+        v[k] = __ldg(reinterpret_cast<const uint4*>(p.q + from * D) + lane % LPR);
+      }
+#pragma unroll
+      for (int k = 0; k < LPR; ++k) {
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        uint32_t amax = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) amax = max(amax, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
-      }
-      const int e2 = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-      // a negative scale turns the row round, so that the multiplier is positive
-      const float inv = __int_as_float((127 - e2) << 23) * (p.scale_log2 < 0.f ? -1.f : 1.f);
-#pragma unroll 2
-      for (int k = 0; k < D / 16; ++k) {
-        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint4 v = __ldg(src + 2 * k + x);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t h[4], l[4];
+        for (int o = LPR / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int e2 = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+        // a negative scale turns the row round, so that the multiplier is positive
+        const float inv = __int_as_float((127 - e2) << 23) * (p.scale_log2 < 0.f ? -1.f : 1.f);
+        uint32_t h[4], l[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = __uint_as_float(w[e] << 16) * inv, b = __uint_as_float(w[e] & 0xffff0000u) * inv;
-            h[e] = e4m3x2_bits(a, b);
-            const float2 f = e4m3x2_value(h[e]);
-            l[e] = e4m3x2_bits(a - f.x, b - f.y);
-          }
-          hi[2 * x] = h[0] | (h[1] << 16);
-          hi[2 * x + 1] = h[2] | (h[3] << 16);
-          lo[2 * x] = l[0] | (l[1] << 16);
-          lo[2 * x + 1] = l[2] | (l[3] << 16);
+        for (int e = 0; e < 4; ++e) {
+          const float a = __uint_as_float(w[e] << 16) * inv, b = __uint_as_float(w[e] & 0xffff0000u) * inv;
+          h[e] = e4m3x2_bits(a, b);
+          const float2 f = e4m3x2_value(h[e]);
+          l[e] = e4m3x2_bits(a - f.x, b - f.y);
         }
-        const uint32_t off = cache_swizzle<D>(in_tile, 16 * k);
-        *reinterpret_cast<uint4*>(q_hi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(q_lo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const uint32_t off = cache_swizzle<D>((warp % 4) * 32 + k * RPS + (int)lane / LPR, 8 * ((int)lane % LPR));
+        *reinterpret_cast<uint2*>(q_hi + off) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        *reinterpret_cast<uint2*>(q_lo + off) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+        // a row that holds a number that is not finite gives NaN
+        const float cr =
+            amax >= 0x7f800000u ? __int_as_float(0x7fc00000) : __int_as_float((e2 + 127) << 23) * fabsf(p.scale_log2);
+        const float mine = __shfl_sync(0xffffffffu, cr, ((int)lane % RPS) * LPR);
+        if ((int)lane / RPS == k) c = mine;
       }
-      // a row that holds a number that is not finite gives NaN
-      c = amax >= 0x7f800000u ? __int_as_float(0x7fc00000) : __int_as_float((e2 + 127) << 23) * fabsf(p.scale_log2);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready[t]));
     }
@@ -442,20 +440,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       const uint32_t meta = it % kChunkMeta;
       ok = cache_wait(&bars->meta_full[meta], (it / kChunkMeta) & 1, bars, p);
       if (!ok) break;
-      float sl[4];  // multipliers of the raw scores of each 32 keys: positive, or NaN
-      int ve[4];    // exponents of their scales of V, less that of the unit (0 at most)
-      const float4 vs = *reinterpret_cast<const float4*>(bars->vs[meta]);
-      const float v_new = fmaxf(fmaxf(fmaxf(vs.x, vs.y), fmaxf(vs.z, vs.w)), v_ref);
-      const int v_down = max((__float_as_int(v_ref) >> 23) - (__float_as_int(v_new) >> 23), -100);
-      {
-        const float4 ks = *reinterpret_cast<const float4*>(bars->ks[meta]);
-        const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, v4[4] = {vs.x, vs.y, vs.z, vs.w};
+      constexpr int G = ONE ? 1 : 4;  // groups of keys with scales of their own
+      float sl[G];  // multipliers of the raw scores: positive, or NaN
+      int ve[G];    // exponents of the scales of V, less that of the unit (0 at most)
+      float ks[G], vs[G], v_new = v_ref;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          sl[g] = c * k4[g];
-          if (sl[g] < 1.17549435e-38f) sl[g] = 1.17549435e-38f;
-          ve[g] = max((__float_as_int(v4[g]) >> 23) - (__float_as_int(v_new) >> 23), -100);
-        }
+      for (int g = 0; g < G; ++g) {
+        ks[g] = bars->ks[meta][g];
+        vs[g] = bars->vs[meta][g];
+        v_new = fmaxf(v_new, vs[g]);
+      }
+      const int v_down = max((__float_as_int(v_ref) >> 23) - (__float_as_int(v_new) >> 23), -100);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        sl[g] = c * ks[g];
+        if (sl[g] < 1.17549435e-38f) sl[g] = 1.17549435e-38f;
+        ve[g] = max((__float_as_int(vs[g]) >> 23) - (__float_as_int(v_new) >> 23), -100);
       }
       v_ref = v_new;
       ok = cache_wait(&bars->s_full[t], sc & 1, bars, p);
@@ -476,14 +476,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       }
       float mx = -INFINITY;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float a0 = s[32 * g], a1 = s[32 * g + 1];
+      for (int g = 0; g < G; ++g) {
+        constexpr int N = 128 / G;
+        float a[4] = {s[N * g], s[N * g + 1], s[N * g + 2], s[N * g + 3]};
 #pragma unroll
-        for (int i = 2; i < 32; i += 4) {
-          a0 = ptx::fmax3(a0, s[32 * g + i], s[32 * g + i + 1]);
-          if (i + 3 < 32) a1 = ptx::fmax3(a1, s[32 * g + i + 2], s[32 * g + i + 3]);
-        }
-        mx = fmaxf(mx, fmaxf(a0, a1) * sl[g]);
+        for (int i = 4; i < N; i += 8)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (i + 2 * x < N) a[x] = ptx::fmax3(a[x], s[N * g + i + 2 * x], s[N * g + i + 2 * x + 1]);
+        mx = fmaxf(mx, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * sl[g]);
       }
       // The reference moves only when the maximum grew by more than 8 (exact:
       // O, l and LSE use the same one).
@@ -505,23 +506,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       };
       // p carries the ratio of its page's scale of V to v_ref: a shift of the
       // exponent, taken back from the sum.
+      float2 lsum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float2 lsum = make_float2(0.f, 0.f);
+      for (int cb = 0; cb < 128; cb += 32) {
+        const int g = cb * G / 128;
         const float shift = (float)ve[g] - m_use;
-        const float2 nm2 = make_float2(shift, shift);
-        const float2 sl2 = make_float2(sl[g], sl[g]);
+        const float2 nm2 = make_float2(shift, shift), sl2 = make_float2(sl[g], sl[g]);
         uint32_t packed[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const float2 x = __ffma2_rn(make_float2(s[32 * g + i], s[32 * g + i + 1]), sl2, nm2);
+          const float2 x = __ffma2_rn(make_float2(s[cb + i], s[cb + i + 1]), sl2, nm2);
           const float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
           lsum = __fadd2_rn(lsum, e);
           packed[i / 2] = pack_f16x2(e.x, e.y);
         }
-        ptx::tmem_st32x32b_x16(tS + 16 * g, packed);
-        l = fmaf(lsum.x + lsum.y, __int_as_float((127 - ve[g]) << 23), l);
-        if (g == 1 && !rescale) release(&bars->p_half[t]);
+        ptx::tmem_st32x32b_x16(tS + cb / 2, packed);
+        if (!ONE || cb == 96) {
+          l = fmaf(lsum.x + lsum.y, __int_as_float((127 - ve[g]) << 23), l);
+          lsum = make_float2(0.f, 0.f);
+        }
+        if (cb == 32 && !rescale) release(&bars->p_half[t]);
       }
       if (rescale) {
         // P V of the last tile is done: the S just read was issued after it.
