@@ -53,7 +53,7 @@ static int walk(const std::vector<int>& lens, const std::vector<int>& starts, in
                 int max_len, int ctas) {
   const int B = (int)lens.size();
   fa::CacheRows rows{lens.data(), starts.empty() ? nullptr : starts.data(), B, H, g, Nq, g * Nq, RT,
-                     (g * Nq + RT - 1) / RT, causal, max_len};
+                     (g * Nq + RT - 1) / RT, causal, max_len, fa::FastDiv::make((uint32_t)g)};
   struct Unit { int b, h, rt; long long t0; int nt; };
   std::vector<Unit> units;
   std::vector<long long> base(B + 1, 0);

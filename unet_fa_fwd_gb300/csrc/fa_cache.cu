@@ -572,7 +572,8 @@ int fa_fwd_cache(const void* q, const fa_cache* cache, const int* table, int tab
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.rows = fa::CacheRows{lens, q_start, B, cache->H, Hq / cache->H, Nq, plan.R, plan.rt, plan.row_tiles,
-                         causal ? 1 : 0, table_width * cache->page_tokens};
+                         causal ? 1 : 0, table_width * cache->page_tokens,
+                         fa::FastDiv::make((uint32_t)(Hq / cache->H))};
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.status = st->status;
   if (need) {

@@ -84,7 +84,7 @@ struct CacheAttnParams {
   }
   // Row of q, out and lse of row r of a key head.
   __device__ __forceinline__ long long row_at(int b, int h, int r) const {
-    const int i = r / rows.g;
+    const int i = (int)rows.by_g.div((uint32_t)r);
     return (((long long)b * rows.H + h) * rows.g + (r - i * rows.g)) * rows.Nq + i;
   }
 };
@@ -193,8 +193,10 @@ __device__ __forceinline__ void cache_plan(const CacheRows& rows, int ctas, int*
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const int grid = cache_active(total, ctas), c = (int)blockIdx.x;
-  const long long t0 = c < grid ? cache_range_begin(total, grid, c) : total;
-  const long long t1 = c < grid ? cache_range_begin(total, grid, c + 1) : total;
+  const long long q = cache_div(total, grid);
+  const int left = (int)(total - q * grid);
+  const long long t0 = c < grid ? q * c + left * c / grid : total;  // cache_range_begin
+  const long long t1 = c < grid ? q * (c + 1) + left * (c + 1) / grid : total;
   long long base = 0, base0 = 0;
   int b0 = 0;
   for (int b = 0; b < rows.B && t0 < total; b += 32) {
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
             // a row that holds a number that is not finite gives NaN
             bars->c[r] = amax >= 0x7f800000u ? __int_as_float(0x7fc00000)
                                              : __int_as_float((e2 + 127) << 23) * p.scale_log2;
-            bars->lim[r] = p.rows.limit(sg.len, sg.first, (row0 + r) / p.rows.g);
+            bars->lim[r] = p.rows.limit(sg.len, sg.first, (int)p.rows.by_g.div((uint32_t)(row0 + r)));
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

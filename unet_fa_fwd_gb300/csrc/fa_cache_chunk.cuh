@@ -393,45 +393,59 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     // that read the last unit's Q are done: their S has been read.
     float c = 0.f;
     {
+      // (Rolled up: this code runs once a unit, and unrolled it cost more time
+      // in instruction misses than in work.)
       constexpr int LPR = D / 8, RPS = 32 / LPR;  // lanes of a row, rows of a step
-      uint4 v[LPR];
+      constexpr int BATCH = 4;                    // loads in flight
+      uint4 next[BATCH];
+      auto fetch = [&](int k0) {
 #pragma unroll
-      for (int k = 0; k < LPR; ++k) {
-        const long long from = __shfl_sync(0xffffffffu, at, k * RPS + (int)lane / LPR);
-        v[k] = __ldg(reinterpret_cast<const uint4*>(p.q + from * D) + lane % LPR);
-      }
-#pragma unroll
-      for (int k = 0; k < LPR; ++k) {
-        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-        uint32_t amax = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) amax = max(amax, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
-#pragma unroll
-        for (int o = LPR / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const int e2 = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-        // a negative scale turns the row round, so that the multiplier is positive
-        const float inv = __int_as_float((127 - e2) << 23) * (p.scale_log2 < 0.f ? -1.f : 1.f);
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = __uint_as_float(w[e] << 16) * inv, b = __uint_as_float(w[e] & 0xffff0000u) * inv;
-          h[e] = e4m3x2_bits(a, b);
-          const float2 f = e4m3x2_value(h[e]);
-          l[e] = e4m3x2_bits(a - f.x, b - f.y);
+        for (int x = 0; x < BATCH; ++x) {
+          const long long from = __shfl_sync(0xffffffffu, at, (k0 + x) * RPS + (int)lane / LPR);
+          next[x] = __ldg(reinterpret_cast<const uint4*>(p.q + from * D) + lane % LPR);
         }
-        const uint32_t off = cache_swizzle<D>((warp % 4) * 32 + k * RPS + (int)lane / LPR, 8 * ((int)lane % LPR));
-        *reinterpret_cast<uint2*>(q_hi + off) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-        *reinterpret_cast<uint2*>(q_lo + off) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
-        // a row that holds a number that is not finite gives NaN
-        const float cr =
-            amax >= 0x7f800000u ? __int_as_float(0x7fc00000) : __int_as_float((e2 + 127) << 23) * fabsf(p.scale_log2);
-        const float mine = __shfl_sync(0xffffffffu, cr, ((int)lane % RPS) * LPR);
-        if ((int)lane / RPS == k) c = mine;
+      };
+      fetch(0);
+#pragma unroll 1
+      for (int k0 = 0; k0 < LPR; k0 += BATCH) {
+        uint4 v[BATCH];
+#pragma unroll
+        for (int x = 0; x < BATCH; ++x) v[x] = next[x];
+        if (k0 + BATCH < LPR) fetch(k0 + BATCH);
+#pragma unroll
+        for (int x = 0; x < BATCH; ++x) {
+          const int k = k0 + x;
+          const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+          uint32_t amax = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) amax = max(amax, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
+#pragma unroll
+          for (int o = LPR / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const int e2 = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+          // a negative scale turns the row round, so that the multiplier is positive
+          const float inv = __int_as_float((127 - e2) << 23) * (p.scale_log2 < 0.f ? -1.f : 1.f);
+          uint32_t h[4], l[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = __uint_as_float(w[e] << 16) * inv, b = __uint_as_float(w[e] & 0xffff0000u) * inv;
+            h[e] = e4m3x2_bits(a, b);
+            const float2 f = e4m3x2_value(h[e]);
+            l[e] = e4m3x2_bits(a - f.x, b - f.y);
+          }
+          const uint32_t off = cache_swizzle<D>((warp % 4) * 32 + k * RPS + (int)lane / LPR, 8 * ((int)lane % LPR));
+          *reinterpret_cast<uint2*>(q_hi + off) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+          *reinterpret_cast<uint2*>(q_lo + off) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+          // a row that holds a number that is not finite gives NaN
+          const float cr = amax >= 0x7f800000u ? __int_as_float(0x7fc00000)
+                                               : __int_as_float((e2 + 127) << 23) * fabsf(p.scale_log2);
+          const float mine = __shfl_sync(0xffffffffu, cr, ((int)lane % RPS) * LPR);
+          if ((int)lane / RPS == k) c = mine;
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready[t]));
     }
-    const int lim = p.rows.limit(sg.len, sg.first, (valid ? row : row0) / p.rows.g);
+    const int lim = p.rows.limit(sg.len, sg.first, (int)p.rows.by_g.div((uint32_t)(valid ? row : row0)));
     const int wlim = __reduce_min_sync(0xffffffffu, lim);
     float m = -INFINITY, l = 0.f;
     float v_ref = 0.f;  // the largest scale of V so far: the unit of O
@@ -529,7 +543,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       }
       if (rescale) {
         // P V of the last tile is done: the S just read was issued after it.
-#pragma unroll
+#pragma unroll 1
         for (int cb = 0; cb < D; cb += 32) {
           uint32_t r[32];
           ptx::tmem_ld32x32b_x32(tO + cb, r);
@@ -548,7 +562,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     ptx::tc_fence_after_sync();
     if (sg.ntiles == sg.total) {
       const float inv = l == 0.f ? 0.f : v_ref / l;
-#pragma unroll
+#pragma unroll 1
       for (int cb = 0; cb < D; cb += 32) {
         uint32_t r[32];
         ptx::tmem_ld32x32b_x32(tO + cb, r);
@@ -571,7 +585,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       const int in_unit = t * 128 + in_tile;
       if (threadIdx.x == 0) p.note_cut(sg, bars->plan);
       float4* dst = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * kChunkRows + in_unit;
-#pragma unroll
+#pragma unroll 1
       for (int cb = 0; cb < D; cb += 32) {
         uint32_t r[32];
         ptx::tmem_ld32x32b_x32(tO + cb, r);

@@ -63,6 +63,7 @@ struct CacheRows {
   const int* lens;     // [B]
   const int* q_start;  // [B] or nullptr: len - Nq
   int B, H, g, Nq, R, RT, row_tiles, causal, max_len;
+  FastDiv by_g;        // division by g
 
   FA_HD int len(int b, bool& bad) const { return cache_clamp(lens[b], max_len, bad); }
   FA_HD long long first(int b, int len) const { return q_start ? (long long)q_start[b] : (long long)len - Nq; }
@@ -76,7 +77,7 @@ struct CacheRows {
   FA_HD int tiles(int len, long long first, int rt) const {
     if (!causal) return cache_tiles(len);
     const int rows = (rt + 1) * (long long)RT < R ? (rt + 1) * RT : R;
-    return cache_tiles(limit(len, first, (rows - 1) / g) + 1);
+    return cache_tiles(limit(len, first, (int)by_g.div((uint32_t)(rows - 1))) + 1);
   }
   // Tiles of all row tiles of a key head.
   FA_HD long long head_tiles(int len, long long first) const {
@@ -89,9 +90,17 @@ struct CacheRows {
 
 FA_HD int cache_active(long long total, int ctas) { return total < ctas ? (int)total : ctas; }
 
-// `grid` below is cache_active(total, ctas).
+// a / b for a >= 0, b > 0 (a 64-bit division costs a kernel's start some half a
+// microsecond, so it is taken only where it is needed).
+FA_HD long long cache_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
+// `grid` below is cache_active(total, ctas): at most a few thousand.
 FA_HD long long cache_range_begin(long long total, int grid, int cta) {
-  return total / grid * cta + total % grid * cta / grid;  // floor(total * cta / grid)
+  const long long q = cache_div(total, grid);
+  return q * cta + (int)(total - q * grid) * cta / grid;  // floor(total * cta / grid)
 }
 
 // The CTA whose range holds tile t.
@@ -131,7 +140,7 @@ struct CacheWalk {
     load();
     if (t >= end) return;
     const long long per_head = r->head_tiles(len, first);
-    h = (int)((t - base) / per_head);
+    h = (int)cache_div(t - base, per_head);
     base += h * per_head;
     unit();
     while (t >= base + nt) {
