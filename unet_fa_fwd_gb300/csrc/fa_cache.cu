@@ -275,13 +275,25 @@ int launch_cache_attn(fa::CacheAttnParams& p, const CachePlan& plan, const fa::D
     std::lock_guard<std::mutex> lock(mu);
     int& r = resident[st.device];
     if (!r) {
-      int n = 0;
+      // By shared memory, registers and tensor memory (the occupancy query
+      // answers 1 for kernels that allocate tensor memory, whose columns it
+      // does not see).
+      int smem = 0, reserved = 0, regs = 0;
+      cudaFuncAttributes attr;
       if (cudaFuncSetAttribute(fa::fa_cache_attn_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                C::SMEM_BYTES) != cudaSuccess ||
-          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fa::fa_cache_attn_kernel<D, RT>, fa::kCacheThreads,
-                                                        C::SMEM_BYTES) != cudaSuccess || n < 1)
+          cudaFuncSetAttribute(fa::fa_cache_attn_kernel<D, RT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared) != cudaSuccess ||
+          cudaFuncGetAttributes(&attr, fa::fa_cache_attn_kernel<D, RT>) != cudaSuccess ||
+          cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, st.device) != cudaSuccess ||
+          cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, st.device) != cudaSuccess ||
+          cudaDeviceGetAttribute(&regs, cudaDevAttrMaxRegistersPerMultiprocessor, st.device) != cudaSuccess)
         return FA_ERR_CUDA;
-      r = n < 512 / C::TMEM_COLS ? n : 512 / C::TMEM_COLS;
+      int n = smem / (C::SMEM_BYTES + reserved);
+      const int by_regs = regs / ((attr.numRegs + 7) / 8 * 8 * fa::kCacheThreads);
+      n = n < by_regs ? n : by_regs;
+      n = n < 512 / C::TMEM_COLS ? n : 512 / C::TMEM_COLS;
+      r = n < 1 ? 1 : n;
     }
     per_sm = r;
   }
