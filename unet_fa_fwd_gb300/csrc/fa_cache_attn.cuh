@@ -97,13 +97,16 @@ struct CacheCfg {
   static constexpr int NO = (3 * RT + 15) / 16 * 16;     // N of O^T: hi, mid, lo
   static constexpr uint32_t LAYOUT = D == 128 ? 2u : (D == 64 ? 4u : 6u);  // swizzle over a token's D bytes
   static constexpr int SBO = 8 * D;
-  static constexpr int STAGES = D == 128 ? 3 : (D == 64 ? 4 : 6);
+  static constexpr int STAGES = D == 128 ? 3 : (D == 64 ? 3 : 4);
   static constexpr int SMEM_Q = (NS * D + 1023) / 1024 * 1024;
   static constexpr int SMEM_P = NO * kCacheTile;         // K-major: 128 keys of a column contiguous
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SMEM_Q + SMEM_P + 2048;
   static constexpr int COL_S = 0, COL_O = 2 * NS;
   static constexpr int TMEM_COLS = 2 * NS + NO <= 64 ? 64 : 128;
   static_assert(2 * NS + NO <= 128, "tensor memory");
+  // CTAs that an SM is to hold (the compiler's register bound): two at D = 128,
+  // by shared memory; the rows' registers decide below that.
+  static constexpr int RESIDENT = D == 128 ? 2 : (RT == 4 ? 4 : (RT == 8 ? 3 : 2));
   static_assert(STAGES <= kCacheStagesMax, "ring barriers");
 };
 
@@ -114,9 +117,10 @@ struct CacheBars {
   uint32_t tmem_base;
   volatile int abort_flag;
   int wg_fail;
-  float ks[kCacheStagesMax][4], vs[kCacheStagesMax][4];  // scales of a tile's pages
-  float c[16];     // row: multiplier of the raw product, times the page's scale of K
-  int lim[16];     // row: its last visible key
+  float ks[kCacheStagesMax][4];
+  alignas(16) float vs[kCacheStagesMax][4];  // scales of a tile's 32-token groups
+  alignas(16) float c[16];  // row: multiplier of the raw product, times the page's scale of K
+  alignas(16) int lim[16];  // row: its last visible key
   float red[4][16];
 };
 static_assert(sizeof(CacheBars) <= 2048, "barrier space");
@@ -222,7 +226,7 @@ __device__ __forceinline__ void cache_plan(const CacheRows& rows, int ctas, int*
 }
 
 template <int D, int RT>
-__global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
+__global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
   using C = CacheCfg<D, RT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sRing = smem;
@@ -301,10 +305,11 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
         }
         const int src = in_batch * ppt + (int)(lane % ppt);
         const int my_id = __shfl_sync(0xffffffffu, id, src);
-        const float my_ks = __shfl_sync(0xffffffffu, ks, src), my_vs = __shfl_sync(0xffffffffu, vs, src);
+        const int group = in_batch * ppt + (int)(lane & 3) * 32 / page;  // page of this lane's 32 tokens
+        const float my_ks = __shfl_sync(0xffffffffu, ks, group), my_vs = __shfl_sync(0xffffffffu, vs, group);
         const int first = (sg.tile0 + j) * ppt;
         const int n = max(0, min(ppt, npages - first));  // pages of this tile that hold tokens
-        if ((int)lane < ppt) {
+        if (lane < 4) {
           bars->ks[s][lane] = my_ks;
           bars->vs[s][lane] = my_vs;
         }
@@ -353,10 +358,8 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
     };
     auto issue_o = [&](uint32_t stage) {
       const uint32_t a = (uint32_t)dv + stage * (C::STAGE_BYTES >> 4);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)  // 32 keys each
-        ptx::mma_ss_f8_x1_el(tmem + C::COL_O, a + k * (32 * D >> 4), (uint32_t)(dv >> 32), (uint32_t)dp + k * 2,
-                             (uint32_t)(dp >> 32), IDESC_O, k ? 1u : 0u);
+      ptx::mma_ss_f8_strided_x4_el<(32 * D >> 4), 2>(tmem + C::COL_O, a, (uint32_t)(dv >> 32), (uint32_t)dp,
+                                                      (uint32_t)(dp >> 32), IDESC_O, 0);  // 32 keys each
     };
     uint32_t it = 0, seg = 0;  // tiles and segments so far
     bool ok = true;
@@ -396,7 +399,10 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
     constexpr float kTop = 7.f, kLimit = 8.75f, kNone = -1e30f;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const uint32_t tS = tmem + lane_base + C::COL_S, tO = tmem + lane_base + C::COL_O;
+    // Byte of key tid in column n of P (128-byte rows, swizzled over them).
+    auto p_byte = [&](int n) -> uint8_t& { return sP[(tid ^ ((n & 7) << 4)) + n * kCacheTile]; };
     uint32_t it = 0;
+    uint32_t stage = 0, stage_phase = 0;
     bool fail = false;
     while (walk.next(sg)) {
       const int row0 = sg.rt * RT, rows = min(RT, p.rows.R - row0);
@@ -438,10 +444,12 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
             bars->lim[r] = p.rows.limit(sg.len, sg.first, (int)p.rows.by_g.div((uint32_t)(row0 + r)));
           }
         }
+        // (limits grow with the row: the first row's is the least)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready));
         ptx::named_barrier_sync(3, 128);
       }
+      const int least = bars->lim[0];
       float m[RT], l[RT], o[RT];
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
@@ -481,25 +489,20 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
 
       bool stop = false;
       for (int j = 0; j < sg.ntiles; ++j) {
-        const uint32_t s = it % C::STAGES;
-        const int key = (sg.tile0 + j) * kCacheTile + tid;
-        const int in_page = tid / p.c.page;
-        if (!cache_wait(&bars->kv_full[s], (it / C::STAGES) & 1, bars, p)) fail = true;
-        const float ks = bars->ks[s][in_page], vs = bars->vs[s][in_page];
-        float vt = bars->vs[s][0];  // the tile's largest scale of V (pages without tokens have 0)
-        for (int i = 1; i < kCacheTile / p.c.page; ++i) vt = fmaxf(vt, bars->vs[s][i]);
+        const int key0 = (sg.tile0 + j) * kCacheTile;
+        if (!cache_wait(&bars->kv_full[stage], stage_phase, bars, p)) fail = true;
+        // This warp's 32 keys are in one page.
+        const float ks = bars->ks[stage][warp], vs = bars->vs[stage][warp];
+        const float4 v4 = *reinterpret_cast<const float4*>(bars->vs[stage]);
+        const float vt = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));  // (0 where a page has no tokens)
         if (!cache_wait(&bars->s_full[it & 1], (it >> 1) & 1, bars, p)) fail = true;
         ptx::tc_fence_after_sync();
         float t[RT];
-        bool need = false;
         {
           auto scores = [&](const uint32_t* sv) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-              const float raw = fmaf(__uint_as_float(sv[2 * r + 1]), 0.0625f, __uint_as_float(sv[2 * r]));
-              t[r] = key <= bars->lim[r] ? raw * (bars->c[r] * ks) : -INFINITY;
-              need = need || t[r] - m[r] > kLimit;
-            }
+            for (int r = 0; r < RT; ++r)
+              t[r] = fmaf(__uint_as_float(sv[2 * r + 1]), 0.0625f, __uint_as_float(sv[2 * r])) * (bars->c[r] * ks);
           };
           if constexpr (C::NS == 16) {
             uint32_t sv[16];
@@ -511,6 +514,14 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
             scores(sv);
           }
         }
+        if (key0 + kCacheTile - 1 > least) {  // some row does not see the whole tile
+#pragma unroll
+          for (int r = 0; r < RT; ++r) t[r] = key0 + tid <= bars->lim[r] ? t[r] : -INFINITY;
+        }
+        float above = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) above = fmaxf(above, t[r] - m[r]);
+        const bool need = above > kLimit;
         if (cache_any(need || fail)) {
           if (pending) take_o();
 #pragma unroll
@@ -537,34 +548,36 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
             }
           }
         }
-        const float ratio = vt > 0.f ? vs / vt : 0.f;
-        float pr[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const float e = ptx::ex2(t[r] - m[r]);
-          l[r] += e;
-          pr[r] = e * ratio;
-        }
-        if (pending) take_o();  // P and O^T are free once the last tile's product is done
+        // vs / vt, a power of two
+        const float ratio = __int_as_float((max((__float_as_int(vs) >> 23) - (__float_as_int(vt) >> 23), -100) + 127) << 23);
+        float2 pr[RT / 2];
 #pragma unroll
         for (int r = 0; r < RT; r += 2) {
-          const uint32_t hi = e4m3x2_bits(pr[r], pr[r + 1]);
-          const float2 h = e4m3x2_value(hi);
-          const float a0 = (pr[r] - h.x) * 16.f, a1 = (pr[r + 1] - h.y) * 16.f;
-          const uint32_t mid = e4m3x2_bits(a0, a1);
-          const float2 g = e4m3x2_value(mid);
-          const uint32_t lo = e4m3x2_bits((a0 - g.x) * 16.f, (a1 - g.y) * 16.f);
-          sP[cache_swizzle<128>(3 * r, tid)] = (uint8_t)hi;
-          sP[cache_swizzle<128>(3 * r + 1, tid)] = (uint8_t)mid;
-          sP[cache_swizzle<128>(3 * r + 2, tid)] = (uint8_t)lo;
-          sP[cache_swizzle<128>(3 * r + 3, tid)] = (uint8_t)(hi >> 8);
-          sP[cache_swizzle<128>(3 * r + 4, tid)] = (uint8_t)(mid >> 8);
-          sP[cache_swizzle<128>(3 * r + 5, tid)] = (uint8_t)(lo >> 8);
+          const float2 e = make_float2(ptx::ex2(t[r] - m[r]), ptx::ex2(t[r + 1] - m[r + 1]));
+          l[r] += e.x;
+          l[r + 1] += e.y;
+          pr[r / 2] = __fmul2_rn(e, make_float2(ratio, ratio));
+        }
+        if (pending) take_o();  // P and O^T are free once the last tile's product is done
+        const float2 up = make_float2(16.f, 16.f), down = make_float2(-16.f, -16.f);
+#pragma unroll
+        for (int r = 0; r < RT; r += 2) {
+          const uint32_t hi = e4m3x2_bits(pr[r / 2].x, pr[r / 2].y);
+          const float2 a = __ffma2_rn(e4m3x2_value(hi), down, __fmul2_rn(pr[r / 2], up));
+          const uint32_t mid = e4m3x2_bits(a.x, a.y);
+          const float2 c = __ffma2_rn(e4m3x2_value(mid), down, __fmul2_rn(a, up));
+          const uint32_t lo = e4m3x2_bits(c.x, c.y);
+          p_byte(3 * r) = (uint8_t)hi;
+          p_byte(3 * r + 1) = (uint8_t)mid;
+          p_byte(3 * r + 2) = (uint8_t)lo;
+          p_byte(3 * r + 3) = (uint8_t)(hi >> 8);
+          p_byte(3 * r + 4) = (uint8_t)(mid >> 8);
+          p_byte(3 * r + 5) = (uint8_t)(lo >> 8);
         }
         // Rows of V past the length may hold anything, NaN among it: zero them.
-        const int held = sg.len - (sg.tile0 + j) * kCacheTile;
+        const int held = sg.len - key0;
         if (held < kCacheTile) {
-          uint8_t* sV = sRing + s * C::STAGE_BYTES + C::TILE_BYTES;
+          uint8_t* sV = sRing + stage * C::STAGE_BYTES + C::TILE_BYTES;
           for (int i = max(held, 0) * D + tid * 16; i < C::TILE_BYTES; i += 128 * 16)
             *reinterpret_cast<uint4*>(sV + i) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -574,6 +587,10 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_attn_kernel(const __gr
         v_scale = vt;
         pending = true;
         ++it;
+        if (++stage == (uint32_t)C::STAGES) {
+          stage = 0;
+          stage_phase ^= 1u;
+        }
       }
       if (!stop && pending) take_o();
       if (cache_any(fail || stop)) break;
