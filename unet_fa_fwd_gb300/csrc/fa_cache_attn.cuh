@@ -225,6 +225,31 @@ __device__ __forceinline__ void cache_plan(const CacheRows& rows, int ctas, int*
   if (lane == 0) *out = CacheRange{total, t0, t1, base0, grid, b0};
 }
 
+// The producer warp's view of a stretch's pages: each lane holds the number and
+// scales of one of 32 pages.  (Fetching the next 32 ahead of their use measured
+// no faster: the ring of tiles covers the two trips to memory.)
+struct CachePages {
+  int id;
+  float ks, vs;
+
+  // The 32 pages from tile j of the stretch on.
+  __device__ __forceinline__ void fetch(const CacheAttnParams& p, const CacheSegment& s, int j, uint32_t lane) {
+    const int ppt = kCacheTile / p.c.page;
+    const int held = s.len == 0 ? 0 : (s.len - 1) / p.c.page + 1;  // pages with tokens
+    const int idx = (s.tile0 + j) * ppt + (int)lane;
+    bool bad = false;
+    id = 0;
+    ks = vs = 0.f;
+    if (idx < held && idx < (s.tile0 + s.ntiles) * ppt) {
+      id = cache_page(p.c.table[(long long)s.b * p.c.width + idx], p.c.num_pages, bad);
+      const long long at = (long long)id * p.c.H + s.h;
+      ks = p.c.scale[0][at];
+      vs = p.c.scale[1][at];
+    }
+    if (bad) atomicCAS(p.status, 0, kStatusIndex);
+  }
+};
+
 template <int D, int RT>
 __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
   using C = CacheCfg<D, RT>;
@@ -239,7 +264,7 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
   if (tid == 0) {
     if (p.cut) p.cut[blockIdx.x].x = -1;
     for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), 2);  // the copies; the scales
       ptx::mbar_init(ptx::smem_u32(&bars->kv_empty[s]), 1);
     }
     ptx::mbar_init(ptx::smem_u32(&bars->s_full[0]), 1);
@@ -275,27 +300,12 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
     const int batch = 32 / ppt;                          // tiles whose pages the lanes hold
     uint32_t it = 0, skipped = 0xffffffffu;
     bool ok = true;
+    CachePages pages;
     while (ok && walk.next(sg)) {
-      const int h = sg.h;
       const int npages = sg.len == 0 ? 0 : (sg.len - 1) / page + 1;
-      const int* row = p.c.table + (long long)sg.b * p.c.width;
-      int id = 0;
-      float ks = 0.f, vs = 0.f;
       for (int j = 0; j < sg.ntiles; ++j, ++it) {
         const int in_batch = j % batch;
-        if (in_batch == 0) {  // the lanes fetch the next 32 pages' numbers and scales
-          const int idx = (sg.tile0 + j) * ppt + (int)lane;
-          bool bad = false;
-          id = 0;
-          ks = vs = 0.f;
-          if (idx < npages && idx < (sg.tile0 + sg.ntiles) * ppt) {
-            id = cache_page(row[idx], p.c.num_pages, bad);
-            const long long at = (long long)id * p.c.H + h;
-            ks = p.c.scale[0][at];
-            vs = p.c.scale[1][at];
-          }
-          if (bad) atomicCAS(p.status, 0, kStatusIndex);
-        }
+        if (in_batch == 0) pages.fetch(p, sg, j, lane);
         const uint32_t s = it % C::STAGES;
         ok = cache_wait(&bars->kv_empty[s], ((it / C::STAGES) & 1) ^ 1, bars, p);
         if (!ok) break;
@@ -303,27 +313,26 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
           skipped = it;
           continue;
         }
-        const int src = in_batch * ppt + (int)(lane % ppt);
-        const int my_id = __shfl_sync(0xffffffffu, id, src);
-        const int group = in_batch * ppt + (int)(lane & 3) * 32 / page;  // page of this lane's 32 tokens
-        const float my_ks = __shfl_sync(0xffffffffu, ks, group), my_vs = __shfl_sync(0xffffffffu, vs, group);
-        const int first = (sg.tile0 + j) * ppt;
-        const int n = max(0, min(ppt, npages - first));  // pages of this tile that hold tokens
-        if (lane < 4) {
-          bars->ks[s][lane] = my_ks;
-          bars->vs[s][lane] = my_vs;
-        }
+        const int my_id = __shfl_sync(0xffffffffu, pages.id, in_batch * ppt + (int)(lane % ppt));
+        const int n = max(0, min(ppt, npages - (sg.tile0 + j) * ppt));  // pages of this tile that hold tokens
         const uint32_t full = ptx::smem_u32(&bars->kv_full[s]);
-        __syncwarp();
         if (lane == 0) ptx::mbar_arrive_expect_tx(full, (uint32_t)(2 * n * page * D));
         __syncwarp();
         if ((int)lane < n) {
           const uint32_t dst = ptx::smem_u32(sRing + s * C::STAGE_BYTES) + lane * page * D;
-          const int at = my_id * p.c.H + h;
+          const int at = my_id * p.c.H + sg.h;
           ptx::tma_load_3d(dst, &p.tm_k, full, 0, 0, at);
           ptx::tma_load_3d(dst + C::TILE_BYTES, &p.tm_v, full, 0, 0, at);
         }
+        // The scales, for which the copies do not wait.
+        const int group = in_batch * ppt + (int)(lane & 3) * 32 / page;  // page of this lane's 32 tokens
+        const float my_ks = __shfl_sync(0xffffffffu, pages.ks, group), my_vs = __shfl_sync(0xffffffffu, pages.vs, group);
+        if (lane < 4) {
+          bars->ks[s][lane] = my_ks;
+          bars->vs[s][lane] = my_vs;
+        }
         __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(full);
       }
     }
     if (!ok && lane == 0) {

@@ -210,26 +210,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       const int page = p.c.page, ppt = kCacheTile / page, batch = 32 / ppt;
       uint32_t it = 0, skipped = 0xffffffffu;
       bool ok = true;
+      CachePages pages;
       while (ok && walk.next(sg)) {
         const int npages = sg.len == 0 ? 0 : (sg.len - 1) / page + 1;
-        const int* row = p.c.table + (long long)sg.b * p.c.width;
-        int id = 0;
-        float ks = 0.f, vs = 0.f;
         for (int j = 0; j < sg.ntiles; ++j, ++it) {
           const int in_batch = j % batch;
-          if (in_batch == 0) {  // the lanes fetch the next 32 pages' numbers and scales
-            const int idx = (sg.tile0 + j) * ppt + (int)lane;
-            bool bad = false;
-            id = 0;
-            ks = vs = 0.f;
-            if (idx < npages && idx < (sg.tile0 + sg.ntiles) * ppt) {
-              id = cache_page(row[idx], p.c.num_pages, bad);
-              const long long at = (long long)id * p.c.H + sg.h;
-              ks = p.c.scale[0][at];
-              vs = p.c.scale[1][at];
-            }
-            if (bad) atomicCAS(p.status, 0, kStatusIndex);
-          }
+          if (in_batch == 0) pages.fetch(p, sg, j, lane);
           const uint32_t s = it % C::K_STAGES, ph = ((it / C::K_STAGES) & 1) ^ 1, meta = it % kChunkMeta;
           ok = cache_wait(&bars->k_empty[s], ph, bars, p) && cache_wait(&bars->v8_empty[s], ph, bars, p);
           if (!ok) break;
@@ -237,21 +223,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
             skipped = it;
             continue;
           }
-          const int src = in_batch * ppt + (int)(lane % ppt);
-          const int my_id = __shfl_sync(0xffffffffu, id, src);
-          const int g = in_batch * ppt + (int)(lane & 3) * 32 / page;  // page of this lane's 32 tokens
-          const float my_ks = __shfl_sync(0xffffffffu, ks, g), my_vs = __shfl_sync(0xffffffffu, vs, g);
+          const int my_id = __shfl_sync(0xffffffffu, pages.id, in_batch * ppt + (int)(lane % ppt));
           const int n = max(0, min(ppt, npages - (sg.tile0 + j) * ppt));  // pages that hold tokens
-          // The scales' slot was last used eight tiles ago; the V slot that is
-          // free now means that tile it - 5 is through the softmax.
-          if (lane < 4) {
-            bars->ks[meta][lane] = my_ks;
-            bars->vs[meta][lane] = my_vs;
-          }
           const uint32_t kf = ptx::smem_u32(&bars->k_full[s]), vf = ptx::smem_u32(&bars->v8_full[s]);
-          __syncwarp();
           if (lane == 0) {
-            ptx::mbar_arrive(ptx::smem_u32(&bars->meta_full[meta]));
             ptx::mbar_arrive_expect_tx(kf, (uint32_t)(n * page * D));
             ptx::mbar_arrive_expect_tx(vf, (uint32_t)(n * page * D));
           }
@@ -262,7 +237,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
             ptx::tma_load_3d(ptx::smem_u32(sK) + off, &p.tm_k, kf, 0, 0, at);
             ptx::tma_load_3d(ptx::smem_u32(sV8) + off, &p.tm_v, vf, 0, 0, at);
           }
+          // The scales, for which the copies do not wait.  Their slot was last
+          // used eight tiles ago; the V slot that is free now means that tile
+          // it - 5 is through the softmax.
+          const int g = in_batch * ppt + (int)(lane & 3) * 32 / page;  // page of this lane's 32 tokens
+          const float my_ks = __shfl_sync(0xffffffffu, pages.ks, g), my_vs = __shfl_sync(0xffffffffu, pages.vs, g);
+          if (lane < 4) {
+            bars->ks[meta][lane] = my_ks;
+            bars->vs[meta][lane] = my_vs;
+          }
           __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->meta_full[meta]));
         }
       }
       if (!ok && lane == 0) {
