@@ -188,9 +188,9 @@ fa::CacheView view(const fa_cache* c, const int* table, int width) {
 template <int D, int PAGE>
 void launch_write(const fa::CacheWriteParams& p, bool vec, unsigned blocks, cudaStream_t s) {
   if (vec)
-    fa::fa_cache_write_kernel<D, PAGE, true><<<blocks, fa::kQuantThreads, 0, s>>>(p);
+    fa::fa_cache_write_kernel<D, PAGE, true><<<blocks, fa::kWriteThreads, 0, s>>>(p);
   else
-    fa::fa_cache_write_kernel<D, PAGE, false><<<blocks, fa::kQuantThreads, 0, s>>>(p);
+    fa::fa_cache_write_kernel<D, PAGE, false><<<blocks, fa::kWriteThreads, 0, s>>>(p);
 }
 
 template <int D>
@@ -478,7 +478,7 @@ int fa_cache_write(const fa_cache* cache, const fa_tensor* k, const fa_tensor* v
   if (rc != FA_OK) return rc;
   p.status = st->status;
   fa::log_launch("fa_cache_write_kernel<D=%d,page %d,%s> grid %lld x %d threads (%d pages a sequence and head at most)",
-                 D, page, vec ? "16-byte loads" : "scalar loads", (long long)blocks, fa::kQuantThreads, p.slots);
+                 D, page, vec ? "16-byte loads" : "scalar loads", (long long)blocks, fa::kWriteThreads, p.slots);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (D) {
     case 32: launch_write<32>(p, vec, (unsigned)blocks, s); break;
@@ -505,7 +505,7 @@ int fa_cache_read(const fa_cache* cache, const int* table, int table_width, cons
         ranges_overlap(outs[i], out, table, (size_t)B * table_width * sizeof(int)))
       return FA_ERR_INVALID_ARGUMENT;
   if (ranges_overlap(k_out, out, v_out, out)) return FA_ERR_INVALID_ARGUMENT;
-  const int64_t per = ((int64_t)N * (D / 16) + fa::kQuantThreads - 1) / fa::kQuantThreads;
+  const int64_t per = ((int64_t)N * (D / 16) + fa::kReadThreads - 1) / fa::kReadThreads;
   if (per * B * H * 2 > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
   fa::CacheReadParams p;
   std::memset(&p, 0, sizeof(p));
@@ -523,12 +523,12 @@ int fa_cache_read(const fa_cache* cache, const int* table, int table_width, cons
   if (rc != FA_OK) return rc;
   p.status = st->status;
   const unsigned blocks = (unsigned)(per * B * H * 2);
-  fa::log_launch("fa_cache_read_kernel<D=%d> grid %u x %d threads", D, blocks, fa::kQuantThreads);
+  fa::log_launch("fa_cache_read_kernel<D=%d> grid %u x %d threads", D, blocks, fa::kReadThreads);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (D) {
-    case 32: fa::fa_cache_read_kernel<32><<<blocks, fa::kQuantThreads, 0, s>>>(p); break;
-    case 64: fa::fa_cache_read_kernel<64><<<blocks, fa::kQuantThreads, 0, s>>>(p); break;
-    default: fa::fa_cache_read_kernel<128><<<blocks, fa::kQuantThreads, 0, s>>>(p); break;
+    case 32: fa::fa_cache_read_kernel<32><<<blocks, fa::kReadThreads, 0, s>>>(p); break;
+    case 64: fa::fa_cache_read_kernel<64><<<blocks, fa::kReadThreads, 0, s>>>(p); break;
+    default: fa::fa_cache_read_kernel<128><<<blocks, fa::kReadThreads, 0, s>>>(p); break;
   }
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
