@@ -96,16 +96,15 @@ def load_library() -> ctypes.CDLL:
             lib.fa_split_workspace_bytes.restype = sz
             lib.fa_split_count.argtypes = [i32, i32, i32, i32, i32]
             lib.fa_split_count.restype = i32
-            tp = ctypes.POINTER(FaTensor)
-            lib.fa_rope.argtypes = [ctypes.POINTER(FaRopeAxes), vp, ctypes.c_longlong, tp, tp, i32, tp,
-                                    tp, i32, i32, i32, i32, i32, i32, i32, vp]
+            # (fa_tensor, fa_rope_axes and fa_cache pointers as addresses or byref)
+            lib.fa_rope.argtypes = [vp, vp, ctypes.c_longlong, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
+                                    i32, vp]
             lib.fa_rope.restype = i32
-            cp = ctypes.POINTER(FaCache)
-            lib.fa_cache_write.argtypes = [cp, tp, tp, vp, i32, vp, vp, i32, i32, vp]
+            lib.fa_cache_write.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, vp]
             lib.fa_cache_write.restype = i32
-            lib.fa_cache_read.argtypes = [cp, vp, i32, vp, vp, vp, vp, i32, i32, vp]
+            lib.fa_cache_read.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, vp]
             lib.fa_cache_read.restype = i32
-            lib.fa_fwd_cache.argtypes = [vp, cp, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32, f32, vp, sz, vp]
+            lib.fa_fwd_cache.argtypes = [vp, vp, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32, f32, vp, sz, vp]
             lib.fa_fwd_cache.restype = i32
             lib.fa_cache_workspace_bytes.argtypes = [i32] * 7
             lib.fa_cache_workspace_bytes.restype = sz

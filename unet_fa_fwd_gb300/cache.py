@@ -56,8 +56,7 @@ def _run(t: torch.Tensor, stream, call, *args):
 
 
 def _raise(name: str, rc: int) -> None:
-    if rc != FA_OK:
-        raise RuntimeError(f"{name} failed: {status_string(rc)}")
+    raise RuntimeError(f"{name} failed: {status_string(rc)}")
 
 
 def _refuse(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> None:
@@ -79,14 +78,19 @@ def _exact(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device:
     return t.data_ptr()
 
 
-def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> FaTensor:
-    """A [B, H, N, D] tensor of any strides, the last axis contiguous."""
+# Four fa_tensor structs side by side (pointer and three strides each).
+_Tensors = ctypes.c_longlong * 16
+_SIZE = ctypes.sizeof(FaTensor)
+
+
+def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> tuple:
+    """A [B, H, N, D] tensor of any strides, the last axis contiguous: the fields of its fa_tensor."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
         _refuse(t, name, dtype, shape, device)
     b, h, n, d = t.stride()
     if d != 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    return FaTensor(t.data_ptr(), b, h, n)
+    return t.data_ptr(), b, h, n
 
 
 class RopeAxes:
@@ -146,24 +150,35 @@ def _rope(q, k, pos, axes, q_out, k_out, new, token_major, pairing, inverse, dev
         raise ValueError("pos must be contiguous along its tokens and axes")
     if pos.get_device() != device:
         raise ValueError(f"pos must be on cuda:{device}, got {pos.device}")
-    qt = _strided(q, "q", dtype, shape, device)
+    fields = _strided(q, "q", dtype, shape, device)
     if k is not None:
         Hk = _bhnd(k, "k")[1]
         k_shape = (B, Hk, N, D)
-        kt = _strided(k, "k", dtype, k_shape, device)
+        kf = _strided(k, "k", dtype, k_shape, device)
     if new:
         q_out = _rope_new(shape, dtype, q.device, token_major)
-        k_out = None if k is None else _rope_new(k_shape, dtype, q.device, token_major)
-    qo = _strided(q_out, "q_out", dtype, shape, device)
-    lib = load_library()
-    if k is None:
-        rc = lib.fa_rope(axes.ref, pos.data_ptr(), ps[0] if len(ps) == 3 else 0, qt, qo, Hq, None, None, 0, B, N, D,
-                         _DTYPES[dtype], _PAIRINGS[pairing], inverse, handle)
+        fields += (q_out.data_ptr(), *q_out.stride()[:3])
     else:
-        ko = _strided(k_out, "k_out", dtype, k_shape, device)
-        rc = lib.fa_rope(axes.ref, pos.data_ptr(), ps[0] if len(ps) == 3 else 0, qt, qo, Hq, kt, ko, Hk, B, N, D,
-                         _DTYPES[dtype], _PAIRINGS[pairing], inverse, handle)
-    _raise("fa_rope", rc)
+        fields += _strided(q_out, "q_out", dtype, shape, device)
+    if k is None:
+        Hk = 0
+        ts = _Tensors(*fields)
+        at = ctypes.addressof(ts)
+        kt = ko = None
+    else:
+        fields += kf
+        if new:
+            k_out = _rope_new(k_shape, dtype, q.device, token_major)
+            fields += (k_out.data_ptr(), *k_out.stride()[:3])
+        else:
+            fields += _strided(k_out, "k_out", dtype, k_shape, device)
+        ts = _Tensors(*fields)
+        at = ctypes.addressof(ts)
+        kt, ko = at + 2 * _SIZE, at + 3 * _SIZE
+    rc = load_library().fa_rope(axes.ref, pos.data_ptr(), ps[0] if len(ps) == 3 else 0, at, at + _SIZE, Hq, kt, ko, Hk,
+                                B, N, D, _DTYPES[dtype], _PAIRINGS[pairing], inverse, handle)
+    if rc != FA_OK:
+        _raise("fa_rope", rc)
     return q_out, k_out
 
 
@@ -241,11 +256,13 @@ def _same_heads(cache: KVCache8, name: str, H: int, D: int) -> None:
 def _write(cache, k, v, table, start, count, device, handle):
     B, H, N, D = shape = _bhnd(k, "k")
     _same_heads(cache, "k", H, D)
-    rc = load_library().fa_cache_write(cache.ref, _strided(k, "k", _BF16, shape, device),
-                                       _strided(v, "v", _BF16, shape, device), _table(table, B, device),
-                                       table.shape[1], _ints(start, "start", B, device),
-                                       _ints(count, "count", B, device), B, N, handle)
-    _raise("fa_cache_write", rc)
+    ts = _Tensors(*_strided(k, "k", _BF16, shape, device), *_strided(v, "v", _BF16, shape, device))
+    at = ctypes.addressof(ts)
+    rc = load_library().fa_cache_write(cache.ref, at, at + _SIZE, _table(table, B, device), table.shape[1],
+                                       _ints(start, "start", B, device), _ints(count, "count", B, device), B, N,
+                                       handle)
+    if rc != FA_OK:
+        _raise("fa_cache_write", rc)
 
 
 def cache_write(cache: KVCache8, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, start: torch.Tensor,
@@ -258,16 +275,21 @@ def cache_write(cache: KVCache8, k: torch.Tensor, v: torch.Tensor, table: torch.
 
 def _read(cache, table, lens, k_out, v_out, n, start, device, handle):
     if k_out is None:
-        shape = (table.shape[0], cache.heads, n, cache.head_dim)
+        B, N = table.shape[0], n
+        shape = (B, cache.heads, N, cache.head_dim)
         k_out = torch.empty(shape, dtype=_BF16, device=cache.k.device)
         v_out = torch.empty(shape, dtype=_BF16, device=cache.k.device)
-    B, H, N, D = shape = _bhnd(k_out, "k_out")
-    _same_heads(cache, "k_out", H, D)
+        kp, vp = k_out.data_ptr(), v_out.data_ptr()
+    else:
+        B, H, N, D = shape = _bhnd(k_out, "k_out")
+        _same_heads(cache, "k_out", H, D)
+        kp = _exact(k_out, "k_out", _BF16, shape, device)
+        vp = _exact(v_out, "v_out", _BF16, shape, device)
     rc = load_library().fa_cache_read(cache.ref, _table(table, B, device), table.shape[1],
-                                      _ints(lens, "lens", B, device), _ints(start, "start", B, device),
-                                      _exact(k_out, "k_out", _BF16, shape, device),
-                                      _exact(v_out, "v_out", _BF16, shape, device), B, N, handle)
-    _raise("fa_cache_read", rc)
+                                      _ints(lens, "lens", B, device), _ints(start, "start", B, device), kp, vp, B, N,
+                                      handle)
+    if rc != FA_OK:
+        _raise("fa_cache_read", rc)
     return k_out, v_out
 
 
@@ -296,9 +318,13 @@ def _attend(q, cache, table, lens, out, lse, workspace, causal, q_start, scale, 
     lib = load_library()
     if out is None:
         need = lib.fa_cache_workspace_bytes(B, Hq, cache.heads, Nq, D, table.shape[1], cache.page_tokens)
-        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        out = torch.empty_like(q)
         lse = torch.empty((B, Hq, Nq), dtype=_F32, device=q.device)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        op, lp = out.data_ptr(), lse.data_ptr()
+    else:
+        op = _exact(out, "out", _BF16, shape, device)
+        lp = _exact(lse, "lse", _F32, (B, Hq, Nq), device)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         if not workspace.is_contiguous() or workspace.get_device() != device:
@@ -307,9 +333,10 @@ def _attend(q, cache, table, lens, out, lse, workspace, causal, q_start, scale, 
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     rc = lib.fa_fwd_cache(qp, cache.ref, tab, table.shape[1], _ints(lens, "lens", B, device),
-                          _ints(q_start, "q_start", B, device), causal, _exact(out, "out", _BF16, shape, device),
-                          _exact(lse, "lse", _F32, (B, Hq, Nq), device), B, Hq, Nq, scale, ws_ptr, ws_bytes, handle)
-    _raise("fa_fwd_cache", rc)
+                          _ints(q_start, "q_start", B, device), causal, op, lp, B, Hq, Nq, scale, ws_ptr, ws_bytes,
+                          handle)
+    if rc != FA_OK:
+        _raise("fa_fwd_cache", rc)
     return out, lse
 
 
