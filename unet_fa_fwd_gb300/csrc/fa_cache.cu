@@ -13,7 +13,7 @@
 
 #include "fa.h"
 #include "fa_cache_attn.cuh"
-#include "fa_cache_chunk.cuh"
+#include "fa_cache_launch.h"
 #include "fa_cache_quant.cuh"
 #include "fa_host.h"
 #include "fa_log.h"
@@ -22,6 +22,8 @@
 namespace {
 
 using fa::aligned16;
+using fa::CachePlan;
+using fa::launch_after;
 using fa::ranges_overlap;
 
 bool head_dim_ok(int D) { return D == 32 || D == 64 || D == 128; }
@@ -208,23 +210,11 @@ void launch_write(const fa::CacheWriteParams& p, bool vec, unsigned blocks, cuda
   }
 }
 
-// The attention's row tiles and workspace.  RT rows of a key head share a pass
-// over its tiles: 4, 8 or 16, the least that holds them all, in the kernel for
-// few rows (a row costs its share of the softmax, a second pass the whole
-// stream of codes again); 256 in the one for many, from kCacheFewRows on.
-constexpr int kCacheFewRows = 32;
-
-struct CachePlan {
-  int R, rt, row_tiles;
-  int64_t units;        // per batch entry
-  int64_t tiles;        // at most, all units
-  size_t part_o, cut, total;  // workspace: partial O; up to their maxima and sums; in all
-};
-
+// The plan of a call.
 CachePlan cache_plan(int B, int Hq, int Hk, int Nq, int D, int width, int page) {
   CachePlan l{};
   l.R = (int)((int64_t)Hq / Hk * Nq);
-  l.rt = l.R > kCacheFewRows ? fa::kChunkRows : (l.R <= 4 ? 4 : (l.R <= 8 ? 8 : 16));
+  l.rt = l.R > fa::kCacheFewRows ? fa::kChunkRows : (l.R <= 4 ? 4 : (l.R <= 8 ? 8 : 16));
   l.row_tiles = (l.R + l.rt - 1) / l.rt;
   l.units = (int64_t)Hk * l.row_tiles;
   const int64_t per = fa::cache_tiles(width * page);
@@ -253,22 +243,6 @@ int encode_cache_map(CUtensorMap* map, void* base, const fa_cache* c) {
                                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
-}
-
-// Launches a merge so that its blocks may start while the kernel before it on
-// the stream finishes (it waits for that kernel itself).
-int launch_after(void (*kernel)(const fa::CacheAttnParams), unsigned blocks, unsigned threads,
-                 const fa::CacheAttnParams& p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D, int RT>
@@ -318,41 +292,10 @@ int launch_cache_attn(fa::CacheAttnParams& p, const CachePlan& plan, const fa::D
   return launch_after(fa::fa_cache_merge_kernel<D, RT>, blocks, 128, p, s);
 }
 
-template <int D, bool ONE>
-int launch_cache_chunk(fa::CacheAttnParams& p, const CachePlan& plan, const fa::DeviceState& st, cudaStream_t s) {
-  using C = fa::ChunkCfg<D>;
-  static std::mutex mu;
-  static bool ready[64] = {};
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!ready[st.device]) {
-      if (cudaFuncSetAttribute(fa::fa_cache_chunk_kernel<D, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               C::SMEM_BYTES) != cudaSuccess)
-        return FA_ERR_CUDA;
-      ready[st.device] = true;
-    }
-  }
-  int64_t grid = st.sm_count < fa::kChunkMaxGrid ? st.sm_count : fa::kChunkMaxGrid;
-  if (grid > plan.tiles) grid = plan.tiles;
-  p.ctas = (int)grid;
-  fa::log_launch("fa_cache_chunk_kernel<D=%d,%s> grid %d x %d threads smem %d B tmem 512 cols stages %d + %d, %lld units "
-                 "a sequence, %lld tiles at most", D, ONE ? "a page a tile" : "pages in tiles", p.ctas,
-                 fa::kChunkThreads, C::SMEM_BYTES, C::K_STAGES, C::V_STAGES, (long long)plan.units,
-                 (long long)plan.tiles);
-  fa::fa_cache_chunk_kernel<D, ONE><<<p.ctas, fa::kChunkThreads, C::SMEM_BYTES, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  if (!plan.total) return FA_OK;  // no unit can be cut
-  const unsigned blocks = (unsigned)p.ctas * (D / 16);
-  fa::log_launch("fa_cache_chunk_merge_kernel<D=%d> grid %u x %d threads", D, blocks, fa::kChunkRows);
-  return launch_after(fa::fa_cache_chunk_merge_kernel<D>, blocks, fa::kChunkRows, p, s);
-}
-
 template <int D>
 int launch_cache_attn(fa::CacheAttnParams& p, const CachePlan& plan, const fa::DeviceState& st, cudaStream_t s) {
+  if (plan.rt == fa::kChunkRows) return fa::launch_cache_chunk(p, plan, D, st, s);
   switch (plan.rt) {
-    case fa::kChunkRows:
-      return p.c.page == fa::kCacheTile ? launch_cache_chunk<D, true>(p, plan, st, s)
-                                        : launch_cache_chunk<D, false>(p, plan, st, s);
     case 4: return launch_cache_attn<D, 4>(p, plan, st, s);
     case 8: return launch_cache_attn<D, 8>(p, plan, st, s);
     default: return launch_cache_attn<D, 16>(p, plan, st, s);

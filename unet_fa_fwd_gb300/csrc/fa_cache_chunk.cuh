@@ -27,21 +27,27 @@
 // fa_cache_attn.cuh: 192 units of 256 rows on 152 SMs would leave a third of
 // the second round idle.
 //
+// PAIR.  With 128 rows or fewer there is one row tile, and its S, softmax and
+// P V would wait for one another; the two warpgroups then take the even and the
+// odd key tiles of the same rows, with a maximum, a sum and an O each, and the
+// second's results are joined to the first's at the end of the stretch.
+// (Deeper rings of codes in the other row tile's shared memory measured slower.)
+//
 // Warps: 0-3 and 4-7 softmax of the two row tiles, 8 producer, 9 MMA issuer,
 // 10-11 V conversion.
 #pragma once
 
 #include "fa_cache_attn.cuh"
+#include "fa_cache_launch.h"
 
 namespace fa {
 
-constexpr int kChunkRows = 256;
 constexpr int kChunkThreads = 384;
 constexpr int kChunkConvert = 64;  // threads that convert V
-constexpr int kChunkMaxGrid = 192;  // one CTA per SM; partial results are sized for this many
-constexpr int kChunkMeta = 8;  // tiles whose scales are kept: more than the pipeline's depth (5)
+constexpr int kChunkMeta = 16;   // tiles whose scales are kept: more than the pipeline's depth
+constexpr int kChunkStagesMax = 8;
 
-template <int D>
+template <int D, bool PAIR>
 struct ChunkCfg {
   static constexpr int T8 = kCacheTile * D;              // 128 rows in e4m3
   static constexpr int T16 = 2 * T8;                     // in f16
@@ -49,15 +55,19 @@ struct ChunkCfg {
   static constexpr int CHUNK = kCacheTile * SW;          // its 128-row blocks of SW bytes
   static constexpr uint32_t LAYOUT8 = D == 128 ? 2u : (D == 64 ? 4u : 6u);
   static constexpr uint32_t LAYOUT16 = D >= 64 ? 2u : 4u;
-  static constexpr int K_STAGES = 3, V_STAGES = 2;       // K and V codes; V in f16
-  static constexpr int SMEM_BYTES = 4 * T8 + 2 * K_STAGES * T8 + V_STAGES * T16 + 2048;
+  static constexpr int Q_TILES = PAIR ? 1 : 2;
+  static constexpr int V_STAGES = 2;                     // V in f16
+  static constexpr int K_STAGES = PAIR || D == 128 ? 3 : 6;  // K and V codes
+  static constexpr int SMEM_BYTES = 2 * Q_TILES * T8 + 2 * K_STAGES * T8 + V_STAGES * T16 + 2048;
+  static_assert(K_STAGES <= kChunkStagesMax && K_STAGES + V_STAGES < kChunkMeta, "rings");
   static constexpr int COL_S = 0, COL_O = 256;           // S and O of tile t: + 128 t, + D t
 };
 
 struct ChunkBars {
-  uint64_t k_full[3], k_empty[3], v8_full[3], v8_empty[3], v_full[2], v_empty[2];
+  uint64_t k_full[kChunkStagesMax], k_empty[kChunkStagesMax], v8_full[kChunkStagesMax], v8_empty[kChunkStagesMax];
+  uint64_t v_full[2], v_empty[2];
   uint64_t meta_full[kChunkMeta];
-  uint64_t q_ready[2], s_full[2], p_half[2], p_ready[2], o_full[2], drain;
+  uint64_t q_ready[2], s_full[2], p_half[2], p_ready[2], o_full[2], joined, drain;
   CacheRange plan;
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -84,12 +94,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 
 // ONE: a page is a whole tile (128 tokens), so a tile has one scale.
-template <int D, bool ONE>
+// PAIR: one row tile, two key tiles at a time (R <= 128).
+template <int D, bool ONE, bool PAIR>
 __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const __grid_constant__ CacheAttnParams p) {
-  using C = ChunkCfg<D>;
+  using C = ChunkCfg<D, PAIR>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;                              // tile t: hi at 2 t, lo at 2 t + 1
-  uint8_t* sK = sQ + 4 * C::T8;
+  uint8_t* sK = sQ + 2 * C::Q_TILES * C::T8;
   uint8_t* sV8 = sK + C::K_STAGES * C::T8;
   uint8_t* sV = sV8 + C::K_STAGES * C::T8;
   ChunkBars* bars = reinterpret_cast<ChunkBars*>(sV + C::V_STAGES * C::T16);
@@ -116,6 +127,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       ptx::mbar_init(ptx::smem_u32(&bars->p_ready[t]), 128);
       ptx::mbar_init(ptx::smem_u32(&bars->o_full[t]), 1);
     }
+    ptx::mbar_init(ptx::smem_u32(&bars->joined), 128);
     ptx::mbar_init(ptx::smem_u32(&bars->drain), 1);
     bars->abort_flag = 0;
     ptx::fence_barrier_init();
@@ -213,6 +225,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       CachePages pages;
       while (ok && walk.next(sg)) {
         const int npages = sg.len == 0 ? 0 : (sg.len - 1) / page + 1;
+        // The unit's rows of Q on their way to L2 while the last unit is finished.
+#pragma unroll 1
+        for (int r = sg.rt * kChunkRows + (int)lane; r < min(p.rows.R, (sg.rt + 1) * kChunkRows); r += 32) {
+          const char* q = reinterpret_cast<const char*>(p.q + p.row_at(sg.b, sg.h, r) * D);
+          for (int x = 0; x < D * 2; x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + x));
+        }
         for (int j = 0; j < sg.ntiles; ++j, ++it) {
           const int in_batch = j % batch;
           if (in_batch == 0) pages.fetch(p, sg, j, lane);
@@ -238,8 +256,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
             ptx::tma_load_3d(ptx::smem_u32(sV8) + off, &p.tm_v, vf, 0, 0, at);
           }
           // The scales, for which the copies do not wait.  Their slot was last
-          // used eight tiles ago; the V slot that is free now means that tile
-          // it - 5 is through the softmax.
+          // used kChunkMeta tiles ago; the V slot that is free now means that
+          // tile it - K_STAGES - V_STAGES is through the softmax.
           const int g = in_batch * ppt + (int)(lane & 3) * 32 / page;  // page of this lane's 32 tokens
           const float my_ks = __shfl_sync(0xffffffffu, pages.ks, g), my_vs = __shfl_sync(0xffffffffu, pages.vs, g);
           if (lane < 4) {
@@ -275,7 +293,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
         const uint32_t d = tmem + C::COL_S + t * 128, b = (uint32_t)dk + stage * (C::T8 >> 4);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {  // hi, then lo on top
-          const uint32_t a = (uint32_t)dq + (2 * t + part) * (C::T8 >> 4);
+          const uint32_t a = (uint32_t)dq + (2 * (PAIR ? 0 : t) + part) * (C::T8 >> 4);
           if constexpr (D == 128)
             ptx::mma_ss_f8_x4_el<2, 4, 6>(d, a, q_hi, b, k_hi, IDESC_S, part);
           else if constexpr (D == 64)
@@ -311,6 +329,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
         ++qc[0];
         ptx::tc_fence_after_sync();
         issue_s(0, it % C::K_STAGES);
+        if constexpr (PAIR) {
+          // S of tile j + 2 follows P V of tile j, in the same columns.
+          const uint32_t end = it + (uint32_t)sg.ntiles, first = it;
+          ptx::mma_commit_el(ptx::smem_u32(&bars->k_empty[it % C::K_STAGES]));
+          auto next_s = [&](uint32_t n) -> bool {
+            if (!take_k(n)) return false;
+            issue_s((int)((n - first) & 1), n % C::K_STAGES);
+            ptx::mma_commit_el(ptx::smem_u32(&bars->k_empty[n % C::K_STAGES]));
+            return true;
+          };
+          if (first + 1 < end) ok = next_s(first + 1);
+          for (; ok && it < end; ++it) {
+            const int t = (int)((it - first) & 1);
+            const uint32_t sv = it % C::V_STAGES;
+            ok = cache_wait(&bars->v_full[sv], (it / C::V_STAGES) & 1, bars, p);
+            if (!ok) break;
+            ptx::tc_fence_after_sync();
+            ok = issue_pv(t, sv, it < first + 2, pc[t] & 1);
+            if (!ok) break;
+            ++pc[t];
+            ptx::mma_commit_el(ptx::smem_u32(&bars->v_empty[sv]));
+            if (it + 2 < end)
+              ok = next_s(it + 2);
+            else
+              ptx::mma_commit_el(ptx::smem_u32(&bars->o_full[t]));
+          }
+          continue;
+        }
         if (two) {
           ok = cache_wait(&bars->q_ready[1], qc[1] & 1, bars, p);
           if (!ok) break;
@@ -361,13 +407,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
   const int in_tile = (warp % 4) * 32 + (int)lane;  // row of the tile, lane of tensor memory
   const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
   const uint32_t tS = tmem + lane_base + C::COL_S + t * 128, tO = tmem + lane_base + C::COL_O + t * D;
-  uint8_t* q_hi = sQ + 2 * t * C::T8;
+  const int qt = PAIR ? 0 : t;  // row tile
+  uint8_t* q_hi = sQ + 2 * qt * C::T8;
   uint8_t* q_lo = q_hi + C::T8;
-  uint32_t it = 0, sc = 0, oc = 0;
+  constexpr int STEP = PAIR ? 2 : 1;
+  uint32_t it = 0, sc = 0, oc = 0, jc = 0;
   bool ok = true;
   while (ok && walk.next(sg)) {
-    const int row0 = sg.rt * kChunkRows + t * 128;
-    if (row0 >= p.rows.R) {  // (tile 1 of a short unit)
+    const int row0 = sg.rt * kChunkRows + qt * 128;
+    // (tile 1 of a unit cut short; the second of a pair where there is one key tile)
+    if (row0 >= p.rows.R || (PAIR && t >= sg.ntiles)) {
       it += (uint32_t)sg.ntiles;
       continue;
     }
@@ -378,10 +427,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     // that read the last unit's Q are done: their S has been read.
     float c = 0.f;
     {
-      // (Rolled up: this code runs once a unit, and unrolled it cost more time
-      // in instruction misses than in work.)
+      // (Rolled up, four steps' loads in flight: this code runs once a unit.
+      // Unrolled it cost more time in instruction misses than in work; with one
+      // load in flight, in waiting for memory.)
       constexpr int LPR = D / 8, RPS = 32 / LPR;  // lanes of a row, rows of a step
-      constexpr int BATCH = 4;                    // loads in flight
+      constexpr int BATCH = 4;
+      const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;  // a negative scale turns the row round
       uint4 next[BATCH];
       auto fetch = [&](int k0) {
 #pragma unroll
@@ -401,25 +452,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
         for (int x = 0; x < BATCH; ++x) {
           const int k = k0 + x;
           const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-          uint32_t amax = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) amax = max(amax, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
+          const uint32_t two = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                        __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+          uint32_t amax = max(two << 16, two & 0xffff0000u);  // magnitude as fp32 bits
 #pragma unroll
           for (int o = LPR / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
           const int e2 = max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-          // a negative scale turns the row round, so that the multiplier is positive
-          const float inv = __int_as_float((127 - e2) << 23) * (p.scale_log2 < 0.f ? -1.f : 1.f);
+          const float inv = __int_as_float((127 - e2) << 23) * sign;
           uint32_t h[4], l[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float a = __uint_as_float(w[e] << 16) * inv, b = __uint_as_float(w[e] & 0xffff0000u) * inv;
-            h[e] = e4m3x2_bits(a, b);
-            const float2 f = e4m3x2_value(h[e]);
-            l[e] = e4m3x2_bits(a - f.x, b - f.y);
+            const float2 a = __fmul2_rn(make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u)),
+                                        make_float2(inv, inv));
+            h[e] = e4m3x2_bits(a.x, a.y);
+            const float2 left = __ffma2_rn(e4m3x2_value(h[e]), make_float2(-1.f, -1.f), a);
+            l[e] = e4m3x2_bits(left.x, left.y);
           }
           const uint32_t off = cache_swizzle<D>((warp % 4) * 32 + k * RPS + (int)lane / LPR, 8 * ((int)lane % LPR));
-          *reinterpret_cast<uint2*>(q_hi + off) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-          *reinterpret_cast<uint2*>(q_lo + off) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+          if (qt == t) {  // (the second of a pair needs the rows' scales only)
+            *reinterpret_cast<uint2*>(q_hi + off) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+            *reinterpret_cast<uint2*>(q_lo + off) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+          }
           // a row that holds a number that is not finite gives NaN
           const float cr = amax >= 0x7f800000u ? __int_as_float(0x7fc00000)
                                                : __int_as_float((e2 + 127) << 23) * fabsf(p.scale_log2);
@@ -428,16 +481,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready[t]));
+      if (qt == t) ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready[t]));
     }
     const int lim = p.rows.limit(sg.len, sg.first, (int)p.rows.by_g.div((uint32_t)(valid ? row : row0)));
     const int wlim = __reduce_min_sync(0xffffffffu, lim);
     float m = -INFINITY, l = 0.f;
     float v_ref = 0.f;  // the largest scale of V so far: the unit of O
-    for (int j = 0; j < sg.ntiles; ++j, ++it) {
+    const int j0 = PAIR ? t : 0;
+    for (int j = j0; j < sg.ntiles; j += STEP) {
       const int kbase = (sg.tile0 + j) * kCacheTile;
-      const uint32_t meta = it % kChunkMeta;
-      ok = cache_wait(&bars->meta_full[meta], (it / kChunkMeta) & 1, bars, p);
+      const uint32_t n = it + (uint32_t)j, meta = n % kChunkMeta;
+      ok = cache_wait(&bars->meta_full[meta], (n / kChunkMeta) & 1, bars, p);
       if (!ok) break;
       constexpr int G = ONE ? 1 : 4;  // groups of keys with scales of their own
       float sl[G];  // multipliers of the raw scores: positive, or NaN
@@ -496,7 +550,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       }
       const float m_use = m == -INFINITY ? 0.f : m;
       l *= alpha;
-      const bool rescale = j > 0 && (v_down < 0 || __any_sync(0xffffffffu, grow));
+      const bool rescale = j > j0 && (v_down < 0 || __any_sync(0xffffffffu, grow));
       alpha *= __int_as_float((v_down + 127) << 23);  // for O, which is in units of v_ref
       auto release = [&](uint64_t* bar) {
         ptx::tmem_wait_st();
@@ -541,46 +595,76 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       release(&bars->p_ready[t]);
     }
     if (!ok) break;
+    it += (uint32_t)sg.ntiles;
     ok = cache_wait(&bars->o_full[t], oc & 1, bars, p);
     if (!ok) break;
     ++oc;
     ptx::tc_fence_after_sync();
-    if (sg.ntiles == sg.total) {
-      const float inv = l == 0.f ? 0.f : v_ref / l;
+    // Partial O four channels at a time, the rows of a warp side by side.  The
+    // second of a pair leaves its results in the upper rows of the CTA's slot
+    // (128 rows or fewer leave them free), where the first takes them.
+    const bool whole = sg.ntiles == sg.total, join = PAIR && sg.ntiles > 1;
+    const long long slot = whole ? 2LL * blockIdx.x : cache_slot((int)blockIdx.x, bars->plan.t0, sg.unit_t0);
+    const int in_unit = t * 128 + in_tile;
+    float4* part = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * kChunkRows;
+    float2* part_ml = reinterpret_cast<float2*>(p.part_ml) + slot * kChunkRows;
+    float own = v_ref, other = 0.f;
+    if (join && t == 0) {
+      ok = cache_wait(&bars->joined, jc & 1, bars, p);
+      if (!ok) break;
+      ++jc;
+      const float2 ml = part_ml[128 + in_tile];
+      const float m_all = fmaxf(l == 0.f ? -INFINITY : m, ml.y == 0.f ? -INFINITY : ml.x);
+      const float w = l == 0.f ? 0.f : ptx::ex2(m - m_all);
+      other = ml.y == 0.f ? 0.f : ptx::ex2(ml.x - m_all);
+      own *= w;
+      l = fmaf(w, l, other * ml.y);
+      m = m_all;
+    }
+    const bool out = whole && t == qt;
+    if (out) {
+      own = l == 0.f ? 0.f : own / l;
+      other = l == 0.f ? 0.f : other / l;
+    }
 #pragma unroll 1
-      for (int cb = 0; cb < D; cb += 32) {
-        uint32_t r[32];
-        ptx::tmem_ld32x32b_x32(tO + cb, r);
+    for (int cb = 0; cb < D; cb += 32) {
+      uint32_t r[32];
+      ptx::tmem_ld32x32b_x32(tO + cb, r);
+      float o[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(r[i]) * own;
+      if (join && t == 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 x = part[(cb / 4 + k) * kChunkRows + 128 + in_tile];
+          o[4 * k] = fmaf(other, x.x, o[4 * k]);
+          o[4 * k + 1] = fmaf(other, x.y, o[4 * k + 1]);
+          o[4 * k + 2] = fmaf(other, x.z, o[4 * k + 2]);
+          o[4 * k + 3] = fmaf(other, x.w, o[4 * k + 3]);
+        }
+      }
+      if (out) {
         if (valid) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + cb);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = ptx::pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]) * inv, __uint_as_float(r[8 * k + 2 * e + 1]) * inv);
-            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_uint4(ptx::pack_bf16x2(o[8 * k], o[8 * k + 1]), ptx::pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                ptx::pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), ptx::pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
         }
-      }
-      if (valid) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-    } else {
-      // Partial O four channels at a time, the rows of a warp side by side.
-      const long long slot = cache_slot((int)blockIdx.x, bars->plan.t0, sg.unit_t0);
-      const int in_unit = t * 128 + in_tile;
-      if (threadIdx.x == 0) p.note_cut(sg, bars->plan);
-      float4* dst = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * kChunkRows + in_unit;
-#pragma unroll 1
-      for (int cb = 0; cb < D; cb += 32) {
-        uint32_t r[32];
-        ptx::tmem_ld32x32b_x32(tO + cb, r);
+      } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          dst[(cb / 4 + k) * kChunkRows] =
-              make_float4(__uint_as_float(r[4 * k]) * v_ref, __uint_as_float(r[4 * k + 1]) * v_ref,
-                          __uint_as_float(r[4 * k + 2]) * v_ref, __uint_as_float(r[4 * k + 3]) * v_ref);
+          part[(cb / 4 + k) * kChunkRows + in_unit] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
-      reinterpret_cast<float2*>(p.part_ml)[slot * kChunkRows + in_unit] = make_float2(m, l);
+    }
+    if (out) {
+      if (valid) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    } else {
+      part_ml[in_unit] = make_float2(m, l);
+      if (t != qt)
+        ptx::mbar_arrive(ptx::smem_u32(&bars->joined));
+      else if (threadIdx.x == 0)
+        p.note_cut(sg, bars->plan);
     }
     ptx::tc_fence_before_sync();  // O has been read: the next unit's products may overwrite it
   }

@@ -1,0 +1,52 @@
+// fa_cache_launch.h — host side of the cached attention shared by its two
+// translation units: the plan of a call, and the launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "fa.h"
+#include "fa_cache_attn.cuh"
+#include "fa_host.h"
+
+namespace fa {
+
+// Rows of a key head that share a pass over its tiles: 4, 8 or 16, the least
+// that holds them all, in the kernel for few rows (fa_cache_attn.cuh, up to
+// kCacheFewRows); 256 in the one for many (fa_cache_chunk.cuh).  16 sequences of
+// up to 8192 tokens with 8 key heads: 24 rows take 59 us at D = 64 and 50 us at
+// D = 32 in the kernel for many, 79 and 75 us in two passes of 16 rows; 32 rows
+// at D = 128 take 85 us in either.
+constexpr int kCacheFewRows = 16;
+constexpr int kChunkRows = 256;
+constexpr int kChunkMaxGrid = 192;  // CTAs of the kernel for many rows (one per SM) that partial results are sized for
+
+struct CachePlan {
+  int R, rt, row_tiles;
+  int64_t units;        // per batch entry
+  int64_t tiles;        // at most, all units
+  size_t part_o, cut, total;  // workspace: partial O; up to their maxima and sums; in all
+};
+
+// Launches a merge so that its blocks may start while the kernel before it on
+// the stream finishes (it waits for that kernel itself).
+inline int launch_after(void (*kernel)(const CacheAttnParams), unsigned blocks, unsigned threads,
+                 const CacheAttnParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// The kernel for many rows and its merge (fa_cache_chunk.cu).
+int launch_cache_chunk(CacheAttnParams& p, const CachePlan& plan, int D, const DeviceState& st, cudaStream_t s);
+
+}  // namespace fa
