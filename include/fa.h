@@ -387,6 +387,13 @@ FA_API int fa_cache_read(const fa_cache* cache, const int* table, int table_widt
  * key head h / (Hq / H).  A row that sees no key (an empty sequence, a row
  * before the first key) gives O = 0, LSE = -inf.
  *
+ * The cache's codes are used as they are; q is held to 2^-17.8 of its row's
+ * largest element or better, the probabilities to 11 bits or 2^-25 of the row's
+ * largest (times the ratio between the scales of V of the pages it sees), sums
+ * are fp32.  A row of q, or a key that it sees, that holds a number that is not
+ * finite gives NaN for the row; such a number in V reaches every row of the call
+ * that sees any key of the same 128-key tile.
+ *
  *   q, out   device bf16 [B, Hq, Nq, D], lse fp32 [B, Hq, Nq], as fa_fwd's
  *   table, lens, q_start  as above; pages may be shared between sequences.
  *            Table entries past a sequence's length are not read.
@@ -394,7 +401,10 @@ FA_API int fa_cache_read(const fa_cache* cache, const int* table, int table_widt
  *            fa_cache_workspace_bytes(...) bytes (may be NULL when that is 0),
  *            not shared with a concurrent call.
  *
- * An index out of range records FA_ERR_INDEX (see fa_cache_read).
+ * One kernel is enqueued on `stream`, and where a sequence may be longer than
+ * 128 tokens a second that joins what the first left in parts.  An index out of
+ * range records FA_ERR_INDEX (see fa_cache_read), a wait that ran out
+ * FA_ERR_TIMEOUT.
  */
 FA_API int fa_fwd_cache(const void* q, const fa_cache* cache, const int* table, int table_width,
                         const int* lens, const int* q_start, int causal, void* out, float* lse, int B, int Hq,
@@ -436,13 +446,15 @@ FA_API int fa_measure_ex2_rate(void* stream, double* ex2_per_clock_per_sm);
  * records the first violation, sets FA_ERR_DEBUG_CHECK in the device status
  * word and makes its CTA drain and exit as after a wait timeout; nothing traps.
  * It stands in for a memory checker where none can run.
+ * (The cache's kernels check the page numbers, lengths and positions that they
+ * read from device memory in both builds.)
  *
  * fa_debug_build — 1 in the debug build, 0 in the release build.
  *
  * fa_debug_report — synchronise `stream`, copy the first recorded violation
  *   to record[8] and clear it: {check id (0 = none; 1 unit schedule, 2
  *   producer/MMA unit mismatch, 3 mask row, 4 e4m3 scale index, 5 output
- *   store), CTA, thread, value a, value b, 0, 0, number of failed checks}.
+ *   store, 6 output row and 7 partial results of the cached attention), CTA, thread, value a, value b, 0, 0, number of failed checks}.
  *   The release build writes zeros.  Returns FA_OK, FA_ERR_INVALID_ARGUMENT
  *   (record NULL) or FA_ERR_CUDA.
  */

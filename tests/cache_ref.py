@@ -56,15 +56,15 @@ def quantised(x, page, start=0):
     return e4m3(x / s[..., None]) * s[..., None], s
 
 
-def tile_weight(v, page):
-    """|v| times the ratio of the largest scale among the pages of a token's 128-token tile to its own
-    page's: v [H, L, D].  (The scales are taken from what the cache holds, whose largest element may
+def weight(v, page, tile):
+    """|v| times the ratio of the largest scale among the pages of a token's 128-token tile (or of the
+    whole sequence) to its own page's: v [H, L, D].  (The scales are taken from what the cache holds, whose largest element may
     have been rounded down past a power of two: the ratio is within a factor of 2.)"""
     H, L, D = v.shape
     pad = torch.zeros(H, -(-L // 128) * 128, D, dtype=v.dtype, device=v.device)
     pad[:, :L] = v.nan_to_num(0.0)
     s = scale_of(pad.abs().view(H, -1, page, D).amax((2, 3)))  # [H, pages]
-    most = s.view(H, -1, 128 // page).amax(2).repeat_interleave(128 // page, 1)
+    most = s.view(H, -1, 128 // page).amax(2).repeat_interleave(128 // page, 1) if tile else s.amax(1, keepdim=True)
     return (pad.abs() * (most / s).repeat_interleave(page, 1)[..., None])[:, :L]
 
 

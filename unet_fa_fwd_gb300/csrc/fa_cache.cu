@@ -537,6 +537,7 @@ int fa_fwd_cache(const void* q, const fa_cache* cache, const int* table, int tab
                          fa::FastDiv::make((uint32_t)(Hq / cache->H))};
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.status = st->status;
+  p.debug_record = st->debug_record;
   if (need) {
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_o);

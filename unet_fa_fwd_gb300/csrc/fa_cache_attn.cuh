@@ -72,8 +72,36 @@ struct CacheAttnParams {
   int ctas;                // of the attention kernel's launch
   float scale_log2;
   int* status;
+  int* debug_record;       // debug builds: first failed check
   unsigned long long timeout_ns;
   int inject_stall;        // test hook: CTA 0 withholds its second tile
+
+  // Debug builds: an output row or a slot of partial results outside its array
+  // is recorded and not accessed (release builds compile the checks to true).
+  __device__ __forceinline__ bool check(bool ok, int id, long long a, long long b) const {
+#ifdef FA_DEBUG
+    if (!ok) {
+      atomicCAS(status, 0, 5);  // FA_ERR_DEBUG_CHECK
+      if (atomicCAS(&debug_record[0], 0, id) == 0) {
+        debug_record[1] = (int)blockIdx.x;
+        debug_record[2] = (int)threadIdx.x;
+        debug_record[3] = (int)a;
+        debug_record[4] = (int)b;
+      }
+      atomicAdd(&debug_record[7], 1);
+    }
+    return ok;
+#else
+    (void)ok; (void)id; (void)a; (void)b;
+    return true;
+#endif
+  }
+  __device__ __forceinline__ bool check_row(long long at) const {
+    return check(at >= 0 && at < (long long)rows.B * rows.H * rows.g * rows.Nq, 6, at, rows.Nq);
+  }
+  __device__ __forceinline__ bool check_slot(long long slot) const {
+    return check(slot >= 0 && slot < 2LL * ctas, 7, slot, ctas);
+  }
 
   // cut[c]: batch entry (-1: no such unit), key head, row tile, and the CTA that
   // holds its last tile times two, plus one if its first piece is in slot 1.
@@ -620,6 +648,7 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
         for (int r = 0; r < RT; ++r) {
           if (r >= rows) break;
           const long long at = p.row_at(sg.b, sg.h, row0 + r);
+          if (!p.check_row(at)) continue;
           if (tid < D) p.out[at * D + tid] = __float2bfloat16_rn(l[r] == 0.f ? 0.f : o[r] / l[r]);
           if (tid == r) p.lse[at] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * 0.6931471805599453f;
         }
@@ -628,7 +657,7 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
         if (tid == 0) p.note_cut(sg, bars->plan);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          if (r >= rows) break;
+          if (r >= rows || !p.check_slot(slot)) break;
           if (tid < D) p.part_o[(slot * RT + r) * D + tid] = o[r];
           if (tid == r) {
             p.part_ml[(slot * RT + r) * 2] = m[r];
@@ -667,6 +696,7 @@ __global__ void __launch_bounds__(128) fa_cache_merge_kernel(const __grid_consta
   // The unit is the first stretch of every CTA but c0.
   auto slot = [&](int c) { return (2LL * c + (c == c0 ? (cut.w & 1) : 0)) * RT + in_tile; };
   const int pieces = c1 - c0 + 1;
+  if (!p.check_slot(2LL * c1)) return;
   auto block = [&](float x, bool max) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -706,6 +736,7 @@ __global__ void __launch_bounds__(128) fa_cache_merge_kernel(const __grid_consta
   *reinterpret_cast<float4*>(&part[g][lane * 4]) = o;
   __syncthreads();
   const long long at = p.row_at(cut.x, cut.y, r);
+  if (!p.check_row(at)) return;
   if (tid < D) {
     float x = 0.f;
 #pragma unroll

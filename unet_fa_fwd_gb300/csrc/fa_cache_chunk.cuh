@@ -608,6 +608,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     const int in_unit = t * 128 + in_tile;
     float4* part = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * kChunkRows;
     float2* part_ml = reinterpret_cast<float2*>(p.part_ml) + slot * kChunkRows;
+    if (p.part_o && !p.check_slot(slot)) break;
+    if (!p.check_row(at)) break;
     float own = v_ref, other = 0.f;
     if (join && t == 0) {
       ok = cache_wait(&bars->joined, jc & 1, bars, p);
@@ -681,7 +683,7 @@ __global__ void __launch_bounds__(kChunkRows) fa_cache_chunk_merge_kernel(const 
   asm volatile("griddepcontrol.wait;" ::: "memory");  // see fa_cache_merge_kernel
   const int4 cut = p.cut[c0];
   const int row = cut.z * kChunkRows + (int)threadIdx.x, c1 = cut.w >> 1;
-  if (cut.x < 0 || row >= p.rows.R) return;
+  if (cut.x < 0 || row >= p.rows.R || !p.check_slot(2LL * c1)) return;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + threadIdx.x;
   auto slot = [&](int c) { return 2LL * c + (c == c0 ? (cut.w & 1) : 0); };
   float m = -INFINITY, l = 0.f;
@@ -707,6 +709,7 @@ __global__ void __launch_bounds__(kChunkRows) fa_cache_chunk_merge_kernel(const 
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const long long at = p.row_at(cut.x, cut.y, row);
+  if (!p.check_row(at)) return;
   uint32_t w[8];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
