@@ -3,7 +3,8 @@
 the fp64 CPU oracle.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME] [--impl native|reference]
-                    [--variant fwd|fp8|causal|key_mask|additive_mask|bool_mask|window]
+                    [--variant fwd|fp8|causal|key_mask|additive_mask|bool_mask|window|
+                               cached_chunk|cached_token]
 
 A step is one attention forward (one kernel launch) over the whole workload,
 inputs resident in device memory.  Default workload: HunyuanVideo 720p
@@ -19,8 +20,11 @@ same workload.  ``--variant`` times another entry point as the step (for
 profiling one path alone; the end-to-end leg and the "also" blocks are then
 skipped): the FP8 Q K^T forward, causal attention, a key-padding mask (last
 quarter of the keys excluded), a per-(query, key) additive fp32 or boolean mask
-(broadcast over heads), or 8x8 window attention on a 64x64 token grid (the
-workload must have 4096 tokens).
+(broadcast over heads), 8x8 window attention on a 64x64 token grid (the
+workload must have 4096 tokens), or a step of generation with the workload's
+sequence in an e4m3 cache: rotary positions on the last 2048 tokens (or the last
+one), their keys and values written to the cache, and their attention to all of
+it.
 """
 from __future__ import annotations
 
@@ -296,6 +300,24 @@ def bench_native(args, world, rank, local):
 
         def step():
             fa.fwd_window(q, k, v, 64, 64, 8, 8, 0, 0, scale=inp["scale"], stream=stream)
+    elif variant in ("cached_chunk", "cached_token"):
+        n = 1 if variant == "cached_token" else min(2048, Nq, Nk)
+        held, page = Nk - n, 128
+        per = -(-Nk // page)
+        cache = fa.KVCache8.empty(B * per, H, page, D, device=device)
+        table = torch.arange(B * per, dtype=torch.int32, device=device).view(B, per)
+        at = torch.full((B,), held, dtype=torch.int32, device=device)
+        lens = torch.full((B,), Nk, dtype=torch.int32, device=device)
+        axes = fa.RopeAxes((D,))
+        pos = torch.arange(held, Nk, dtype=torch.int32, device=device)[:, None]
+        if held:
+            fa.cache_write(cache, k[:, :, :held], v[:, :, :held], table, torch.zeros_like(at))
+        flops = 4.0 * B * H * D * (n * Nk - n * (n - 1) // 2)
+
+        def step():
+            qr, kr = fa.rope(q[:, :, Nq - n:], k[:, :, held:], pos, axes, stream=stream)
+            fa.cache_write(cache, kr, v[:, :, held:], table, at, stream=stream)
+            fa.fwd_cache(qr, cache, table, lens, causal=True, scale=inp["scale"], stream=stream)
     else:
         raise SystemExit(f"unknown variant {variant}")
 
@@ -748,7 +770,8 @@ def main(argv=None):
     ap.add_argument("--heads", type=int, default=None,
                     help="override the workload's head count (smaller cases for profiling)")
     ap.add_argument("--variant", default="fwd",
-                    choices=["fwd", "fp8", "causal", "key_mask", "additive_mask", "bool_mask", "window"])
+                    choices=["fwd", "fp8", "causal", "key_mask", "additive_mask", "bool_mask", "window",
+                             "cached_chunk", "cached_token"])
     ap.add_argument("--cpu-budget", type=float, default=12.0, help="seconds of oracle work for cpu_baseline")
     ap.add_argument("--ref-budget", type=float, default=90.0, help="seconds of oracle work, reference arm")
     ap.add_argument("--no-cpu-baseline", action="store_true")

@@ -158,6 +158,44 @@ __device__ __forceinline__ uint64_t cache_desc(uint32_t saddr, uint32_t lbo, uin
          (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)layout << 61;
 }
 
+// Four e4m3 MMAs of one product, operand A stepping by AS and B by BS (16-byte
+// units) each; the first overwrites the accumulator.  Issued by one elected
+// lane of a converged warp.
+template <int AS, int BS>
+__device__ __forceinline__ void cache_mma4(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                           uint32_t idesc) {
+  asm volatile(
+      "{\n"
+      ".reg .pred n, y, e;\n"
+      ".reg .b32 el, al, bl;\n"
+      ".reg .b64 da, db;\n"
+      "elect.sync el|e, 0xffffffff;\n"
+      "setp.ne.u32 n, 0, 0;\n"
+      "setp.eq.u32 y, 0, 0;\n"
+      "mov.b64 da, {%1, %2};\n"
+      "mov.b64 db, {%3, %4};\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, n;\n"
+      "add.u32 al, %1, %6;\n"
+      "add.u32 bl, %3, %7;\n"
+      "mov.b64 da, {al, %2};\n"
+      "mov.b64 db, {bl, %4};\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, y;\n"
+      "add.u32 al, %1, %8;\n"
+      "add.u32 bl, %3, %9;\n"
+      "mov.b64 da, {al, %2};\n"
+      "mov.b64 db, {bl, %4};\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, y;\n"
+      "add.u32 al, %1, %10;\n"
+      "add.u32 bl, %3, %11;\n"
+      "mov.b64 da, {al, %2};\n"
+      "mov.b64 db, {bl, %4};\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, y;\n"
+      "}\n"
+      ::"r"(d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(AS), "n"(BS), "n"(2 * AS), "n"(2 * BS),
+        "n"(3 * AS), "n"(3 * BS)
+      : "memory");
+}
+
 // Byte (row, col) of a K-major operand of W-byte rows, swizzled over W bytes.
 template <int W>
 __device__ __forceinline__ uint32_t cache_swizzle(int row, int col) {
@@ -395,8 +433,8 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
     };
     auto issue_o = [&](uint32_t stage) {
       const uint32_t a = (uint32_t)dv + stage * (C::STAGE_BYTES >> 4);
-      ptx::mma_ss_f8_strided_x4_el<(32 * D >> 4), 2>(tmem + C::COL_O, a, (uint32_t)(dv >> 32), (uint32_t)dp,
-                                                      (uint32_t)(dp >> 32), IDESC_O, 0);  // 32 keys each
+      cache_mma4<(32 * D >> 4), 2>(tmem + C::COL_O, a, (uint32_t)(dv >> 32), (uint32_t)dp, (uint32_t)(dp >> 32),
+                                   IDESC_O);  // 32 keys each
     };
     uint32_t it = 0, seg = 0;  // tiles and segments so far
     bool ok = true;

@@ -32,29 +32,6 @@ def ss(n, kind, elect=False):
       : "memory");
 }}
 '''
-def ss_strided(n, kind):
-    """As ss, operand A stepping by AS and B by BS (16-byte units) a MMA."""
-    lines = ['"{\\n"', '".reg .pred p, q;\\n"', '".reg .b32 al, bl;\\n"', '".reg .b64 da, db;\\n"',
-             '".reg .pred e;\\n"', '".reg .b32 el;\\n"', '"elect.sync el|e, 0xffffffff;\\n"',
-             '"setp.ne.b32 p, %6, 0;\\n"', '"setp.eq.u32 q, 0, 0;\\n"',
-             '"mov.b64 da, {%1, %2};\\n"', '"mov.b64 db, {%3, %4};\\n"',
-             f'"@e tcgen05.mma.cta_group::1.kind::{kind} [%0], da, db, %5, p;\\n"']
-    for i in range(1, n):
-        lines += [f'"add.u32 al, %1, %{6 + i};\\n"', f'"add.u32 bl, %3, %{6 + n - 1 + i};\\n"',
-                  '"mov.b64 da, {al, %2};\\n"', '"mov.b64 db, {bl, %4};\\n"',
-                  f'"@e tcgen05.mma.cta_group::1.kind::{kind} [%0], da, db, %5, q;\\n"']
-    lines.append('"}\\n"')
-    imm = "".join(f', "n"(AS * {i})' for i in range(1, n)) + "".join(f', "n"(BS * {i})' for i in range(1, n))
-    body = "\n      ".join(lines)
-    return f'''template <int AS, int BS>
-__device__ __forceinline__ void mma_ss{'_f8' if kind != 'f16' else ''}_strided_x{n}_el(uint32_t d, uint32_t a_lo, uint32_t a_hi,
-                                          uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc_first) {{
-  asm volatile(
-      {body}
-      ::"r"(d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc_first){imm}
-      : "memory");
-}}
-'''
 def ts(n, elect=False):
     g = "@e " if elect else ""
     lines = ['"{\\n"', '".reg .pred p, q;\\n"', '".reg .b32 ta, bl;\\n"', '".reg .b64 db;\\n"']
@@ -91,7 +68,6 @@ for n in (1, 2, 4, 8):
     out.append(ss(n, "f16", True))
 for n in (1, 2, 4):
     out.append(ss(n, "f8f6f4", True))
-out.append(ss_strided(4, "f8f6f4"))
 out.append(ts(4, True))
 out.append(ts(8, True))
 open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "mma_batch.inc"), "w").write("\n".join(out))
