@@ -162,6 +162,9 @@ def test_bad_caches_are_refused(lib, call, kw, code):
     (_attend, dict(Hq=5)), (_attend, dict(Hq=0)), (_attend, dict(Nq=0)), (_attend, dict(B=0)),
     (_attend, dict(scale=math.nan)), (_attend, dict(scale=math.inf)),
     (_attend, dict(B=1 << 16, Nq=1 << 14)),                     # 2^32 rows
+    (_attend, dict(B=1 << 30, Hq=1 << 30, Nq=1 << 30)),         # sizes whose products pass 64 bits
+    (_write, dict(cache=dict(num_pages=1, H=1 << 29), B=1 << 30, N=1922, k=(FAR[3], 0, 0, 0), v=(FAR[4], 0, 0, 0))),
+    (_read, dict(cache=dict(num_pages=1, H=1 << 28), k=FAR[11], v=FAR[12], B=1 << 30, N=1 << 16)),
 ])
 def test_bad_arguments_are_refused(lib, call, kw):
     assert call(lib, **kw) == 1
@@ -175,6 +178,16 @@ def test_bad_arguments_are_refused(lib, call, kw):
 def test_valid_calls_reach_the_device(lib, call, kw, monkeypatch):
     monkeypatch.setenv("FA_FAULT_INJECT", "launch")
     assert call(lib, **kw) == 3
+
+
+def test_workspace_bytes(lib):
+    size = lib.fa_cache_workspace_bytes
+    # sequences of at most one tile need none; past that, room for 2 x 1024 stretches of 4 rows at most
+    assert size(64, 32, 8, 1, 128, 2, 64) == 0
+    assert size(64, 32, 8, 1, 128, 128, 64) == 2 * 1024 * 4 * (128 + 2) * 4 + 1024 * 16
+    for bad in ((0, 1, 1, 1, 64, 9, 64), (1, 3, 2, 1, 64, 9, 64), (1, 1, 1, 1, 48, 9, 64),
+                (1 << 30, 1 << 30, 1 << 30, 1 << 30, 64, 9, 64), (1, 1, 1, 1, 64, 1 << 30, 64)):
+        assert size(*bad) == 0
 
 
 # ---- the Python entry points ----
@@ -191,6 +204,12 @@ def test_python_checks():
         fa.rope(x, x, pos, axes)
     with pytest.raises(ValueError, match="CUDA"):
         fa.fa_rope(x, None, pos, axes, x, None)
+    with pytest.raises(TypeError, match="q_out"):
+        fa.fa_rope(x, None, pos, axes, None, None)
+    with pytest.raises(TypeError, match="out"):
+        fa.fa_fwd_cache(x, None, None, None, None, None, None)
+    with pytest.raises(TypeError, match="k_out"):
+        fa.fa_cache_read(None, None, None, None, None)
     with pytest.raises(ValueError, match=r"\[B, H, N, D\]"):
         fa.rope(x[0], None, pos, axes)
     with pytest.raises(ValueError, match="CUDA"):

@@ -78,6 +78,11 @@ def _exact(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device:
     return t.data_ptr()
 
 
+def _given(out: torch.Tensor | None, name: str) -> None:
+    if out is None:
+        raise TypeError(f"{name} must be a tensor")
+
+
 # Four fa_tensor structs side by side (pointer and three strides each).
 _Tensors = ctypes.c_longlong * 16
 _SIZE = ctypes.sizeof(FaTensor)
@@ -187,6 +192,7 @@ def fa_rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, axes: Ro
     """Enqueue the rotation into caller-provided outputs (any strides; the inputs themselves for in
     place).  q [B, Hq, N, D] and k [B, Hk, N, D] (or None) of one dtype, bf16, fp16 or fp32; pos int32
     [B, N, A] or [N, A]."""
+    _given(q_out, "q_out")
     if (k is None) != (k_out is None):
         raise ValueError("pass k and k_out together, or neither")
     _run(q, stream, _rope, q, k, pos, axes, q_out, k_out, False, False, pairing, bool(inverse))
@@ -196,7 +202,8 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, axes: RopeA
          inverse: bool = False, token_major: bool = False, stream=None):
     """Allocate outputs and turn q and k (k may be None) by their positions; returns (q, k),
     contiguous [B, H, N, D] as the attention takes them, or with ``token_major`` views of contiguous
-    [B, N, H, D] tensors.  Inputs may have any strides (slices of a projection)."""
+    [B, N, H, D] tensors.  Inputs may have any strides (slices of a projection).  Autograd does not
+    record the call: the gradients are :func:`rope_bwd`'s."""
     _bhnd(q, "q")
     return _run(q, stream, _rope, q, k, pos, axes, None, None, True, token_major, pairing, bool(inverse))
 
@@ -297,6 +304,7 @@ def fa_cache_read(cache: KVCache8, table: torch.Tensor, lens: torch.Tensor, k_ou
                   v_out: torch.Tensor, start: torch.Tensor | None = None, stream=None) -> None:
     """Read tokens start[b] (0 if None) .. start[b] + N - 1 of each sequence into caller-provided bf16
     [B, H, N, D]; positions from lens[b] on give zeros."""
+    _given(k_out, "k_out")
     _run(cache.k, stream, _read, cache, table, lens, k_out, v_out, None, start)
 
 
@@ -345,6 +353,7 @@ def fa_fwd_cache(q: torch.Tensor, cache: KVCache8, table: torch.Tensor, lens: to
                  q_start: torch.Tensor | None = None, scale: float | None = None, stream=None) -> None:
     """Enqueue the attention to the cache into caller-provided ``out`` and ``lse``; ``workspace`` holds
     at least cache_workspace_bytes(...) bytes (None when that is 0)."""
+    _given(out, "out")
     _run(cache.k, stream, _attend, q, cache, table, lens, out, lse, workspace, bool(causal), q_start, scale)
 
 

@@ -28,6 +28,9 @@ using fa::ranges_overlap;
 
 bool head_dim_ok(int D) { return D == 32 || D == 64 || D == 128; }
 
+// a * b * c (each >= 0) is at most INT_MAX.
+bool fits_int(int64_t a, int64_t b, int64_t c) { return (__int128)a * b * c <= INT_MAX; }
+
 // ---- strided [B][H][N][D] tensors (the last axis contiguous) ----
 
 // Elements from the first to one past the last; 0 when that (or an offset)
@@ -419,8 +422,8 @@ int fa_cache_write(const fa_cache* cache, const fa_tensor* k, const fa_tensor* v
   p.B = B;
   p.N = N;
   p.slots = (N + page - 2) / page + 1;  // N tokens from anywhere in a page
+  if (!fits_int(2LL * B, H, p.slots)) return FA_ERR_INVALID_ARGUMENT;
   const int64_t blocks = 2LL * B * H * p.slots;
-  if (blocks > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
 
   fa::DeviceState* st = nullptr;
   rc = fa::current_device(&st);
@@ -446,6 +449,8 @@ int fa_cache_read(const fa_cache* cache, const int* table, int table_width, cons
       !ints_ok(first, true))
     return FA_ERR_INVALID_ARGUMENT;
   const int D = cache->D, H = cache->H;
+  const int64_t per = ((int64_t)N * (D / 16) + fa::kReadThreads - 1) / fa::kReadThreads;
+  if (!fits_int(2LL * B, H, per)) return FA_ERR_INVALID_ARGUMENT;
   const size_t out = (size_t)B * H * N * D * 2, ints = (size_t)B * sizeof(int);
   void* outs[2] = {k_out, v_out};
   for (int i = 0; i < 2; ++i)
@@ -454,8 +459,6 @@ int fa_cache_read(const fa_cache* cache, const int* table, int table_width, cons
         ranges_overlap(outs[i], out, table, (size_t)B * table_width * sizeof(int)))
       return FA_ERR_INVALID_ARGUMENT;
   if (ranges_overlap(k_out, out, v_out, out)) return FA_ERR_INVALID_ARGUMENT;
-  const int64_t per = ((int64_t)N * (D / 16) + fa::kReadThreads - 1) / fa::kReadThreads;
-  if (per * B * H * 2 > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
   fa::CacheReadParams p;
   std::memset(&p, 0, sizeof(p));
   p.c = view(cache, table, table_width);
@@ -484,7 +487,7 @@ int fa_cache_read(const fa_cache* cache, const int* table, int table_width, cons
 
 size_t fa_cache_workspace_bytes(int B, int Hq, int Hk, int Nq, int D, int table_width, int page_tokens) {
   if (B < 1 || Hk < 1 || Hq < 1 || Hq % Hk || Nq < 1 || !head_dim_ok(D) || table_width < 1 || page_tokens < 1 ||
-      (int64_t)Hq / Hk * Nq > INT_MAX || (int64_t)table_width * page_tokens > INT_MAX)
+      !fits_int(B, Hq, Nq) || (int64_t)table_width * page_tokens > INT_MAX)
     return 0;
   return cache_plan(B, Hq, Hk, Nq, D, table_width, page_tokens).total;
 }
@@ -500,9 +503,9 @@ int fa_fwd_cache(const void* q, const fa_cache* cache, const int* table, int tab
     return FA_ERR_INVALID_ARGUMENT;
   if (Nq < 1 || Hq < 1 || Hq % cache->H) return FA_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(scale)) return FA_ERR_INVALID_ARGUMENT;
+  if (!fits_int(B, Hq, Nq)) return FA_ERR_INVALID_ARGUMENT;
   const int D = cache->D;
   const int64_t rows = (int64_t)B * Hq * Nq;
-  if ((int64_t)B * Hq > INT_MAX || rows > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
   const size_t qb = (size_t)rows * D * 2, lb = (size_t)rows * 4, ints = (size_t)B * sizeof(int);
   if (ranges_overlap(out, qb, q, qb) || ranges_overlap(out, qb, lse, lb) || ranges_overlap(lse, lb, q, qb) ||
       overlaps_cache(cache, bytes, out, qb) || overlaps_cache(cache, bytes, lse, lb) ||
