@@ -392,7 +392,9 @@ FA_API int fa_cache_read(const fa_cache* cache, const int* table, int table_widt
  * largest (times the ratio between the scales of V of the pages it sees), sums
  * are fp32.  A row of q, or a key that it sees, that holds a number that is not
  * finite gives NaN for the row; such a number in V reaches every row of the call
- * that sees any key of the same 128-key tile.
+ * that sees any key of the same 128-key tile.  Scores are fp32 numbers: past
+ * 2^16 in magnitude a probability may be off by the part 2^-23 of its score, and
+ * past 2^24 results mean nothing.
  *
  *   q, out   device bf16 [B, Hq, Nq, D], lse fp32 [B, Hq, Nq], as fa_fwd's
  *   table, lens, q_start  as above; pages may be shared between sequences.

@@ -339,6 +339,40 @@ def test_a_sink_and_a_long_tail(rows):
     assert float((out[..., 1] - 1).abs().max()) <= 2.0 ** -8
 
 
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_huge_scores_of_few_rows(sign):
+    """Equal scores of +-1.1e31 on every key: a uniform softmax, with LSE the score itself.  (Equal
+    keys give equal scores, so every p is a power of two: O is the mean but for fp32 sums and the last
+    rounding, 2^-8 |O| + 2^-20 of the mean of |v|.  LSE: 2^-17.8 from q, less than 2^-18 from the rest.)"""
+    L, D = 700, 64
+    cache, table = _new(1, L, 1, 64, D, 95)
+    k, v = torch.full((1, 1, L, D), sign * 1.2e15, dtype=BF16, device="cuda"), _rand((1, 1, L, D), 96)
+    fa.cache_write(cache, k, v, table, _ints([0]))
+    ks, vs = fa.cache_read(cache, table, _ints([L]), L)
+    q = torch.full((1, 1, 1, D), 1.2e15, dtype=BF16, device="cuda")
+    out, lse = fa.fwd_cache(q, cache, table, _ints([L]), scale=0.125)
+    score = float((q[0, 0, 0].double() * ks[0, 0, 0].double()).sum()) * 0.125
+    assert 1e31 < abs(score) < 1.3e31
+    mean, size = vs[0, 0].double().mean(0), vs[0, 0].double().abs().mean(0)
+    assert bool(((out[0, 0].double() - mean).abs() <= 2.0 ** -8 * mean.abs() + 2.0 ** -20 * size).all())
+    assert bool(((lse.double() - score).abs() <= 2.0 ** -17 * abs(score)).all())
+
+
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("rows", [1, 20, 140])
+def test_large_scores(rows, sign):
+    """Scores around +-2^15."""
+    L, D = 700, 64
+    cache, table = _new(1, L, 1, 64, D, 97)
+    k, v = _rand((1, 1, L, D), 98), _rand((1, 1, L, D), 99)
+    k[..., 0] = sign * 512.0
+    fa.cache_write(cache, k, v, table, _ints([0]))
+    ks, vs = fa.cache_read(cache, table, _ints([L]), L)
+    q = _rand((1, 1, rows, D), 100)
+    q[..., 0] = 512.0
+    _check_all(q, cache, table, [L], ks, vs, False, scale=0.125)
+
+
 @pytest.mark.parametrize("g", [4, 24, 150])
 def test_rows_that_are_not_finite_stay_apart(g):
     """A NaN or infinite query row gives NaN and leaves the other rows alone; so does a NaN key for the

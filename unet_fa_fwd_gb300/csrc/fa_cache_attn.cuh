@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
     // p is kept between 2^-25 and 2^8.75 (e4m3's largest is 448) by a running
     // reference m: on the first tile, and whenever a score passes m + 8.75, m
     // becomes the row's maximum less 7.
-    constexpr float kTop = 7.f, kLimit = 8.75f, kNone = -1e30f;
+    constexpr float kTop = 7.f, kLimit = 8.75f, kNone = -3.402823466e38f;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const uint32_t tS = tmem + lane_base + C::COL_S, tO = tmem + lane_base + C::COL_O;
     // Byte of key tid in column n of P (128-byte rows, swizzled over them).
