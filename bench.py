@@ -260,6 +260,10 @@ def bench_native(args, world, rank, local):
     in_bytes = sum(t.numel() * t.element_size() for t in (q, k, v)) + (
         0 if mask is None else mask.numel() * 4)
     stream = torch.cuda.current_stream(device)
+    l2_what = "of Q/K/V"
+    traffic = read_traffic(args.workload)
+    step_bytes = accounting.algorithmic_bytes(B, H, Nq, Nk, D, masked=mask is not None)
+    exps = float(B) * H * Nq * Nk
 
     variant = args.variant
     if variant == "fwd":
@@ -312,7 +316,11 @@ def bench_native(args, world, rank, local):
         pos = torch.arange(held, Nk, dtype=torch.int32, device=device)[:, None]
         if held:
             fa.cache_write(cache, k[:, :, :held], v[:, :, :held], table, torch.zeros_like(at))
-        flops = 4.0 * B * H * D * (n * Nk - n * (n - 1) // 2)
+        exps = float(B) * H * (n * Nk - n * (n - 1) // 2)
+        flops = 4.0 * D * exps
+        # q, k in and out of the rotation; k, v into the cache; all its codes, q, O and LSE
+        step_bytes = B * H * (D * (8 * n + 6 * n + 2 * Nk + 4 * n) + 4 * n)
+        in_bytes, l2_what, traffic = 2 * B * H * Nk * D, "of cached keys and values", None
 
         def step():
             qr, kr = fa.rope(q[:, :, Nq - n:], k[:, :, held:], pos, axes, stream=stream)
@@ -653,7 +661,6 @@ def bench_native(args, world, rank, local):
     ex2_rate = fa.measure_ex2_rate(stream)
     sm_count = torch.cuda.get_device_properties(device).multi_processor_count
     clk_mhz = clock_summary.get("sm_mhz") or float(peaks.get("sm_max_mhz", 2070.0))
-    exps = float(B) * H * Nq * Nk
     secondary = {"bound": "mufu_ex2", "ex2_per_clk_per_sm": round(ex2_rate, 2),
                  "sm_mhz": clk_mhz, "exp_bound_ms": round(exps / (ex2_rate * sm_count * clk_mhz * 1e6) * 1e3, 4),
                  "tensor_bound_ms": round(flops / (peak * 1e12) * 1e3, 4)}
@@ -689,7 +696,7 @@ def bench_native(args, world, rank, local):
                        "variant": variant, "B": B, "H": H, "Nq": Nq,
                        "Nk": Nk, "D": D,
                        "masked": mask is not None, "parallelism": f"replicas{world}",
-                       "l2": f"inputs larger than L2 ({in_bytes / 1e6:.0f} MB of Q/K/V per step)"},
+                       "l2": f"inputs larger than L2 ({in_bytes / 1e6:.0f} MB {l2_what} per step)"},
             "pct_of_peak": round(100.0 * kernel_tflops / peak, 2),
             "step_ms": {"median": round(statistics.median(step_ms), 4),
                         "min": round(min(step_ms), 4), "max": round(max(step_ms), 4)},
@@ -703,16 +710,14 @@ def bench_native(args, world, rank, local):
             "gpu_launches": kernels_per_step * args.steps,
             "roofline": {"bound": "tensor", "achieved": round(kernel_tflops, 2), "peak": peak,
                          "unit": "TFLOP/s", "frac": round(kernel_tflops / peak, 4),
-                         "traffic": read_traffic(args.workload),
+                         "traffic": traffic,
                          "peak_source": f"{peak_src} bf16_tflops (burst; kernel timed alone)",
                          "frac_of_sustained": (round(kernel_tflops / float(peak_sustained), 4)
                                                if peak_sustained else None),
                          "secondary": secondary,
                          "algorithmic_flops_per_launch": flops,
-                         "hbm_gbs": round(accounting.algorithmic_bytes(
-                             B, H, Nq, Nk, D, masked=mask is not None) / (ms_per_step * 1e6), 1),
-                         "algorithmic_bytes_per_launch": accounting.algorithmic_bytes(
-                             B, H, Nq, Nk, D, masked=mask is not None)},
+                         "hbm_gbs": round(step_bytes / (ms_per_step * 1e6), 1),
+                         "algorithmic_bytes_per_launch": step_bytes},
             "cpu_baseline": cpu,
         }
         if also:
