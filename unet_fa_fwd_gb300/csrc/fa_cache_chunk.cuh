@@ -49,7 +49,6 @@ namespace fa {
 
 constexpr int kChunkThreads = 384;
 constexpr int kChunkConvert = 64;  // threads that convert V
-constexpr int kChunkMeta = 16;   // tiles whose scales are kept: more than the pipeline's depth
 constexpr int kChunkStagesMax = 8;
 
 template <int D, bool PAIR>
@@ -61,8 +60,8 @@ struct ChunkCfg {
   static constexpr uint32_t LAYOUT8 = D == 128 ? 2u : (D == 64 ? 4u : 6u);
   static constexpr uint32_t LAYOUT16 = D >= 64 ? 2u : 4u;
   static constexpr int Q_TILES = PAIR ? 1 : 2;
-  static constexpr int V_STAGES = 2;                     // V in f16
-  static constexpr int K_STAGES = PAIR || D == 128 ? 3 : 6;  // K and V codes
+  static constexpr int V_STAGES = kChunkVStages;         // V in f16
+  static constexpr int K_STAGES = chunk_k_stages(D, PAIR);  // K and V codes
   static constexpr int SMEM_BYTES = 2 * Q_TILES * T8 + 2 * K_STAGES * T8 + V_STAGES * T16 + 2048;
   static_assert(K_STAGES <= kChunkStagesMax && K_STAGES + V_STAGES < kChunkMeta, "rings");
   static constexpr int COL_S = 0, COL_O = 256;           // S and O of tile t: + 128 t, + D t
@@ -493,9 +492,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     float m = -INFINITY, l = 0.f;
     float v_ref = 0.f;  // the largest scale of V so far: the unit of O
     const int j0 = PAIR ? t : 0;
+    // S of the stretch's first tile before that tile's scales: it is issued after
+    // K of the tile was announced, so every earlier tile's scales have come, and
+    // the parity below names one phase only.  A warpgroup that skipped a stretch
+    // has waited for nothing of it: the slot could still be at the phase of tile
+    // n - 32, whose parity is the same.  (From one tile of a stretch to the next
+    // the waits that are there suffice; S first on every tile cost 4 %: the chain
+    // from S to P is what bounds the kernel.)
     for (int j = j0; j < sg.ntiles; j += STEP) {
       const int kbase = (sg.tile0 + j) * kCacheTile;
       const uint32_t n = it + (uint32_t)j, meta = n % kChunkMeta;
+      // On a stretch's first tile, S before the scales: it is issued after K of the
+      // tile was announced, so every earlier tile's scales have come, and the
+      // parity of the tile's own names one phase only.  A warpgroup that skipped
+      // a stretch has waited for nothing of it: the slot could still be at the
+      // phase of tile n - 32, whose parity is the same.  (From one tile of a
+      // stretch to the next the waits that are there suffice.  S first on every
+      // tile costs 5 %: the chain from S to P is the bound.)
+      if (j == j0) {
+        ok = cache_wait(&bars->s_full[t], sc & 1, bars, p);
+        if (!ok) break;
+      }
       ok = cache_wait(&bars->meta_full[meta], (n / kChunkMeta) & 1, bars, p);
       if (!ok) break;
       constexpr int G = ONE ? 1 : 4;  // groups of keys with scales of their own

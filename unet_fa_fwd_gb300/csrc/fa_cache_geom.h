@@ -184,6 +184,14 @@ struct CacheWalk {
   }
 };
 
+// ---- the rings of the kernel for many rows ----
+// Tile n of a CTA's range uses stage n % chunk_k_stages of the K and V codes,
+// stage n % kChunkVStages of V in f16 and slot n % kChunkMeta of the scales.
+constexpr int kChunkRows = 256;    // rows of a unit: two row tiles of 128 (one of them with PAIR)
+constexpr int kChunkVStages = 2;
+constexpr int kChunkMeta = 16;     // more than the pipeline's depth
+constexpr int chunk_k_stages(int D, bool pair) { return pair || D == 128 ? 3 : 6; }
+
 // Partial results: a CTA has at most two stretches that are not whole units,
 // its first (slot 0) and its last (slot 1 when the unit starts inside the range).
 FA_HD int cache_slot(int c, long long range_t0, long long unit_t0) { return 2 * c + (unit_t0 > range_t0 ? 1 : 0); }

@@ -15,12 +15,11 @@ namespace fa {
 
 // Rows of a key head that share a pass over its tiles: 4, 8 or 16, the least
 // that holds them all, in the kernel for few rows (fa_cache_attn.cuh, up to
-// kCacheFewRows); 256 in the one for many (fa_cache_chunk.cuh).  16 sequences of
+// kCacheFewRows); kChunkRows in the one for many (fa_cache_chunk.cuh).  16 sequences of
 // up to 8192 tokens with 8 key heads: 24 rows take 59 us at D = 64 and 50 us at
 // D = 32 in the kernel for many, 79 and 75 us in two passes of 16 rows; 32 rows
 // at D = 128 take 85 us in either.
 constexpr int kCacheFewRows = 16;
-constexpr int kChunkRows = 256;
 constexpr int kChunkMaxGrid = 192;  // CTAs of the kernel for many rows (one per SM) that partial results are sized for
 
 struct CachePlan {
