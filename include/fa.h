@@ -391,10 +391,10 @@ FA_API int fa_cache_read(const fa_cache* cache, const int* table, int table_widt
  * largest element or better, the probabilities to 11 bits or 2^-25 of the row's
  * largest (times the ratio between the scales of V of the pages it sees), sums
  * are fp32.  A row of q, or a key that it sees, that holds a number that is not
- * finite gives NaN for the row; such a number in V reaches every row of the call
- * that sees any key of the same 128-key tile.  Scores are fp32 numbers: past
- * 2^16 in magnitude a probability may be off by the part 2^-23 of its score, and
- * past 2^24 results mean nothing.
+ * finite gives NaN for the row; such a number in V gives NaN in O (in its
+ * channel, perhaps in others) for the rows that see its key, and for no other.
+ * Scores are fp32 numbers: past 2^16 in magnitude a probability may be off by the
+ * part 2^-23 of its score, and past 2^24 results mean nothing.
  *
  *   q, out   device bf16 [B, Hq, Nq, D], lse fp32 [B, Hq, Nq], as fa_fwd's
  *   table, lens, q_start  as above; pages may be shared between sequences.

@@ -1,0 +1,107 @@
+"""What a row of the cached attention does not see does not reach it: numbers in
+V that are not finite (0 times NaN is NaN on the tensor cores), and scales of
+pages past the row's last key.
+
+A row is a function of q and of the keys that it sees.  Two caches that agree
+on those, page for page, give it the same bits: the other keys' probabilities
+are exact zeros, and every unit that results are held in follows from what the
+row sees.
+"""
+import math
+
+import pytest
+import torch
+
+import unet_fa_fwd_gb300 as fa
+
+from . import cache_ref as ref
+from .test_gpu_cache import BF16, _close, _ints, _new, _rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    fa.load_library()
+    torch.cuda.set_device(0)
+    assert fa.read_device_status() == 0
+    yield
+    assert fa.read_device_status() == 0
+
+
+# rows of a key head: few (4, 8, 16), pairs of key tiles, two row tiles, several units
+SHAPES = [(1, 4), (2, 4), (3, 5), (1, 30), (4, 30), (1, 200), (1, 300), (2, 290)]
+
+
+def _filled(k, v, page):
+    """A cache holding k, v [1, H, L, D]."""
+    L = k.shape[2]
+    cache, table = _new(1, L, k.shape[1], page, k.shape[3], 300)
+    fa.cache_write(cache, k, v, table, _ints([0]))
+    return cache, table
+
+
+def _rows(L, Nq, edge):
+    """Rows (causal, at the end of L keys) that see nothing from key `edge` on, and those that do."""
+    cut = min(max(edge - (L - Nq), 0), Nq)
+    assert 0 < cut < Nq
+    return slice(0, cut), slice(cut, Nq)
+
+
+@pytest.mark.parametrize("D,page", [(32, 32), (64, 64), (128, 32), (128, 128)])
+@pytest.mark.parametrize("g,Nq", SHAPES)
+@pytest.mark.parametrize("where", ["tile", "next tile"])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_a_value_that_is_not_finite(D, page, g, Nq, where, value):
+    """One channel of V at key `edge`, inside a tile or its first key: the rows before it keep their
+    bits, those that see it give NaN in that channel, and no LSE changes.  (A tile's first key: so many
+    heads that a CTA walks the tile with the one before it.)"""
+    H, edge = (2, 384 + 77) if where == "tile" else (700 if g * Nq <= 16 else 160, 384)
+    L = edge + (Nq + 1) // 2
+    q, k, v = _rand((1, H * g, Nq, D), 301), _rand((1, H, L, D), 302), _rand((1, H, L, D), 303)
+    bad = torch.arange(H, device="cuda") % 2 == 1  # in every second key head
+    v[0, bad, edge, D - 3] = 0.0
+    cache, table = _filled(k, v, page)
+    want, lse = fa.fwd_cache(q, cache, table, _ints([L]), causal=True)
+    v[0, bad, edge, D - 3] = value
+    cache, table = _filled(k, v, page)
+    out, got = fa.fwd_cache(q, cache, table, _ints([L]), causal=True)
+    before, after = _rows(L, Nq, edge)
+    bad = bad.repeat_interleave(g)
+    assert torch.equal(out[0, ~bad], want[0, ~bad]) and torch.equal(got, lse)
+    assert torch.equal(out[0, bad][:, before], want[0, bad][:, before])
+    assert bool(out[0, bad][:, after, D - 3].isnan().all())
+
+
+@pytest.mark.parametrize("g,Nq", SHAPES)
+@pytest.mark.parametrize("far", [False, True])
+def test_values_that_are_not_finite_before_every_row(g, Nq, far):
+    """A NaN that all rows see reaches all of them in its channel (and none of the other channels,
+    where its tile is seen whole); also where its tile's scores lie so far below the others that
+    fp32 holds its weights as 0."""
+    q, k, v = _rand((1, g, Nq, 64), 304), _rand((1, 1, 700, 64), 305), _rand((1, 1, 700, 64), 306)
+    v[0, 0, 130, 5] = math.nan
+    if far:  # scores of -400
+        q[..., 0], k[:, :, 128:256, 0] = 8.0, -400.0
+    cache, table = _filled(k, v, 64)
+    out, lse = fa.fwd_cache(q, cache, table, _ints([700]), causal=True)
+    bad = out.isnan()
+    assert bool(bad[..., 5].all()) and int(bad.sum()) == g * Nq and bool(lse.isfinite().all())
+
+
+@pytest.mark.parametrize("g,Nq", SHAPES)
+@pytest.mark.parametrize("page", [32, 128])
+def test_rows_that_see_no_key(g, Nq, page):
+    """Rows before the first key, with NaN in every V: O = 0 and LSE = -inf."""
+    q, k, v = _rand((1, g, Nq, 64), 307), _rand((1, 1, 300, 64), 308), _rand((1, 1, 300, 64), 309)
+    v[...] = math.nan
+    none = Nq // 2
+    cache, table = _filled(k, v, page)
+    for start in (-none, -Nq):
+        gone = min(-start, Nq)
+        out, lse = fa.fwd_cache(q, cache, table, _ints([300]), causal=True, q_start=_ints([start]))
+        assert not bool(out[:, :, :gone].any()) and bool(torch.isneginf(lse[:, :, :gone]).all())
+        assert bool(out[:, :, gone:].isnan().all()) and bool(lse[:, :, gone:].isfinite().all())
+    out, lse = fa.fwd_cache(q, cache, table, _ints([0]), causal=True)
+    assert not bool(out.any()) and bool(torch.isneginf(lse).all())

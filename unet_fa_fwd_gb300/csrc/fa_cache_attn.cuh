@@ -24,6 +24,11 @@
 // fp32 registers (so a page's scale of V is applied outside the MMA, and O is
 // rescaled there when the running maximum moves).
 //
+// A row must not get anything from keys that it does not see, but on the tensor
+// cores 0 times NaN is NaN.  So in the tiles of which some row does not see
+// every key (with causal, one or two a unit) a key whose V holds a NaN goes in
+// as zeros; the rows that do see it are noted and give NaN at the end.
+//
 // Within a tile pages may differ in their scale of V: p carries the ratio of
 // the page's scale to the tile's largest (a power of two <= 1), so the 2^-25
 // above is relative to the largest V of the 128 tokens.
@@ -150,6 +155,7 @@ struct CacheBars {
   uint32_t tmem_base;
   volatile int abort_flag;
   int wg_fail;
+  uint32_t nan_rows;  // rows of the unit that see a key of which a NaN in V was taken out
   float ks[kCacheStagesMax][4];
   alignas(16) float vs[kCacheStagesMax][4];  // scales of a tile's 32-token groups
   alignas(16) float c[16];  // row: multiplier of the raw product, times the page's scale of K
@@ -206,6 +212,12 @@ template <int W>
 __device__ __forceinline__ uint32_t cache_swizzle(int row, int col) {
   const int x = W == 128 ? (row & 7) : (W == 64 ? ((row >> 1) & 3) : ((row >> 2) & 1));
   return (uint32_t)(row * W + ((((col >> 4) ^ x) << 4) | (col & 15)));
+}
+
+// The bytes of four e4m3 codes that are NaN (0x7f or 0xff): their highest bits.
+__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t e4m3_nan(const uint4& v) {
+  return e4m3_nan(v.x) | e4m3_nan(v.y) | e4m3_nan(v.z) | e4m3_nan(v.w);
 }
 
 // The rest of a wait whose phase has not come at the first look.  (Out of line:
@@ -533,6 +545,7 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
             bars->lim[r] = p.rows.limit(sg.len, sg.first, (int)p.rows.by_g.div((uint32_t)(row0 + r)));
           }
         }
+        if (tid == 0) bars->nan_rows = 0;
         // (limits grow with the row: the first row's is the least)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready));
@@ -648,6 +661,23 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
           pr[r / 2] = __fmul2_rn(e, make_float2(ratio, ratio));
         }
         if (pending) take_o();  // P and O^T are free once the last tile's product is done
+        uint8_t* sV = sRing + stage * C::STAGE_BYTES + C::TILE_BYTES;
+        const int held = sg.len - key0;
+        if (least < key0 + min(held, kCacheTile) - 1) {  // some row does not see every key: this thread's key
+          // (Rolled up: cold code costs its instruction misses.)
+          uint32_t nan = 0;
+#pragma unroll 1
+          for (int i = 0; i < D / 16; ++i)
+            nan |= e4m3_nan(*reinterpret_cast<const uint4*>(sV + tid * D + (i + tid) % (D / 16) * 16));
+          if (nan) {
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) *reinterpret_cast<uint4*>(sV + tid * D + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+            uint32_t see = 0;
+#pragma unroll 1
+            for (int r = 0; r < RT; ++r) see |= (key0 + tid <= bars->lim[r] ? 1u : 0u) << r;
+            atomicOr(&bars->nan_rows, see);
+          }
+        }
         const float2 up = make_float2(16.f, 16.f), down = make_float2(-16.f, -16.f);
 #pragma unroll
         for (int r = 0; r < RT; r += 2) {
@@ -664,9 +694,7 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
           p_byte(3 * r + 5) = (uint8_t)(lo >> 8);
         }
         // Rows of V past the length may hold anything, NaN among it: zero them.
-        const int held = sg.len - key0;
         if (held < kCacheTile) {
-          uint8_t* sV = sRing + stage * C::STAGE_BYTES + C::TILE_BYTES;
           for (int i = max(held, 0) * D + tid * 16; i < C::TILE_BYTES; i += 128 * 16)
             *reinterpret_cast<uint4*>(sV + i) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -684,6 +712,10 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
       if (!stop && pending) take_o();
       if (cache_any(fail || stop)) break;
 
+      if (const uint32_t nan = bars->nan_rows) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) o[r] = (nan >> r) & 1u ? __int_as_float(0x7fc00000) : o[r];
+      }
       // The row's sum over the 128 threads.
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
@@ -777,8 +809,7 @@ __global__ void __launch_bounds__(128) fa_cache_merge_kernel(const __grid_consta
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = g; i < pieces; i += G) {
-    const float w = weight[i];
-    if (w == 0.f) continue;
+    const float w = weight[i];  // (of a piece with no visible key: 0, and its O is 0)
     const float4 x = *reinterpret_cast<const float4*>(p.part_o + slot(c0 + i) * D + lane * 4);
     o.x = fmaf(w, x.x, o.x);
     o.y = fmaf(w, x.y, o.y);

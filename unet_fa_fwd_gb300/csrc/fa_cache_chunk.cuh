@@ -23,6 +23,11 @@
 // stands for at most v_ref / scale times as much of p; O is in units of v_ref
 // and rescaled when that grows.
 //
+// In the tiles of which some row of the unit does not see every key (the
+// diagonal's with causal, and a sequence's last) codes of V that are NaN become
+// zeros, so that 0 times NaN does not reach the rows that do not see their keys.
+// A row that does see one finds out at its end (chunk_sees_nan) and gives NaN.
+//
 // Units' tiles are cut into equal ranges, one per CTA (1 CTA per SM), as in
 // fa_cache_attn.cuh: 192 units of 256 rows on 152 SMs would leave a third of
 // the second round idle.
@@ -75,6 +80,7 @@ struct ChunkBars {
   CacheRange plan;
   uint32_t tmem_base;
   volatile int abort_flag;
+  volatile int v_nan;  // a NaN was taken out of some tile's V
   alignas(16) float ks[kChunkMeta][4];
   alignas(16) float vs[kChunkMeta][4];  // scales of a tile's 32-token groups
 };
@@ -89,6 +95,26 @@ __device__ __forceinline__ void chunk_f16(const uint4& v, uint4 (&out)[2]) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[k]) : "h"((uint16_t)(w[k / 2] >> (16 * (k & 1)))));
   out[0] = make_uint4(o[0], o[1], o[2], o[3]);
   out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// The last key that every row of a stretch's unit sees (limits grow with the row).
+__device__ __forceinline__ int chunk_least(const CacheRows& rows, const CacheSegment& sg) {
+  return rows.limit(sg.len, sg.first, (int)rows.by_g.div((uint32_t)sg.rt * kChunkRows));
+}
+
+// Whether one of the keys first .. last of a sequence has a NaN in V (one
+// thread; out of line and slow, for rows of a CTA that has met one).
+template <int D>
+__device__ __noinline__ bool chunk_sees_nan(const CacheView& c, int b, int h, int first, int last) {
+  const int shift = 31 - __clz(c.page);  // page is a power of two
+  bool bad = false;
+  uint32_t nan = 0;
+  for (int key = first; key <= last && !nan; ++key) {
+    const long long at = (long long)cache_page(c.table[(long long)b * c.width + (key >> shift)], c.num_pages, bad) * c.H + h;
+    const uint4* row = reinterpret_cast<const uint4*>(c.code[1] + ((at << shift) + (key & (c.page - 1))) * D);
+    for (int i = 0; i < D / 16; ++i) nan |= e4m3_nan(row[i]);
+  }
+  return nan != 0;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -134,6 +160,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     ptx::mbar_init(ptx::smem_u32(&bars->joined), 128);
     ptx::mbar_init(ptx::smem_u32(&bars->drain), 1);
     bars->abort_flag = 0;
+    bars->v_nan = 0;
     ptx::fence_barrier_init();
   }
   if (warp == 8) cache_plan(p.rows, p.ctas, p.status, lane, &bars->plan);
@@ -171,18 +198,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     uint32_t it = 0;
     bool ok = true;
     while (ok && walk.next(sg)) {
+      const int least = chunk_least(p.rows, sg);
       for (int j = 0; j < sg.ntiles; ++j, ++it) {
         const uint32_t s8 = it % C::K_STAGES, s16 = it % C::V_STAGES;
-        ok = cache_wait(&bars->v8_full[s8], (it / C::K_STAGES) & 1, bars, p) &&
-             cache_wait(&bars->v_empty[s16], ((it / C::V_STAGES) & 1) ^ 1, bars, p);
+        ok = cache_wait(&bars->v8_full[s8], (it / C::K_STAGES) & 1, bars, p);
         if (!ok) break;
-        const uint8_t* src = sV8 + s8 * C::T8;
+        uint8_t* src = sV8 + s8 * C::T8;
         uint8_t* dst = sV + s16 * C::T16;
         // Rows past the length may hold anything, NaN among it: zeros.
         const int held = sg.len - (sg.tile0 + j) * kCacheTile;
         // Piece k of this lane: its row and 16-channel column, its 32 bytes of f16.
         auto row_of = [&](int k) { return ((k / HALVES) * 2 + w) * RPI + in_row; };
         auto col_of = [&](int k) { return (HALVES == 2 ? (k & 1) * 4 : 0) + in_col; };
+        // NaN in this lane's own pieces: before the wait for room in the ring, which
+        // hides it, and rolled up (cold code costs its instruction misses).
+        if ((sg.tile0 + j + 1) * kCacheTile - 1 > least) {
+#pragma unroll 1
+          for (int k = 0; k < STEPS; ++k) {
+            uint4* piece = reinterpret_cast<uint4*>(src + cache_swizzle<D>(row_of(k), 16 * col_of(k)));
+            if (!e4m3_nan(*piece) || row_of(k) >= held) continue;
+            auto clean = [](uint32_t codes) { return codes & ~((e4m3_nan(codes) >> 7) * 255u); };
+            *piece = make_uint4(clean(piece->x), clean(piece->y), clean(piece->z), clean(piece->w));
+            bars->v_nan = 1;
+          }
+        }
+        ok = cache_wait(&bars->v_empty[s16], ((it / C::V_STAGES) & 1) ^ 1, bars, p);
+        if (!ok) break;
         constexpr int BATCH = STEPS < 8 ? STEPS : 8;  // loads in flight together
 #pragma unroll 1
         for (int k0 = 0; k0 < STEPS; k0 += BATCH) {
@@ -644,6 +685,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       own *= w;
       l = fmaf(w, l, other * ml.y);
       m = m_all;
+    }
+    if (bars->v_nan) {  // the tiles that were looked through, as far as this row sees
+      const int from = max(sg.tile0, (chunk_least(p.rows, sg) + 1) / kCacheTile) * kCacheTile;
+      const int to = min(lim, (sg.tile0 + sg.ntiles) * kCacheTile - 1);
+      if (chunk_sees_nan<D>(p.c, sg.b, sg.h, from, to)) own = __int_as_float(0x7fc00000);
     }
     const bool out = whole && t == qt;
     if (out) {
