@@ -105,3 +105,46 @@ def test_rows_that_see_no_key(g, Nq, page):
         assert bool(out[:, :, gone:].isnan().all()) and bool(lse[:, :, gone:].isfinite().all())
     out, lse = fa.fwd_cache(q, cache, table, _ints([0]), causal=True)
     assert not bool(out.any()) and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("D,page", [(32, 32), (64, 32), (64, 64), (128, 32)])
+@pytest.mark.parametrize("g,Nq", SHAPES)
+@pytest.mark.parametrize("where", ["tile", "next tile"])
+@pytest.mark.parametrize("least,most", [(0, 30), (-100, 110)])
+def test_scales_of_pages_that_are_not_seen(D, page, g, Nq, where, least, most):
+    """V is 2^least before key `edge` (the first of a page, inside a tile or opening one) and 2^most times
+    that from it on: the rows before it keep their bits, and are as exact as the pages that they see
+    allow.  K's size changes by 2^40 there too."""
+    H, edge = (2, 384 + 64) if where == "tile" else (700 if g * Nq <= 16 else 160, 384)
+    L = edge + (Nq + 1) // 2
+    q, k, v = _rand((1, H * g, Nq, D), 310), _rand((1, H, L, D), 311), _rand((1, H, L, D), 312)
+    v *= 2.0 ** least
+    cache, table = _filled(k, v, page)
+    want, lse = fa.fwd_cache(q, cache, table, _ints([L]), causal=True)
+    for _ in range(2):
+        v[:, :, edge:] *= 2.0 ** ((most - least) / 2)
+    k[:, :, edge:] *= 2.0 ** 40
+    cache, table = _filled(k, v, page)
+    out, got = fa.fwd_cache(q, cache, table, _ints([L]), causal=True)
+    before, _ = _rows(L, Nq, edge)
+    assert torch.equal(out[:, :, before], want[:, :, before]) and torch.equal(got[:, :, before], lse[:, :, before])
+    ks, vs = (x[0, :2, :edge] for x in fa.cache_read(cache, table, _ints([L]), L))
+    exact = ref.attend(q[0, :2 * g, before], ks, vs, D ** -0.5, True, L - Nq)
+    _close(out[0, :2 * g, before], got[0, :2 * g, before], exact, vs, page, "", g * Nq <= 16)
+
+
+@pytest.mark.parametrize("g,Nq", SHAPES)
+@pytest.mark.parametrize("page", [32, 64, 128])
+def test_scales_that_grow_along_the_diagonal(g, Nq, page):
+    """Pages whose V grows by 2^8 for every 32 tokens: each row against the definition on the keys that
+    it sees, with the error that the pages which it sees allow."""
+    L, D = 700, 64
+    q, k, v = _rand((1, g, Nq, D), 313), _rand((1, 1, L, D), 314), _rand((1, 1, L, D), 315)
+    v *= torch.exp2(torch.arange(L, device="cuda") // page * (page / 4.0) - 88)[:, None]
+    cache, table = _filled(k, v, page)
+    out, lse = fa.fwd_cache(q, cache, table, _ints([L]), causal=True)
+    ks, vs = (x[0] for x in fa.cache_read(cache, table, _ints([L]), L))
+    for i in range(Nq):
+        n = L - Nq + i + 1
+        exact = ref.attend(q[0, :, i:i + 1], ks[:, :n], vs[:, :n], D ** -0.5)
+        _close(out[0, :, i:i + 1], lse[0, :, i:i + 1], exact, vs[:, :n], page, i, g * Nq <= 16)

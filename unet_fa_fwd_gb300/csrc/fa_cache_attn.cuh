@@ -31,7 +31,8 @@
 //
 // Within a tile pages may differ in their scale of V: p carries the ratio of
 // the page's scale to the tile's largest (a power of two <= 1), so the 2^-25
-// above is relative to the largest V of the 128 tokens.
+// above is relative to the largest V of the 128 tokens.  Where some row does not
+// see every key, the largest is each row's own, of the pages that it sees.
 //
 // All units' tiles (fa_cache_geom.h) are cut into equal ranges, one per CTA, so
 // ragged lengths and few heads balance alike; a unit cut between CTAs leaves
@@ -161,6 +162,9 @@ struct CacheBars {
   alignas(16) float c[16];  // row: multiplier of the raw product, times the page's scale of K
   alignas(16) int lim[16];  // row: its last visible key
   float red[4][16];
+  // A warp's copies: the largest scale of V that a row sees of the last tile, and
+  // the ratio of the warp's page's to it.
+  alignas(16) float row_vs[4][16], row_ratio[4][16];
 };
 static_assert(sizeof(CacheBars) <= 2048, "barrier space");
 
@@ -560,16 +564,17 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
       }
       float v_scale = 0.f;   // of the tile whose O^T is still to be added
       bool pending = false;
-      // Adds the last tile's O^T, in units of the current m, to o.
-      auto take_o = [&]() {
+      auto tile_unit = [&](int) { return v_scale; };
+      // Adds the last tile's O^T, in units of the current m and of unit(r), to o.
+      auto take_o = [&](auto unit) {
         if (!cache_wait(&bars->pv_done, (it - 1) & 1, bars, p)) fail = true;
         ptx::tc_fence_after_sync();
-        uint32_t r0[16];
+        [[maybe_unused]] uint32_t r0[16];
         if constexpr (RT == 4) {
           ptx::tmem_ld32x32b_x16(tO, r0);
 #pragma unroll
           for (int r = 0; r < RT; ++r)
-            o[r] += v_scale * (__uint_as_float(r0[3 * r]) + 0.0625f * __uint_as_float(r0[3 * r + 1]) +
+            o[r] += unit(r) * (__uint_as_float(r0[3 * r]) + 0.0625f * __uint_as_float(r0[3 * r + 1]) +
                                0.00390625f * __uint_as_float(r0[3 * r + 2]));
         } else {
           uint32_t r1[32];
@@ -584,7 +589,7 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
           }
 #pragma unroll
           for (int r = 0; r < RT; ++r)
-            o[r] += v_scale * (f[3 * r] + 0.0625f * f[3 * r + 1] + 0.00390625f * f[3 * r + 2]);
+            o[r] += unit(r) * (f[3 * r] + 0.0625f * f[3 * r + 1] + 0.00390625f * f[3 * r + 2]);
         }
         pending = false;
       };
@@ -625,7 +630,7 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
         for (int r = 0; r < RT; ++r) above = fmaxf(above, t[r] - m[r]);
         const bool need = above > kLimit;
         if (cache_any(need || fail)) {
-          if (pending) take_o();
+          if (pending) take_o(tile_unit);
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
             float x = t[r];
@@ -650,8 +655,11 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
             }
           }
         }
-        // vs / vt, a power of two
-        const float ratio = __int_as_float((max((__float_as_int(vs) >> 23) - (__float_as_int(vt) >> 23), -100) + 127) << 23);
+        const int held = sg.len - key0;
+        const bool mixed = least < key0 + min(held, kCacheTile) - 1;  // some row does not see every key
+        // vs / vt, a power of two (below, for each row's own vt)
+        auto exponent = [&](float unit) { return max((__float_as_int(vs) >> 23) - (__float_as_int(unit) >> 23), -100); };
+        const float ratio = __int_as_float(((mixed ? 0 : exponent(vt)) + 127) << 23);
         float2 pr[RT / 2];
 #pragma unroll
         for (int r = 0; r < RT; r += 2) {
@@ -660,11 +668,23 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
           l[r + 1] += e.y;
           pr[r / 2] = __fmul2_rn(e, make_float2(ratio, ratio));
         }
-        if (pending) take_o();  // P and O^T are free once the last tile's product is done
+        if (pending) take_o(tile_unit);  // P and O^T are free once the last tile's product is done
         uint8_t* sV = sRing + stage * C::STAGE_BYTES + C::TILE_BYTES;
-        const int held = sg.len - key0;
-        if (least < key0 + min(held, kCacheTile) - 1) {  // some row does not see every key: this thread's key
-          // (Rolled up: cold code costs its instruction misses.)
+        if (mixed) {
+          if ((int)lane < RT) {
+            const int groups = (bars->lim[lane] - key0) >> 5;  // the last group of 32 keys that the row sees
+            float x = groups >= 0 ? v4.x : 0.f;
+            if (groups >= 1) x = fmaxf(x, v4.y);
+            if (groups >= 2) x = fmaxf(x, v4.z);
+            if (groups >= 3) x = fmaxf(x, v4.w);
+            bars->row_vs[warp][lane] = x;
+            bars->row_ratio[warp][lane] = __int_as_float((min(exponent(x), 0) + 127) << 23);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < RT; r += 2)
+            pr[r / 2] = __fmul2_rn(pr[r / 2], *reinterpret_cast<const float2*>(&bars->row_ratio[warp][r]));
+          // NaN in V: this thread's key.  (Rolled up: cold code costs its instruction misses.)
           uint32_t nan = 0;
 #pragma unroll 1
           for (int i = 0; i < D / 16; ++i)
@@ -708,8 +728,12 @@ __global__ void __launch_bounds__(kCacheThreads, CacheCfg<D, RT>::RESIDENT) fa_c
           stage = 0;
           stage_phase ^= 1u;
         }
+        // (At once, so that the tiles that all rows see whole have one unit.  16 rows
+        // at D = 64, where an instruction more a tile shows: 146 us for 64 sequences
+        // of 8192 keys and 8 heads, 148 with a choice of units in every tile.)
+        if (mixed) take_o([&](int r) { return bars->row_vs[warp][r]; });
       }
-      if (!stop && pending) take_o();
+      if (!stop && pending) take_o(tile_unit);
       if (cache_any(fail || stop)) break;
 
       if (const uint32_t nan = bars->nan_rows) {

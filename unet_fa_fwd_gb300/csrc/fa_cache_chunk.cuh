@@ -19,9 +19,9 @@
 // and those two warps became the bound: 394 us for 2048 rows of 24 heads on
 // 16896 keys of 128, 510 us by moving bits, where f16 alone brought it to 292.)
 // P is rounded to f16: 11 bits, or 2^-25 of the row's largest p.  It carries its
-// page's scale of V relative to the largest scale so far, v_ref, so that 2^-25
-// stands for at most v_ref / scale times as much of p; O is in units of v_ref
-// and rescaled when that grows.
+// page's scale of V relative to the largest that the row has seen so far, v_ref, so
+// that 2^-25 stands for at most v_ref / scale times as much of p; O is in units of
+// v_ref and rescaled when that grows.
 //
 // In the tiles of which some row of the unit does not see every key (the
 // diagonal's with causal, and a sequence's last) codes of V that are NaN become
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     const int lim = p.rows.limit(sg.len, sg.first, (int)p.rows.by_g.div((uint32_t)(valid ? row : row0)));
     const int wlim = __reduce_min_sync(0xffffffffu, lim);
     float m = -INFINITY, l = 0.f;
-    float v_ref = 0.f;  // the largest scale of V so far: the unit of O
+    float v_ref = 0.f;  // the largest scale of V that the row has seen so far: the unit of O
     const int j0 = PAIR ? t : 0;
     // S of the stretch's first tile before that tile's scales: it is issued after
     // K of the tile was announced, so every earlier tile's scales have come, and
@@ -564,14 +564,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       for (int g = 0; g < G; ++g) {
         ks[g] = bars->ks[meta][g];
         vs[g] = bars->vs[meta][g];
-        v_new = fmaxf(v_new, vs[g]);
+        // (pages past the row's last key leave its unit alone)
+        if (kbase + g * (128 / G) <= lim) v_new = fmaxf(v_new, vs[g]);
       }
       const int v_down = max((__float_as_int(v_ref) >> 23) - (__float_as_int(v_new) >> 23), -100);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         sl[g] = c * ks[g];
         if (sl[g] < 1.17549435e-38f) sl[g] = 1.17549435e-38f;
-        ve[g] = max((__float_as_int(vs[g]) >> 23) - (__float_as_int(v_new) >> 23), -100);
+        ve[g] = min(max((__float_as_int(vs[g]) >> 23) - (__float_as_int(v_new) >> 23), -100), 0);
       }
       v_ref = v_new;
       ok = cache_wait(&bars->s_full[t], sc & 1, bars, p);
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       }
       const float m_use = m == -INFINITY ? 0.f : m;
       l *= alpha;
-      const bool rescale = j > j0 && (v_down < 0 || __any_sync(0xffffffffu, grow));
+      const bool rescale = j > j0 && __any_sync(0xffffffffu, grow || v_down < 0);
       alpha *= __int_as_float((v_down + 127) << 23);  // for O, which is in units of v_ref
       auto release = [&](uint64_t* bar) {
         ptx::tmem_wait_st();
