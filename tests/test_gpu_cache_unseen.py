@@ -148,3 +148,22 @@ def test_scales_that_grow_along_the_diagonal(g, Nq, page):
         n = L - Nq + i + 1
         exact = ref.attend(q[0, :, i:i + 1], ks[:, :n], vs[:, :n], D ** -0.5)
         _close(out[0, :, i:i + 1], lse[0, :, i:i + 1], exact, vs[:, :n], page, i, g * Nq <= 16)
+
+
+@pytest.mark.parametrize("g,Nq", SHAPES)
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_padded_rows_of_q_that_see_no_key(g, Nq, value):
+    """Rows of q that are not finite (padding) and see nothing: O = 0 and LSE = -inf, as any row without
+    keys; in an empty sequence too."""
+    q, k, v = _rand((2, g, Nq, 64), 316), _rand((1, 1, 300, 64), 317), _rand((1, 1, 300, 64), 318)
+    cache, table = _filled(k, v, 64)
+    table = table.repeat(2, 1)
+    none = Nq // 2
+    ks, vs = (x[0] for x in fa.cache_read(cache, table[:1].contiguous(), _ints([300]), 300))
+    want = ref.attend(q[0, :, none:], ks, vs, 0.125, True, 0)
+    q[0, :, :none] = value
+    q[1] = value
+    out, lse = fa.fwd_cache(q, cache, table, _ints([300, 0]), causal=True, q_start=_ints([-none, 0]))
+    for x, gone in ((0, slice(0, none)), (1, slice(0, Nq))):
+        assert not bool(out[x, :, gone].any()) and bool(torch.isneginf(lse[x, :, gone]).all())
+    _close(out[0, :, none:], lse[0, :, none:], want, vs, 64, "", g * Nq <= 16)

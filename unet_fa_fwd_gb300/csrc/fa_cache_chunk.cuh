@@ -529,6 +529,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
       if (qt == t) ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready[t]));
     }
     const int lim = p.rows.limit(sg.len, sg.first, (int)p.rows.by_g.div((uint32_t)(valid ? row : row0)));
+    if (lim < 0) c = 0.f;  // a row of q that sees no key counts for nothing, NaN or not
     const int wlim = __reduce_min_sync(0xffffffffu, lim);
     float m = -INFINITY, l = 0.f;
     float v_ref = 0.f;  // the largest scale of V that the row has seen so far: the unit of O
