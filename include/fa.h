@@ -302,6 +302,8 @@ typedef struct fa_rope_axes {
  *             among them); outputs too, as long as no element is written
  *             twice.  An output may be exactly its input (in place); else the
  *             outputs share no element with the inputs or each other.
+ *             (Rows of axes that do not nest, millions of which interleave, are
+ *             refused where a bounded search does not tell them apart.)
  *   D in {32, 64, 128}.  Speed, not results, depends on alignment: rows that
  *   start 16-byte aligned are read and written 16 bytes at a time.
  *

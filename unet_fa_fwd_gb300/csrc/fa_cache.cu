@@ -46,48 +46,95 @@ int64_t extent(const fa_tensor& t, int B, int H, int N, int D) {
   return e > ((__int128)1 << 58) ? 0 : (int64_t)e;
 }
 
-// No element is written twice: ordered by stride, each axis steps over all
-// that the smaller ones span.
-bool writes_once(const fa_tensor& t, int B, int H, int N, int D) {
-  long long st[3] = {t.stride_b, t.stride_h, t.stride_n};
-  int n[3] = {B, H, N};
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 3; ++j)
-      if (st[j] < st[i]) {
-        const long long s = st[i]; st[i] = st[j]; st[j] = s;
-        const int m = n[i]; n[i] = n[j]; n[j] = m;
-      }
-  int64_t span = D;
-  for (int i = 0; i < 3; ++i) {
-    if (n[i] == 1) continue;
-    if (st[i] < span) return false;
-    span += st[i] * (n[i] - 1);
+// One axis of a difference of two rows' offsets: a multiple of `stride` from
+// lo to hi times.
+struct Step {
+  int64_t stride, lo, hi;
+};
+
+// Whether some choice of multiples brings `at` + their sum within a row's D
+// elements of 0 (`moved`: a multiple other than 0 has been chosen, or need not
+// be).  Steps go from the largest stride to the smallest; a multiple that the
+// rest cannot bring back is left out, which leaves two or three for axes that
+// nest.  Layouts of which `budget` choices do not decide count as meeting.
+bool meets(const Step* t, int n, __int128 at, int D, bool moved, int& budget) {
+  if (--budget < 0) return true;
+  if (n == 0) return moved && at > -D && at < D;
+  __int128 rest_lo = 0, rest_hi = 0;
+  for (int i = 1; i < n; ++i) {
+    rest_lo += (__int128)t[i].stride * t[i].lo;
+    rest_hi += (__int128)t[i].stride * t[i].hi;
   }
-  return true;
+  // -D < at + z * stride + rest < D
+  const __int128 from = -D + 1 - at - rest_hi, to = D - 1 - at - rest_lo;
+  auto floor_div = [](__int128 a, int64_t b) { return a >= 0 ? a / b : -((-a + b - 1) / b); };
+  __int128 lo = floor_div(from + t->stride - 1, t->stride), hi = floor_div(to, t->stride);
+  if (lo < t->lo) lo = t->lo;
+  if (hi > t->hi) hi = t->hi;
+  for (__int128 z = lo; z <= hi; ++z)
+    if (meets(t + 1, n - 1, at + z * t->stride, D, moved || z != 0, budget)) return true;
+  return false;
 }
 
-// Two tensors share no element: their ranges are apart, or both are slices of
-// one token-major buffer (same strides) whose head blocks do not meet.
+constexpr int kMeetsBudget = 20000;
+
+bool meets(Step (&t)[6], int n, __int128 at, int D, bool moved) {
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (t[j].stride > t[i].stride) {
+        const Step s = t[i]; t[i] = t[j]; t[j] = s;
+      }
+  int budget = kMeetsBudget;
+  return meets(t, n, at, D, moved, budget);
+}
+
+// No element is written twice.
+bool writes_once(const fa_tensor& x, int B, int H, int N, int D) {
+  const long long st[3] = {x.stride_b, x.stride_h, x.stride_n};
+  const int size[3] = {B, H, N};
+  Step t[6];
+  int n = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (size[i] == 1) continue;
+    if (st[i] < D) return false;
+    t[n++] = Step{st[i], -(int64_t)(size[i] - 1), size[i] - 1};
+  }
+  return !meets(t, n, 0, D, false);
+}
+
+// Two tensors of one element type share no element: their ranges are apart, or
+// their rows interleave without meeting (slices of one buffer, in any order of
+// its axes).
 bool apart(const fa_tensor& a, int Ha, const fa_tensor& b, int Hb, int B, int N, int D, int size) {
   if (!ranges_overlap(a.data, (size_t)extent(a, B, Ha, N, D) * size, b.data,
                       (size_t)extent(b, B, Hb, N, D) * size))
     return true;
-  if (a.stride_b != b.stride_b || a.stride_h != b.stride_h || a.stride_n != b.stride_n) return false;
-  const bool a_first = a.data < b.data;
-  const int64_t bytes = a_first ? static_cast<char*>(b.data) - static_cast<char*>(a.data)
-                                : static_cast<char*>(a.data) - static_cast<char*>(b.data);
-  if (bytes % size) return false;
-  const int64_t d = bytes / size;
-  const int Hlo = a_first ? Ha : Hb, Hhi = a_first ? Hb : Ha;
-  const int64_t lo = a.stride_h * (Hlo - 1) + D, hi = d + a.stride_h * (Hhi - 1) + D;  // head blocks of a token
-  if (d < lo) return false;
-  if (N > 1 && a.stride_n < hi) return false;
-  const int64_t span = hi + (N > 1 ? a.stride_n * (N - 1) : 0);
-  return B == 1 || a.stride_b >= span;
+  const long long sa[3] = {a.stride_b, a.stride_h, a.stride_n}, sb[3] = {b.stride_b, b.stride_h, b.stride_n};
+  const int na[3] = {B, Ha, N}, nb[3] = {B, Hb, N};
+  Step t[6];
+  int n = 0;
+  auto add = [&](int64_t stride, int64_t lo, int64_t hi) {  // (equal strides of the two tensors are one step)
+    if (stride == 0 || lo == hi) return;
+    for (int i = 0; i < n; ++i)
+      if (t[i].stride == stride) {
+        t[i].lo += lo;
+        t[i].hi += hi;
+        return;
+      }
+    t[n++] = Step{stride, lo, hi};
+  };
+  for (int i = 0; i < 3; ++i) {
+    add(sa[i], 0, na[i] - 1);
+    add(sb[i], -(int64_t)(nb[i] - 1), 0);
+  }
+  const __int128 bytes = (__int128) reinterpret_cast<uintptr_t>(a.data) - reinterpret_cast<uintptr_t>(b.data);
+  return !meets(t, n, bytes / size, D, true);  // (both are aligned to their elements)
 }
 
-bool same(const fa_tensor& a, const fa_tensor& b) {
-  return a.data == b.data && a.stride_b == b.stride_b && a.stride_h == b.stride_h && a.stride_n == b.stride_n;
+// One tensor in one place.
+bool same(const fa_tensor& a, const fa_tensor& b, int B, int H, int N) {
+  return a.data == b.data && (B == 1 || a.stride_b == b.stride_b) && (H == 1 || a.stride_h == b.stride_h) &&
+         (N == 1 || a.stride_n == b.stride_n);
 }
 
 // Every row starts 16-byte aligned.
@@ -349,7 +396,7 @@ int fa_rope(const fa_rope_axes* axes, const int* pos, long long pos_stride_b, co
   }
   for (int i = 0; i < nt; ++i)
     for (int j = 0; j < nt; ++j) {
-      if (!(i == j && same(out[i], in[j])) && !apart(out[i], H[i], in[j], H[j], B, N, D, size))
+      if (!(i == j && same(out[i], in[j], B, H[i], N)) && !apart(out[i], H[i], in[j], H[j], B, N, D, size))
         return FA_ERR_INVALID_ARGUMENT;
       if (i < j && !apart(out[i], H[i], out[j], H[j], B, N, D, size)) return FA_ERR_INVALID_ARGUMENT;
     }
