@@ -78,14 +78,17 @@ bool meets(const Step* t, int n, __int128 at, int D, bool moved, int& budget) {
 
 constexpr int kMeetsBudget = 20000;
 
-bool meets(Step (&t)[6], int n, __int128 at, int D, bool moved) {
+bool meets(const Step* t, int n, __int128 at, int D, bool moved) {
+  int budget = kMeetsBudget;
+  return meets(t, n, at, D, moved, budget);
+}
+
+void sort_steps(Step* t, int n) {
   for (int i = 0; i < n; ++i)
     for (int j = i + 1; j < n; ++j)
       if (t[j].stride > t[i].stride) {
         const Step s = t[i]; t[i] = t[j]; t[j] = s;
       }
-  int budget = kMeetsBudget;
-  return meets(t, n, at, D, moved, budget);
 }
 
 // No element is written twice.
@@ -99,7 +102,14 @@ bool writes_once(const fa_tensor& x, int B, int H, int N, int D) {
     if (st[i] < D) return false;
     t[n++] = Step{st[i], -(int64_t)(size[i] - 1), size[i] - 1};
   }
-  return !meets(t, n, 0, D, false);
+  sort_steps(t, n);
+  int64_t span = D;  // axes that nest, each stepping over all that the smaller ones span, need no search
+  int i = n;
+  while (i > 0 && t[i - 1].stride >= span) {
+    span += t[i - 1].stride * t[i - 1].hi;
+    --i;
+  }
+  return i == 0 || !meets(t, n, 0, D, false);
 }
 
 // Two tensors of one element type share no element: their ranges are apart, or
@@ -127,6 +137,7 @@ bool apart(const fa_tensor& a, int Ha, const fa_tensor& b, int Hb, int B, int N,
     add(sa[i], 0, na[i] - 1);
     add(sb[i], -(int64_t)(nb[i] - 1), 0);
   }
+  sort_steps(t, n);
   const __int128 bytes = (__int128) reinterpret_cast<uintptr_t>(a.data) - reinterpret_cast<uintptr_t>(b.data);
   return !meets(t, n, bytes / size, D, true);  // (both are aligned to their elements)
 }
