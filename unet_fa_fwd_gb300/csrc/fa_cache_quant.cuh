@@ -79,10 +79,13 @@ __global__ void __launch_bounds__(kWriteThreads) fa_cache_write_kernel(const __g
 
   bool bad = false;
   const int most = (int)min((long long)p.c.width * PAGE, (long long)INT32_MAX);
-  const int start = cache_clamp(p.start[b], most, bad);
+  const int given = p.start[b], start = cache_clamp(given, most, bad);
   const int count = p.count ? cache_clamp(p.count[b], p.N, bad) : p.N;
-  int end = start + count;  // no overflow: the host checks width * PAGE + N
-  end = cache_clamp(end, most, bad);
+  long long end = (long long)given + count;  // token i belongs at given + i, also before 0
+  if (end > most) {
+    bad = true;
+    end = most;
+  }
   const int index = start / PAGE + slot;  // page of the sequence
   const long long pos0 = (long long)index * PAGE;
   const bool any = pos0 < end && count > 0;
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(kWriteThreads) fa_cache_write_kernel(const __g
   const int last = (int)min((long long)PAGE, end - pos0);     // tokens it holds afterwards
 
   const __nv_bfloat16* x = p.x[kv] + b * p.xb[kv] + h * p.xh[kv];
-  const long long first = pos0 - start;                       // token of the call in row 0 of the page
+  const long long first = pos0 - given;                       // token of the call in row 0 of the page
   uint4 raw[PER];
   uint32_t amax = 0;  // of the finite elements, as bf16 bits
 #pragma unroll
