@@ -43,6 +43,7 @@ if ROOT not in sys.path:
 
 METRIC = "attention fwd TFLOP/s and % of GB300 dense-bf16 peak (1 GPU), vs CPU oracle"
 FALLBACK_BF16_TFLOPS = 1900.0
+FALLBACK_HBM_GBS = 6800.0
 KERNEL_NAME = "fa_fwd_kernel"
 
 
@@ -72,6 +73,21 @@ def read_peaks():
         return peaks, "measured"
     except (OSError, ValueError):
         return {"bf16_tflops": FALLBACK_BF16_TFLOPS}, "fallback"
+
+
+def roofline(flops: float, nbytes: float, ms: float, peaks: dict, peak_src: str) -> dict:
+    """What bounds a step of ``flops`` operations and ``nbytes`` bytes that took ``ms``: the tensor cores
+    or HBM, whichever takes longer at its measured rate, and the part of that rate reached."""
+    tflops, gbs = flops / (ms * 1e9), nbytes / (ms * 1e6)
+    peak = float(peaks.get("bf16_tflops", FALLBACK_BF16_TFLOPS))
+    hbm = float(peaks.get("hbm_gbs", FALLBACK_HBM_GBS))
+    sustained = peaks.get("bf16_tflops_sustained")
+    if nbytes / (hbm * 1e9) > flops / (peak * 1e12):
+        return {"bound": "hbm", "achieved": round(gbs, 1), "peak": hbm, "unit": "GB/s", "frac": round(gbs / hbm, 4),
+                "peak_source": f"{peak_src} hbm_gbs (copy)"}
+    return {"bound": "tensor", "achieved": round(tflops, 2), "peak": peak, "unit": "TFLOP/s",
+            "frac": round(tflops / peak, 4), "peak_source": f"{peak_src} bf16_tflops (burst; kernel timed alone)",
+            "frac_of_sustained": round(tflops / float(sustained), 4) if sustained else None}
 
 
 def read_traffic(workload: str):
@@ -654,7 +670,7 @@ def bench_native(args, world, rank, local):
 
     peaks, peak_src = read_peaks()
     peak = float(peaks.get("bf16_tflops", FALLBACK_BF16_TFLOPS))
-    peak_sustained = peaks.get("bf16_tflops_sustained")
+    roof = roofline(flops, step_bytes, ms_per_step, peaks, peak_src)
 
     # ---- secondary bound: one exponential per score on the MUFU pipe ----
     clock_summary = clocks.summary()
@@ -708,13 +724,7 @@ def bench_native(args, world, rank, local):
                                 "another) / download i-1 overlap kernel i"}
                     if e2e_steps else None),
             "gpu_launches": kernels_per_step * args.steps,
-            "roofline": {"bound": "tensor", "achieved": round(kernel_tflops, 2), "peak": peak,
-                         "unit": "TFLOP/s", "frac": round(kernel_tflops / peak, 4),
-                         "traffic": traffic,
-                         "peak_source": f"{peak_src} bf16_tflops (burst; kernel timed alone)",
-                         "frac_of_sustained": (round(kernel_tflops / float(peak_sustained), 4)
-                                               if peak_sustained else None),
-                         "secondary": secondary,
+            "roofline": {**roof, "traffic": traffic, "secondary": secondary,
                          "algorithmic_flops_per_launch": flops,
                          "hbm_gbs": round(step_bytes / (ms_per_step * 1e6), 1),
                          "algorithmic_bytes_per_launch": step_bytes},
