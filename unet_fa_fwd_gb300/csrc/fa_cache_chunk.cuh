@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
         auto col_of = [&](int k) { return (HALVES == 2 ? (k & 1) * 4 : 0) + in_col; };
         // NaN in this lane's own pieces: before the wait for room in the ring, which
         // hides it, and rolled up (cold code costs its instruction misses).
-        if ((sg.tile0 + j + 1) * kCacheTile - 1 > least) {
+        if ((sg.tile0 + j) * kCacheTile + (kCacheTile - 1) > least) {
 #pragma unroll 1
           for (int k = 0; k < STEPS; ++k) {
             uint4* piece = reinterpret_cast<uint4*>(src + cache_swizzle<D>(row_of(k), 16 * col_of(k)));
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     }
     if (bars->v_nan) {  // the tiles that were looked through, as far as this row sees
       const int from = max(sg.tile0, (chunk_least(p.rows, sg) + 1) / kCacheTile) * kCacheTile;
-      const int to = min(lim, (sg.tile0 + sg.ntiles) * kCacheTile - 1);
+      const int to = min(lim, (sg.tile0 + sg.ntiles - 1) * kCacheTile + (kCacheTile - 1));
       if (chunk_sees_nan<D>(p.c, sg.b, sg.h, from, to)) own = __int_as_float(0x7fc00000);
     }
     const bool out = whole && t == qt;
