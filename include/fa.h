@@ -290,13 +290,16 @@ typedef struct fa_rope_axes {
  * The D/2 pairs of a row are dealt to the axes in order, dims[a]/2 each; pair j
  * of axis a of token n turns by pos[b][n][a] * scale[a] * theta[a]^(-2j/dims[a]):
  * (x0, x1) -> (x0 cos - x1 sin, x0 sin + x1 cos).  A token at position 0 on
- * every axis is unchanged.  inverse != 0 turns the other way, which is also
- * the gradient: dx = fa_rope(dy, inverse).  (For a broadcast input the caller
- * sums the gradient over the broadcast axis.)
+ * every axis is unchanged (one with numbers that are not finite: 0 times those
+ * is NaN).  inverse != 0 turns the other way, which is also the gradient:
+ * dx = fa_rope(dy, inverse).  (For a broadcast input the caller sums the
+ * gradient over the broadcast axis.)
  *
  *   pos       device int32 [B, N, count], batch stride pos_stride_b elements
  *             (0: one set of positions for every batch entry); any int32
- *             value: the angle is reduced exactly
+ *             value: the turns per unit of position, f, are held to
+ *             |f| (5 + |ln theta|) 2^-53 and 2^-64, and their product with the
+ *             position is reduced exactly
  *   q, q_out  [B, Hq, N, D] of `dtype`; k, k_out [B, Hk, N, D], or both NULL.
  *             Inputs may have any strides (slices of a token-major projection
  *             among them); outputs too, as long as no element is written
@@ -322,7 +325,9 @@ FA_API int fa_rope(const fa_rope_axes* axes, const int* pos, long long pos_strid
  *   k, v              device, e4m3 codes [num_pages, H, page_tokens, D], 16-byte aligned
  *   k_scale, v_scale  device fp32 [num_pages, H]: an element is code * scale.
  *                     The scale is the least power of two s in [2^-117, 2^119]
- *                     with max |x| <= 448 s over the page's tokens of the head.
+ *                     with max |x| <= 448 s over the page's tokens of the head
+ *                     (tokens that a later, smaller start takes back count while
+ *                     earlier ones of their page are kept).
  *   page_tokens in {32, 64, 128};  D in {32, 64, 128}
  *
  * Nothing needs clearing: a page's scale and codes are read only where tokens
@@ -390,9 +395,9 @@ FA_API int fa_cache_read(const fa_cache* cache, const int* table, int table_widt
  * before the first key) gives O = 0, LSE = -inf.
  *
  * The cache's codes are used as they are; q is held to 2^-17.8 of its row's
- * largest element or better, the probabilities to 11 bits or 2^-25 of the row's
- * largest (times the ratio between the scales of V of the pages it sees), sums
- * are fp32.  A row's results follow from its q and the keys that it sees alone
+ * largest element (2^-110 if that is more) or better, the probabilities to 11
+ * bits or 2^-25 of the row's largest (times the ratio between the scales of V of
+ * the pages it sees), sums are fp32.  A row's results follow from its q and the keys that it sees alone
  * (in the pages as they are: a later token may have grown its page's scale).  A
  * row of q, or a key that it sees, that holds a number that is not finite gives
  * NaN for the row; such a number in V gives NaN in O (in its channel, perhaps in

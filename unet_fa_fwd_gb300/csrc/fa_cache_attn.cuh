@@ -38,10 +38,10 @@
 // ragged lengths and few heads balance alike; a unit cut between CTAs leaves
 // fp32 partial results that fa_cache_merge_kernel joins in a fixed order.
 //
-// HBM bound: one query of 24 heads of 128 on 119056 keys takes 108 us, 6.8 TB/s;
-// 64 sequences of up to 8192 tokens, 32 query heads to 8 key heads, 125 us,
-// 6.5 TB/s; 4 us more to join the pieces.  Two CTAs an SM at D = 128 keep 96 KB
-// of codes in flight each (one CTA an SM: 130 and 160 us).
+// HBM bound: one query of 24 heads of 128 on 119056 keys takes 110 us, 6.7 TB/s;
+// 64 sequences of up to 8192 tokens, 32 query heads to 8 key heads, 126 us,
+// 6.5 TB/s, both with the join of the pieces.  Two CTAs an SM at D = 128 keep 96
+// KB of codes in flight each (one CTA an SM: 130 and 160 us).
 //
 // Warps: 0-3 softmax (thread = key of the tile, and channel of O), 4 producer
 // (page numbers, scales, TMA), 5 MMA issuer and owner of tensor memory.  Waits

@@ -32,10 +32,12 @@
 // fa_cache_attn.cuh: 192 units of 256 rows on 152 SMs would leave a third of
 // the second round idle.
 //
-// Those 2048 rows, causal, take 254 us, and 10 us more to join the cut units:
-// 1.46 to 1.49 PFLOP/s, tensor pipe 69 % active.  What is left is the softmax
+// Those 2048 rows, causal, take 255 to 260 us with the join of the cut units:
+// 1.53 to 1.56 PFLOP/s, tensor pipe 70 % active.  What is left is the softmax
 // between a tile's two products and what a stretch costs once (Q's two parts,
-// the epilogue); without cut units (19 heads) the rate is 1.70 PFLOP/s.
+// the epilogue); without cut units (19 heads, not causal) the rate is 1.68
+// PFLOP/s.  10800 rows on themselves, the last row tile of 48, take 563 us, 1.27
+// PFLOP/s: 43 row tiles with 1 to 85 key tiles each.
 //
 // PAIR.  With 128 rows or fewer there is one row tile, and its S, softmax and
 // P V would wait for one another; the two warpgroups then take the even and the

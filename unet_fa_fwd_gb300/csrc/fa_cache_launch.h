@@ -15,10 +15,12 @@ namespace fa {
 
 // Rows of a key head that share a pass over its tiles: 4, 8 or 16, the least
 // that holds them all, in the kernel for few rows (fa_cache_attn.cuh, up to
-// kCacheFewRows); kChunkRows in the one for many (fa_cache_chunk.cuh).  16 sequences of
-// up to 8192 tokens with 8 key heads: 24 rows take 59 us at D = 64 and 50 us at
-// D = 32 in the kernel for many, 79 and 75 us in two passes of 16 rows; 32 rows
-// at D = 128 take 85 us in either.
+// kCacheFewRows); kChunkRows in the one for many (fa_cache_chunk.cuh).  More rows
+// in two passes of 16 instead: 16 sequences of up to 8192 tokens with 8 key
+// heads, 24 rows 83 us for 58 at D = 64 and 80 for 52 at D = 32, 32 rows 97 for 83
+// at D = 128; 8 of up to 4111 with 4 key heads, 20 rows at D = 64, 32 for 31.
+// (Where a CTA gets a tile or two, two passes are ahead: 17 rows of one key head
+// on those, 26 us for 34.)
 constexpr int kCacheFewRows = 16;
 constexpr int kChunkMaxGrid = 192;  // CTAs of the kernel for many rows (one per SM) that partial results are sized for
 

@@ -6,10 +6,13 @@
 //   (x0, x1) -> (x0 cos - x1 sin, x0 sin + x1 cos).
 // The gradient is the rotation by -angle.
 //
-// The angle is reduced exactly: F = frequency / (2 pi) as a 64-bit fixed-point
-// fraction of a turn, so pos * F modulo 2^64 is the phase of any int32
-// position with an error of |pos| * 2^-65 turns; its top 32 bits are cut to an
-// eighth of a turn either side of a quadrant before they become fp32.
+// F = frequency / (2 pi) is a 64-bit fixed-point fraction of a turn, and pos * F
+// modulo 2^64 is the phase: the reduction to one turn loses nothing, at any int32
+// position.  F itself comes from 64-bit floating point (an exponent, a power, two
+// products): with f turns per unit of position it is off by e = |f| (5 +
+// |ln theta|) 2^-53 at most and cut to 2^-64, so the phase is off by
+// |pos| (e + 2^-64) turns.  Its top 32 bits are cut to an eighth of a turn either
+// side of a quadrant before they become fp32.
 //
 // HBM bound: every element is read and written once.  A thread owns one
 // 16-byte piece of a token's row (two, half a row apart, when the pairs are
