@@ -397,13 +397,13 @@ FA_API int fa_cache_read(const fa_cache* cache, const int* table, int table_widt
  * The cache's codes are used as they are; q is held to 2^-17.8 of its row's
  * largest element (2^-110 if that is more) or better, the probabilities to 11
  * bits or 2^-25 of the row's largest (times the ratio between the scales of V of
- * the pages it sees), sums are fp32.  A row's results follow from its q and the keys that it sees alone
- * (in the pages as they are: a later token may have grown its page's scale).  A
- * row of q, or a key that it sees, that holds a number that is not finite gives
- * NaN for the row; such a number in V gives NaN in O (in its channel, perhaps in
- * others) for the rows that see its key.
- * Scores are fp32 numbers: past 2^16 in magnitude a probability may be off by the
- * part 2^-23 of its score, and past 2^24 results mean nothing.
+ * the pages it sees), sums are fp32.  A row's results follow from its q and the
+ * keys that it sees alone (in the pages as they are: a later token may have grown
+ * its page's scale).  A row of q, or a key that it sees, that holds a number that
+ * is not finite gives NaN for the row; such a number in V gives NaN in O (in its
+ * channel, perhaps in others) for the rows that see its key.  Scores are fp32
+ * numbers: past 2^16 in magnitude a probability may be off by the part 2^-23 of
+ * its score, and past 2^24 results mean nothing.
  *
  *   q, out   device bf16 [B, Hq, Nq, D], lse fp32 [B, Hq, Nq], as fa_fwd's
  *   table, lens, q_start  as above; pages may be shared between sequences.

@@ -536,13 +536,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) fa_cache_chunk_kernel(const 
     float m = -INFINITY, l = 0.f;
     float v_ref = 0.f;  // the largest scale of V that the row has seen so far: the unit of O
     const int j0 = PAIR ? t : 0;
-    // S of the stretch's first tile before that tile's scales: it is issued after
-    // K of the tile was announced, so every earlier tile's scales have come, and
-    // the parity below names one phase only.  A warpgroup that skipped a stretch
-    // has waited for nothing of it: the slot could still be at the phase of tile
-    // n - 32, whose parity is the same.  (From one tile of a stretch to the next
-    // the waits that are there suffice; S first on every tile cost 4 %: the chain
-    // from S to P is what bounds the kernel.)
     for (int j = j0; j < sg.ntiles; j += STEP) {
       const int kbase = (sg.tile0 + j) * kCacheTile;
       const uint32_t n = it + (uint32_t)j, meta = n % kChunkMeta;
