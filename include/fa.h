@@ -317,6 +317,60 @@ FA_API int fa_rope(const fa_rope_axes* axes, const int* pos, long long pos_strid
                    const fa_tensor* q_out, int Hq, const fa_tensor* k, const fa_tensor* k_out, int Hk, int B,
                    int N, int D, int dtype, int pairing, int inverse, void* stream);
 
+/* The norm of fa_norm_rope: mean of squares + eps (finite, >= 0) under the root,
+ * and a weight for each of the D elements of a row, of queries and of keys (NULL:
+ * none).  weight_dtype: FA_DTYPE_FP32 or the tensors' type. */
+typedef struct fa_norm {
+    const void* q_weight;
+    const void* k_weight;
+    int weight_dtype;
+    float eps;
+} fa_norm;
+
+/*
+ * fa_norm_rope — norm of q and k for each head with the rotary positions in the
+ * same pass: y = R(pos) (w o x / sqrt(mean(x^2) + eps)), the mean over the D
+ * elements of a row, R the rotation of fa_rope.
+ *
+ *   q, q_out, k, k_out, pos, axes, pairing: as fa_rope (any strides, in place too;
+ *   k and k_out may both be NULL, then there is no k_weight)
+ *
+ * Arithmetic is fp32 (rows whose squares sum past its range give zeros), rounded
+ * once to `dtype`.  A row of zeros gives zeros if eps > 0.  One kernel is enqueued
+ * on `stream`.  Errors as fa_rope; FA_ERR_UNSUPPORTED for another weight type.
+ */
+FA_API int fa_norm_rope(const fa_rope_axes* axes, const fa_norm* norm, const int* pos, long long pos_stride_b,
+                        const fa_tensor* q, const fa_tensor* q_out, int Hq, const fa_tensor* k,
+                        const fa_tensor* k_out, int Hk, int B, int N, int D, int dtype, int pairing, void* stream);
+
+/*
+ * fa_norm_rope_bwd — gradients of fa_norm_rope: with r = 1 / sqrt(mean(x^2) + eps),
+ * n = x r and g = R(-pos) dy, dx = r (g o w - n mean(g o w o n)) and dw = the sum of
+ * g o n over the rows of all heads, tokens and batch entries.
+ *
+ *   dq_out, dk_out  the gradients of the outputs (dy), q, k the inputs of the forward
+ *                   (x), dq, dk the results (dx), all of `dtype`, any strides; a
+ *                   result may be exactly its own dy or x, else it shares no element
+ *                   with the other tensors.  dk_out, k, dk may all be NULL.
+ *   dq_weight, dk_weight  device fp32 [D]: dw, for exactly the weights that norm gives
+ *                   (NULL where it gives none)
+ *   workspace       device scratch, 16-byte aligned, at least
+ *                   fa_norm_rope_workspace_bytes(D) bytes where a weight is given, not
+ *                   shared with a concurrent call
+ *
+ * Sums are fp32, in a fixed order: results repeat bit for bit on one GPU.  One
+ * kernel is enqueued on `stream`, with weights a second that joins their partial
+ * sums.  Errors as fa_norm_rope.
+ */
+FA_API int fa_norm_rope_bwd(const fa_rope_axes* axes, const fa_norm* norm, const int* pos, long long pos_stride_b,
+                            const fa_tensor* dq_out, const fa_tensor* q, const fa_tensor* dq, int Hq,
+                            const fa_tensor* dk_out, const fa_tensor* k, const fa_tensor* dk, int Hk,
+                            float* dq_weight, float* dk_weight, int B, int N, int D, int dtype, int pairing,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes fa_norm_rope_bwd needs with weights (0 for an invalid D). */
+FA_API size_t fa_norm_rope_workspace_bytes(int D);
+
 /*
  * A paged key/value cache in 8 bits.  A page holds page_tokens consecutive
  * tokens of a sequence for every head; which pages a sequence owns, in order,

@@ -25,7 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfa_fwd.so")
 LIB_DEBUG = os.path.join(PKG, "libfa_fwd_debug.so")
 OBJ_DIR = os.path.join(PKG, "_build")
-UNITS = ["fa_fwd.cu", "fa_cache.cu", "fa_cache_chunk.cu", "fa_attn_d32.cu", "fa_attn_d64.cu", "fa_attn_d128.cu"]
+UNITS = ["fa_fwd.cu", "fa_cache.cu", "fa_cache_chunk.cu", "fa_norm.cu", "fa_attn_d32.cu", "fa_attn_d64.cu", "fa_attn_d128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -49,6 +49,12 @@ class FaRopeAxes(ctypes.Structure):
                 ("scale", ctypes.c_double * 4)]
 
 
+class FaNorm(ctypes.Structure):
+    """The C struct fa_norm."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
 class FaCache(ctypes.Structure):
     """The C struct fa_cache."""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
@@ -100,6 +106,14 @@ def load_library() -> ctypes.CDLL:
             lib.fa_rope.argtypes = [vp, vp, ctypes.c_longlong, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
                                     i32, vp]
             lib.fa_rope.restype = i32
+            ll = ctypes.c_longlong
+            lib.fa_norm_rope.argtypes = [vp, vp, vp, ll, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, vp]
+            lib.fa_norm_rope.restype = i32
+            lib.fa_norm_rope_bwd.argtypes = [vp, vp, vp, ll, vp, vp, vp, i32, vp, vp, vp, i32, vp, vp, i32, i32, i32,
+                                             i32, i32, vp, sz, vp]
+            lib.fa_norm_rope_bwd.restype = i32
+            lib.fa_norm_rope_workspace_bytes.argtypes = [i32]
+            lib.fa_norm_rope_workspace_bytes.restype = sz
             lib.fa_cache_write.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, vp]
             lib.fa_cache_write.restype = i32
             lib.fa_cache_read.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, vp]

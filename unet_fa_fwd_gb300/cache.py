@@ -131,6 +131,20 @@ def _bhnd(t: torch.Tensor, name: str) -> tuple:
     return t.shape
 
 
+def _positions(pos: torch.Tensor, B: int, N: int, A: int, device: int) -> int:
+    """The batch stride of a checked position array (0: one for all batch entries)."""
+    if pos.dtype is not _I32:
+        raise TypeError(f"pos must be torch.int32, got {pos.dtype}")
+    if pos.shape != (B, N, A) and pos.shape != (N, A):
+        raise ValueError(f"pos must have shape {(B, N, A)} or {(N, A)}, got {tuple(pos.shape)}")
+    ps = pos.stride()
+    if (A > 1 and ps[-1] != 1) or (N > 1 and ps[-2] != A):
+        raise ValueError("pos must be contiguous along its tokens and axes")
+    if pos.get_device() != device:
+        raise ValueError(f"pos must be on cuda:{device}, got {pos.device}")
+    return ps[0] if len(ps) == 3 else 0
+
+
 def _rope_new(shape, dtype, device, token_major) -> torch.Tensor:
     B, H, N, D = shape
     if token_major:
@@ -145,16 +159,7 @@ def _rope(q, k, pos, axes, q_out, k_out, new, token_major, pairing, inverse, dev
         raise TypeError(f"q must be bf16, fp16 or fp32, got {dtype}")
     if pairing not in _PAIRINGS:
         raise ValueError(f"pairing must be one of {tuple(_PAIRINGS)}, got {pairing!r}")
-    A = len(axes.dims)
-    if pos.dtype is not _I32:
-        raise TypeError(f"pos must be torch.int32, got {pos.dtype}")
-    if pos.shape != (B, N, A) and pos.shape != (N, A):
-        raise ValueError(f"pos must have shape {(B, N, A)} or {(N, A)}, got {tuple(pos.shape)}")
-    ps = pos.stride()
-    if (A > 1 and ps[-1] != 1) or (N > 1 and ps[-2] != A):
-        raise ValueError("pos must be contiguous along its tokens and axes")
-    if pos.get_device() != device:
-        raise ValueError(f"pos must be on cuda:{device}, got {pos.device}")
+    pos_b = _positions(pos, B, N, len(axes.dims), device)
     fields = _strided(q, "q", dtype, shape, device)
     if k is not None:
         Hk = _bhnd(k, "k")[1]
@@ -180,7 +185,7 @@ def _rope(q, k, pos, axes, q_out, k_out, new, token_major, pairing, inverse, dev
         ts = _Tensors(*fields)
         at = ctypes.addressof(ts)
         kt, ko = at + 2 * _SIZE, at + 3 * _SIZE
-    rc = load_library().fa_rope(axes.ref, pos.data_ptr(), ps[0] if len(ps) == 3 else 0, at, at + _SIZE, Hq, kt, ko, Hk,
+    rc = load_library().fa_rope(axes.ref, pos.data_ptr(), pos_b, at, at + _SIZE, Hq, kt, ko, Hk,
                                 B, N, D, _DTYPES[dtype], _PAIRINGS[pairing], inverse, handle)
     if rc != FA_OK:
         _raise("fa_rope", rc)

@@ -1,0 +1,247 @@
+// fa_norm_rope.cuh — norm of queries and keys for each head with the rotary
+// positions in the same pass, and its gradient.
+//
+//   r = 1 / sqrt(mean(x^2) + eps),  n = x r,  y = R(pos) (w o n)
+// (R: the rotation of fa_rope.cuh; w: a weight for each of the D elements, or
+// none).  With g = R(-pos) dy, the gradient of the normalised row:
+//   dw = sum over rows of g o n,   dx = r (g o w - n mean(g o w o n)).
+//
+// HBM bound: x (and dy) are read once and y (dx) written once; r is computed
+// again in the gradient, so nothing is kept for it.  A thread owns one 16-byte
+// piece of a token's row (two, half a row apart, when the pairs are the row's
+// halves) and walks heads with its pairs' sines and its weights in registers;
+// the threads of a row are neighbours in a warp and sum by shuffles.
+//
+// dw: a thread adds up its elements over all its rows, a block's threads are
+// joined in a fixed order into one row of partial sums, and a second kernel adds
+// the blocks' rows in a fixed order: no atomics, results repeat bit for bit.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "fa_rope.cuh"
+
+namespace fa {
+
+constexpr int kNormThreads = 256;
+constexpr int kNormMaxBlocks = 1024;  // blocks of the gradient (rows of partial sums)
+constexpr int kNormReduceRows = 32;   // rows of threads of the second kernel
+
+struct NormTensor {
+  const void* x;
+  const void* dy;  // gradient: of the output
+  void* out;       // y, or dx
+  long long x_b, x_h, x_n, dy_b, dy_h, dy_n, out_b, out_h, out_n;  // strides in elements
+  const void* w;   // [D] or nullptr
+  int H;
+};
+
+struct NormParams {
+  NormTensor t[2];   // q, k (k.H = 0: none)
+  const int* pos;    // [B][N][A], batch stride pos_b (0: shared)
+  long long pos_b;
+  int A, N, heads, heads_per_item, groups;
+  int w_f32;         // weights are fp32, else of the tensors' type
+  float eps;
+  long long tokens;  // B * N
+  long long items;   // token blocks x head groups
+  float* part;       // gradient with weights: [gridDim.x][2][D]
+  unsigned long long freq[kRopeMaxPairs];
+  unsigned char axis[kRopeMaxPairs];
+};
+
+// E elements at p, 16 bytes' worth: one access where rows are 16-byte aligned
+// (VEC), else one by one.
+template <typename T, int E, bool VEC>
+struct alignas(16) NormVec {
+  T v[E];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC) {
+      *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = p[i];
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (VEC) {
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) p[i] = v[i];
+    }
+  }
+};
+
+// Sum over the `CHUNKS` neighbouring lanes of a row, in every one of them.
+template <int CHUNKS>
+__device__ __forceinline__ float norm_row_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < CHUNKS; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+
+template <typename T, int D, bool VEC, bool HALVES, bool BACK>
+__global__ void __launch_bounds__(kNormThreads) fa_norm_rope_kernel(const __grid_constant__ NormParams p) {
+  constexpr int E = 16 / sizeof(T);
+  constexpr int PIECES = HALVES ? 2 : 1;
+  constexpr int CHUNKS = D / (E * PIECES);  // threads per token
+  constexpr int NE = E * PIECES;            // elements per thread
+  constexpr int PAIRS = NE / 2;
+  constexpr int BATCH = BACK ? 2 : 4;       // heads whose loads are in flight together
+  static_assert(CHUNKS <= 32 && 32 % CHUNKS == 0, "a row's threads share a warp");
+  using Vec = NormVec<T, E, VEC>;
+  const int chunk = threadIdx.x % CHUNKS;
+  // element i of this thread: column chunk * E + i, the second piece half a row on
+  auto column = [&](int i) { return chunk * E + (i < E ? i : i - E + D / 2); };
+
+  float acc[BACK ? 2 : 1][NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    acc[0][i] = 0.f;
+    if constexpr (BACK) acc[1][i] = 0.f;
+  }
+  for (long long item = blockIdx.x; item < p.items; item += gridDim.x) {
+    const long long tb = item / p.groups;
+    const int h0 = (int)(item - tb * p.groups) * p.heads_per_item;
+    const int h1 = min(h0 + p.heads_per_item, p.heads);
+    long long token = tb * (kNormThreads / CHUNKS) + threadIdx.x / CHUNKS;
+    const bool live = token < p.tokens;  // threads past the end read the last token and write nothing
+    if (!live) token = p.tokens - 1;
+    const long long b = token / p.N;
+    const long long n = token - b * p.N;
+    float c[PAIRS], s[PAIRS];
+    const int* pos = p.pos + b * p.pos_b + n * p.A;
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j) {
+      const int pair = chunk * PAIRS + j;
+      const long long at = pos[p.axis[pair]];
+      rope_cos_sin((unsigned long long)at * p.freq[pair], c[j], s[j]);
+    }
+#pragma unroll
+    for (int ti = 0; ti < 2; ++ti) {
+      const NormTensor& t = p.t[ti];
+      const int base = ti ? p.t[0].H : 0;
+      const int lo = max(h0, base) - base, hi = min(h1, base + t.H) - base;
+      if (lo >= hi) continue;
+      float w[NE];
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        w[i] = !t.w ? 1.f : (p.w_f32 ? static_cast<const float*>(t.w)[column(i)]
+                                     : rope_f(static_cast<const T*>(t.w)[column(i)]));
+      const T* xp = static_cast<const T*>(t.x) + b * t.x_b + n * t.x_n + chunk * E;
+      const T* dp = static_cast<const T*>(t.dy) + b * t.dy_b + n * t.dy_n + chunk * E;
+      T* op = static_cast<T*>(t.out) + b * t.out_b + n * t.out_n + chunk * E;
+      for (int h = lo; h < hi; h += BATCH) {
+        Vec xv[BATCH][PIECES], dv[BACK ? BATCH : 1][PIECES];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+          const long long hh = min(h + u, hi - 1);  // (past the end: the last head again, not written)
+#pragma unroll
+          for (int k = 0; k < PIECES; ++k) {
+            xv[u][k].load(xp + hh * t.x_h + k * (D / 2));
+            if constexpr (BACK) dv[u][k].load(dp + hh * t.dy_h + k * (D / 2));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+          float x[NE], y[NE];
+          float sq = 0.f, along = 0.f;
+#pragma unroll
+          for (int i = 0; i < NE; ++i) {
+            x[i] = rope_f(xv[u][i / E].v[i % E]);
+            sq = fmaf(x[i], x[i], sq);
+          }
+          if constexpr (BACK) {
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+              const int i0 = HALVES ? j : 2 * j, i1 = HALVES ? E + j : 2 * j + 1;
+              const float d0 = rope_f(dv[u][i0 / E].v[i0 % E]), d1 = rope_f(dv[u][i1 / E].v[i1 % E]);
+              y[i0] = d0 * c[j] + d1 * s[j];  // g
+              y[i1] = d1 * c[j] - d0 * s[j];
+              along = fmaf(y[i0] * w[i0], x[i0], along);
+              along = fmaf(y[i1] * w[i1], x[i1], along);
+            }
+            along = norm_row_sum<CHUNKS>(along);
+          }
+          sq = norm_row_sum<CHUNKS>(sq);
+          const float r = rsqrtf(fmaf(sq, 1.f / D, p.eps));
+          if constexpr (BACK) {
+            const float mean = along * r * (1.f / D);
+            const bool count = live && h + u < hi;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+              const float nrm = x[i] * r;
+              if (count) acc[ti][i] = fmaf(y[i], nrm, acc[ti][i]);
+              y[i] = r * (y[i] * w[i] - nrm * mean);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+              const int i0 = HALVES ? j : 2 * j, i1 = HALVES ? E + j : 2 * j + 1;
+              const float a = x[i0] * r * w[i0], e = x[i1] * r * w[i1];
+              y[i0] = a * c[j] - e * s[j];
+              y[i1] = a * s[j] + e * c[j];
+            }
+          }
+          if (live && h + u < hi) {
+#pragma unroll
+            for (int k = 0; k < PIECES; ++k) {
+              Vec o;
+#pragma unroll
+              for (int i = 0; i < E; ++i) o.v[i] = rope_t<T>(y[k * E + i]);
+              o.store(op + (long long)(h + u) * t.out_h + k * (D / 2));
+            }
+          }
+        }
+      }
+    }
+  }
+  if constexpr (BACK) {
+    if (p.part == nullptr) return;
+    // The warp's rows, then the block's warps, in a fixed order.
+    __shared__ float sum[kNormThreads / 32][2][D];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+    for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        float v = acc[ti][i];
+#pragma unroll
+        for (int m = CHUNKS; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        if (lane < CHUNKS) sum[warp][ti][column(i)] = v;
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += kNormThreads) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < kNormThreads / 32; ++k) v += (&sum[k][0][0])[i];
+      p.part[(long long)blockIdx.x * 2 * D + i] = v;
+    }
+  }
+}
+
+// Weights' gradients from the blocks' partial sums [rows][2][D]: a block of 32
+// columns x kNormReduceRows rows of threads.
+static __global__ void __launch_bounds__(32 * kNormReduceRows)
+    fa_norm_weight_kernel(const float* part, int rows, int D, float* dwq, float* dwk) {
+  __shared__ float sum[kNormReduceRows][32];
+  const int lane = threadIdx.x % 32, row = threadIdx.x / 32;
+  const int i = blockIdx.x * 32 + lane;  // of 2 D
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are there
+  float v = 0.f;
+  for (int k = row; k < rows; k += kNormReduceRows) v += part[(long long)k * 2 * D + i];
+  sum[row][lane] = v;
+  __syncthreads();
+  if (row == 0) {
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kNormReduceRows; ++k) v += sum[k][lane];
+    float* out = i < D ? dwq : dwk;
+    if (out) out[i < D ? i : i - D] = v;
+  }
+}
+
+}  // namespace fa
