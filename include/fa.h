@@ -372,6 +372,47 @@ FA_API int fa_norm_rope_bwd(const fa_rope_axes* axes, const fa_norm* norm, const
 FA_API size_t fa_norm_rope_workspace_bytes(int D);
 
 /*
+ * fa_bwd — gradients of the attention forward (fa_fwd, fa_fwd_ex) with respect
+ * to q, k and v, from what it left:
+ *   P = exp(scale Q K^T + mask - LSE),  delta_i = dO_i . O_i - dLSE_i,
+ *   dS = P o (dO V^T - delta),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
+ * The probabilities are recomputed tile by tile and never reach device memory.
+ *
+ *   dout, q, out  bf16 [B, Hq, Nq, D]: the gradient of O, the queries, O
+ *   k, v          bf16 [B, Hk, Nk, D]; Hq is a multiple of Hk: query head h reads key
+ *                 head h / (Hq / Hk) (the forward takes such keys repeated), whose
+ *                 gradients are the sums over its query heads
+ *   lse           device fp32 [B, Hq, Nq], contiguous, the forward's
+ *   dlse          the gradient of LSE, as lse, or NULL (zero)
+ *   mask, causal  as fa_fwd_ex's (a mask of `heads` 1 or Hq); they have no gradient
+ *   dq, dk, dv    bf16, as q, k, v: written whole
+ *   workspace     device scratch, 16-byte aligned, at least
+ *                 fa_bwd_workspace_bytes(...) bytes, not shared with a concurrent call
+ *
+ * All tensors may have any strides (slices of token-major buffers) whose rows
+ * start 16-byte aligned; no axis is broadcast (stride 0).  Results share no
+ * element with the other tensors or each other (tensors of two lengths: no range).
+ *
+ * A row that sees no key (LSE = -inf) has no gradient: its dQ is 0 and it adds
+ * nothing to dK and dV; keys that no row sees have dK = dV = 0.  P and dS are
+ * rounded to bf16 for the products that take them; everything else is fp32, in a
+ * fixed order: results repeat bit for bit on one GPU.  Numbers in q, k, v, out or
+ * dout that are not finite, in masked places too, may turn any gradient of
+ * their heads into NaN.
+ *
+ * Three kernels are enqueued on `stream`, and one more for each of the last two
+ * whose units were cut to fill the GPU.  Errors as fa_fwd_ex, waits that ran out
+ * included (FA_ERR_TIMEOUT in the device status word).
+ */
+FA_API int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const fa_tensor* v,
+                  const fa_tensor* out, const float* lse, const float* dlse, const fa_mask* mask, int causal,
+                  const fa_tensor* dq, const fa_tensor* dk, const fa_tensor* dv, int B, int Hq, int Hk, int Nq,
+                  int Nk, int D, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes fa_bwd needs (0 for invalid sizes). */
+FA_API size_t fa_bwd_workspace_bytes(int B, int Hq, int Hk, int Nq, int Nk, int D);
+
+/*
  * A paged key/value cache in 8 bits.  A page holds page_tokens consecutive
  * tokens of a sequence for every head; which pages a sequence owns, in order,
  * is the caller's int32 table [B, table_width].

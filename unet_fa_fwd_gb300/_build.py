@@ -2,11 +2,12 @@
 
 ``libfa_fwd.so`` (release) and ``libfa_fwd_debug.so`` (the same sources with
 ``-DFA_DEBUG``: device-side bounds and schedule checks that record a violation
-instead of making the access).  Each is six translation units (the C ABI and
+instead of making the access).  Each is eleven translation units (the C ABI and
 helper kernels in ``fa_fwd.cu``, the rotary and cache operators in
-``fa_cache.cu`` and ``fa_cache_chunk.cu``, the attention kernel's instantiations per head
-dimension in ``fa_attn_d32.cu`` / ``fa_attn_d64.cu`` / ``fa_attn_d128.cu``);
-all twelve objects are compiled in parallel, then each library is linked with
+``fa_cache.cu`` and ``fa_cache_chunk.cu``, the norm with rotary positions in
+``fa_norm.cu``, the attention gradient's C ABI in ``fa_bwd.cu``, the attention
+kernel's and its gradient's instantiations per head dimension in
+``fa_attn_d*.cu`` and ``fa_bwd_d*.cu``); all objects are compiled in parallel, then each library is linked with
 the static CUDA runtime.  There is no link-time dependency on the driver
 library (the tensor-map encoder is looked up at run time).
 """
@@ -25,7 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfa_fwd.so")
 LIB_DEBUG = os.path.join(PKG, "libfa_fwd_debug.so")
 OBJ_DIR = os.path.join(PKG, "_build")
-UNITS = ["fa_fwd.cu", "fa_cache.cu", "fa_cache_chunk.cu", "fa_norm.cu", "fa_attn_d32.cu", "fa_attn_d64.cu", "fa_attn_d128.cu"]
+UNITS = ["fa_fwd.cu", "fa_cache.cu", "fa_cache_chunk.cu", "fa_norm.cu", "fa_bwd.cu", "fa_attn_d32.cu", "fa_attn_d64.cu",
+         "fa_attn_d128.cu", "fa_bwd_d32.cu", "fa_bwd_d64.cu", "fa_bwd_d128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,6 +1,6 @@
-"""What training an attention layer needs around the forward: the norm of queries
-and keys for each head with the rotary positions in the same pass, and its gradient:
-argument marshalling into ``include/fa.h``, as :mod:`.binding` and :mod:`.cache`.
+"""What training an attention layer needs around the forward: the attention's
+gradient, and the norm of queries and keys for each head with the rotary positions
+in the same pass, with its gradient: argument marshalling into ``include/fa.h``, as :mod:`.binding` and :mod:`.cache`.
 
 Autograd records none of these calls; the gradients are calls of their own::
 
@@ -14,15 +14,18 @@ Outputs and workspaces are allocated on the stream that the call runs on.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
-from .binding import FA_OK, FaNorm, load_library
-from .cache import (_DTYPES, _F32, _PAIRINGS, _SIZE, RopeAxes, _bhnd, _exact, _given, _positions, _raise, _rope_new,
+from .binding import (FA_MASK_ADDITIVE, FA_MASK_BOOL, FA_MASK_KEY_PADDING, FA_OK, FaMask, FaNorm,
+                      load_library)
+from .cache import (_BF16, _DTYPES, _F32, _PAIRINGS, _SIZE, RopeAxes, _bhnd, _exact, _given, _positions, _raise, _rope_new,
                     _run, _strided)
 
-# Six fa_tensor structs side by side (pointer and three strides each).
+# Six and eight fa_tensor structs side by side (pointer and three strides each).
 _Tensors6 = ctypes.c_longlong * 24
+_Tensors8 = ctypes.c_longlong * 32
 
 
 def _norm(q, k, q_weight, k_weight, eps, device) -> FaNorm:
@@ -178,3 +181,81 @@ def norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Tensor, k:
     _bhnd(q, "q")
     return _run(q, stream, _norm_rope_bwd, dq, dk, q, k, pos, axes, q_weight, k_weight, eps, None, None, None, None,
                 None, True, token_major, pairing)
+
+
+def bwd_workspace_bytes(B: int, Hq: int, Hk: int, Nq: int, Nk: int, D: int) -> int:
+    return int(load_library().fa_bwd_workspace_bytes(B, Hq, Hk, Nq, Nk, D))
+
+
+def _mask(key_mask, full_mask, B, Hq, Nq, Nk, device):
+    if key_mask is not None and full_mask is not None:
+        raise ValueError("pass key_mask or full_mask, not both")
+    if key_mask is not None:
+        return ctypes.byref(FaMask(FA_MASK_KEY_PADDING, _exact(key_mask, "key_mask", _F32, (B, Nk), device), 1))
+    if full_mask is None:
+        return None
+    if full_mask.dim() != 4 or full_mask.shape[1] not in (1, Hq):
+        raise ValueError("full_mask must be [B, 1|Hq, Nq, Nk]")
+    if full_mask.dtype not in (_F32, torch.bool, torch.uint8):
+        raise TypeError("full_mask must be float32 (additive) or bool/uint8")
+    heads = full_mask.shape[1]
+    at = _exact(full_mask, "full_mask", full_mask.dtype, (B, heads, Nq, Nk), device)
+    return ctypes.byref(FaMask(FA_MASK_ADDITIVE if full_mask.dtype is _F32 else FA_MASK_BOOL, at, heads))
+
+
+def _bwd(dout, q, k, v, out, lse, dlse, key_mask, full_mask, causal, scale, dq, dk, dv, workspace, new, token_major,
+         device, handle):
+    B, Hq, Nq, D = q_shape = _bhnd(q, "q")
+    Hk, Nk = _bhnd(k, "k")[1:3]
+    k_shape = (B, Hk, Nk, D)
+    fields = ()
+    for t, name, shape in ((dout, "dout", q_shape), (q, "q", q_shape), (k, "k", k_shape), (v, "v", k_shape),
+                           (out, "out", q_shape)):
+        fields += _strided(t, name, _BF16, shape, device)
+    lib = load_library()
+    if new:
+        dq, dk, dv = (_rope_new(shape, _BF16, q.device, token_major) for shape in (q_shape, k_shape, k_shape))
+        workspace = torch.empty(lib.fa_bwd_workspace_bytes(B, Hq, Hk, Nq, Nk, D), dtype=torch.uint8, device=q.device)
+        for t in (dq, dk, dv):
+            fields += (t.data_ptr(), *t.stride()[:3])
+    else:
+        for t, name, shape in ((dq, "dq", q_shape), (dk, "dk", k_shape), (dv, "dv", k_shape)):
+            fields += _strided(t, name, _BF16, shape, device)
+    lse_at = _exact(lse, "lse", _F32, (B, Hq, Nq), device)
+    dlse_at = None if dlse is None else _exact(dlse, "dlse", _F32, (B, Hq, Nq), device)
+    ws_ptr, ws_bytes = _workspace(workspace, device)
+    ts = _Tensors8(*fields)
+    at = ctypes.addressof(ts)
+    rc = lib.fa_bwd(*(at + i * _SIZE for i in range(5)), lse_at, dlse_at,
+                    _mask(key_mask, full_mask, B, Hq, Nq, Nk, device), causal,
+                    *(at + i * _SIZE for i in range(5, 8)), B, Hq, Hk, Nq, Nk, D,
+                    1.0 / math.sqrt(D) if scale is None else scale, ws_ptr, ws_bytes, handle)
+    if rc != FA_OK:
+        _raise("fa_bwd", rc)
+    return dq, dk, dv
+
+
+def fa_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+           lse: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, workspace: torch.Tensor,
+           key_mask: torch.Tensor | None = None, full_mask: torch.Tensor | None = None, causal: bool = False,
+           scale: float | None = None, dlse: torch.Tensor | None = None, stream=None) -> None:
+    """Enqueue the attention's gradient into caller-provided ``dq``, ``dk``, ``dv`` (any strides whose rows start
+    16-byte aligned); ``workspace`` holds bwd_workspace_bytes(...) bytes."""
+    for t, name in ((dq, "dq"), (dk, "dk"), (dv, "dv"), (workspace, "workspace")):
+        _given(t, name)
+    _run(q, stream, _bwd, dout, q, k, v, out, lse, dlse, key_mask, full_mask, bool(causal), scale, dq, dk, dv,
+         workspace, False, False)
+
+
+def bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+        key_mask: torch.Tensor | None = None, full_mask: torch.Tensor | None = None, causal: bool = False,
+        scale: float | None = None, dlse: torch.Tensor | None = None, token_major: bool = False, stream=None):
+    """Allocate outputs and workspace and compute the gradients of :func:`~unet_fa_fwd_gb300.fwd` and
+    :func:`~unet_fa_fwd_gb300.fwd_ex` from what they were given and returned: ``dout`` (and ``dlse``) are the
+    gradients of O (and LSE).  bf16 [B, H, N, D] tensors of any strides whose rows start 16-byte aligned; k and v
+    may have fewer heads than q (shared by neighbouring query heads, whose gradients add up).  Masks as
+    fwd_ex's.  Returns (dq, dk, dv), contiguous or with ``token_major`` views of contiguous [B, N, H, D] tensors.
+    Autograd does not record the call."""
+    _bhnd(q, "q")
+    return _run(q, stream, _bwd, dout, q, k, v, out, lse, dlse, key_mask, full_mask, bool(causal), scale, None, None,
+                None, None, True, token_major)
