@@ -400,8 +400,8 @@ FA_API size_t fa_norm_rope_workspace_bytes(int D);
  * dout that are not finite, in masked places too, may turn any gradient of
  * their heads into NaN.
  *
- * Three kernels are enqueued on `stream`, and one more for each of the last two
- * whose units were cut to fill the GPU.  Errors as fa_fwd_ex, waits that ran out
+ * Two kernels are enqueued on `stream`, one ahead of them for a boolean mask and one
+ * after them where units were cut to fill the GPU.  Errors as fa_fwd_ex, waits that ran out
  * included (FA_ERR_TIMEOUT in the device status word).
  */
 FA_API int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const fa_tensor* v,
@@ -409,8 +409,9 @@ FA_API int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k,
                   const fa_tensor* dq, const fa_tensor* dk, const fa_tensor* dv, int B, int Hq, int Hk, int Nq,
                   int Nk, int D, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes fa_bwd needs (0 for invalid sizes). */
-FA_API size_t fa_bwd_workspace_bytes(int B, int Hq, int Hk, int Nq, int Nk, int D);
+/* Workspace bytes fa_bwd needs (0 for invalid sizes).  bool_mask_heads: `heads` of a
+ * boolean mask, which is kept there as bits; 0 for any other mask. */
+FA_API size_t fa_bwd_workspace_bytes(int B, int Hq, int Hk, int Nq, int Nk, int D, int bool_mask_heads);
 
 /*
  * A paged key/value cache in 8 bits.  A page holds page_tokens consecutive

@@ -109,7 +109,7 @@ def load_library() -> ctypes.CDLL:
             ll = ctypes.c_longlong
             lib.fa_bwd.argtypes = [vp] * 8 + [i32] + [vp] * 3 + [i32] * 6 + [f32, vp, sz, vp]
             lib.fa_bwd.restype = i32
-            lib.fa_bwd_workspace_bytes.argtypes = [i32] * 6
+            lib.fa_bwd_workspace_bytes.argtypes = [i32] * 7
             lib.fa_bwd_workspace_bytes.restype = sz
             lib.fa_norm_rope.argtypes = [vp, vp, vp, ll, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, vp]
             lib.fa_norm_rope.restype = i32

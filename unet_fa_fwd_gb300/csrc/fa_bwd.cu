@@ -30,6 +30,14 @@ int launch_bwd_prep(const BwdPrepParams& p, int D, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+int launch_bwd_bits(const BwdBitsParams& p, cudaStream_t s) {
+  const long long blocks = (p.blocks + 7) / 8;
+  if (blocks > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
+  log_launch("fa_bwd_bits_kernel grid %lld x 256 threads", blocks);
+  fa_bwd_bits_kernel<<<(unsigned)blocks, 256, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 }  // namespace fa
 
 namespace {
@@ -54,21 +62,30 @@ bool sizes_ok(int B, int Hq, int Hk, int Nq, int Nk, int D) {
          qt * 128 <= most && kt * 128 <= most;
 }
 
+// Sizes of a full mask that the entry points take.
+bool mask_ok(int B, int Hq, int Nq, int Nk, int heads) {
+  return (heads == 1 || heads == Hq) && (__int128)B * heads * Nq * Nk <= ((__int128)1 << 58);
+}
+
 // The workspace, in order (each part 256-byte aligned).  Partial sums are for
-// the most CTAs a plan has: it does not depend on the GPU.
+// the most CTAs a plan has: it does not depend on the GPU.  bool_heads: heads of
+// a boolean mask (0: no such mask), whose bits are kept by rows and by keys.
 struct Layout {
-  size_t nlse, delta, part_kv, part_q, total;
+  size_t nlse, delta, part_kv, part_q, bits_q, bits_k, total;
 };
 
-Layout layout(int B, int Hq, int Nq, int D) {
-  const size_t rows = (size_t)B * Hq * (((size_t)Nq + 127) / 128 * 128);
+Layout layout(int B, int Hq, int Nq, int Nk, int D, int bool_heads) {
+  const size_t qt = ((size_t)Nq + 127) / 128, kt = ((size_t)Nk + 127) / 128, rows = (size_t)B * Hq * qt * 128;
   const size_t slots = 2 * (size_t)fa::kBwdMaxCtas, tile = 128 * (size_t)D * sizeof(float);
+  const size_t masks = (size_t)B * bool_heads;
   Layout l{};
   size_t off = 0;
   l.nlse = off;     off += align256(rows * sizeof(float));
   l.delta = off;    off += align256(rows * sizeof(float));
   l.part_kv = off;  off += slots * 2 * tile;
-  l.part_q = l.part_kv;  // (dQ's kernel runs after the join of dK and dV)
+  l.part_q = off;   off += slots * tile;
+  l.bits_q = off;   off += align256(masks * Nq * kt * 16);
+  l.bits_k = off;   off += align256(masks * Nk * qt * 16);
   l.total = off;
   return l;
 }
@@ -106,11 +123,11 @@ fa::BwdTensor view(const fa_tensor& t) {
   return fa::BwdTensor{static_cast<__nv_bfloat16*>(t.data), t.stride_b, t.stride_h, t.stride_n};
 }
 
-int launch(const fa::BwdParams& p, int D, bool kv, int mask, int device, cudaStream_t s) {
+int launch(const fa::BwdParams& p, int D, int mask, int device, cudaStream_t s) {
   switch (D) {
-    case 32: return fa::launch_bwd_d32(p, kv, mask, device, s);
-    case 64: return fa::launch_bwd_d64(p, kv, mask, device, s);
-    default: return fa::launch_bwd_d128(p, kv, mask, device, s);
+    case 32: return fa::launch_bwd_d32(p, mask, device, s);
+    case 64: return fa::launch_bwd_d64(p, mask, device, s);
+    default: return fa::launch_bwd_d128(p, mask, device, s);
   }
 }
 
@@ -118,8 +135,10 @@ int launch(const fa::BwdParams& p, int D, bool kv, int mask, int device, cudaStr
 
 extern "C" {
 
-size_t fa_bwd_workspace_bytes(int B, int Hq, int Hk, int Nq, int Nk, int D) {
-  return sizes_ok(B, Hq, Hk, Nq, Nk, D) ? layout(B, Hq, Nq, D).total : 0;
+size_t fa_bwd_workspace_bytes(int B, int Hq, int Hk, int Nq, int Nk, int D, int bool_mask_heads) {
+  if (!sizes_ok(B, Hq, Hk, Nq, Nk, D)) return 0;
+  if (bool_mask_heads != 0 && !mask_ok(B, Hq, Nq, Nk, bool_mask_heads)) return 0;
+  return layout(B, Hq, Nq, Nk, D, bool_mask_heads).total;
 }
 
 int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa_tensor* out,
@@ -153,16 +172,14 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
       mask_bytes = (size_t)B * Nk * 4;
     } else if (kind == FA_MASK_ADDITIVE || kind == FA_MASK_BOOL) {
       mask_heads = mask->heads;
-      if (mask_heads != 1 && mask_heads != Hq) return FA_ERR_INVALID_ARGUMENT;
-      const __int128 n = (__int128)B * mask_heads * Nq * Nk;
-      if (n > ((__int128)1 << 58)) return FA_ERR_INVALID_ARGUMENT;
-      mask_bytes = (size_t)n * (kind == FA_MASK_ADDITIVE ? 4 : 1);
+      if (!mask_ok(B, Hq, Nq, Nk, mask_heads)) return FA_ERR_INVALID_ARGUMENT;
+      mask_bytes = (size_t)B * mask_heads * Nq * Nk * (kind == FA_MASK_ADDITIVE ? 4 : 1);
     } else {
       return FA_ERR_INVALID_ARGUMENT;
     }
     if (kind != FA_MASK_BOOL && (reinterpret_cast<uintptr_t>(mask_data) & 3u)) return FA_ERR_INVALID_ARGUMENT;
   }
-  const Layout l = layout(B, Hq, Nq, D);
+  const Layout l = layout(B, Hq, Nq, Nk, D, kind == FA_MASK_BOOL ? mask_heads : 0);
   if (!workspace || !aligned16(workspace) || workspace_bytes < l.total) return FA_ERR_INVALID_ARGUMENT;
   // Results share no element with what is read or with each other, and nothing
   // of the call lies in the workspace.
@@ -224,11 +241,52 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
                  : kind == FA_MASK_ADDITIVE  ? fa::kBwdMaskAdd
                  : kind == FA_MASK_BOOL      ? fa::kBwdMaskBool
                                              : fa::kBwdMaskNone;
-  CUtensorMap mq, mdo, mk_, mv;
-  if (encode(&mq, *q, B, Hq, Nq, D) != FA_OK || encode(&mdo, *dout, B, Hq, Nq, D) != FA_OK ||
-      encode(&mk_, *k, B, Hk, Nk, D) != FA_OK || encode(&mv, *v, B, Hk, Nk, D) != FA_OK)
+  p.mask_vec = Nk % 4 == 0 && aligned16(mask_data);
+  p.bits_q = reinterpret_cast<uint32_t*>(ws + l.bits_q);
+  p.bits_k = reinterpret_cast<uint32_t*>(ws + l.bits_k);
+  p.words_q = kt * 4;
+  p.words_k = qt * 4;
+  p.dq = view(*dq);
+  p.dk = view(*dk);
+  p.dv = view(*dv);
+  p.part[0] = reinterpret_cast<float*>(ws + l.part_kv);
+  p.part[1] = reinterpret_cast<float*>(ws + l.part_q);
+  p.div_hq = fa::FastDiv::make((uint32_t)Hq);
+  p.div_hk = fa::FastDiv::make((uint32_t)Hk);
+  if (encode(&p.q, *q, B, Hq, Nq, D) != FA_OK || encode(&p.dout, *dout, B, Hq, Nq, D) != FA_OK ||
+      encode(&p.k, *k, B, Hk, Nk, D) != FA_OK || encode(&p.v, *v, B, Hk, Nk, D) != FA_OK)
     return FA_ERR_CUDA;
+  for (int kv = 1; kv >= 0; --kv) {
+    fa::BwdUnits u{};
+    u.heads = B * (kv ? Hk : Hq);
+    u.tiles = kv ? kt : qt;
+    u.other = kv ? qt : kt;
+    u.group = kv ? group : 1;
+    u.causal = p.causal;
+    u.rows_q = !kv;
+    // Units of equal weight together where they are causal, unless a head alone
+    // fills the SMs (its tiles then stay in L2).
+    u.spread = p.causal && u.tiles < st->sm_count ? 1 : 0;
+    u.div_heads = fa::FastDiv::make((uint32_t)u.heads);
+    u.div_tiles = fa::FastDiv::make((uint32_t)u.tiles);
+    p.plan[kv ? 0 : 1] = fa::bwd_plan(u, st->sm_count, kJoinCost);
+  }
 
+  if (kind == FA_MASK_BOOL) {
+    fa::BwdBitsParams bp;
+    bp.mask = static_cast<const uint8_t*>(mask_data);
+    bp.bits_q = reinterpret_cast<uint32_t*>(ws + l.bits_q);
+    bp.bits_k = reinterpret_cast<uint32_t*>(ws + l.bits_k);
+    bp.Nq = Nq;
+    bp.Nk = Nk;
+    bp.words_q = p.words_q;
+    bp.words_k = p.words_k;
+    bp.blocks_q = qt * 4;
+    bp.blocks_k = kt;
+    bp.blocks = (long long)B * mask_heads * bp.blocks_q * bp.blocks_k;
+    rc = fa::launch_bwd_bits(bp, s);
+    if (rc != FA_OK) return rc;
+  }
   fa::BwdPrepParams pp;
   std::memset(&pp, 0, sizeof(pp));
   pp.out = view(*out);
@@ -244,33 +302,7 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   pp.div_h = fa::FastDiv::make((uint32_t)Hq);
   rc = fa::launch_bwd_prep(pp, D, s);
   if (rc != FA_OK) return rc;
-
-  for (int kv = 1; kv >= 0; --kv) {
-    fa::BwdUnits u{};
-    u.heads = B * (kv ? Hk : Hq);
-    u.tiles = kv ? kt : qt;
-    u.other = kv ? qt : kt;
-    u.group = kv ? group : 1;
-    u.causal = p.causal;
-    u.rows_q = !kv;
-    // Units of equal weight together where they are causal, unless a head alone
-    // fills the SMs (its tiles then stay in L2).
-    u.spread = p.causal && u.tiles < st->sm_count ? 1 : 0;
-    u.div_heads = fa::FastDiv::make((uint32_t)u.heads);
-    u.div_tiles = fa::FastDiv::make((uint32_t)u.tiles);
-    p.plan = fa::bwd_plan(u, st->sm_count, kJoinCost);
-    p.div_h = fa::FastDiv::make((uint32_t)(kv ? Hk : Hq));
-    p.out0 = view(kv ? *dv : *dq);
-    p.out1 = view(kv ? *dk : *dq);
-    p.part = reinterpret_cast<float*>(ws + (kv ? l.part_kv : l.part_q));
-    p.map[0] = kv ? mk_ : mq;
-    p.map[1] = kv ? mv : mdo;
-    p.map[2] = kv ? mq : mk_;
-    p.map[3] = kv ? mdo : mv;
-    rc = launch(p, D, kv != 0, mk, st->device, s);
-    if (rc != FA_OK) return rc;
-  }
-  return FA_OK;
+  return launch(p, D, mk, st->device, s);
 }
 
 }  // extern "C"

@@ -3,8 +3,8 @@
 
 namespace fa {
 
-int launch_bwd_d32(const BwdParams& prm, bool kv, int mask, int device, cudaStream_t s) {
-  return launch_bwd<32>(prm, kv, mask, device, s);
+int launch_bwd_d32(const BwdParams& prm, int mask, int device, cudaStream_t s) {
+  return launch_bwd<32>(prm, mask, device, s);
 }
 
 }  // namespace fa

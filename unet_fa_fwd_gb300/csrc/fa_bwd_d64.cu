@@ -3,8 +3,8 @@
 
 namespace fa {
 
-int launch_bwd_d64(const BwdParams& prm, bool kv, int mask, int device, cudaStream_t s) {
-  return launch_bwd<64>(prm, kv, mask, device, s);
+int launch_bwd_d64(const BwdParams& prm, int mask, int device, cudaStream_t s) {
+  return launch_bwd<64>(prm, mask, device, s);
 }
 
 }  // namespace fa

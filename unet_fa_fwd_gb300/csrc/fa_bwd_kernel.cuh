@@ -7,19 +7,22 @@
 // P is recomputed from L (no running maximum), so a tile's work is two products
 // into tensor memory, one pass of the threads, and the products of its results.
 //
-// Two kernels, each over units of 128 rows: keys (dK, dV; products S^T, dP^T, dV, dK)
-// and queries (dQ; S, dP, dQ).  Seven products for the five that one kernel
-// would need: such a kernel has to add dQ up in device memory across the key
-// units, whose order changes the result from run to run, and moves 64 KB of it a
-// tile through shared memory or L2 atomics, where it would wait about as long as
-// the two products take (an SM reads 128 bytes a clock of operands: 64 KB for a
-// 128 x 128 x 128 product of shared memory's operands takes as long as the
-// product).  Here every sum stays in tensor memory and results repeat bit for bit.
+// Two kinds of unit, of 128 rows: keys (dK, dV; products S^T, dP^T, dV, dK) and
+// queries (dQ; S, dP, dQ).  Seven products for the five that one kind would need:
+// it would have to add dQ up in device memory across the key units, whose order
+// changes the result from run to run, and move 64 KB of it a tile through shared
+// memory or L2 atomics, where it would wait about as long as the two products
+// take (an SM reads 128 bytes a clock of operands: the 64 KB of a 128 x 128 x 128
+// product whose operands are in shared memory take as long as the product).
+// Here every sum stays in tensor memory and results repeat bit for bit.
 //
-// A CTA (one per SM) of 384 threads:
-//   warps 0-3, 4-7  two warpgroups; a thread has a row of the unit (one lane of
-//                   tensor memory) and half of a tile's 128 columns
-//   warp 8          TMA producer      warp 9  MMA issuer (owns tensor memory)
+// One launch holds both kinds: the first CTAs (one per SM) walk key units, the
+// rest query units, which start as SMs get free.  640 threads a CTA:
+//   warps 0-15   four warpgroups; a thread has a row of the unit (one lane of
+//                tensor memory) and 32 of a tile's 128 columns
+//   warp 16      TMA producer      warp 17  MMA issuer (owns tensor memory)
+// Four warps a sub-partition hide the latency of tensor memory and of the
+// exponentials, which two (64 columns a thread) did not.
 // P and dS go back to tensor memory as bf16, the A operand of the products that
 // take them; both sides' rows are operands K-major for S and dP and MN-major for
 // the gradients, from one copy in shared memory.
@@ -48,48 +51,63 @@ struct BwdTensor {
 };
 
 struct BwdParams {
-  BwdPlan plan;
+  BwdPlan plan[2];  // key units, query units
   int Hq, Hk, group, Nq, Nk, nqp;  // nqp: queries rounded up to whole tiles
   int causal;
   float scale, scale_log2;
   const float* nlse;    // [B Hq][nqp]: -L, -inf for rows that see nothing and rows past Nq
   const float* delta;   // [B Hq][nqp]
-  const void* mask;     // fp32 [B][Nk], or fp32 / uint8 [B][mask_heads][Nq][Nk]
-  int mask_heads, mask_vec;
-  BwdTensor out0, out1;  // dV and dK, or dQ
-  float* part;           // partial sums of cut units
+  const void* mask;     // fp32 [B][Nk] or [B][mask_heads][Nq][Nk]
+  int mask_heads;
+  int mask_vec;         // its rows are 16-byte aligned
+  // Boolean masks as bits (1: the pair is kept), by query rows and by key rows.
+  const uint32_t* bits_q;  // [B][mask_heads][Nq][words_q]
+  const uint32_t* bits_k;  // [B][mask_heads][Nk][words_k]
+  int words_q, words_k;
+  BwdTensor dq, dk, dv;
+  float* part[2];       // partial sums of cut units
   unsigned long long timeout_ns;
   int* status;
   int* debug_record;
   int inject_stall;
-  FastDiv div_h, div_group;  // by the unit side's heads, by group
-  // the unit's rows (0, 1) and the tiles it walks (2, 3): K, V, Q, dO or Q, dO, K, V
-  CUtensorMap map[4];
+  FastDiv div_hq, div_hk, div_group;
+  CUtensorMap q, k, v, dout;
 };
 
-template <int D, bool KV>
+constexpr int kBwdGroups = 4;                    // warpgroups of rows
+constexpr int kBwdWarps = 4 * kBwdGroups;
+constexpr int kBwdCols = 128 / kBwdGroups;       // columns a thread has of a tile
+constexpr int kBwdThreads = 32 * (kBwdWarps + 4);
+
+template <int D, int MK>
 struct BwdCfg {
   using F = Cfg<D>;
   static constexpr int TILE = 128 * D * 2;  // bytes of a 128-row tile
-  // Rings of the walked tiles.  dK dV: Q (read again by dK, two iterations
-  // long) and dO; dQ: K and V.  At D = 128 the five slots that fit.
-  static constexpr int RING0 = D == 128 ? 3 : 4;
+  // A fp32 mask's values are staged by each warp for itself, MASK_COLS columns at a time.
+  static constexpr int MASK_COLS = MK != kBwdMaskAdd ? 0 : (D == 128 ? 16 : 32);
+  static constexpr int MASK_BYTES = kBwdWarps * 32 * MASK_COLS * 4;
+  // Rings of the walked tiles (key units: Q, read again by dK an iteration
+  // later, and dO; query units: K and V).  At D = 128 the slots that fit.
+  static constexpr int RING0 = D == 128 ? (MK == kBwdMaskAdd ? 2 : 3) : 4;
   static constexpr int RING1 = D == 128 ? 2 : 4;
-  static constexpr int STATS = 2;               // dK dV: slots of -L and delta of 128 queries
-  static constexpr int STAT_BYTES = KV ? 1024 : 0;
+  static constexpr int STAT_BYTES = 2 * 1024;  // key units: two slots of -L and delta of 128 queries
   static constexpr int SMEM_BAR = 512;
-  static constexpr int SMEM_USED = (2 + RING0 + RING1) * TILE + STATS * STAT_BYTES + SMEM_BAR;
+  static constexpr int SMEM_USED = (2 + RING0 + RING1) * TILE + STAT_BYTES + MASK_BYTES + SMEM_BAR;
   // (more than half of the SM's, so that one CTA has its tensor memory alone)
   static constexpr int SMEM_BYTES = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
-  // Tensor memory: accumulators, S (two where they fit), dP.
+  // The launch reserves 96 registers a thread; the rows' warpgroups take from the other.
+  static constexpr int REGS_ROWS = 104, REGS_OTHER = 64;
+  static_assert(128 * kBwdGroups * REGS_ROWS + 128 * REGS_OTHER <= kBwdThreads * 96, "register split");
+};
+
+// Tensor memory of a kind of unit: accumulators, S (two where they fit), dP.
+template <int D, bool KV>
+struct BwdCols {
   static constexpr int ACC = KV ? 2 * D : D;
   static constexpr int NS = ACC + 3 * 128 <= 512 ? 2 : 1;
-  static constexpr int COL_S = ACC, COL_DP = ACC + NS * 128;
-  static_assert(COL_DP + 128 <= 512, "tensor-memory columns");
-  static constexpr int THREADS = 384;
-  static constexpr int REGS_ROWS = 208, REGS_OTHER = 88;
-  static_assert(2 * 128 * REGS_ROWS + 128 * REGS_OTHER <= THREADS * 168, "register split");
+  static constexpr int S = ACC, DP = ACC + NS * 128;
+  static_assert(DP + 128 <= 512, "tensor-memory columns");
 };
 
 constexpr int kBwdMaxRing = 4;
@@ -173,14 +191,13 @@ __device__ __forceinline__ void bwd_mma_scores(uint32_t d, uint32_t a_lo, uint32
     ptx::mma_ss_x2_el<C::s_off(1)>(d, a_lo, hi, b_lo, hi, IDESC, 0);
 }
 
-// acc += X T: X bf16 in tensor memory (64 columns' worth at x, the other half
-// at x + 64), T a 128-row tile, MN-major.
+// acc += X T: X bf16 in tensor memory, each warpgroup's 32 columns at the start
+// of the 32 that they were computed from; T a 128-row tile, MN-major.
 template <int D>
 __device__ __forceinline__ void bwd_mma_grad(uint32_t acc, uint32_t x, uint32_t t_lo, uint32_t t_hi, bool first) {
   constexpr uint32_t IDESC = make_idesc(128, D, true);
   constexpr uint32_t STEP = (16 * Cfg<D>::SW) >> 4;
-  ptx::mma_ts_x4_el<STEP>(acc, x, t_lo, t_hi, IDESC, first ? 0u : 1u);
-  ptx::mma_ts_x4_el<STEP>(acc, x + 64, t_lo + 4 * STEP, t_hi, IDESC, 1u);
+  ptx::mma_ts_x8_by2_el<STEP>(acc, x, t_lo, t_hi, IDESC, first ? 0u : 1u);
 }
 
 template <int D>
@@ -192,19 +209,77 @@ __device__ __forceinline__ void bwd_load_tile(uint32_t dst, const CUtensorMap* m
     ptx::tma_load_4d(dst + c * C::CHUNK_BYTES, map, bar, c * C::CHUNK_ELEMS, row, h, b);
 }
 
-// Mask values of 32 columns of a thread's row, as what is added to t (log2
-// domain; -inf: excluded).  at(c): the address of column c's value.
-template <int MK, typename At>
-__device__ __forceinline__ void bwd_mask32(float (&m)[32], At at) {
-  constexpr float kLog2e = 1.4426950408889634f;
+// Staging of a fp32 mask [rows][Nk]: a warp copies the values of its 32 rows and
+// SC columns of a tile into `buf` (its own), for itself.  Key units (KV): a
+// thread's row is a key and columns are queries, kept as [SC][32]; query units: a
+// row's SC values together, 16-byte pieces swizzled so that the lanes' reads of
+// their rows do not meet.  Values outside the mask read 0.
+template <bool KV, int SC>
+struct BwdStage {
+  static constexpr int PIECES = SC / 4;
+  static __device__ __forceinline__ int swizzle(int r) { return SC == 32 ? (r & 7) : ((r >> 1) & 3); }
+  static __device__ __forceinline__ void copy(uint32_t buf, const float* base, int row0, int col0, int Nq, int Nk,
+                                              int vec, int lane) {
+    const int q0 = KV ? col0 : row0, k0 = KV ? row0 : col0;
+    if (vec) {
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    if constexpr (MK == kBwdMaskBool)
-      m[c] = __ldg(static_cast<const uint8_t*>(static_cast<const void*>(at(c)))) ? 0.f : -INFINITY;
-    else
-      m[c] = __ldg(static_cast<const float*>(static_cast<const void*>(at(c)))) * kLog2e;
+      for (int i = 0; i < PIECES; ++i) {
+        int q, k;
+        uint32_t dst;
+        if constexpr (KV) {
+          const int c = 4 * i + lane / 8, g = lane % 8;
+          q = q0 + c;
+          k = k0 + 4 * g;
+          dst = buf + (c * 32 + 4 * g) * 4;
+        } else {
+          const int r = i * (32 / PIECES) + lane / PIECES, g = lane % PIECES;
+          q = q0 + r;
+          k = k0 + 4 * g;
+          dst = buf + r * SC * 4 + ((g ^ swizzle(r)) << 4);
+        }
+        const bool in = q < Nq && k < Nk;  // (Nk is a multiple of 4)
+        const float* src = in ? base + (size_t)q * Nk + k : base;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+      }
+    } else {
+#pragma unroll 8
+      for (int i = 0; i < SC; ++i) {
+        int q, k;
+        uint32_t dst;
+        if constexpr (KV) {
+          q = q0 + i;
+          k = k0 + lane;
+          dst = buf + (i * 32 + lane) * 4;
+        } else {
+          const int r = i * (32 / SC) + lane / SC, c = lane % SC;
+          q = q0 + r;
+          k = k0 + c;
+          dst = buf + r * SC * 4 + (((c / 4) ^ swizzle(r)) << 4) + (c % 4) * 4;
+        }
+        const bool in = q < Nq && k < Nk;
+        const float* src = in ? base + (size_t)q * Nk + k : base;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+      }
+    }
   }
-}
+  // 16 columns from c0 of the lane's row, times log2(e).
+  static __device__ __forceinline__ void read(const float* buf, int c0, int lane, float (&m)[16]) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    if constexpr (KV) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) m[c] = buf[(c0 + c) * 32 + lane] * kLog2e;
+    } else {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float4 v = *reinterpret_cast<const float4*>(buf + lane * SC + (((c0 / 4 + g) ^ swizzle(lane)) << 2));
+        m[4 * g] = v.x * kLog2e;
+        m[4 * g + 1] = v.y * kLog2e;
+        m[4 * g + 2] = v.z * kLog2e;
+        m[4 * g + 3] = v.w * kLog2e;
+      }
+    }
+  }
+};
 
 // 2^(s sl2 + add) of a pair.
 __device__ __forceinline__ float2 bwd_exp(float s0, float s1, float sl2, float2 add) {
@@ -212,41 +287,36 @@ __device__ __forceinline__ float2 bwd_exp(float s0, float s1, float sl2, float2 
   return make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
 }
 
-// The columns [0, D) of a thread's accumulator row at `t`, NC of them, times
-// `mul`, rounded to the row at `dst` (16-byte aligned), or as they are to a slot
-// of partial sums (laid out [columns / 4][128 rows][4]).
+// NC columns of a thread's accumulator row at `t`, times `mul`, rounded to `dst`
+// (16-byte aligned), or as they are to a slot of partial sums (laid out
+// [columns / 4][128 rows][4]).
 template <int NC>
 __device__ __forceinline__ void bwd_store_row(uint32_t t, float mul, bool zero, bool ok, __nv_bfloat16* dst) {
 #pragma unroll
-  for (int cb = 0; cb < NC; cb += 16) {
-    uint32_t r[16];
+  for (int cb = 0; cb < NC; cb += 8) {
+    uint32_t r[8];
     if (zero) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) r[i] = 0u;
+      for (int i = 0; i < 8; ++i) r[i] = 0u;
     } else {
-      ptx::tmem_ld32x32b_x16(t + cb, r);
+      ptx::tmem_ld32x32b_x8(t + cb, r);
     }
-    if (ok) {
+    uint32_t w[4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = ptx::pack_bf16x2(__uint_as_float(r[8 * q + 2 * i]) * mul, __uint_as_float(r[8 * q + 2 * i + 1]) * mul);
-        *reinterpret_cast<uint4*>(dst + cb + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
+    for (int i = 0; i < 4; ++i)
+      w[i] = ptx::pack_bf16x2(__uint_as_float(r[2 * i]) * mul, __uint_as_float(r[2 * i + 1]) * mul);
+    if (ok) *reinterpret_cast<uint4*>(dst + cb) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 template <int NC>
 __device__ __forceinline__ void bwd_store_part(uint32_t t, bool ok, float* dst, int row) {
 #pragma unroll
-  for (int cb = 0; cb < NC; cb += 16) {
-    uint32_t r[16];
-    ptx::tmem_ld32x32b_x16(t + cb, r);
+  for (int cb = 0; cb < NC; cb += 8) {
+    uint32_t r[8];
+    ptx::tmem_ld32x32b_x8(t + cb, r);
     if (ok) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 2; ++q)
         *reinterpret_cast<uint4*>(dst + ((size_t)(cb / 4 + q) * 128 + row) * 4) =
             make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
     }
@@ -271,98 +341,70 @@ struct BwdIter {
   }
 };
 
-// KV: dK and dV of 128 keys; else dQ of 128 queries.
+// A CTA's units of one kind: dK and dV of 128 keys (KV), or dQ of 128 queries.
 template <int D, int MK, bool KV>
-__global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const __grid_constant__ BwdParams p) {
-  using C = BwdCfg<D, KV>;
+__device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* smem, BwdBars* bars, uint32_t tmem) {
+  using C = BwdCfg<D, MK>;
+  using T = BwdCols<D, KV>;
   using F = Cfg<D>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sA = smem;
+  const BwdPlan& plan = p.plan[KV ? 0 : 1];
+  uint8_t* sA = smem;  // the unit's rows: K and V, or Q and dO
   uint8_t* sB = sA + C::TILE;
-  uint8_t* sR0 = sB + C::TILE;
+  uint8_t* sR0 = sB + C::TILE;  // the tiles it walks
   uint8_t* sR1 = sR0 + C::RING0 * C::TILE;
   float* sStat = reinterpret_cast<float*>(sR1 + C::RING1 * C::TILE);
-  BwdBars* bars = reinterpret_cast<BwdBars*>(sR1 + C::RING1 * C::TILE + C::STATS * C::STAT_BYTES);
   const int warp = threadIdx.x / 32;
   const uint32_t lane = threadIdx.x % 32;
-
-  if (ptx::smem_u32(smem) & 1023u) {  // (the swizzled layouts need it; dynamic shared memory starts there)
-    if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusTimeout);
-    return;
-  }
-  if (threadIdx.x == 0) {
-    auto init = [](uint64_t& b, uint32_t n) { ptx::mbar_init(ptx::smem_u32(&b), n); };
-    init(bars->a_full, 1);
-    init(bars->a_empty, 1);
-    init(bars->b_full, 1);
-    init(bars->b_empty, 1);
-    for (int i = 0; i < C::RING0; ++i) init(bars->r0_full[i], 1), init(bars->r0_empty[i], 1);
-    for (int i = 0; i < C::RING1; ++i) init(bars->r1_full[i], 1), init(bars->r1_empty[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      init(bars->st_full[i], 1);
-      init(bars->st_empty[i], 8);
-      init(bars->s_full[i], 1);
-      init(bars->p_ready[i], 8);
-      init(bars->ds_ready[i], 8);
-    }
-    init(bars->dp_full, 1);
-    init(bars->dp_free, 8);
-    init(bars->acc_full, 1);
-    init(bars->drain, 1);
-    bars->abort_flag = 0;
-    ptx::fence_barrier_init();
-  }
-  if (warp == 9) {
-    ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), 512);
-    ptx::tmem_relinquish();
-  }
-  ptx::tc_fence_before_sync();
-  __syncthreads();
-  ptx::tc_fence_after_sync();
-  const uint32_t tmem = bars->tmem_base;
   auto finish = [&]() {
-    ptx::named_barrier_sync(1, C::THREADS);
-    if (warp == 9) {
+    ptx::named_barrier_sync(1, kBwdThreads);
+    if (warp == kBwdWarps + 1) {
       ptx::tc_fence_after_sync();
       ptx::tmem_dealloc(tmem, 512);
     }
   };
   auto piece_ok = [&](const BwdPiece& pc) {
-    return bwd_check(p, bars, pc.head >= 0 && pc.head < p.plan.units.heads && pc.tile >= 0 &&
-                                  pc.tile < p.plan.units.tiles && pc.it0 >= 0 &&
-                                  pc.it1 <= p.plan.units.iterations(pc.tile) && pc.it0 <= pc.it1,
+    return bwd_check(p, bars, pc.head >= 0 && pc.head < plan.units.heads && pc.tile >= 0 &&
+                                  pc.tile < plan.units.tiles && pc.it0 >= 0 &&
+                                  pc.it1 <= plan.units.iterations(pc.tile) && pc.it0 <= pc.it1,
                      kCheckGradUnit, pc.head, pc.tile);
   };
+  const int heads = KV ? p.Hk : p.Hq;
+  const FastDiv& div_h = KV ? p.div_hk : p.div_hq;
 
-  if (warp >= 8) {
+  if (warp >= kBwdWarps) {
     ptx::setmaxnreg_dec<C::REGS_OTHER>();
-    if (warp == 8) {
+    if (warp == kBwdWarps) {
       // ---------------------------------------------------------- producer --
       if (lane == 0) {
-        for (int i = 0; i < 4; ++i) ptx::tma_prefetch_desc(&p.map[i]);
+        const CUtensorMap *mA = KV ? &p.k : &p.q, *mB = KV ? &p.v : &p.dout;
+        const CUtensorMap *m0 = KV ? &p.q : &p.k, *m1 = KV ? &p.dout : &p.v;
+        ptx::tma_prefetch_desc(mA);
+        ptx::tma_prefetch_desc(m0);
+        ptx::tma_prefetch_desc(mB);
+        ptx::tma_prefetch_desc(m1);
         uint32_t na = 0, nb = 0, j = 0;  // tiles of the unit's rows, iterations begun
         uint32_t n0 = 0, n1 = 0, nst = 0;  // copies issued to each ring
         bool ok = true;
         BwdWalk walk;
         BwdPiece pc;
-        while (ok && walk.next(p.plan, blockIdx.x, pc)) {
+        while (ok && walk.next(plan, cta, pc)) {
           if (!piece_ok(pc)) break;
           if (pc.it0 == pc.it1) continue;
-          const int b = (int)p.div_h.div((uint32_t)pc.head), h = pc.head - b * (KV ? p.Hk : p.Hq);
+          const int b = (int)div_h.div((uint32_t)pc.head), h = pc.head - b * heads;
           // heads of the tiles walked: a group of query heads, or the key head
           const int h_other = KV ? h * p.group : (int)p.div_group.div((uint32_t)h);
-          auto load_unit = [&](int i, uint8_t* dst, uint64_t& full, uint64_t& empty, uint32_t& n) {
+          auto load_unit = [&](const CUtensorMap* map, uint8_t* dst, uint64_t& full, uint64_t& empty, uint32_t& n) {
             if (!bwd_wait(empty, (n & 1) ^ 1, bars, p)) return false;
             ptx::mbar_arrive_expect_tx(ptx::smem_u32(&full), C::TILE);
-            bwd_load_tile<D>(ptx::smem_u32(dst), &p.map[i], ptx::smem_u32(&full), pc.tile * 128, h, b);
+            bwd_load_tile<D>(ptx::smem_u32(dst), map, ptx::smem_u32(&full), pc.tile * 128, h, b);
             ++n;
             return true;
           };
           BwdIter at;
-          at.start(p.plan.units, pc.tile, pc.it0);
+          at.start(plan.units, pc.tile, pc.it0);
           for (int it = pc.it0; ok && it < pc.it1; ++it, ++j, at.next()) {
             const int ho = h_other + (KV ? at.g : 0);
-            if (it == pc.it0) ok = load_unit(0, sA, bars->a_full, bars->a_empty, na);
+            if (it == pc.it0) ok = load_unit(mA, sA, bars->a_full, bars->a_empty, na);
             if (!ok) break;
             const uint32_t s0 = j % C::RING0, s1 = j % C::RING1;
             ok = bwd_wait(bars->r0_empty[s0], ((j / C::RING0) & 1) ^ 1, bars, p);
@@ -373,9 +415,9 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
             }
             uint32_t full = ptx::smem_u32(&bars->r0_full[s0]);
             ptx::mbar_arrive_expect_tx(full, C::TILE);
-            bwd_load_tile<D>(ptx::smem_u32(sR0 + s0 * C::TILE), &p.map[2], full, at.tile * 128, ho, b);
+            bwd_load_tile<D>(ptx::smem_u32(sR0 + s0 * C::TILE), m0, full, at.tile * 128, ho, b);
             ++n0;
-            if (it == pc.it0) ok = load_unit(1, sB, bars->b_full, bars->b_empty, nb);
+            if (it == pc.it0) ok = load_unit(mB, sB, bars->b_full, bars->b_empty, nb);
             if (!ok) break;
             if constexpr (KV) {
               const uint32_t ss = j & 1;
@@ -392,7 +434,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
             if (!ok) break;
             full = ptx::smem_u32(&bars->r1_full[s1]);
             ptx::mbar_arrive_expect_tx(full, C::TILE);
-            bwd_load_tile<D>(ptx::smem_u32(sR1 + s1 * C::TILE), &p.map[3], full, at.tile * 128, ho, b);
+            bwd_load_tile<D>(ptx::smem_u32(sR1 + s1 * C::TILE), m1, full, at.tile * 128, ho, b);
             ++n1;
           }
         }
@@ -411,7 +453,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
         for (uint32_t s = 0; s < 2; ++s) landed(bars->st_full[s], (nst + 1 - s) / 2);
       }
       __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == kBwdWarps + 1) {
       // --------------------------------------------------------------- MMA --
       // Descriptors: K-major (scores) and MN-major (gradients) views of the tiles.
       const uint64_t k_major = smem_desc(0, 16, F::SBO, F::LAYOUT);
@@ -430,53 +472,53 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
         const uint32_t s = i % C::RING0;
         if (!bwd_wait_warp(bars->r0_full[s], (i / C::RING0) & 1, bars, p)) return false;
         ptx::tc_fence_after_sync();
-        bwd_mma_scores<D>(tmem + C::COL_S + (i % C::NS) * 128, k_lo + a16, k_lo + r0 + s * TILE16, k_hi);
-        commit(bars->s_full[i % C::NS]);
+        bwd_mma_scores<D>(tmem + T::S + (i % T::NS) * 128, k_lo + a16, k_lo + r0 + s * TILE16, k_hi);
+        commit(bars->s_full[i % T::NS]);
         return true;
       };
       auto dprob = [&](uint32_t i) -> bool {
         const uint32_t s = i % C::RING1;
         if (!bwd_wait_warp(bars->r1_full[s], (i / C::RING1) & 1, bars, p)) return false;
         ptx::tc_fence_after_sync();
-        bwd_mma_scores<D>(tmem + C::COL_DP, k_lo + b16, k_lo + r1 + s * TILE16, k_hi);
+        bwd_mma_scores<D>(tmem + T::DP, k_lo + b16, k_lo + r1 + s * TILE16, k_hi);
         commit(bars->dp_full);
         if constexpr (!KV) commit(bars->r1_empty[s]);  // V is not needed again
         return true;
       };
       BwdWalk walk;
       BwdPiece pc;
-      while (ok && walk.next(p.plan, blockIdx.x, pc)) {
+      while (ok && walk.next(plan, cta, pc)) {
         const uint32_t n = (uint32_t)(pc.it1 - pc.it0);
         if (n == 0) continue;
         ok = bwd_wait_warp(bars->a_full, nu & 1, bars, p) && scores(j);
         if (ok && n == 1) commit(bars->a_empty);
         ok = ok && bwd_wait_warp(bars->b_full, nu & 1, bars, p) && dprob(j);
         if (ok && n == 1) commit(bars->b_empty);
-        if (ok && C::NS == 2 && n > 1) {
+        if (ok && T::NS == 2 && n > 1) {
           ok = scores(j + 1);
           if (ok && n == 2) commit(bars->a_empty);
         }
         if (!ok) break;
         for (uint32_t i = 0; ok && i < n; ++i, ++j) {
-          const uint32_t s0 = j % C::RING0, s1 = j % C::RING1, sb = j % C::NS;
-          const uint32_t tS = tmem + C::COL_S + sb * 128;
+          const uint32_t s0 = j % C::RING0, s1 = j % C::RING1, sb = j % T::NS;
+          const uint32_t tS = tmem + T::S + sb * 128;
           if constexpr (KV) {
             // dV += P^T dO
-            ok = bwd_wait_warp(bars->p_ready[sb], (j / C::NS) & 1, bars, p);
+            ok = bwd_wait_warp(bars->p_ready[sb], (j / T::NS) & 1, bars, p);
             if (!ok) break;
             ptx::tc_fence_after_sync();
             bwd_mma_grad<D>(tmem, tS, mn_lo + r1 + s1 * TILE16, mn_hi, i == 0);
             commit(bars->r1_empty[s1]);
-            if (i + C::NS < n) {
-              ok = scores(j + C::NS);
+            if (i + T::NS < n) {
+              ok = scores(j + T::NS);
               if (!ok) break;
-              if (i + C::NS + 1 == n) commit(bars->a_empty);
+              if (i + T::NS + 1 == n) commit(bars->a_empty);
             }
             // dK += dS^T Q
             ok = bwd_wait_warp(bars->ds_ready[0], j & 1, bars, p);
             if (!ok) break;
             ptx::tc_fence_after_sync();
-            bwd_mma_grad<D>(tmem + D, tmem + C::COL_DP, mn_lo + r0 + s0 * TILE16, mn_hi, i == 0);
+            bwd_mma_grad<D>(tmem + D, tmem + T::DP, mn_lo + r0 + s0 * TILE16, mn_hi, i == 0);
             commit(bars->r0_empty[s0]);
             if (i + 1 < n) {
               ok = dprob(j + 1);
@@ -492,15 +534,15 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
               if (i + 2 == n) commit(bars->b_empty);
             }
             // dQ += dS K
-            ok = bwd_wait_warp(bars->ds_ready[sb], (j / C::NS) & 1, bars, p);
+            ok = bwd_wait_warp(bars->ds_ready[sb], (j / T::NS) & 1, bars, p);
             if (!ok) break;
             ptx::tc_fence_after_sync();
             bwd_mma_grad<D>(tmem, tS, mn_lo + r0 + s0 * TILE16, mn_hi, i == 0);
             commit(bars->r0_empty[s0]);
-            if (i + C::NS < n) {
-              ok = scores(j + C::NS);
+            if (i + T::NS < n) {
+              ok = scores(j + T::NS);
               if (!ok) break;
-              if (i + C::NS + 1 == n) commit(bars->a_empty);
+              if (i + T::NS + 1 == n) commit(bars->a_empty);
             }
           }
         }
@@ -531,82 +573,114 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&b));
     };
+    using Stage = BwdStage<KV, MK == kBwdMaskAdd ? C::MASK_COLS : 32>;
+    float* sMask = sStat + C::STAT_BYTES / 4 + warp * 32 * C::MASK_COLS;
     uint32_t j = 0, nu = 0;
     bool ok = true;
     BwdWalk walk;
     BwdPiece pc;
-    while (ok && walk.next(p.plan, blockIdx.x, pc)) {
+    while (ok && walk.next(plan, cta, pc)) {
       ok = __all_sync(0xffffffffu, piece_ok(pc));
       if (!ok) break;
-      const int b = (int)p.div_h.div((uint32_t)pc.head), h = pc.head - b * (KV ? p.Hk : p.Hq);
+      const int b = (int)div_h.div((uint32_t)pc.head), h = pc.head - b * heads;
       const int my = pc.tile * 128 + row;  // this thread's key or query
-      const int mine = min(my, (KV ? p.Nk : p.Nq) - 1);
       float nlse = 0.f, delta = 0.f, key_add = 0.f;
       if constexpr (!KV) {
         const size_t at = (size_t)pc.head * p.nqp + my;
         nlse = __ldg(p.nlse + at);
         delta = __ldg(p.delta + at);
       } else if constexpr (MK == kBwdMaskKey) {
-        key_add = __ldg(static_cast<const float*>(p.mask) + (size_t)b * p.Nk + mine) * kLog2e;
+        key_add = __ldg(static_cast<const float*>(p.mask) + (size_t)b * p.Nk + min(my, p.Nk - 1)) * kLog2e;
       }
       BwdIter at;
-      at.start(p.plan.units, pc.tile, pc.it0);
-      for (int it = pc.it0; it < pc.it1; ++it, ++j, at.next()) {
-        const uint32_t sb = j % C::NS;
-        const uint32_t tS = t0 + C::COL_S + sb * 128 + wg * 64, tDP = t0 + C::COL_DP + wg * 64;
-        const int col0 = at.tile * 128 + wg * 64;  // this thread's first query or key of the tile
-        // The first mask values, loaded before S is ready.
-        float m[MK == kBwdMaskNone || (KV && MK == kBwdMaskKey) ? 1 : 32];
-        auto load_mask = [&](int half) {
-          if constexpr (MK == kBwdMaskAdd || MK == kBwdMaskBool) {
-            constexpr int SZ = MK == kBwdMaskBool ? 1 : 4;
-            const int hq = KV ? h * p.group + at.g : h;
-            const char* base = static_cast<const char*>(p.mask) +
-                               ((size_t)b * p.mask_heads + (p.mask_heads == 1 ? 0 : hq)) * p.Nq * p.Nk * SZ;
-            if constexpr (KV) {  // neighbouring lanes read neighbouring keys
-              bwd_mask32<MK>(m, [&](int c) {
-                return base + ((size_t)min(col0 + half * 32 + c, p.Nq - 1) * p.Nk + mine) * SZ;
-              });
-            } else {
-              const char* mrow = base + (size_t)mine * p.Nk * SZ;
-              bwd_mask32<MK>(m, [&](int c) { return mrow + (size_t)min(col0 + half * 32 + c, p.Nk - 1) * SZ; });
-            }
-          } else if constexpr (!KV && MK == kBwdMaskKey) {
-            const float* mrow = static_cast<const float*>(p.mask) + (size_t)b * p.Nk;
-            bwd_mask32<MK>(m, [&](int c) { return mrow + min(col0 + half * 32 + c, p.Nk - 1); });
-          }
-        };
-        load_mask(0);
+      at.start(plan.units, pc.tile, pc.it0);
+      // The first mask values of the iteration at `i`, which are fetched an iteration ahead.
+      uint32_t bits = 0;
+      auto mask_head = [&](const BwdIter& i) {
+        return (size_t)b * p.mask_heads + (p.mask_heads == 1 ? 0 : (KV ? h * p.group + i.g : h));
+      };
+      auto stage = [&](const BwdIter& i, int c0) {
+        Stage::copy(ptx::smem_u32(sMask), static_cast<const float*>(p.mask) + mask_head(i) * p.Nq * p.Nk,
+                    pc.tile * 128 + (warp % 4) * 32, i.tile * 128 + wg * kBwdCols + c0, p.Nq, p.Nk, p.mask_vec,
+                    (int)lane);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      auto fetch = [&](const BwdIter& i) {
+        if constexpr (MK == kBwdMaskBool) {
+          const int rows = KV ? p.Nk : p.Nq, words = KV ? p.words_k : p.words_q;
+          bits = __ldg((KV ? p.bits_k : p.bits_q) + (mask_head(i) * rows + min(my, rows - 1)) * words + i.tile * 4 + wg);
+        } else if constexpr (MK == kBwdMaskAdd) {
+          stage(i, 0);
+        }
+      };
+      if (pc.it0 < pc.it1) fetch(at);
+      for (int it = pc.it0; it < pc.it1; ++it, ++j) {
+        const uint32_t sb = j % T::NS;
+        const uint32_t tS = t0 + T::S + sb * 128 + wg * kBwdCols, tDP = t0 + T::DP + wg * kBwdCols;
+        const int col0 = at.tile * 128 + wg * kBwdCols;  // this thread's first query or key of the tile
+        const BwdIter now = at;
+        at.next();
         const float4 *l4 = nullptr, *d4 = nullptr;
         if constexpr (KV) {
           ok = bwd_wait_warp(bars->st_full[j & 1], (j / 2) & 1, bars, p);
           if (!ok) break;
-          l4 = reinterpret_cast<const float4*>(sStat + (j & 1) * 256 + wg * 64);
+          l4 = reinterpret_cast<const float4*>(sStat + (j & 1) * 256 + wg * kBwdCols);
           d4 = l4 + 32;
         }
         // Pairs that the row does not see: above the diagonal, and keys past Nk
         // (as columns; as rows their gradients are not stored).
-        int lo = 0, hi = 64;  // columns seen
+        uint32_t seen = ~0u;
         if constexpr (KV) {
-          if (p.causal) lo = my - col0;
+          if (p.causal) {
+            const int lo = my - col0;  // columns from lo on
+            seen = lo <= 0 ? ~0u : (lo >= 32 ? 0u : ~0u << lo);
+          }
         } else {
-          hi = min(hi, p.Nk - col0);
-          if (p.causal) hi = min(hi, my - col0 + 1);
+          int n = min(32, p.Nk - col0);  // columns below n
+          if (p.causal) n = min(n, my - col0 + 1);
+          seen = n >= 32 ? ~0u : (n <= 0 ? 0u : ~0u >> (32 - n));
         }
-        const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < 64);
-        ok = bwd_wait_warp(bars->s_full[sb], (j / C::NS) & 1, bars, p);
+        if constexpr (MK == kBwdMaskBool) {
+          seen &= bits;
+          if (it + 1 < pc.it1) fetch(at);
+        }
+        const bool edge = __any_sync(0xffffffffu, seen != ~0u);
+        ok = bwd_wait_warp(bars->s_full[sb], (j / T::NS) & 1, bars, p);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        float pr[64];
+        float pr[kBwdCols];
+        {
+          uint32_t r[kBwdCols];
+          ptx::tmem_ld32x32b_x32(tS, r);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t r[32];
-          ptx::tmem_ld32x32b_x32(tS + half * 32, r);
+          for (int c = 0; c < kBwdCols; ++c) pr[c] = __uint_as_float(r[c]);
+        }
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
+        for (int cb = 0; cb < kBwdCols; cb += 16) {
+          float m[16];
+          if constexpr (MK == kBwdMaskAdd) {
+            if (cb % C::MASK_COLS == 0) {
+              asm volatile("cp.async.wait_all;" ::: "memory");
+              __syncwarp();
+            }
+            Stage::read(sMask, cb % C::MASK_COLS, (int)lane, m);
+            if ((cb + 16) % C::MASK_COLS == 0) {  // the buffer has been read
+              __syncwarp();
+              if (cb + 16 < kBwdCols)
+                stage(now, cb + 16);
+              else if (it + 1 < pc.it1)
+                fetch(at);
+            }
+          } else if constexpr (MK == kBwdMaskKey && !KV) {
+            const float* mrow = static_cast<const float*>(p.mask) + (size_t)b * p.Nk;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) m[c] = __ldg(mrow + min(col0 + cb + c, p.Nk - 1)) * kLog2e;
+          }
+#pragma unroll
+          for (int c = cb; c < cb + 16; c += 4) {
             float2 a0, a1;
             if constexpr (KV) {
-              const float4 l = l4[half * 8 + c / 4];
+              const float4 l = l4[c / 4];
               a0 = make_float2(l.x, l.y);
               a1 = make_float2(l.z, l.w);
               if constexpr (MK == kBwdMaskKey) {
@@ -616,32 +690,27 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
             } else {
               a0 = a1 = make_float2(nlse, nlse);
             }
-            if constexpr (sizeof(m) > sizeof(float)) {
-              a0 = __fadd2_rn(a0, make_float2(m[c], m[c + 1]));
-              a1 = __fadd2_rn(a1, make_float2(m[c + 2], m[c + 3]));
+            if constexpr (MK == kBwdMaskAdd || (MK == kBwdMaskKey && !KV)) {
+              a0 = __fadd2_rn(a0, make_float2(m[c - cb], m[c - cb + 1]));
+              a1 = __fadd2_rn(a1, make_float2(m[c - cb + 2], m[c - cb + 3]));
             }
-            const float2 e0 = bwd_exp(__uint_as_float(r[c]), __uint_as_float(r[c + 1]), sl2, a0);
-            const float2 e1 = bwd_exp(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]), sl2, a1);
-            const int k = half * 32 + c;
-            pr[k] = e0.x;
-            pr[k + 1] = e0.y;
-            pr[k + 2] = e1.x;
-            pr[k + 3] = e1.y;
-          }
-          if (half == 0) load_mask(1);
-          if (edge) {
-#pragma unroll
-            for (int c = half * 32; c < half * 32 + 32; ++c)
-              if (c < lo || c >= hi) pr[c] = 0.f;
-          }
-          if constexpr (KV) {  // over the columns just read
-            uint32_t packed[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) packed[c] = ptx::pack_bf16x2(pr[half * 32 + 2 * c], pr[half * 32 + 2 * c + 1]);
-            ptx::tmem_st32x32b_x16(tS + half * 16, packed);
+            const float2 e0 = bwd_exp(pr[c], pr[c + 1], sl2, a0), e1 = bwd_exp(pr[c + 2], pr[c + 3], sl2, a1);
+            pr[c] = e0.x;
+            pr[c + 1] = e0.y;
+            pr[c + 2] = e1.x;
+            pr[c + 3] = e1.y;
           }
         }
-        if constexpr (KV) {
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < kBwdCols; ++c)
+            if (!((seen >> c) & 1u)) pr[c] = 0.f;
+        }
+        if constexpr (KV) {  // over the columns just read
+          uint32_t packed[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) packed[c] = ptx::pack_bf16x2(pr[2 * c], pr[2 * c + 1]);
+          ptx::tmem_st32x32b_x16(tS, packed);
           ptx::tmem_wait_st();
           ptx::tc_fence_before_sync();
           arrive(bars->p_ready[sb]);
@@ -651,8 +720,8 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
         ptx::tc_fence_after_sync();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t r[32], packed[16];
-          ptx::tmem_ld32x32b_x32(tDP + half * 32, r);
+          uint32_t r[16], packed[8];
+          ptx::tmem_ld32x32b_x16(tDP + half * 16, r);
           if constexpr (!KV) {
             if (half == 1) {  // dP has been read
               ptx::tc_fence_before_sync();
@@ -660,10 +729,10 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
             }
           }
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
+          for (int c = 0; c < 16; c += 4) {
             float4 d = make_float4(delta, delta, delta, delta);
-            if constexpr (KV) d = d4[half * 8 + c / 4];
-            const int k = half * 32 + c;
+            if constexpr (KV) d = d4[half * 4 + c / 4];
+            const int k = half * 16 + c;
             const float2 x0 = __fadd2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])),
                                          make_float2(-d.x, -d.y));
             const float2 x1 = __fadd2_rn(make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])),
@@ -674,7 +743,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
             packed[c / 2 + 1] = ptx::pack_bf16x2(s1.x, s1.y);
           }
           // over columns that have been read: dP's (dK dV), or S's
-          ptx::tmem_st32x32b_x16((KV ? tDP : tS) + half * 16, packed);
+          ptx::tmem_st32x32b_x8((KV ? tDP : tS) + half * 8, packed);
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before_sync();
@@ -687,8 +756,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
       }
       if (!ok) break;
 
-      // The unit's gradients: dV by the first warpgroup and dK by the second, or
-      // half of dQ's columns by each.
+      // The unit's gradients, a quarter of the accumulators' columns each.
       const bool zero = pc.it0 == pc.it1;
       if (!zero) {
         ok = bwd_wait_warp(bars->acc_full, nu & 1, bars, p);
@@ -696,24 +764,71 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, 1) fa_bwd_kernel(const
         ++nu;
         ptx::tc_fence_after_sync();
       }
-      constexpr int NC = KV ? D : D / 2;
+      constexpr int NC = T::ACC / kBwdGroups;
       const uint32_t tA = t0 + wg * NC;
-      const int rows = KV ? p.Nk : p.Nq;
       if (pc.slot < 0) {
-        const BwdTensor& o = KV && wg == 1 ? p.out1 : p.out0;
-        const bool in = my < rows && bwd_check(p, bars, b * (KV ? p.Hk : p.Hq) + h < p.plan.units.heads,
-                                               kCheckGradStore, pc.head, my);
-        __nv_bfloat16* dst = o.p + b * o.b + h * o.h + (long long)my * o.n + (KV ? 0 : wg * NC);
-        bwd_store_row<NC>(tA, KV && wg == 0 ? 1.f : p.scale, zero, in, dst);
+        const bool is_dv = KV && wg < kBwdGroups / 2;
+        const BwdTensor& o = KV ? (is_dv ? p.dv : p.dk) : p.dq;
+        const int col = KV ? (wg % (kBwdGroups / 2)) * NC : wg * NC;
+        const bool in = my < (KV ? p.Nk : p.Nq) && bwd_check(p, bars, pc.head < plan.units.heads && col + NC <= D,
+                                                            kCheckGradStore, pc.head, my);
+        bwd_store_row<NC>(tA, is_dv ? 1.f : p.scale, zero, in, o.p + b * o.b + h * o.h + (long long)my * o.n + col);
       } else {
-        const bool in = bwd_check(p, bars, pc.slot < 2 * p.plan.ctas, kCheckGradSlot, pc.slot, pc.head);
-        bwd_store_part<NC>(tA, in, p.part + ((size_t)pc.slot * 2 + wg) * (128 * NC), row);
+        const bool in = bwd_check(p, bars, pc.slot < 2 * plan.ctas, kCheckGradSlot, pc.slot, pc.head);
+        bwd_store_part<NC>(tA, in, p.part[KV ? 0 : 1] + (size_t)pc.slot * (128 * T::ACC) + wg * NC * 128, row);
       }
       ptx::tc_fence_before_sync();
     }
     ptx::tc_fence_before_sync();
   }
   finish();
+}
+
+template <int D, int MK>
+__global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_kernel(const __grid_constant__ BwdParams p) {
+  using C = BwdCfg<D, MK>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  BwdBars* bars = reinterpret_cast<BwdBars*>(smem + (2 + C::RING0 + C::RING1) * C::TILE + C::STAT_BYTES + C::MASK_BYTES);
+  if (ptx::smem_u32(smem) & 1023u) {  // (the swizzled layouts need it; dynamic shared memory starts there)
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusTimeout);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    auto init = [](uint64_t& b, uint32_t n) { ptx::mbar_init(ptx::smem_u32(&b), n); };
+    init(bars->a_full, 1);
+    init(bars->a_empty, 1);
+    init(bars->b_full, 1);
+    init(bars->b_empty, 1);
+    for (int i = 0; i < C::RING0; ++i) init(bars->r0_full[i], 1), init(bars->r0_empty[i], 1);
+    for (int i = 0; i < C::RING1; ++i) init(bars->r1_full[i], 1), init(bars->r1_empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      init(bars->st_full[i], 1);
+      init(bars->st_empty[i], kBwdWarps);
+      init(bars->s_full[i], 1);
+      init(bars->p_ready[i], kBwdWarps);
+      init(bars->ds_ready[i], kBwdWarps);
+    }
+    init(bars->dp_full, 1);
+    init(bars->dp_free, kBwdWarps);
+    init(bars->acc_full, 1);
+    init(bars->drain, 1);
+    bars->abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (threadIdx.x / 32 == kBwdWarps + 1) {
+    ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // -L, delta and a mask's bits are there
+  const int cta = blockIdx.x, keys = p.plan[0].ctas;
+  if (cta < keys)
+    bwd_units<D, MK, true>(p, cta, smem, bars, tmem);
+  else
+    bwd_units<D, MK, false>(p, cta - keys, smem, bars, tmem);
 }
 
 // -L and delta of every query row, and of the rows that fill up the last tile:
@@ -732,6 +847,7 @@ struct BwdPrepParams {
 template <int D>
 __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant__ BwdPrepParams p) {
   constexpr int L = D / 8;  // lanes a row
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long i = (long long)blockIdx.x * (256 / L) + threadIdx.x / L;
   const int piece = threadIdx.x % L;
   const bool live = i < p.rows;
@@ -765,39 +881,92 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
   }
 }
 
-// Joins the partial sums of cut units, in the order of their pieces.  Block
-// (c, y, z): the unit that starts in CTA c's range, 8 columns, dV / dK (or dQ's halves).
-template <int D, bool KV>
-__global__ void __launch_bounds__(128) fa_bwd_join_kernel(const __grid_constant__ BwdParams p) {
-  constexpr int NC = KV ? D : D / 2;
-  int unit, last, slot;
-  if (!bwd_join(p.plan, blockIdx.x, unit, last, slot)) return;
-  const int row = threadIdx.x, col = blockIdx.y * 8, half = blockIdx.z;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are there
-  float acc[8] = {};
-  for (int c = blockIdx.x; c <= last; ++c) {
-    if (c > (int)blockIdx.x) {
-      slot = 2 * c;
-      if (p.plan.cut[c].unit == p.plan.cut[c + 1].unit && p.plan.cut[c].it == p.plan.cut[c + 1].it) continue;
+// A boolean mask as bits, by query rows and by key rows: a warp turns 32 rows of
+// 128 bytes into words, one ballot a row and 32 keys.
+struct BwdBitsParams {
+  const uint8_t* mask;  // [B mask_heads][Nq][Nk]
+  uint32_t *bits_q, *bits_k;
+  int Nq, Nk, words_q, words_k;
+  int blocks_q, blocks_k;  // 32-row and 128-key blocks of a head, whole tiles of both
+  long long blocks;
+};
+
+static __global__ void __launch_bounds__(256) fa_bwd_bits_kernel(const __grid_constant__ BwdBitsParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long i = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+  if (i >= p.blocks) return;
+  const int lane = threadIdx.x % 32;
+  const long long per = (long long)p.blocks_q * p.blocks_k;
+  const long long bh = i / per;
+  const int bq = (int)((i - bh * per) / p.blocks_k), bk = (int)(i - bh * per - (long long)bq * p.blocks_k);
+  const uint8_t* base = p.mask + bh * p.Nq * p.Nk;
+  uint32_t row[4] = {}, col[4] = {};
+#pragma unroll 4
+  for (int y = 0; y < 32; ++y) {
+    const int q = bq * 32 + y;
+    uint8_t v[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int k = bk * 128 + g * 32 + lane;
+      v[g] = q < p.Nq && k < p.Nk ? base[(size_t)q * p.Nk + k] : 0;
     }
-    const float4* src = reinterpret_cast<const float4*>(p.part + ((size_t)slot * 2 + half) * (128 * NC)) +
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint32_t w = __ballot_sync(0xffffffffu, v[g] != 0);
+      if (lane == y) row[g] = w;
+      col[g] |= (v[g] != 0 ? 1u : 0u) << y;
+    }
+  }
+  const int q = bq * 32 + lane;
+  if (q < p.Nq)
+    *reinterpret_cast<uint4*>(p.bits_q + ((size_t)bh * p.Nq + q) * p.words_q + bk * 4) =
+        make_uint4(row[0], row[1], row[2], row[3]);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int k = bk * 128 + g * 32 + lane;
+    if (k < p.Nk) p.bits_k[((size_t)bh * p.Nk + k) * p.words_k + bq] = col[g];
+  }
+}
+
+// Joins the partial sums of cut units, in the order of their pieces.  Block
+// (c, y): the unit that starts in CTA c's range (key units' CTAs, then query
+// units'), 8 columns of its accumulators.
+template <int D>
+__global__ void __launch_bounds__(128) fa_bwd_join_kernel(const __grid_constant__ BwdParams p) {
+  const bool kv = blockIdx.x < (unsigned)p.plan[0].ctas;
+  const int cta = kv ? (int)blockIdx.x : (int)blockIdx.x - p.plan[0].ctas;
+  const int col = blockIdx.y * 8, row = threadIdx.x, acc_cols = kv ? 2 * D : D;
+  if (col >= acc_cols) return;
+  const BwdPlan& plan = p.plan[kv ? 0 : 1];
+  int unit, last, slot;
+  if (!bwd_join(plan, cta, unit, last, slot)) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are there
+  const float* part = p.part[kv ? 0 : 1];
+  float acc[8] = {};
+  for (int c = cta; c <= last; ++c) {
+    if (c > cta) {
+      slot = 2 * c;
+      if (plan.cut[c].unit == plan.cut[c + 1].unit && plan.cut[c].it == plan.cut[c + 1].it) continue;
+    }
+    const float4* src = reinterpret_cast<const float4*>(part + (size_t)slot * (128 * acc_cols)) +
                         (size_t)(col / 4) * 128 + row;
     const float4 a = src[0], e = src[128];
     acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
     acc[4] += e.x; acc[5] += e.y; acc[6] += e.z; acc[7] += e.w;
   }
   int head, tile;
-  p.plan.units.locate(unit, head, tile);
-  const int heads = KV ? p.Hk : p.Hq;
-  const int b = (int)p.div_h.div((uint32_t)head), h = head - b * heads;
+  plan.units.locate(unit, head, tile);
+  const int heads = kv ? p.Hk : p.Hq;
+  const int b = (int)(kv ? p.div_hk : p.div_hq).div((uint32_t)head), h = head - b * heads;
   const int my = tile * 128 + row;
-  if (my >= (KV ? p.Nk : p.Nq)) return;
-  const BwdTensor& o = KV && half == 1 ? p.out1 : p.out0;
-  const float mul = KV && half == 0 ? 1.f : p.scale;
+  if (my >= (kv ? p.Nk : p.Nq)) return;
+  const bool is_dv = kv && col < D;
+  const BwdTensor& o = kv ? (is_dv ? p.dv : p.dk) : p.dq;
+  const float mul = is_dv ? 1.f : p.scale;
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = ptx::pack_bf16x2(acc[2 * i] * mul, acc[2 * i + 1] * mul);
-  *reinterpret_cast<uint4*>(o.p + b * o.b + h * o.h + (long long)my * o.n + (KV ? 0 : half * NC) + col) =
+  *reinterpret_cast<uint4*>(o.p + b * o.b + h * o.h + (long long)my * o.n + (col < D ? col : col - D)) =
       make_uint4(w[0], w[1], w[2], w[3]);
 }
 

@@ -9,14 +9,15 @@
 
 namespace fa {
 
-// -L and delta.
+// -L and delta, and a boolean mask's bits.
 int launch_bwd_prep(const BwdPrepParams& p, int D, cudaStream_t s);
+int launch_bwd_bits(const BwdBitsParams& p, cudaStream_t s);
 
-// dK and dV (kv) or dQ, of prm.plan, with its join where units are cut.  mask:
-// kBwdMask*.  FA_OK, FA_ERR_UNSUPPORTED (a build whose register split does not
-// fit) or FA_ERR_CUDA.
-int launch_bwd_d32(const BwdParams& prm, bool kv, int mask, int device, cudaStream_t s);
-int launch_bwd_d64(const BwdParams& prm, bool kv, int mask, int device, cudaStream_t s);
-int launch_bwd_d128(const BwdParams& prm, bool kv, int mask, int device, cudaStream_t s);
+// dQ, dK and dV of prm.plan, with the join where units are cut.  mask: kBwdMask*.
+// FA_OK, FA_ERR_UNSUPPORTED (a build whose register split does not fit) or
+// FA_ERR_CUDA.
+int launch_bwd_d32(const BwdParams& prm, int mask, int device, cudaStream_t s);
+int launch_bwd_d64(const BwdParams& prm, int mask, int device, cudaStream_t s);
+int launch_bwd_d128(const BwdParams& prm, int mask, int device, cudaStream_t s);
 
 }  // namespace fa

@@ -32,7 +32,9 @@ def ss(n, kind, elect=False):
       : "memory");
 }}
 '''
-def ts(n, elect=False):
+def ts(n, elect=False, chunk=0):
+    """chunk: A lies in pieces of that many MMAs, each at the start of twice its columns (0: in one piece)."""
+    at = [8 * i if not chunk else 16 * chunk * (i // chunk) + 8 * (i % chunk) for i in range(n)]
     g = "@e " if elect else ""
     lines = ['"{\\n"', '".reg .pred p, q;\\n"', '".reg .b32 ta, bl;\\n"', '".reg .b64 db;\\n"']
     if elect:
@@ -41,14 +43,14 @@ def ts(n, elect=False):
               '"mov.b64 db, {%2, %3};\\n"',
               f'"{g}tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\\n"']
     for i in range(1, n):
-        lines += [f'"add.u32 ta, %1, {8 * i};\\n"', f'"add.u32 bl, %2, %{5 + i};\\n"',
+        lines += [f'"add.u32 ta, %1, {at[i]};\\n"', f'"add.u32 bl, %2, %{5 + i};\\n"',
                   '"mov.b64 db, {bl, %3};\\n"',
                   f'"{g}tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, q;\\n"']
     lines.append('"}\\n"')
     body = "\n      ".join(lines)
     imm = "".join(f', "n"(BSTEP * {i})' for i in range(1, n))
     return f'''template <int BSTEP>
-__device__ __forceinline__ void mma_ts_x{n}{'_el' if elect else ''}(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
+__device__ __forceinline__ void mma_ts_x{n}{f'_by{chunk}' if chunk else ''}{'_el' if elect else ''}(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
                                           uint32_t idesc, uint32_t acc_first) {{
   asm volatile(
       {body}
@@ -70,4 +72,5 @@ for n in (1, 2, 4):
     out.append(ss(n, "f8f6f4", True))
 out.append(ts(4, True))
 out.append(ts(8, True))
+out.append(ts(8, True, 2))
 open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "mma_batch.inc"), "w").write("\n".join(out))

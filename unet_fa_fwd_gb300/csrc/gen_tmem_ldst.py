@@ -33,7 +33,7 @@ __device__ __forceinline__ void tmem_st32x32b_x{n}(uint32_t taddr, const uint32_
 }}
 '''
 out = []
-for n in (16, 32, 64, 128):
+for n in (8, 16, 32, 64, 128):
     out.append(ld(n))
 for n in (8, 16, 32):
     out.append(st(n))

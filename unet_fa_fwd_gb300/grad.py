@@ -183,8 +183,9 @@ def norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Tensor, k:
                 None, True, token_major, pairing)
 
 
-def bwd_workspace_bytes(B: int, Hq: int, Hk: int, Nq: int, Nk: int, D: int) -> int:
-    return int(load_library().fa_bwd_workspace_bytes(B, Hq, Hk, Nq, Nk, D))
+def bwd_workspace_bytes(B: int, Hq: int, Hk: int, Nq: int, Nk: int, D: int, bool_mask_heads: int = 0) -> int:
+    """``bool_mask_heads``: heads (1 or Hq) of a boolean mask, which is kept as bits; 0 for any other mask."""
+    return int(load_library().fa_bwd_workspace_bytes(B, Hq, Hk, Nq, Nk, D, bool_mask_heads))
 
 
 def _mask(key_mask, full_mask, B, Hq, Nq, Nk, device):
@@ -215,7 +216,9 @@ def _bwd(dout, q, k, v, out, lse, dlse, key_mask, full_mask, causal, scale, dq, 
     lib = load_library()
     if new:
         dq, dk, dv = (_rope_new(shape, _BF16, q.device, token_major) for shape in (q_shape, k_shape, k_shape))
-        workspace = torch.empty(lib.fa_bwd_workspace_bytes(B, Hq, Hk, Nq, Nk, D), dtype=torch.uint8, device=q.device)
+        heads = 0 if full_mask is None or full_mask.dtype is _F32 or full_mask.dim() != 4 else full_mask.shape[1]
+        workspace = torch.empty(lib.fa_bwd_workspace_bytes(B, Hq, Hk, Nq, Nk, D, heads), dtype=torch.uint8,
+                                device=q.device)
         for t in (dq, dk, dv):
             fields += (t.data_ptr(), *t.stride()[:3])
     else:
