@@ -18,11 +18,17 @@
 //
 // One launch holds both kinds: the first CTAs (one per SM) walk key units, the
 // rest query units, which start as SMs get free.  640 threads a CTA:
-//   warps 0-15   four warpgroups; a thread has a row of the unit (one lane of
-//                tensor memory) and 32 of a tile's 128 columns
+//   warps 0-15   four warpgroups, each with 32 of a tile's 128 columns; a warp
+//                has 32 rows of the unit (lanes of tensor memory)
 //   warp 16      TMA producer      warp 17  MMA issuer (owns tensor memory)
 // Four warps a sub-partition hide the latency of tensor memory and of the
 // exponentials, which two (64 columns a thread) did not.
+// L and delta are a query's: in query units a row's, so that a thread has one row
+// and 32 columns; in key units a column's, where a thread has 4 rows and 8 columns
+// (the 16 x 256 bit shape of tensor memory's accesses) and so a fourth of the reads
+// of shared memory, whose 128 bytes a clock bound the kernel at D = 128: the
+// operands and arriving tiles of a 128 x 128 tile take 2048 clocks (as long as its
+// products), L and delta 512 more with a row a thread, 128 so.
 // P and dS go back to tensor memory as bf16, the A operand of the products that
 // take them; both sides' rows are operands K-major for S and dP and MN-major for
 // the gradients, from one copy in shared memory.
@@ -211,13 +217,14 @@ __device__ __forceinline__ void bwd_load_tile(uint32_t dst, const CUtensorMap* m
 
 // Staging of a fp32 mask [rows][Nk]: a warp copies the values of its 32 rows and
 // SC columns of a tile into `buf` (its own), for itself.  Key units (KV): a
-// thread's row is a key and columns are queries, kept as [SC][32]; query units: a
-// row's SC values together, 16-byte pieces swizzled so that the lanes' reads of
-// their rows do not meet.  Values outside the mask read 0.
+// warp's rows are keys and columns are queries, kept as [SC][32], each pair of
+// queries turned by 8 keys more; query units: a row's SC values together, 16-byte
+// pieces swizzled.  So the lanes' reads do not meet.  Values outside the mask read 0.
 template <bool KV, int SC>
 struct BwdStage {
   static constexpr int PIECES = SC / 4;
   static __device__ __forceinline__ int swizzle(int r) { return SC == 32 ? (r & 7) : ((r >> 1) & 3); }
+  static __device__ __forceinline__ int turned(int key, int c) { return (key + 8 * (c / 2)) & 31; }
   static __device__ __forceinline__ void copy(uint32_t buf, const float* base, int row0, int col0, int Nq, int Nk,
                                               int vec, int lane) {
     const int q0 = KV ? col0 : row0, k0 = KV ? row0 : col0;
@@ -230,7 +237,7 @@ struct BwdStage {
           const int c = 4 * i + lane / 8, g = lane % 8;
           q = q0 + c;
           k = k0 + 4 * g;
-          dst = buf + (c * 32 + 4 * g) * 4;
+          dst = buf + (c * 32 + turned(4 * g, c)) * 4;
         } else {
           const int r = i * (32 / PIECES) + lane / PIECES, g = lane % PIECES;
           q = q0 + r;
@@ -249,7 +256,7 @@ struct BwdStage {
         if constexpr (KV) {
           q = q0 + i;
           k = k0 + lane;
-          dst = buf + (i * 32 + lane) * 4;
+          dst = buf + (i * 32 + turned(lane, i)) * 4;
         } else {
           const int r = i * (32 / SC) + lane / SC, c = lane % SC;
           q = q0 + r;
@@ -262,12 +269,16 @@ struct BwdStage {
       }
     }
   }
-  // 16 columns from c0 of the lane's row, times log2(e).
+  // The lane's 16 values of the columns c0 .. c0 + 15 (key units: of 4 rows and 4
+  // columns, in the order of bwd_elements), times log2(e).
   static __device__ __forceinline__ void read(const float* buf, int c0, int lane, float (&m)[16]) {
     constexpr float kLog2e = 1.4426950408889634f;
     if constexpr (KV) {
 #pragma unroll
-      for (int c = 0; c < 16; ++c) m[c] = buf[(c0 + c) * 32 + lane] * kLog2e;
+      for (int e = 0; e < 16; ++e) {
+        const int c = c0 + 8 * (e / 8) + 2 * (lane % 4) + e % 2, key = lane / 4 + 8 * (e / 2 % 4);
+        m[e] = buf[c * 32 + turned(key, c)] * kLog2e;
+      }
     } else {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -280,6 +291,19 @@ struct BwdStage {
     }
   }
 };
+
+// The 32 elements that a thread has of a tile, from the 32 columns at `t`.  Query
+// units: its row's 32 columns.  Key units (bwd_elements): element 8 i + 2 r + c is
+// row lane / 4 + 8 r, column 8 i + 2 (lane % 4) + c.
+template <bool KV>
+__device__ __forceinline__ void bwd_load_elements(uint32_t t, uint32_t (&r)[32]) {
+  if constexpr (KV)
+    ptx::tmem_ld2x16x256b_x4(t, r);
+  else
+    ptx::tmem_ld32x32b_x32(t, r);
+}
+// Pairs of a key unit's elements in that order, as the 16 columns at `t`.
+__device__ __forceinline__ void bwd_store_pairs(uint32_t t, const uint32_t (&w)[16]) { ptx::tmem_st2x16x128b_x4(t, w); }
 
 // 2^(s sl2 + add) of a pair.
 __device__ __forceinline__ float2 bwd_exp(float s0, float s1, float sl2, float2 add) {
@@ -509,21 +533,37 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
             ptx::tc_fence_after_sync();
             bwd_mma_grad<D>(tmem, tS, mn_lo + r1 + s1 * TILE16, mn_hi, i == 0);
             commit(bars->r1_empty[s1]);
-            if (i + T::NS < n) {
-              ok = scores(j + T::NS);
-              if (!ok) break;
-              if (i + T::NS + 1 == n) commit(bars->a_empty);
+            if constexpr (T::NS == 1) {  // dS takes dP's place
+              if (i + 1 < n) {
+                ok = scores(j + 1);
+                if (!ok) break;
+                if (i + 2 == n) commit(bars->a_empty);
+              }
+            } else {  // dS lies beside P: dP is free once it has been read
+              if (i + 1 < n) {
+                ok = bwd_wait_warp(bars->dp_free, j & 1, bars, p) && dprob(j + 1);
+                if (!ok) break;
+                if (i + 2 == n) commit(bars->b_empty);
+              }
             }
             // dK += dS^T Q
-            ok = bwd_wait_warp(bars->ds_ready[0], j & 1, bars, p);
+            ok = bwd_wait_warp(bars->ds_ready[sb], (j / T::NS) & 1, bars, p);
             if (!ok) break;
             ptx::tc_fence_after_sync();
-            bwd_mma_grad<D>(tmem + D, tmem + T::DP, mn_lo + r0 + s0 * TILE16, mn_hi, i == 0);
+            bwd_mma_grad<D>(tmem + D, T::NS == 1 ? tmem + T::DP : tS + 16, mn_lo + r0 + s0 * TILE16, mn_hi, i == 0);
             commit(bars->r0_empty[s0]);
-            if (i + 1 < n) {
-              ok = dprob(j + 1);
-              if (!ok) break;
-              if (i + 2 == n) commit(bars->b_empty);
+            if constexpr (T::NS == 1) {
+              if (i + 1 < n) {
+                ok = dprob(j + 1);
+                if (!ok) break;
+                if (i + 2 == n) commit(bars->b_empty);
+              }
+            } else {
+              if (i + 2 < n) {
+                ok = scores(j + 2);
+                if (!ok) break;
+                if (i + 3 == n) commit(bars->a_empty);
+              }
             }
           } else {
             if (i + 1 < n) {
@@ -565,7 +605,11 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
   {
     // --------------------------------------------------------- the threads --
     const int wg = warp / 4;
-    const int row = (warp % 4) * 32 + (int)lane;
+    const int row = (warp % 4) * 32 + (int)lane;  // of the accumulators
+    // Key units: the first of the four rows, 8 apart, and the first column of the
+    // pairs, 8 apart, of this thread in a tile.
+    constexpr int ROWS = KV ? 4 : 1;
+    const int row4 = KV ? (warp % 4) * 32 + (int)lane / 4 : row, col2 = 2 * ((int)lane % 4);
     const uint32_t t0 = tmem + ((uint32_t)((warp % 4) * 32) << 16);
     const float sl2 = p.scale_log2;
     constexpr float kLog2e = 1.4426950408889634f;
@@ -583,19 +627,21 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       ok = __all_sync(0xffffffffu, piece_ok(pc));
       if (!ok) break;
       const int b = (int)div_h.div((uint32_t)pc.head), h = pc.head - b * heads;
-      const int my = pc.tile * 128 + row;  // this thread's key or query
-      float nlse = 0.f, delta = 0.f, key_add = 0.f;
+      const int my = pc.tile * 128 + row, my4 = pc.tile * 128 + row4;  // this thread's key or query
+      float nlse = 0.f, delta = 0.f, key_add[4] = {};
       if constexpr (!KV) {
         const size_t at = (size_t)pc.head * p.nqp + my;
         nlse = __ldg(p.nlse + at);
         delta = __ldg(p.delta + at);
       } else if constexpr (MK == kBwdMaskKey) {
-        key_add = __ldg(static_cast<const float*>(p.mask) + (size_t)b * p.Nk + min(my, p.Nk - 1)) * kLog2e;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          key_add[r] = __ldg(static_cast<const float*>(p.mask) + (size_t)b * p.Nk + min(my4 + 8 * r, p.Nk - 1)) * kLog2e;
       }
       BwdIter at;
       at.start(plan.units, pc.tile, pc.it0);
       // The first mask values of the iteration at `i`, which are fetched an iteration ahead.
-      uint32_t bits = 0;
+      uint32_t bits[ROWS] = {};
       auto mask_head = [&](const BwdIter& i) {
         return (size_t)b * p.mask_heads + (p.mask_heads == 1 ? 0 : (KV ? h * p.group + i.g : h));
       };
@@ -608,7 +654,10 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       auto fetch = [&](const BwdIter& i) {
         if constexpr (MK == kBwdMaskBool) {
           const int rows = KV ? p.Nk : p.Nq, words = KV ? p.words_k : p.words_q;
-          bits = __ldg((KV ? p.bits_k : p.bits_q) + (mask_head(i) * rows + min(my, rows - 1)) * words + i.tile * 4 + wg);
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r)
+            bits[r] = __ldg((KV ? p.bits_k : p.bits_q) + (mask_head(i) * rows + min(my4 + 8 * r, rows - 1)) * words +
+                            i.tile * 4 + wg);
         } else if constexpr (MK == kBwdMaskAdd) {
           stage(i, 0);
         }
@@ -620,38 +669,44 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         const int col0 = at.tile * 128 + wg * kBwdCols;  // this thread's first query or key of the tile
         const BwdIter now = at;
         at.next();
-        const float4 *l4 = nullptr, *d4 = nullptr;
+        const float *lcol = nullptr, *dcol = nullptr;  // -L and delta of this thread's columns
         if constexpr (KV) {
           ok = bwd_wait_warp(bars->st_full[j & 1], (j / 2) & 1, bars, p);
           if (!ok) break;
-          l4 = reinterpret_cast<const float4*>(sStat + (j & 1) * 256 + wg * kBwdCols);
-          d4 = l4 + 32;
+          lcol = sStat + (j & 1) * 256 + wg * kBwdCols + col2;
+          dcol = lcol + 128;
         }
         // Pairs that the row does not see: above the diagonal, and keys past Nk
         // (as columns; as rows their gradients are not stored).
-        uint32_t seen = ~0u;
-        if constexpr (KV) {
-          if (p.causal) {
-            const int lo = my - col0;  // columns from lo on
-            seen = lo <= 0 ? ~0u : (lo >= 32 ? 0u : ~0u << lo);
+        uint32_t seen[ROWS];
+        bool edge = false;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          seen[r] = ~0u;
+          if constexpr (KV) {
+            if (p.causal) {
+              const int lo = my4 + 8 * r - col0;  // columns from lo on
+              seen[r] = lo <= 0 ? ~0u : (lo >= 32 ? 0u : ~0u << lo);
+            }
+          } else {
+            int n = min(32, p.Nk - col0);  // columns below n
+            if (p.causal) n = min(n, my - col0 + 1);
+            seen[r] = n >= 32 ? ~0u : (n <= 0 ? 0u : ~0u >> (32 - n));
           }
-        } else {
-          int n = min(32, p.Nk - col0);  // columns below n
-          if (p.causal) n = min(n, my - col0 + 1);
-          seen = n >= 32 ? ~0u : (n <= 0 ? 0u : ~0u >> (32 - n));
+          if constexpr (MK == kBwdMaskBool) seen[r] &= bits[r];
+          edge = edge || seen[r] != ~0u;
         }
         if constexpr (MK == kBwdMaskBool) {
-          seen &= bits;
           if (it + 1 < pc.it1) fetch(at);
         }
-        const bool edge = __any_sync(0xffffffffu, seen != ~0u);
+        edge = __any_sync(0xffffffffu, edge);
         ok = bwd_wait_warp(bars->s_full[sb], (j / T::NS) & 1, bars, p);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        float pr[kBwdCols];
+        float pr[kBwdCols];  // in the order of bwd_elements
         {
           uint32_t r[kBwdCols];
-          ptx::tmem_ld32x32b_x32(tS, r);
+          bwd_load_elements<KV>(tS, r);
 #pragma unroll
           for (int c = 0; c < kBwdCols; ++c) pr[c] = __uint_as_float(r[c]);
         }
@@ -677,40 +732,39 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
             for (int c = 0; c < 16; ++c) m[c] = __ldg(mrow + min(col0 + cb + c, p.Nk - 1)) * kLog2e;
           }
 #pragma unroll
-          for (int c = cb; c < cb + 16; c += 4) {
-            float2 a0, a1;
+          for (int c = cb; c < cb + 16; c += 2) {
+            float2 a = make_float2(nlse, nlse);
             if constexpr (KV) {
-              const float4 l = l4[c / 4];
-              a0 = make_float2(l.x, l.y);
-              a1 = make_float2(l.z, l.w);
-              if constexpr (MK == kBwdMaskKey) {
-                a0 = __fadd2_rn(a0, make_float2(key_add, key_add));
-                a1 = __fadd2_rn(a1, make_float2(key_add, key_add));
-              }
-            } else {
-              a0 = a1 = make_float2(nlse, nlse);
+              a = *reinterpret_cast<const float2*>(lcol + c / 8 * 8);
+              if constexpr (MK == kBwdMaskKey) a = __fadd2_rn(a, make_float2(key_add[c / 2 % 4], key_add[c / 2 % 4]));
             }
-            if constexpr (MK == kBwdMaskAdd || (MK == kBwdMaskKey && !KV)) {
-              a0 = __fadd2_rn(a0, make_float2(m[c - cb], m[c - cb + 1]));
-              a1 = __fadd2_rn(a1, make_float2(m[c - cb + 2], m[c - cb + 3]));
-            }
-            const float2 e0 = bwd_exp(pr[c], pr[c + 1], sl2, a0), e1 = bwd_exp(pr[c + 2], pr[c + 3], sl2, a1);
-            pr[c] = e0.x;
-            pr[c + 1] = e0.y;
-            pr[c + 2] = e1.x;
-            pr[c + 3] = e1.y;
+            if constexpr (MK == kBwdMaskAdd || (MK == kBwdMaskKey && !KV))
+              a = __fadd2_rn(a, make_float2(m[c - cb], m[c - cb + 1]));
+            const float2 e = bwd_exp(pr[c], pr[c + 1], sl2, a);
+            pr[c] = e.x;
+            pr[c + 1] = e.y;
           }
         }
         if (edge) {
+          if constexpr (KV) {
 #pragma unroll
-          for (int c = 0; c < kBwdCols; ++c)
-            if (!((seen >> c) & 1u)) pr[c] = 0.f;
+            for (int r = 0; r < ROWS; ++r) {
+              const uint32_t w = seen[r] >> col2;
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                if (!((w >> (c / 2 * 8 + c % 2)) & 1u)) pr[c / 2 * 8 + 2 * r + c % 2] = 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kBwdCols; ++c)
+              if (!((seen[0] >> c) & 1u)) pr[c] = 0.f;
+          }
         }
         if constexpr (KV) {  // over the columns just read
           uint32_t packed[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) packed[c] = ptx::pack_bf16x2(pr[2 * c], pr[2 * c + 1]);
-          ptx::tmem_st32x32b_x16(tS, packed);
+          bwd_store_pairs(tS, packed);
           ptx::tmem_wait_st();
           ptx::tc_fence_before_sync();
           arrive(bars->p_ready[sb]);
@@ -718,41 +772,50 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         ok = bwd_wait_warp(bars->dp_full, j & 1, bars, p);
         if (!ok) break;
         ptx::tc_fence_after_sync();
+        constexpr bool DP_FREE = !KV || T::NS == 2;  // dS goes over S's columns, not dP's
+        auto dp_read = [&]() {
+          if constexpr (DP_FREE) {
+            ptx::tc_fence_before_sync();
+            arrive(bars->dp_free);
+          }
+        };
+        if constexpr (KV) {
+          uint32_t r[32], packed[16];
+          bwd_load_elements<true>(tDP, r);
+          dp_read();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t r[16], packed[8];
-          ptx::tmem_ld32x32b_x16(tDP + half * 16, r);
-          if constexpr (!KV) {
-            if (half == 1) {  // dP has been read
-              ptx::tc_fence_before_sync();
-              arrive(bars->dp_free);
+          for (int i = 0; i < 4; ++i) {
+            const float2 d = *reinterpret_cast<const float2*>(dcol + 8 * i);
+#pragma unroll
+            for (int k = 8 * i; k < 8 * i + 8; k += 2) {
+              const float2 x = __fadd2_rn(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])),
+                                          make_float2(-d.x, -d.y));
+              const float2 s = __fmul2_rn(x, make_float2(pr[k], pr[k + 1]));
+              packed[k / 2] = ptx::pack_bf16x2(s.x, s.y);
             }
           }
+          bwd_store_pairs(DP_FREE ? tS + 16 : tDP, packed);
+        } else {
 #pragma unroll
-          for (int c = 0; c < 16; c += 4) {
-            float4 d = make_float4(delta, delta, delta, delta);
-            if constexpr (KV) d = d4[half * 4 + c / 4];
-            const int k = half * 16 + c;
-            const float2 x0 = __fadd2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])),
-                                         make_float2(-d.x, -d.y));
-            const float2 x1 = __fadd2_rn(make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])),
-                                         make_float2(-d.z, -d.w));
-            const float2 s0 = __fmul2_rn(x0, make_float2(pr[k], pr[k + 1]));
-            const float2 s1 = __fmul2_rn(x1, make_float2(pr[k + 2], pr[k + 3]));
-            packed[c / 2] = ptx::pack_bf16x2(s0.x, s0.y);
-            packed[c / 2 + 1] = ptx::pack_bf16x2(s1.x, s1.y);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t r[16], packed[8];
+            ptx::tmem_ld32x32b_x16(tDP + half * 16, r);
+            if (half == 1) dp_read();
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const int k = half * 16 + c;
+              const float2 x = __fadd2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])),
+                                          make_float2(-delta, -delta));
+              const float2 s = __fmul2_rn(x, make_float2(pr[k], pr[k + 1]));
+              packed[c / 2] = ptx::pack_bf16x2(s.x, s.y);
+            }
+            ptx::tmem_st32x32b_x8(tS + half * 8, packed);
           }
-          // over columns that have been read: dP's (dK dV), or S's
-          ptx::tmem_st32x32b_x8((KV ? tDP : tS) + half * 8, packed);
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before_sync();
-        if constexpr (KV) {
-          arrive(bars->ds_ready[0]);
-          arrive(bars->st_empty[j & 1]);
-        } else {
-          arrive(bars->ds_ready[sb]);
-        }
+        arrive(bars->ds_ready[sb]);
+        if constexpr (KV) arrive(bars->st_empty[j & 1]);
       }
       if (!ok) break;
 
@@ -873,8 +936,11 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
     if (in) {
       const size_t at = (size_t)bh * p.Nq + n;
       const float lse = p.lse[at];
-      if (lse != -INFINITY) nlse = -lse * 1.4426950408889634f;
       if (p.dlse) sum -= p.dlse[at];
+      if (lse != -INFINITY)
+        nlse = -lse * 1.4426950408889634f;
+      else
+        sum = 0.f;  // (dLSE of a row that sees nothing may be anything)
     }
     p.nlse[i] = nlse;
     p.delta[i] = in ? sum : 0.f;
