@@ -71,7 +71,7 @@ bool mask_ok(int B, int Hq, int Nq, int Nk, int heads) {
 // the most CTAs a plan has: it does not depend on the GPU.  bool_heads: heads of
 // a boolean mask (0: no such mask), whose bits are kept by rows and by keys.
 struct Layout {
-  size_t nlse, delta, part_kv, part_q, bits_q, bits_k, total;
+  size_t nlse, ndelta, part_kv, part_q, bits_q, bits_k, total;
 };
 
 Layout layout(int B, int Hq, int Nq, int Nk, int D, int bool_heads) {
@@ -81,7 +81,7 @@ Layout layout(int B, int Hq, int Nq, int Nk, int D, int bool_heads) {
   Layout l{};
   size_t off = 0;
   l.nlse = off;     off += align256(rows * sizeof(float));
-  l.delta = off;    off += align256(rows * sizeof(float));
+  l.ndelta = off;    off += align256(rows * sizeof(float));
   l.part_kv = off;  off += slots * 2 * tile;
   l.part_q = off;   off += slots * tile;
   l.bits_q = off;   off += align256(masks * Nq * kt * 16);
@@ -228,7 +228,7 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   p.scale = scale;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.nlse = reinterpret_cast<float*>(ws + l.nlse);
-  p.delta = reinterpret_cast<float*>(ws + l.delta);
+  p.ndelta = reinterpret_cast<float*>(ws + l.ndelta);
   p.mask = mask_data;
   p.mask_heads = mask_heads;
   p.div_group = fa::FastDiv::make((uint32_t)group);
@@ -294,7 +294,7 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   pp.lse = lse;
   pp.dlse = dlse;
   pp.nlse = reinterpret_cast<float*>(ws + l.nlse);
-  pp.delta = reinterpret_cast<float*>(ws + l.delta);
+  pp.ndelta = reinterpret_cast<float*>(ws + l.ndelta);
   pp.Hq = Hq;
   pp.Nq = Nq;
   pp.nqp = p.nqp;
