@@ -46,7 +46,7 @@ int launch_bwd_one(const BwdParams& prm, int device, cudaStream_t s) {
       // increase would wait forever.
       cudaFuncAttributes attr;
       if (cudaFuncGetAttributes(&attr, fa_bwd_kernel<D, MK>) != cudaSuccess) return FA_ERR_CUDA;
-      if (128 * C::GROUPS * C::REGS_ROWS + 128 * C::REGS_OTHER > attr.numRegs * C::THREADS)
+      if (128 * kBwdGroups * C::REGS_ROWS + 128 * C::REGS_OTHER > attr.numRegs * kBwdThreads)
         return FA_ERR_UNSUPPORTED;
       ready[device] = true;
     }
@@ -55,10 +55,10 @@ int launch_bwd_one(const BwdParams& prm, int device, cudaStream_t s) {
   const BwdPlan &k = prm.plan[0], &q = prm.plan[1];
   log_launch("fa_bwd_kernel<D=%d,mask %s> grid %d + %d x %d threads smem %d B, dK dV: %d units of %d x 128 rows (%d "
              "whole, %d cuts inside units), dQ: %d of %d (%d, %d), Hq %d Hk %d Nq %d Nk %d causal %d",
-             D, kNames[MK], k.ctas, q.ctas, C::THREADS, C::SMEM_BYTES, k.units.count(), k.units.tiles, k.whole,
+             D, kNames[MK], k.ctas, q.ctas, kBwdThreads, C::SMEM_BYTES, k.units.count(), k.units.tiles, k.whole,
              k.joins, q.units.count(), q.units.tiles, q.whole, q.joins, prm.Hq, prm.Hk, prm.Nq, prm.Nk, prm.causal);
   const unsigned ctas = (unsigned)(k.ctas + q.ctas);
-  const int rc = launch_bwd_after(fa_bwd_kernel<D, MK>, dim3(ctas), C::THREADS, C::SMEM_BYTES, s, prm);
+  const int rc = launch_bwd_after(fa_bwd_kernel<D, MK>, dim3(ctas), kBwdThreads, C::SMEM_BYTES, s, prm);
   if (rc != FA_OK || k.joins + q.joins == 0) return rc;
   log_launch("fa_bwd_join_kernel<D=%d> grid %u x %d x 128 threads", D, ctas, 2 * D / 8);
   return launch_bwd_after(fa_bwd_join_kernel<D>, dim3(ctas, 2 * D / 8), 128, 0, s, prm);

@@ -17,9 +17,12 @@
 // Here every sum stays in tensor memory and results repeat bit for bit.
 //
 // One launch holds both kinds: the first CTAs (one per SM) walk key units, the
-// rest query units, which start as SMs get free.  Four warpgroups (D = 128) or two
-// share a tile's columns; a warp has 32 rows of the unit (lanes of tensor memory).
-// Behind them a warp issues the TMA copies and one the MMAs (it owns tensor memory).
+// rest query units, which start as SMs get free.  640 threads a CTA:
+//   warps 0-15   four warpgroups, each with 32 of a tile's 128 columns; a warp
+//                has 32 rows of the unit (lanes of tensor memory)
+//   warp 16      TMA producer      warp 17  MMA issuer (owns tensor memory)
+// Four warps a sub-partition hide the latency of tensor memory and of the
+// exponentials, which two (64 columns a thread) did not.
 // L and delta are a query's: in query units a row's, so that a thread has one row
 // and 32 columns; in key units a column's, where a thread has 4 rows and 8 columns
 // (the 16 x 256 bit shape of tensor memory's accesses) and so a fourth of the reads
@@ -77,39 +80,31 @@ struct BwdParams {
   CUtensorMap q, k, v, dout;
 };
 
-template <bool X>
-struct Bool {
-  static constexpr bool value = X;
-};
+constexpr int kBwdGroups = 4;                    // warpgroups of rows
+constexpr int kBwdWarps = 4 * kBwdGroups;
+constexpr int kBwdCols = 128 / kBwdGroups;       // columns a thread has of a tile
+constexpr int kBwdThreads = 32 * (kBwdWarps + 4);
 
 template <int D, int MK>
 struct BwdCfg {
   using F = Cfg<D>;
-  static constexpr int GROUPS = D == 128 ? 4 : 2;  // warpgroups of rows
-  static constexpr int WARPS = 4 * GROUPS;
-  static constexpr int COLS = 128 / GROUPS;        // columns a warp has of a tile
-  static constexpr int THREADS = 32 * (WARPS + 4);
-  static constexpr int TILE = 128 * D * 2;         // bytes of a 128-row tile
-  // A fp32 mask's values are staged by each warp for itself, MASK_COLS columns at
-  // a time in buffers of MASK_BUF.
-  static constexpr int MASK_COLS = MK != kBwdMaskAdd ? 0 : (D == 128 ? 16 : 64);
-  static constexpr int MASK_BUF = D == 128 ? 16 : 32;
-  static constexpr int MASK_BYTES = WARPS * 32 * MASK_COLS * 4;
-  // Rings of the walked tiles (key units: Q, read again by dK one or two steps
-  // later, and dO; query units: K and V).  The slots that fit, six at most.
-  static constexpr int RING0 = D == 128 ? (MK == kBwdMaskAdd ? 2 : 3) : (D == 64 && MK == kBwdMaskAdd ? 4 : 6);
-  static constexpr int RING1 = D == 128 ? 2 : (D == 64 && MK == kBwdMaskAdd ? 3 : 4);
-  static constexpr int STATS = D == 128 ? 2 : 4;  // key units: slots of -L and -delta of 128 queries
-  static constexpr int STAT_BYTES = STATS * 1024;
+  static constexpr int TILE = 128 * D * 2;  // bytes of a 128-row tile
+  // A fp32 mask's values are staged by each warp for itself, MASK_COLS columns at a time.
+  static constexpr int MASK_COLS = MK != kBwdMaskAdd ? 0 : (D == 128 ? 16 : 32);
+  static constexpr int MASK_BYTES = kBwdWarps * 32 * MASK_COLS * 4;
+  // Rings of the walked tiles (key units: Q, read again by dK an iteration
+  // later, and dO; query units: K and V).  At D = 128 the slots that fit.
+  static constexpr int RING0 = D == 128 ? (MK == kBwdMaskAdd ? 2 : 3) : 4;
+  static constexpr int RING1 = D == 128 ? 2 : 4;
+  static constexpr int STAT_BYTES = 2 * 1024;  // key units: two slots of -L and -delta of 128 queries
   static constexpr int SMEM_BAR = 512;
   static constexpr int SMEM_USED = (2 + RING0 + RING1) * TILE + STAT_BYTES + MASK_BYTES + SMEM_BAR;
   // (more than half of the SM's, so that one CTA has its tensor memory alone)
   static constexpr int SMEM_BYTES = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
-  // The launch reserves REGS registers a thread; the rows' warpgroups take from the other.
-  static constexpr int REGS = D == 128 ? 96 : 168;
-  static constexpr int REGS_ROWS = D == 128 ? 104 : 208, REGS_OTHER = D == 128 ? 64 : 88;
-  static_assert(128 * GROUPS * REGS_ROWS + 128 * REGS_OTHER <= THREADS * REGS, "register split");
+  // The launch reserves 96 registers a thread; the rows' warpgroups take from the other.
+  static constexpr int REGS_ROWS = 104, REGS_OTHER = 64;
+  static_assert(128 * kBwdGroups * REGS_ROWS + 128 * REGS_OTHER <= kBwdThreads * 96, "register split");
 };
 
 // Tensor memory of a kind of unit: accumulators, S (two where they fit), dP.
@@ -118,17 +113,16 @@ struct BwdCols {
   static constexpr int ACC = KV ? 2 * D : D;
   static constexpr int NS = ACC + 3 * 128 <= 512 ? 2 : 1;
   static constexpr int S = ACC, DP = ACC + NS * 128;
-  static constexpr bool FUSED = D <= 64;  // a step of the threads: see bwd_units
   static_assert(DP + 128 <= 512, "tensor-memory columns");
 };
 
-constexpr int kBwdMaxRing = 6, kBwdMaxStats = 4;
+constexpr int kBwdMaxRing = 4;
 
 struct BwdBars {
   uint64_t a_full, a_empty, b_full, b_empty;  // the unit's rows
   uint64_t r0_full[kBwdMaxRing], r0_empty[kBwdMaxRing], r1_full[kBwdMaxRing], r1_empty[kBwdMaxRing];
-  uint64_t st_full[kBwdMaxStats], st_empty[kBwdMaxStats];
-  uint64_t s_full[2], p_ready, dp_full, dp_free, ds_ready[2], acc_full, drain;
+  uint64_t st_full[2], st_empty[2];
+  uint64_t s_full[2], p_ready[2], dp_full, dp_free, ds_ready[2], acc_full, drain;
   uint32_t tmem_base;
   volatile int abort_flag;
 };
@@ -159,16 +153,13 @@ __device__ __forceinline__ bool bwd_wait_warp(uint64_t& bar, uint32_t parity, Bw
   return __all_sync(0xffffffffu, bwd_wait_slow(b, parity, bars, p.timeout_ns, p.status));
 }
 
-// Up to three phases (nullptr: none) by a whole warp, asked for at once.
-__device__ __forceinline__ bool bwd_wait_warp(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2,
-                                              uint32_t p2, BwdBars* bars, const BwdParams& p) {
-  bool there = true;
-  if (b0) there = ptx::mbar_try_wait(ptx::smem_u32(b0), p0);
-  if (b1) there = ptx::mbar_try_wait(ptx::smem_u32(b1), p1) && there;
-  if (b2) there = ptx::mbar_try_wait(ptx::smem_u32(b2), p2) && there;
+// Two phases (the first nullptr: one) by a whole warp, asked for at once.
+__device__ __forceinline__ bool bwd_wait_warp(uint64_t* b0, uint32_t p0, uint64_t& b1, uint32_t p1, BwdBars* bars,
+                                              const BwdParams& p) {
+  bool there = ptx::mbar_try_wait(ptx::smem_u32(&b1), p1);
+  if (b0) there = ptx::mbar_try_wait(ptx::smem_u32(b0), p0) && there;
   if (__all_sync(0xffffffffu, there)) return true;
-  return (!b0 || bwd_wait_warp(*b0, p0, bars, p)) && (!b1 || bwd_wait_warp(*b1, p1, bars, p)) &&
-         (!b2 || bwd_wait_warp(*b2, p2, bars, p));
+  return (!b0 || bwd_wait_warp(*b0, p0, bars, p)) && bwd_wait_warp(b1, p1, bars, p);
 }
 
 // Debug builds: see fa_check.
@@ -215,13 +206,13 @@ __device__ __forceinline__ void bwd_mma_scores(uint32_t d, uint32_t a_lo, uint32
     ptx::mma_ss_x2_el<C::s_off(1)>(d, a_lo, hi, b_lo, hi, IDESC, 0);
 }
 
-// acc += X T: X bf16 in tensor memory, 16 values (8 columns) at the start of each
-// 16 columns from x on; T a 128-row tile, MN-major.
+// acc += X T: X bf16 in tensor memory, each warpgroup's 32 columns at the start
+// of the 32 that they were computed from; T a 128-row tile, MN-major.
 template <int D>
 __device__ __forceinline__ void bwd_mma_grad(uint32_t acc, uint32_t x, uint32_t t_lo, uint32_t t_hi, bool first) {
   constexpr uint32_t IDESC = make_idesc(128, D, true);
   constexpr uint32_t STEP = (16 * Cfg<D>::SW) >> 4;
-  ptx::mma_ts_x8_by1_el<STEP>(acc, x, t_lo, t_hi, IDESC, first ? 0u : 1u);
+  ptx::mma_ts_x8_by2_el<STEP>(acc, x, t_lo, t_hi, IDESC, first ? 0u : 1u);
 }
 
 template <int D>
@@ -310,34 +301,18 @@ struct BwdStage {
   }
 };
 
-// The 16 elements that a thread has of the 16 columns at `t`.  Query units: its
-// row's.  Key units (bwd_elements): element 8 i + 2 r + c is row lane / 4 + 8 r,
-// column 8 i + 2 (lane % 4) + c.
+// The 32 elements that a thread has of a tile, from the 32 columns at `t`.  Query
+// units: its row's 32 columns.  Key units (bwd_elements): element 8 i + 2 r + c is
+// row lane / 4 + 8 r, column 8 i + 2 (lane % 4) + c.
 template <bool KV>
-__device__ __forceinline__ void bwd_load16(uint32_t t, uint32_t (&r)[16]) {
+__device__ __forceinline__ void bwd_load_elements(uint32_t t, uint32_t (&r)[32]) {
   if constexpr (KV)
-    ptx::tmem_ld_quad16(t, r);
+    ptx::tmem_ld2x16x256b_x4(t, r);
   else
-    ptx::tmem_ld32x32b_x16(t, r);
+    ptx::tmem_ld32x32b_x32(t, r);
 }
-template <bool KV>
-__device__ __forceinline__ void bwd_load16(uint32_t t, uint32_t (&r)[16], uint32_t u, uint32_t (&s)[16]) {
-  if constexpr (KV)
-    ptx::tmem_ld_quad16_two(t, r, u, s);
-  else
-    ptx::tmem_ld_row16_two(t, r, u, s);
-}
-// Their pairs, rounded to bf16, as the 8 columns at `t`.
-template <bool KV>
-__device__ __forceinline__ void bwd_store16(uint32_t t, const float* x) {
-  uint32_t w[8];
-#pragma unroll
-  for (int c = 0; c < 8; ++c) w[c] = ptx::pack_bf16x2(x[2 * c], x[2 * c + 1]);
-  if constexpr (KV)
-    ptx::tmem_st_quad8(t, w);
-  else
-    ptx::tmem_st32x32b_x8(t, w);
-}
+// Pairs of a key unit's elements in that order, as the 16 columns at `t`.
+__device__ __forceinline__ void bwd_store_pairs(uint32_t t, const uint32_t (&w)[16]) { ptx::tmem_st2x16x128b_x4(t, w); }
 
 // 2^(s sl2 + add) of a pair.
 __device__ __forceinline__ float2 bwd_exp(float s0, float s1, float sl2, float2 add) {
@@ -415,8 +390,8 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);
   const uint32_t lane = threadIdx.x % 32;
   auto finish = [&]() {
-    ptx::named_barrier_sync(1, C::THREADS);
-    if (warp == C::WARPS + 1) {
+    ptx::named_barrier_sync(1, kBwdThreads);
+    if (warp == kBwdWarps + 1) {
       ptx::tc_fence_after_sync();
       ptx::tmem_dealloc(tmem, 512);
     }
@@ -430,9 +405,9 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
   const int heads = KV ? p.Hk : p.Hq;
   const FastDiv& div_h = KV ? p.div_hk : p.div_hq;
 
-  if (warp >= C::WARPS) {
+  if (warp >= kBwdWarps) {
     ptx::setmaxnreg_dec<C::REGS_OTHER>();
-    if (warp == C::WARPS) {
+    if (warp == kBwdWarps) {
       // ---------------------------------------------------------- producer --
       if (lane == 0) {
         const CUtensorMap *mA = KV ? &p.k : &p.q, *mB = KV ? &p.v : &p.dout;
@@ -479,8 +454,8 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
             if (it == pc.it0) ok = load_unit(mB, sB, bars->b_full, bars->b_empty, nb);
             if (!ok) break;
             if constexpr (KV) {
-              const uint32_t ss = j % C::STATS;
-              ok = bwd_wait(bars->st_empty[ss], ((j / C::STATS) & 1) ^ 1, bars, p);
+              const uint32_t ss = j & 1;
+              ok = bwd_wait(bars->st_empty[ss], ((j / 2) & 1) ^ 1, bars, p);
               if (!ok) break;
               full = ptx::smem_u32(&bars->st_full[ss]);
               ptx::mbar_arrive_expect_tx(full, 1024);
@@ -509,10 +484,10 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         landed(bars->b_full, nb);
         for (uint32_t s = 0; s < C::RING0; ++s) landed(bars->r0_full[s], (n0 + C::RING0 - 1 - s) / C::RING0);
         for (uint32_t s = 0; s < C::RING1; ++s) landed(bars->r1_full[s], (n1 + C::RING1 - 1 - s) / C::RING1);
-        for (uint32_t s = 0; s < C::STATS; ++s) landed(bars->st_full[s], (nst + C::STATS - 1 - s) / C::STATS);
+        for (uint32_t s = 0; s < 2; ++s) landed(bars->st_full[s], (nst + 1 - s) / 2);
       }
       __syncwarp();
-    } else if (warp == C::WARPS + 1) {
+    } else if (warp == kBwdWarps + 1) {
       // --------------------------------------------------------------- MMA --
       // Descriptors: K-major (scores) and MN-major (gradients) views of the tiles.
       const uint64_t k_major = smem_desc(0, 16, F::SBO, F::LAYOUT);
@@ -524,7 +499,6 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       constexpr uint32_t TILE16 = C::TILE >> 4;
       uint32_t nu = 0;  // pieces
       uint32_t j = 0;   // iterations
-      uint32_t st = 0;  // steps
       bool ok = true;
       auto commit = [&](uint64_t& b) { ptx::mma_commit_el(ptx::smem_u32(&b)); };
       // S (dP) of iteration i: the unit's rows by the ring's tile.
@@ -559,64 +533,53 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
           if (ok && n == 2) commit(bars->a_empty);
         }
         if (!ok) break;
-        if constexpr (T::FUSED) {
-          for (uint32_t i = 0; ok && i <= n; ++i, ++st) {
-            ok = bwd_wait_warp(bars->ds_ready[st & 1], (st / 2) & 1, bars, p);
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            const uint32_t x = tmem + (i < n ? T::S + ((j + i) & 1) * 128 : T::DP);
-            if (KV && i < n) {  // dV += P^T dO
-              const uint32_t s = (j + i) % C::RING1;
-              bwd_mma_grad<D>(tmem, x, mn_lo + r1 + s * TILE16, mn_hi, i == 0);
-              commit(bars->r1_empty[s]);
-            }
-            if (i > 0) {  // dK += dS^T Q, or dQ += dS K, of the iteration before
-              const uint32_t s = (j + i - 1) % C::RING0;
-              bwd_mma_grad<D>(tmem + (KV ? D : 0), KV && i < n ? x + 8 : x, mn_lo + r0 + s * TILE16, mn_hi, i == 1);
-              commit(bars->r0_empty[s]);
-            }
-            if (i + 2 < n) {
-              ok = scores(j + i + 2);
-              if (!ok) break;
-              if (i + 3 == n) commit(bars->a_empty);
-            }
-            if (i + 1 < n) {
-              ok = bwd_wait_warp(bars->dp_free, (j + i) & 1, bars, p) && dprob(j + i + 1);
-              if (!ok) break;
-              if (i + 2 == n) commit(bars->b_empty);
-            }
-          }
-          j += n;
-        }
-        for (uint32_t i = 0; !T::FUSED && ok && i < n; ++i, ++j) {
+        for (uint32_t i = 0; ok && i < n; ++i, ++j) {
           const uint32_t s0 = j % C::RING0, s1 = j % C::RING1, sb = j % T::NS;
           const uint32_t tS = tmem + T::S + sb * 128;
           if constexpr (KV) {
             // dV += P^T dO
-            ok = bwd_wait_warp(bars->p_ready, j & 1, bars, p);
+            ok = bwd_wait_warp(bars->p_ready[sb], (j / T::NS) & 1, bars, p);
             if (!ok) break;
             ptx::tc_fence_after_sync();
             bwd_mma_grad<D>(tmem, tS, mn_lo + r1 + s1 * TILE16, mn_hi, i == 0);
             commit(bars->r1_empty[s1]);
-            if (i + 1 < n) {
-              ok = scores(j + 1);
-              if (!ok) break;
-              if (i + 2 == n) commit(bars->a_empty);
+            if constexpr (T::NS == 1) {  // dS takes dP's place
+              if (i + 1 < n) {
+                ok = scores(j + 1);
+                if (!ok) break;
+                if (i + 2 == n) commit(bars->a_empty);
+              }
+            } else {  // dS lies beside P: dP is free once it has been read
+              if (i + 1 < n) {
+                ok = bwd_wait_warp(bars->dp_free, j & 1, bars, p) && dprob(j + 1);
+                if (!ok) break;
+                if (i + 2 == n) commit(bars->b_empty);
+              }
             }
             // dK += dS^T Q
-            ok = bwd_wait_warp(bars->ds_ready[0], j & 1, bars, p);
+            ok = bwd_wait_warp(bars->ds_ready[sb], (j / T::NS) & 1, bars, p);
             if (!ok) break;
             ptx::tc_fence_after_sync();
-            bwd_mma_grad<D>(tmem + D, tmem + T::DP, mn_lo + r0 + s0 * TILE16, mn_hi, i == 0);
+            bwd_mma_grad<D>(tmem + D, T::NS == 1 ? tmem + T::DP : tS + 16, mn_lo + r0 + s0 * TILE16, mn_hi, i == 0);
             commit(bars->r0_empty[s0]);
-            if (i + 1 < n) {
-              ok = dprob(j + 1);
-              if (!ok) break;
-              if (i + 2 == n) commit(bars->b_empty);
+            if constexpr (T::NS == 1) {
+              if (i + 1 < n) {
+                ok = dprob(j + 1);
+                if (!ok) break;
+                if (i + 2 == n) commit(bars->b_empty);
+              }
+            } else {
+              if (i + 2 < n) {
+                ok = scores(j + 2);
+                if (!ok) break;
+                if (i + 3 == n) commit(bars->a_empty);
+              }
             }
           } else {
             if (i + 1 < n) {
-              ok = bwd_wait_warp(bars->dp_free, j & 1, bars, p) && dprob(j + 1);
+              ok = bwd_wait_warp(bars->dp_free, j & 1, bars, p);
+              if (!ok) break;
+              ok = dprob(j + 1);
               if (!ok) break;
               if (i + 2 == n) commit(bars->b_empty);
             }
@@ -664,10 +627,9 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&b));
     };
-    using Stage = BwdStage<KV, C::MASK_BUF>;
-    constexpr int WORDS = C::COLS / 32;
+    using Stage = BwdStage<KV, MK == kBwdMaskAdd ? C::MASK_COLS : 32>;
     float* sMask = sStat + C::STAT_BYTES / 4 + warp * 32 * C::MASK_COLS;
-    uint32_t j = 0, st = 0, nu = 0;  // iterations, steps, pieces
+    uint32_t j = 0, nu = 0;
     bool ok = true;
     BwdWalk walk;
     BwdPiece pc;
@@ -689,16 +651,14 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       BwdIter at;
       at.start(plan.units, pc.tile, pc.it0);
       // The first mask values of the iteration at `i`, which are fetched an iteration ahead.
-      uint32_t bits[ROWS][WORDS] = {};
+      uint32_t bits[ROWS] = {};
       auto mask_head = [&](const BwdIter& i) {
         return (size_t)b * p.mask_heads + (p.mask_heads == 1 ? 0 : (KV ? h * p.group + i.g : h));
       };
       auto stage = [&](const BwdIter& i, int c0) {
-#pragma unroll
-        for (int c = 0; c < C::MASK_COLS; c += C::MASK_BUF)
-          Stage::copy(ptx::smem_u32(sMask) + c * 128, static_cast<const float*>(p.mask) + mask_head(i) * p.Nq * p.Nk,
-                      pc.tile * 128 + (warp % 4) * 32, i.tile * 128 + wg * C::COLS + c0 + c, p.Nq, p.Nk, p.mask_vec,
-                      (int)lane);
+        Stage::copy(ptx::smem_u32(sMask), static_cast<const float*>(p.mask) + mask_head(i) * p.Nq * p.Nk,
+                    pc.tile * 128 + (warp % 4) * 32, i.tile * 128 + wg * kBwdCols + c0, p.Nq, p.Nk, p.mask_vec,
+                    (int)lane);
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
       auto fetch = [&](const BwdIter& i) {
@@ -706,194 +666,169 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
           const int rows = KV ? p.Nk : p.Nq, words = KV ? p.words_k : p.words_q;
 #pragma unroll
           for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-            for (int w = 0; w < WORDS; ++w)
-              bits[r][w] = __ldg((KV ? p.bits_k : p.bits_q) + (mask_head(i) * rows + min(my4 + 8 * r, rows - 1)) * words +
-                                 i.tile * 4 + wg * WORDS + w);
+            bits[r] = __ldg((KV ? p.bits_k : p.bits_q) + (mask_head(i) * rows + min(my4 + 8 * r, rows - 1)) * words +
+                            i.tile * 4 + wg);
         } else if constexpr (MK == kBwdMaskAdd) {
           stage(i, 0);
         }
       };
       if (pc.it0 < pc.it1) fetch(at);
-      float pr[C::COLS];  // P of a tile, in the order of bwd_load16
-      uint32_t seen[ROWS][WORDS];
-      bool edge = false;
-      // Pairs of the tile at `i` that the rows do not see: above the diagonal, and
-      // keys past Nk (as columns; as rows their gradients are not stored).
-      auto look = [&](const BwdIter& i, bool more) {
-        const int col0 = i.tile * 128 + wg * C::COLS;  // this warp's first query or key of the tile
-        edge = false;
-        // (tiles that are seen whole)
-        const bool below = !p.causal || (KV ? i.tile > pc.tile : i.tile < pc.tile);
-        if (MK != kBwdMaskBool && below && (KV || (i.tile + 1) * 128 <= p.Nk)) return;
+      for (int it = pc.it0; it < pc.it1; ++it, ++j) {
+        const uint32_t sb = j % T::NS;
+        const uint32_t tS = t0 + T::S + sb * 128 + wg * kBwdCols, tDP = t0 + T::DP + wg * kBwdCols;
+        const int col0 = at.tile * 128 + wg * kBwdCols;  // this thread's first query or key of the tile
+        const BwdIter now = at;
+        at.next();
+        const float *lcol = nullptr, *dcol = nullptr;  // -L and -delta of this thread's columns
+        if constexpr (KV) {
+          lcol = sStat + (j & 1) * 256 + wg * kBwdCols + col2;
+          dcol = lcol + 128;
+        }
+        // Pairs that the row does not see: above the diagonal, and keys past Nk
+        // (as columns; as rows their gradients are not stored).
+        uint32_t seen[ROWS];
+        bool edge = false;
+        // (a tile that is seen whole needs no look)
+        const bool below = !p.causal || (KV ? now.tile > pc.tile : now.tile < pc.tile);
+        const bool whole = MK != kBwdMaskBool && below && (KV || (now.tile + 1) * 128 <= p.Nk);
+        if (!whole) {
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-#pragma unroll
-          for (int w = 0; w < WORDS; ++w) {
-            uint32_t x = ~0u;
+          for (int r = 0; r < ROWS; ++r) {
+            seen[r] = ~0u;
             if constexpr (KV) {
               if (p.causal) {
-                const int lo = my4 + 8 * r - col0 - 32 * w;  // columns from lo on
-                x = lo <= 0 ? ~0u : (lo >= 32 ? 0u : ~0u << lo);
+                const int lo = my4 + 8 * r - col0;  // columns from lo on
+                seen[r] = lo <= 0 ? ~0u : (lo >= 32 ? 0u : ~0u << lo);
               }
             } else {
-              int n = min(32, p.Nk - col0 - 32 * w);  // columns below n
-              if (p.causal) n = min(n, my - col0 - 32 * w + 1);
-              x = n >= 32 ? ~0u : (n <= 0 ? 0u : ~0u >> (32 - n));
+              int n = min(32, p.Nk - col0);  // columns below n
+              if (p.causal) n = min(n, my - col0 + 1);
+              seen[r] = n >= 32 ? ~0u : (n <= 0 ? 0u : ~0u >> (32 - n));
             }
-            if constexpr (MK == kBwdMaskBool) x &= bits[r][w];
-            seen[r][w] = x;
-            edge = edge || x != ~0u;
+            if constexpr (MK == kBwdMaskBool) seen[r] &= bits[r];
+            edge = edge || seen[r] != ~0u;
           }
+          if constexpr (MK == kBwdMaskBool) {
+            if (it + 1 < pc.it1) fetch(at);
+          }
+          edge = __any_sync(0xffffffffu, edge);
         }
-        if constexpr (MK == kBwdMaskBool) {
-          if (more) fetch(at);
-        }
-        edge = __any_sync(0xffffffffu, edge);
-      };
-      // The 16 columns from cb on: dS (DS) of `d`, with P as it stands, to the 8
-      // columns at `t`, and P (S) of `s`, of the tile at `now` (`more`: there is one
-      // after it, at `at`).  The two are taken in turn, pair by pair: exponentials
-      // run beside the multiplications.
-      auto columns = [&](auto has_s, const uint32_t (&s)[16], auto has_ds, const uint32_t (&d)[16], int cb, uint32_t t,
-                         const float* dcol, const float* lcol, const BwdIter& now, bool more) {
-        constexpr bool S = decltype(has_s)::value, DS = decltype(has_ds)::value;
-        float m[16], ds[16];
-        if constexpr (!S) {
-        } else if constexpr (MK == kBwdMaskAdd) {
-          if (cb % C::MASK_COLS == 0) {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncwarp();
-          }
-          Stage::read(sMask + cb % C::MASK_COLS / C::MASK_BUF * (C::MASK_BUF * 32), cb % C::MASK_BUF, (int)lane, m);
-          if ((cb + 16) % C::MASK_COLS == 0) {  // the buffer has been read
-            __syncwarp();
-            if (cb + 16 < C::COLS)
-              stage(now, cb + 16);
-            else if (more)
-              fetch(at);
-          }
-        } else if constexpr (MK == kBwdMaskKey && !KV) {
-          const float* mrow = static_cast<const float*>(p.mask) + (size_t)b * p.Nk;
-          const int col0 = now.tile * 128 + wg * C::COLS + cb;
+        ok = bwd_wait_warp(KV ? &bars->st_full[j & 1] : nullptr, (j / 2) & 1, bars->s_full[sb], (j / T::NS) & 1, bars, p);
+        if (!ok) break;
+        ptx::tc_fence_after_sync();
+        float pr[kBwdCols];  // in the order of bwd_elements
+        {
+          uint32_t r[kBwdCols];
+          bwd_load_elements<KV>(tS, r);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) m[c] = __ldg(mrow + min(col0 + c, p.Nk - 1)) * kLog2e;
+          for (int c = 0; c < kBwdCols; ++c) pr[c] = __uint_as_float(r[c]);
         }
 #pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-          const float2 was = make_float2(pr[cb + c], pr[cb + c + 1]);
-          if constexpr (S) {
+        for (int cb = 0; cb < kBwdCols; cb += 16) {
+          float m[16];
+          if constexpr (MK == kBwdMaskAdd) {
+            if (cb % C::MASK_COLS == 0) {
+              asm volatile("cp.async.wait_all;" ::: "memory");
+              __syncwarp();
+            }
+            Stage::read(sMask, cb % C::MASK_COLS, (int)lane, m);
+            if ((cb + 16) % C::MASK_COLS == 0) {  // the buffer has been read
+              __syncwarp();
+              if (cb + 16 < kBwdCols)
+                stage(now, cb + 16);
+              else if (it + 1 < pc.it1)
+                fetch(at);
+            }
+          } else if constexpr (MK == kBwdMaskKey && !KV) {
+            const float* mrow = static_cast<const float*>(p.mask) + (size_t)b * p.Nk;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) m[c] = __ldg(mrow + min(col0 + cb + c, p.Nk - 1)) * kLog2e;
+          }
+#pragma unroll
+          for (int c = cb; c < cb + 16; c += 2) {
             float2 a = make_float2(nlse, nlse);
             if constexpr (KV) {
-              a = *reinterpret_cast<const float2*>(lcol + cb + c / 8 * 8);
+              a = *reinterpret_cast<const float2*>(lcol + c / 8 * 8);
               if constexpr (MK == kBwdMaskKey) a = __fadd2_rn(a, make_float2(key_add[c / 2 % 4], key_add[c / 2 % 4]));
             }
             if constexpr (MK == kBwdMaskAdd || (MK == kBwdMaskKey && !KV))
-              a = __fadd2_rn(a, make_float2(m[c], m[c + 1]));
-            const float2 e = bwd_exp(__uint_as_float(s[c]), __uint_as_float(s[c + 1]), sl2, a);
-            pr[cb + c] = e.x;
-            pr[cb + c + 1] = e.y;
-          }
-          if constexpr (DS) {
-            float2 a = make_float2(ndelta, ndelta);
-            if constexpr (KV) a = *reinterpret_cast<const float2*>(dcol + cb + c / 8 * 8);
-            const float2 x = __fadd2_rn(make_float2(__uint_as_float(d[c]), __uint_as_float(d[c + 1])), a);
-            const float2 y = __fmul2_rn(x, was);
-            ds[c] = y.x;
-            ds[c + 1] = y.y;
+              a = __fadd2_rn(a, make_float2(m[c - cb], m[c - cb + 1]));
+            const float2 e = bwd_exp(pr[c], pr[c + 1], sl2, a);
+            pr[c] = e.x;
+            pr[c + 1] = e.y;
           }
         }
-        if constexpr (DS) bwd_store16<KV>(t, ds);
-        if (S && edge) {
+        if (edge) {
+          if constexpr (KV) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint32_t w = KV ? seen[c / 2 % ROWS][cb / 32] >> (cb % 32 + col2) : seen[0][cb / 32] >> (cb % 32);
-            if (!((w >> (KV ? c / 8 * 8 + c % 2 : c)) & 1u)) pr[cb + c] = 0.f;
+            for (int r = 0; r < ROWS; ++r) {
+              const uint32_t w = seen[r] >> col2;
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                if (!((w >> (c / 2 * 8 + c % 2)) & 1u)) pr[c / 2 * 8 + 2 * r + c % 2] = 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kBwdCols; ++c)
+              if (!((seen[0] >> c) & 1u)) pr[c] = 0.f;
           }
         }
-      };
-      constexpr Bool<true> yes;
-      constexpr Bool<false> no;
-      auto dp_read = [&]() {  // dP is in registers
-        ptx::tc_fence_before_sync();
-        arrive(bars->dp_free);
-      };
-      auto stat = [&](uint32_t i) { return sStat + (i % C::STATS) * 256 + wg * C::COLS + col2; };
-      const uint32_t tDP = t0 + T::DP + wg * C::COLS;
-      // A step: P of iteration j (S) and dS of the one before (DS).
-      auto step = [&](auto has_s, auto has_ds, bool more) {
-        constexpr bool S = decltype(has_s)::value, DS = decltype(has_ds)::value;
-        const uint32_t tS = t0 + T::S + (j & 1) * 128 + wg * C::COLS;
-        const BwdIter now = at;
-        if constexpr (S) {
-          at.next();
-          look(now, more);
-        }
-        if (!bwd_wait_warp(KV && S ? &bars->st_full[j % C::STATS] : nullptr, (j / C::STATS) & 1,
-                           S ? &bars->s_full[j & 1] : nullptr, (j / 2) & 1, DS ? &bars->dp_full : nullptr, (j - 1) & 1,
-                           bars, p))
-          return false;
-        ptx::tc_fence_after_sync();
+        if constexpr (KV) {  // over the columns just read
+          uint32_t packed[16];
 #pragma unroll
-        for (int cb = 0; cb < C::COLS; cb += 16) {
-          uint32_t s[16], d[16];
-          if constexpr (S && DS)
-            bwd_load16<KV>(tS + cb, s, tDP + cb, d);
-          else if constexpr (S)
-            bwd_load16<KV>(tS + cb, s);
-          else
-            bwd_load16<KV>(tDP + cb, d);
-          if (DS && cb == C::COLS - 16) dp_read();
-          columns(has_s, s, has_ds, d, cb, S ? tS + cb + (KV ? 8 : 0) : tDP + cb, stat(j - 1) + 128, stat(j), now, more);
-          if constexpr (S && KV) bwd_store16<KV>(tS + cb, pr + cb);
-        }
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before_sync();
-        arrive(bars->ds_ready[st & 1]);
-        if constexpr (KV && DS) arrive(bars->st_empty[(j - 1) % C::STATS]);
-        if constexpr (S) ++j;
-        ++st;
-        return true;
-      };
-      if (T::FUSED && pc.it0 < pc.it1) {
-        ok = step(yes, no, pc.it0 + 1 < pc.it1);
-        for (int it = pc.it0 + 1; ok && it < pc.it1; ++it) ok = step(yes, yes, it + 1 < pc.it1);
-        ok = ok && step(no, yes, false);
-      }
-      for (int it = pc.it0; !T::FUSED && it < pc.it1; ++it, ++j) {
-        const uint32_t sb = j % T::NS;
-        const uint32_t tS = t0 + T::S + sb * 128 + wg * C::COLS;
-        const BwdIter now = at;
-        at.next();
-        const bool more = it + 1 < pc.it1;
-        look(now, more);
-        ok = bwd_wait_warp(KV ? &bars->st_full[j % C::STATS] : nullptr, (j / C::STATS) & 1, &bars->s_full[sb],
-                           (j / T::NS) & 1, nullptr, 0, bars, p);
-        if (!ok) break;
-        ptx::tc_fence_after_sync();
-        uint32_t x0[16], x1[16];
-        bwd_load16<KV>(tS, x0, tS + 16, x1);
-        columns(yes, x0, no, x0, 0, 0, nullptr, stat(j), now, more);
-        if constexpr (KV) bwd_store16<KV>(tS, pr);
-        columns(yes, x1, no, x1, 16, 0, nullptr, stat(j), now, more);
-        if constexpr (KV) {
-          bwd_store16<KV>(tS + 16, pr + 16);
+          for (int c = 0; c < 16; ++c) packed[c] = ptx::pack_bf16x2(pr[2 * c], pr[2 * c + 1]);
+          bwd_store_pairs(tS, packed);
           ptx::tmem_wait_st();
           ptx::tc_fence_before_sync();
-          arrive(bars->p_ready);
+          arrive(bars->p_ready[sb]);
         }
         ok = bwd_wait_warp(bars->dp_full, j & 1, bars, p);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        bwd_load16<KV>(tDP, x0, tDP + 16, x1);
-        if constexpr (!KV) dp_read();
-        // over columns that have been read: dP's (dK dV), or S's
-        columns(no, x0, yes, x0, 0, KV ? tDP : tS, stat(j) + 128, nullptr, now, more);
-        columns(no, x1, yes, x1, 16, (KV ? tDP : tS) + 16, stat(j) + 128, nullptr, now, more);
+        constexpr bool DP_FREE = !KV || T::NS == 2;  // dS goes over S's columns, not dP's
+        auto dp_read = [&]() {
+          if constexpr (DP_FREE) {
+            ptx::tc_fence_before_sync();
+            arrive(bars->dp_free);
+          }
+        };
+        if constexpr (KV) {
+          uint32_t r[32], packed[16];
+          bwd_load_elements<true>(tDP, r);
+          dp_read();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 d = *reinterpret_cast<const float2*>(dcol + 8 * i);
+#pragma unroll
+            for (int k = 8 * i; k < 8 * i + 8; k += 2) {
+              const float2 x = __fadd2_rn(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])),
+                                          d);
+              const float2 s = __fmul2_rn(x, make_float2(pr[k], pr[k + 1]));
+              packed[k / 2] = ptx::pack_bf16x2(s.x, s.y);
+            }
+          }
+          bwd_store_pairs(DP_FREE ? tS + 16 : tDP, packed);
+        } else {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t r[16], packed[8];
+            ptx::tmem_ld32x32b_x16(tDP + half * 16, r);
+            if (half == 1) dp_read();
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const int k = half * 16 + c;
+              const float2 x = __fadd2_rn(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])),
+                                          make_float2(ndelta, ndelta));
+              const float2 s = __fmul2_rn(x, make_float2(pr[k], pr[k + 1]));
+              packed[c / 2] = ptx::pack_bf16x2(s.x, s.y);
+            }
+            ptx::tmem_st32x32b_x8(tS + half * 8, packed);
+          }
+        }
         ptx::tmem_wait_st();
         ptx::tc_fence_before_sync();
         arrive(bars->ds_ready[sb]);
-        if constexpr (KV) arrive(bars->st_empty[j % C::STATS]);
+        if constexpr (KV) arrive(bars->st_empty[j & 1]);
       }
       if (!ok) break;
 
@@ -905,12 +840,12 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         ++nu;
         ptx::tc_fence_after_sync();
       }
-      constexpr int NC = T::ACC / C::GROUPS;
+      constexpr int NC = T::ACC / kBwdGroups;
       const uint32_t tA = t0 + wg * NC;
       if (pc.slot < 0) {
-        const bool is_dv = KV && wg < C::GROUPS / 2;
+        const bool is_dv = KV && wg < kBwdGroups / 2;
         const BwdTensor& o = KV ? (is_dv ? p.dv : p.dk) : p.dq;
-        const int col = KV ? (wg % (C::GROUPS / 2)) * NC : wg * NC;
+        const int col = KV ? (wg % (kBwdGroups / 2)) * NC : wg * NC;
         const bool in = my < (KV ? p.Nk : p.Nq) && bwd_check(p, bars, pc.head < plan.units.heads && col + NC <= D,
                                                             kCheckGradStore, pc.head, my);
         bwd_store_row<NC>(tA, is_dv ? 1.f : p.scale, zero, in, o.p + b * o.b + h * o.h + (long long)my * o.n + col);
@@ -926,7 +861,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
 }
 
 template <int D, int MK>
-__global__ void __launch_bounds__(BwdCfg<D, MK>::THREADS, 1) fa_bwd_kernel(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_kernel(const __grid_constant__ BwdParams p) {
   using C = BwdCfg<D, MK>;
   extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + (2 + C::RING0 + C::RING1) * C::TILE + C::STAT_BYTES + C::MASK_BYTES);
@@ -942,17 +877,21 @@ __global__ void __launch_bounds__(BwdCfg<D, MK>::THREADS, 1) fa_bwd_kernel(const
     init(bars->b_empty, 1);
     for (int i = 0; i < C::RING0; ++i) init(bars->r0_full[i], 1), init(bars->r0_empty[i], 1);
     for (int i = 0; i < C::RING1; ++i) init(bars->r1_full[i], 1), init(bars->r1_empty[i], 1);
-    for (int i = 0; i < C::STATS; ++i) init(bars->st_full[i], 1), init(bars->st_empty[i], C::WARPS);
-    for (int i = 0; i < 2; ++i) init(bars->s_full[i], 1), init(bars->ds_ready[i], C::WARPS);
-    init(bars->p_ready, C::WARPS);
+    for (int i = 0; i < 2; ++i) {
+      init(bars->st_full[i], 1);
+      init(bars->st_empty[i], kBwdWarps);
+      init(bars->s_full[i], 1);
+      init(bars->p_ready[i], kBwdWarps);
+      init(bars->ds_ready[i], kBwdWarps);
+    }
     init(bars->dp_full, 1);
-    init(bars->dp_free, C::WARPS);
+    init(bars->dp_free, kBwdWarps);
     init(bars->acc_full, 1);
     init(bars->drain, 1);
     bars->abort_flag = 0;
     ptx::fence_barrier_init();
   }
-  if (threadIdx.x / 32 == C::WARPS + 1) {
+  if (threadIdx.x / 32 == kBwdWarps + 1) {
     ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), 512);
     ptx::tmem_relinquish();
   }

@@ -72,5 +72,5 @@ for n in (1, 2, 4):
     out.append(ss(n, "f8f6f4", True))
 out.append(ts(4, True))
 out.append(ts(8, True))
-out.append(ts(8, True, 1))
+out.append(ts(8, True, 2))
 open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "mma_batch.inc"), "w").write("\n".join(out))

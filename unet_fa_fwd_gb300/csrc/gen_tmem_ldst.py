@@ -32,59 +32,38 @@ __device__ __forceinline__ void tmem_st32x32b_x{n}(uint32_t taddr, const uint32_
       : "memory");
 }}
 '''
-SHAPES = {
-    # 16 columns of the warp's 32 lanes: (name, what, [(shape, lane offset, elements' places)])
-    "row": ("r[c] is this thread's lane, column c", [("32x32b.x16", 0, list(range(16)))]),
-    "quad": ("r[8 i + 2 j + c] is lane t / 4 + 8 j, column 8 i + 2 (t % 4) + c",
-             [("16x256b.x2", 16 * h, [8 * (k // 4) + 4 * h + k % 4 for k in range(8)]) for h in (0, 1)]),
-}
-STORES = {
-    "quad": ("r[4 i + j] is lane t / 4 + 8 j, column 4 i + t % 4",
-             [("16x128b.x2", 16 * h, [4 * (k // 2) + 2 * h + k % 2 for k in range(4)]) for h in (0, 1)]),
-}
-def ld16(name, arrays):
-    """16 consecutive columns at each of `arrays` addresses, waited for once."""
-    what, parts = SHAPES[name]
-    outs, ins, lines = [], [], []
-    n = 16 * arrays
-    for a in range(arrays):
-        outs += [f'"=r"({"rs"[a]}[{i}])' for i in range(16)]
-        for shape, lane, at in parts:
-            regs = ",".join(f"%{16 * a + i}" for i in at)
-            lines.append(f'"tcgen05.ld.sync.aligned.{shape}.b32 {{{regs}}}, [%{n + len(ins)}];\\n"')
-            t = "taddr" if a == 0 else "saddr"
-            ins.append(f'"r"({t} + ({lane}u << 16))' if lane else f'"r"({t})')
-    body = "\n      ".join(lines)
-    two = arrays == 2
-    return f'''// 16 consecutive 32-bit TMEM columns of the warp's 32 lanes{" at each address" if two else ""}, waited for:
-// {what}.
-__device__ __forceinline__ void tmem_ld_{name}16{"_two" if two else ""}(uint32_t taddr, uint32_t (&r)[16]{", uint32_t saddr, uint32_t (&s)[16]" if two else ""}) {{
+def ld2(n):
+    """Two loads of 16 lanes by 256 bits: an element's place is 8 * (8-column block) + 2 * (row / 8) + its column."""
+    at = [[8 * (k // 4) + 4 * h + k % 4 for k in range(4 * n)] for h in (0, 1)]
+    outs = ", ".join(f'"=r"(r[{i}])' for i in range(8 * n))
+    lines = "\n      ".join(f'"tcgen05.ld.sync.aligned.16x256b.x{n}.b32 {{{{{",".join(f"%{i}" for i in at[h])}}}}}, [%{8 * n + h}];\\n"'
+                             for h in (0, 1)).replace("{{", "{").replace("}}", "}")
+    return f'''// {8 * n} consecutive 32-bit TMEM columns of the warp's 32 lanes, waited for: r[8 i + 2 j + c]
+// is lane t / 4 + 8 j, column 8 i + 2 (t % 4) + c.
+__device__ __forceinline__ void tmem_ld2x16x256b_x{n}(uint32_t taddr, uint32_t (&r)[{8 * n}]) {{
   __syncwarp();
   asm volatile(
-      {body}
+      {lines}
       "tcgen05.wait::ld.sync.aligned;\\n"
-      : {", ".join(outs)}
-      : {", ".join(ins)}
+      : {outs}
+      : "r"(taddr), "r"(taddr + (16u << 16))
       : "memory");
 }}
 '''
-def st8(name):
-    what, parts = STORES[name]
-    lines, addr = [], []
-    for i, (shape, lane, at) in enumerate(parts):
-        regs = ",".join(f"%{len(parts) + k}" for k in at)
-        lines.append(f'"tcgen05.st.sync.aligned.{shape}.b32 [%{i}], {{{regs}}};\\n"')
-        addr.append(f'"r"(taddr + ({lane}u << 16))' if lane else '"r"(taddr)')
-    body = "\n      ".join(lines)
-    ins = ", ".join(f'"r"(r[{i}])' for i in range(8))
-    return f'''// Store 8 consecutive 32-bit TMEM columns of the warp's 32 lanes (not waited for):
-// {what}.
-__device__ __forceinline__ void tmem_st_{name}8(uint32_t taddr, const uint32_t (&r)[8]) {{
+def st2(n):
+    """The same pairs of columns, packed in one: two stores of 16 lanes by 128 bits."""
+    at = [[4 * (k // 2) + 2 * h + k % 2 + 2 for k in range(2 * n)] for h in (0, 1)]
+    ins = ", ".join(f'"r"(r[{i}])' for i in range(4 * n))
+    lines = "\n      ".join(f'"tcgen05.st.sync.aligned.16x128b.x{n}.b32 [%{h}], {{{{{",".join(f"%{i}" for i in at[h])}}}}};\\n"'
+                             for h in (0, 1)).replace("{{", "{").replace("}}", "}")
+    return f'''// Store {4 * n} consecutive 32-bit TMEM columns of the warp's 32 lanes (not waited for): r[4 i + j]
+// is lane t / 4 + 8 j, column 4 i + t % 4.
+__device__ __forceinline__ void tmem_st2x16x128b_x{n}(uint32_t taddr, const uint32_t (&r)[{4 * n}]) {{
   __syncwarp();
   asm volatile(
-      {body}
+      {lines}
       :
-      : {", ".join(addr)}, {ins}
+      : "r"(taddr), "r"(taddr + (16u << 16)), {ins}
       : "memory");
 }}
 '''
@@ -93,7 +72,8 @@ for n in (8, 16, 32, 64, 128):
     out.append(ld(n))
 for n in (8, 16, 32):
     out.append(st(n))
-out += [ld16("row", 2), ld16("quad", 1), ld16("quad", 2), st8("quad")]
+out.append(ld2(4))
+out.append(st2(4))
 open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "tmem_ldst.inc"), "w").write(
 "// Long-hand tcgen05.ld / tcgen05.st wrappers (32x32b shape: thread t of warp w\n"
 "// addresses TMEM lane 32*(w%4)+t).  Each load waits (tcgen05.wait::ld) inside the\n"
