@@ -899,6 +899,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_kernel(const __grid_con
   __syncthreads();
   ptx::tc_fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // -L, -delta and a mask's bits are there
   const int cta = blockIdx.x, keys = p.plan[0].ctas;
   if (cta < keys)
@@ -961,50 +962,39 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
 }
 
 // A boolean mask as bits, by query rows and by key rows: a warp turns 32 rows of
-// 128 bytes into words, one ballot a row and 32 keys.
+// 32 bytes into words, one ballot a row.  Latency bound: a warp's 32 loads are in
+// flight together (2 x 1777 x 1777 pairs: 4 us, with 128 bytes a row a warp and 16
+// loads at a time 20).
 struct BwdBitsParams {
   const uint8_t* mask;  // [B mask_heads][Nq][Nk]
   uint32_t *bits_q, *bits_k;
-  int Nq, Nk, words_q, words_k;
-  int blocks_q, blocks_k;  // 32-row and 128-key blocks of a head, whole tiles of both
-  long long blocks;
+  int Nq, Nk, words_q, words_k;  // words of a row: 32-key and 32-row blocks of whole tiles
+  long long blocks;              // words_k x words_q of every head
 };
 
 static __global__ void __launch_bounds__(256) fa_bwd_bits_kernel(const __grid_constant__ BwdBitsParams p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long i = (long long)blockIdx.x * 8 + threadIdx.x / 32;
   if (i >= p.blocks) return;
   const int lane = threadIdx.x % 32;
-  const long long per = (long long)p.blocks_q * p.blocks_k;
+  const long long per = (long long)p.words_k * p.words_q;
   const long long bh = i / per;
-  const int bq = (int)((i - bh * per) / p.blocks_k), bk = (int)(i - bh * per - (long long)bq * p.blocks_k);
-  const uint8_t* base = p.mask + bh * p.Nq * p.Nk;
-  uint32_t row[4] = {}, col[4] = {};
-#pragma unroll 4
+  const int bq = (int)((i - bh * per) / p.words_q), bk = (int)(i - bh * per - (long long)bq * p.words_q);
+  const int k = bk * 32 + lane;
+  const uint8_t* base = p.mask + bh * p.Nq * p.Nk + min(k, p.Nk - 1);
+  uint32_t v[32];  // (past the last row or key: that one again)
+#pragma unroll
+  for (int y = 0; y < 32; ++y) v[y] = __ldg(base + (size_t)min(bq * 32 + y, p.Nq - 1) * p.Nk);
+  uint32_t row = 0, col = 0;
+#pragma unroll
   for (int y = 0; y < 32; ++y) {
-    const int q = bq * 32 + y;
-    uint8_t v[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int k = bk * 128 + g * 32 + lane;
-      v[g] = q < p.Nq && k < p.Nk ? base[(size_t)q * p.Nk + k] : 0;
-    }
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const uint32_t w = __ballot_sync(0xffffffffu, v[g] != 0);
-      if (lane == y) row[g] = w;
-      col[g] |= (v[g] != 0 ? 1u : 0u) << y;
-    }
+    const bool keep = v[y] != 0 && k < p.Nk && bq * 32 + y < p.Nq;
+    const uint32_t w = __ballot_sync(0xffffffffu, keep);
+    if (lane == y) row = w;
+    col |= (keep ? 1u : 0u) << y;
   }
   const int q = bq * 32 + lane;
-  if (q < p.Nq)
-    *reinterpret_cast<uint4*>(p.bits_q + ((size_t)bh * p.Nq + q) * p.words_q + bk * 4) =
-        make_uint4(row[0], row[1], row[2], row[3]);
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int k = bk * 128 + g * 32 + lane;
-    if (k < p.Nk) p.bits_k[((size_t)bh * p.Nk + k) * p.words_k + bq] = col[g];
-  }
+  if (q < p.Nq) p.bits_q[((size_t)bh * p.Nq + q) * p.words_q + bk] = row;
+  if (k < p.Nk) p.bits_k[((size_t)bh * p.Nk + k) * p.words_k + bq] = col;
 }
 
 // Joins the partial sums of cut units, in the order of their pieces.  Block

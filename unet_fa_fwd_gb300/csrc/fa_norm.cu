@@ -28,30 +28,34 @@ size_t part_bytes(int D) { return (size_t)fa::kNormMaxBlocks * 2 * D * sizeof(fl
 
 template <typename T, int D, bool VEC, bool HALVES, bool BACK>
 int launch(NormParams& p, int sm_count, float* dwq, float* dwk, cudaStream_t s) {
-  constexpr int E = 16 / sizeof(T), CHUNKS = D / (E * (HALVES ? 2 : 1)), TOKENS = fa::kNormThreads / CHUNKS;
-  constexpr int BATCH = BACK ? 2 : 4;
-  const long long blocks = (p.tokens + TOKENS - 1) / TOKENS;
-  // Heads are dealt to several blocks a token until the SMs' 4 blocks are
-  // filled; sines and weights are computed once for each of them.
-  const int batches = (p.heads + BATCH - 1) / BATCH;
-  const long long fill = (4LL * sm_count + blocks - 1) / blocks;
-  const int groups = (int)(fill < batches ? fill : batches);
-  const int per = (batches + groups - 1) / groups;
-  p.heads_per_item = per * BATCH;
-  p.groups = (batches + per - 1) / per;
-  if (blocks > LLONG_MAX / p.groups) return FA_ERR_INVALID_ARGUMENT;
-  p.items = blocks * p.groups;
-  long long grid = p.items;
-  if (BACK) {  // a row of partial sums for each block
-    const long long most = 4LL * sm_count < fa::kNormMaxBlocks ? 4LL * sm_count : fa::kNormMaxBlocks;
-    grid = grid < most ? grid : most;
-  } else if (grid > INT_MAX) {
-    grid = INT_MAX;
+  using Shape = fa::NormShape<T, D, HALVES, BACK>;
+  const long long blocks = p.blocks = (p.tokens + Shape::TOKENS - 1) / Shape::TOKENS;
+  for (int i = 0; i < 2; ++i) p.batches[i] = (p.t[i].H + Shape::BATCH - 1) / Shape::BATCH;
+  const int batches = p.batches[0] + p.batches[1];
+  if (blocks > LLONG_MAX / batches / (2 * fa::kNormMaxBlocks)) return FA_ERR_INVALID_ARGUMENT;
+  long long grid;
+  if (BACK) {
+    // The blocks that are resident share the batches of heads evenly, q's before
+    // k's: each leaves a row of partial sums for either.
+    p.items = blocks * batches;
+    const long long most = (long long)fa::kNormBackPerSm * sm_count;
+    grid = most < fa::kNormMaxBlocks ? most : fa::kNormMaxBlocks;
+    grid = p.items < grid ? p.items : grid;
+  } else {
+    // Heads are dealt to several blocks a token until the SMs' 4 blocks are
+    // filled; sines and weights are computed once for each of them.
+    const int all = (p.heads + Shape::BATCH - 1) / Shape::BATCH;
+    const long long fill = (4LL * sm_count + blocks - 1) / blocks;
+    const int groups = (int)(fill < all ? fill : all), per = (all + groups - 1) / groups;
+    p.heads_per_item = per * Shape::BATCH;
+    p.groups = (all + per - 1) / per;
+    p.items = blocks * p.groups;
+    grid = p.items < INT_MAX ? p.items : INT_MAX;
   }
   fa::log_launch("fa_norm_rope_kernel<D=%d,%d-byte elements,%s,%s,%s> grid %lld x %d threads, %lld tokens, %d heads "
-                 "(%d an item)", D, (int)sizeof(T), VEC ? "16-byte accesses" : "single elements",
+                 "(%d batches)", D, (int)sizeof(T), VEC ? "16-byte accesses" : "single elements",
                  HALVES ? "halves" : "adjacent", BACK ? "gradient" : "forward", grid, fa::kNormThreads, p.tokens,
-                 p.heads, p.heads_per_item);
+                 p.heads, batches);
   fa::fa_norm_rope_kernel<T, D, VEC, HALVES, BACK><<<(unsigned)grid, fa::kNormThreads, 0, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (!BACK || !p.part) return FA_OK;

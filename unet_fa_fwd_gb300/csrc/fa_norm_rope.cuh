@@ -8,8 +8,8 @@
 //
 // HBM bound: x (and dy) are read once and y (dx) written once; r is computed
 // again in the gradient, so nothing is kept for it.  A thread owns one 16-byte
-// piece of a token's row (two, half a row apart, when the pairs are the row's
-// halves) and walks heads with its pairs' sines and its weights in registers;
+// piece of a token's row (when the pairs are the row's halves two, half a row
+// apart, of 8 elements together in 16 bits) and walks heads with its pairs' sines and its weights in registers;
 // the threads of a row are neighbours in a warp and sum by shuffles.
 //
 // dw: a thread adds up its elements over all its rows, a block's threads are
@@ -26,6 +26,7 @@
 namespace fa {
 
 constexpr int kNormThreads = 256;
+constexpr int kNormBackPerSm = 2;     // blocks of the gradient that are resident
 constexpr int kNormMaxBlocks = 1024;  // blocks of the gradient (rows of partial sums)
 constexpr int kNormReduceRows = 32;   // rows of threads of the second kernel
 
@@ -42,23 +43,38 @@ struct NormParams {
   NormTensor t[2];   // q, k (k.H = 0: none)
   const int* pos;    // [B][N][A], batch stride pos_b (0: shared)
   long long pos_b;
-  int A, N, heads, heads_per_item, groups;
+  int A, N, heads;
+  int heads_per_item, groups;      // forward
+  int batches[2];                  // gradient: batches of heads of q, of k
   int w_f32;         // weights are fp32, else of the tensors' type
   float eps;
   long long tokens;  // B * N
-  long long items;   // token blocks x head groups
+  long long blocks;  // blocks of tokens
+  long long items;   // forward: token blocks x head groups; gradient: x batches of heads, q's before k's
   float* part;       // gradient with weights: [gridDim.x][2][D]
   unsigned long long freq[kRopeMaxPairs];
   unsigned char axis[kRopeMaxPairs];
 };
 
-// E elements at p, 16 bytes' worth: one access where rows are 16-byte aligned
+// How a row is dealt to threads.
+template <typename T, int D, bool HALVES, bool BACK>
+struct NormShape {
+  static constexpr int PIECES = HALVES ? 2 : 1;
+  static constexpr int E = HALVES && sizeof(T) == 2 ? 4 : 16 / (int)sizeof(T);  // elements of a piece
+  static constexpr int NE = E * PIECES, CHUNKS = D / NE;                        // of a thread; threads a row
+  static constexpr int BATCH = 4;  // heads whose loads are in flight together
+  static constexpr int TOKENS = kNormThreads / CHUNKS;
+};
+
+// E elements at p, 16 or 8 bytes' worth: one access where rows are 16-byte aligned
 // (VEC), else one by one.
 template <typename T, int E, bool VEC>
 struct alignas(16) NormVec {
   T v[E];
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (VEC) {
+    if constexpr (VEC && E * sizeof(T) == 8) {
+      *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
+    } else if constexpr (VEC) {
       *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
     } else {
 #pragma unroll
@@ -66,7 +82,9 @@ struct alignas(16) NormVec {
     }
   }
   __device__ __forceinline__ void store(T* p) const {
-    if constexpr (VEC) {
+    if constexpr (VEC && E * sizeof(T) == 8) {
+      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
+    } else if constexpr (VEC) {
       *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
     } else {
 #pragma unroll
@@ -84,29 +102,21 @@ __device__ __forceinline__ float norm_row_sum(float v) {
 }
 
 template <typename T, int D, bool VEC, bool HALVES, bool BACK>
-__global__ void __launch_bounds__(kNormThreads) fa_norm_rope_kernel(const __grid_constant__ NormParams p) {
-  constexpr int E = 16 / sizeof(T);
-  constexpr int PIECES = HALVES ? 2 : 1;
-  constexpr int CHUNKS = D / (E * PIECES);  // threads per token
-  constexpr int NE = E * PIECES;            // elements per thread
+__global__ void __launch_bounds__(kNormThreads, VEC && !BACK ? 3 : 2)
+    fa_norm_rope_kernel(const __grid_constant__ NormParams p) {
+  using Shape = NormShape<T, D, HALVES, BACK>;
+  constexpr int E = Shape::E, PIECES = Shape::PIECES, NE = Shape::NE, CHUNKS = Shape::CHUNKS, BATCH = Shape::BATCH;
   constexpr int PAIRS = NE / 2;
-  constexpr int BATCH = BACK ? 2 : 4;       // heads whose loads are in flight together
   static_assert(CHUNKS <= 32 && 32 % CHUNKS == 0, "a row's threads share a warp");
   using Vec = NormVec<T, E, VEC>;
+  if constexpr (BACK) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the weights' kernel waits itself
   const int chunk = threadIdx.x % CHUNKS;
   // element i of this thread: column chunk * E + i, the second piece half a row on
   auto column = [&](int i) { return chunk * E + (i < E ? i : i - E + D / 2); };
 
-  float acc[BACK ? 2 : 1][NE];
-#pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    acc[0][i] = 0.f;
-    if constexpr (BACK) acc[1][i] = 0.f;
-  }
-  for (long long item = blockIdx.x; item < p.items; item += gridDim.x) {
-    const long long tb = item / p.groups;
-    const int h0 = (int)(item - tb * p.groups) * p.heads_per_item;
-    const int h1 = min(h0 + p.heads_per_item, p.heads);
+  float acc[NE] = {};  // dw of one tensor
+  // Heads h0 .. h1 - 1 of a block of tokens.
+  auto rows = [&](long long tb, int h0, int h1) {
     long long token = tb * (kNormThreads / CHUNKS) + threadIdx.x / CHUNKS;
     const bool live = token < p.tokens;  // threads past the end read the last token and write nothing
     if (!live) token = p.tokens - 1;
@@ -174,7 +184,7 @@ __global__ void __launch_bounds__(kNormThreads) fa_norm_rope_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
               const float nrm = x[i] * r;
-              if (count) acc[ti][i] = fmaf(y[i], nrm, acc[ti][i]);
+              if (count) acc[i] = fmaf(y[i], nrm, acc[i]);
               y[i] = r * (y[i] * w[i] - nrm * mean);
             }
           } else {
@@ -198,27 +208,47 @@ __global__ void __launch_bounds__(kNormThreads) fa_norm_rope_kernel(const __grid
         }
       }
     }
-  }
-  if constexpr (BACK) {
-    if (p.part == nullptr) return;
-    // The warp's rows, then the block's warps, in a fixed order.
-    __shared__ float sum[kNormThreads / 32][2][D];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  };
+  if constexpr (BACK) {  // an even share of all batches, in order
+    __shared__ float sum[kNormThreads / 32][D];
+    const long long split = p.blocks * p.batches[0];
+    long long i = p.items * blockIdx.x / gridDim.x;
+    const long long end = p.items * (blockIdx.x + 1LL) / gridDim.x;
+#pragma unroll 1
+    for (int ti = 0; ti < 2; ++ti) {
+      const long long base = ti ? split : 0, stop = ti ? end : min(end, split);
+      const int batches = p.batches[ti], from = ti ? p.t[0].H : 0, to = ti ? p.heads : p.t[0].H;
+      while (i < stop) {
+        const long long tb = (i - base) / batches;
+        const int first = (int)(i - base - tb * batches), n = (int)min((long long)(batches - first), stop - i);
+        rows(tb, from + first * BATCH, min(from + (first + n) * BATCH, to));
+        i += n;
+      }
+      if (p.part == nullptr) continue;
+      // The warp's rows, then the block's warps, in a fixed order.
+      const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+      if (ti) __syncthreads();  // (the first tensor's sums have been read)
 #pragma unroll
-    for (int ti = 0; ti < 2; ++ti)
-#pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        float v = acc[ti][i];
+      for (int k = 0; k < NE; ++k) {
+        float v = acc[k];
 #pragma unroll
         for (int m = CHUNKS; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-        if (lane < CHUNKS) sum[warp][ti][column(i)] = v;
+        if (lane < CHUNKS) sum[warp][column(k)] = v;
+        acc[k] = 0.f;
       }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += kNormThreads) {
-      float v = 0.f;
+      __syncthreads();
+      for (int c = threadIdx.x; c < D; c += kNormThreads) {
+        float v = 0.f;
 #pragma unroll
-      for (int k = 0; k < kNormThreads / 32; ++k) v += (&sum[k][0][0])[i];
-      p.part[(long long)blockIdx.x * 2 * D + i] = v;
+        for (int k = 0; k < kNormThreads / 32; ++k) v += sum[k][c];
+        p.part[((long long)blockIdx.x * 2 + ti) * D + c] = v;
+      }
+    }
+  } else {
+    for (long long item = blockIdx.x; item < p.items; item += gridDim.x) {
+      const long long tb = item / p.groups;
+      const int h0 = (int)(item - tb * p.groups) * p.heads_per_item;
+      rows(tb, h0, min(h0 + p.heads_per_item, p.heads));
     }
   }
 }
