@@ -281,7 +281,7 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
     bp.Nk = Nk;
     bp.words_q = p.words_q;
     bp.words_k = p.words_k;
-    bp.blocks = (long long)B * mask_heads * p.words_k * p.words_q;
+    bp.blocks = (long long)B * mask_heads * p.words_k * kt;
     rc = fa::launch_bwd_bits(bp, s);
     if (rc != FA_OK) return rc;
   }

@@ -962,39 +962,62 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
 }
 
 // A boolean mask as bits, by query rows and by key rows: a warp turns 32 rows of
-// 32 bytes into words, one ballot a row.  Latency bound: a warp's 32 loads are in
-// flight together (2 x 1777 x 1777 pairs: 4 us, with 128 bytes a row a warp and 16
-// loads at a time 20).
+// 128 bytes, a lane 4 of each.  Rows start at any byte: a lane reads the aligned
+// words that its bytes lie in (words with no byte of the row are not read) and
+// shifts them together.
 struct BwdBitsParams {
   const uint8_t* mask;  // [B mask_heads][Nq][Nk]
   uint32_t *bits_q, *bits_k;
   int Nq, Nk, words_q, words_k;  // words of a row: 32-key and 32-row blocks of whole tiles
-  long long blocks;              // words_k x words_q of every head
+  long long blocks;              // 32 rows x 128 keys of every head
 };
 
 static __global__ void __launch_bounds__(256) fa_bwd_bits_kernel(const __grid_constant__ BwdBitsParams p) {
   const long long i = (long long)blockIdx.x * 8 + threadIdx.x / 32;
   if (i >= p.blocks) return;
-  const int lane = threadIdx.x % 32;
-  const long long per = (long long)p.words_k * p.words_q;
+  const int lane = threadIdx.x % 32, tiles_k = p.words_q / 4;
+  const long long per = (long long)p.words_k * tiles_k;
   const long long bh = i / per;
-  const int bq = (int)((i - bh * per) / p.words_q), bk = (int)(i - bh * per - (long long)bq * p.words_q);
-  const int k = bk * 32 + lane;
-  const uint8_t* base = p.mask + bh * p.Nq * p.Nk + min(k, p.Nk - 1);
-  uint32_t v[32];  // (past the last row or key: that one again)
+  const int bq = (int)((i - bh * per) / tiles_k), bk = (int)(i - bh * per - (long long)bq * tiles_k);
+  const int k = bk * 128 + lane * 4;  // this lane's first key
+  const int rows = min(32, p.Nq - bq * 32), valid = min(max(p.Nk - k, 0), 4);
+  const uint32_t keep = valid == 4 ? ~0u : (1u << (8 * valid)) - 1;
+  const uint8_t* at = p.mask + (bh * p.Nq + bq * 32) * p.Nk + k;
+  uint32_t col[4] = {}, word = 0;
 #pragma unroll
-  for (int y = 0; y < 32; ++y) v[y] = __ldg(base + (size_t)min(bq * 32 + y, p.Nq - 1) * p.Nk);
-  uint32_t row = 0, col = 0;
+  for (int y0 = 0; y0 < 32; y0 += 8) {
+    uint32_t lo[8], hi[8];
 #pragma unroll
-  for (int y = 0; y < 32; ++y) {
-    const bool keep = v[y] != 0 && k < p.Nk && bq * 32 + y < p.Nq;
-    const uint32_t w = __ballot_sync(0xffffffffu, keep);
-    if (lane == y) row = w;
-    col |= (keep ? 1u : 0u) << y;
+    for (int y = 0; y < 8; ++y) {
+      const uint8_t* q = at + (long long)(y0 + y) * p.Nk;
+      const int off = (int)(reinterpret_cast<uintptr_t>(q) & 3);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(q - off);
+      const bool live = y0 + y < rows && valid > 0;
+      lo[y] = live ? __ldg(w) : 0;
+      hi[y] = live && off + valid > 4 ? __ldg(w + 1) : 0;
+    }
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const int off = (int)(reinterpret_cast<uintptr_t>(at + (long long)(y0 + y) * p.Nk) & 3);
+      uint32_t t = __funnelshift_r(lo[y], hi[y], 8 * off) & keep;
+      t |= t >> 4;  // bit 0 of each byte: any of its bits (what shifts in from the next byte stays above bit 0)
+      t |= t >> 2;
+      t |= t >> 1;
+      t &= 0x01010101u;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) col[c] |= ((t >> (8 * c)) & 1u) << (y0 + y);
+      uint32_t r = (t * 0x01020408u) >> 24 << (4 * (lane % 8));  // the four bits together
+      r |= __shfl_xor_sync(0xffffffffu, r, 1);
+      r |= __shfl_xor_sync(0xffffffffu, r, 2);
+      r |= __shfl_xor_sync(0xffffffffu, r, 4);
+      if (lane % 8 == y) word = r;
+    }
+    const int q = bq * 32 + y0 + lane % 8;
+    if (q < p.Nq) p.bits_q[((size_t)bh * p.Nq + q) * p.words_q + bk * 4 + lane / 8] = word;
   }
-  const int q = bq * 32 + lane;
-  if (q < p.Nq) p.bits_q[((size_t)bh * p.Nq + q) * p.words_q + bk] = row;
-  if (k < p.Nk) p.bits_k[((size_t)bh * p.Nk + k) * p.words_k + bq] = col;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c < valid) p.bits_k[((size_t)bh * p.Nk + k + c) * p.words_k + bq] = col[c];
 }
 
 // Joins the partial sums of cut units, in the order of their pieces.  Block
