@@ -148,7 +148,7 @@ def _positions(pos: torch.Tensor, B: int, N: int, A: int, device: int) -> int:
 def _rope_new(shape, dtype, device, token_major) -> torch.Tensor:
     B, H, N, D = shape
     if token_major:
-        return torch.empty((B, N, H, D), dtype=dtype, device=device).transpose(1, 2)
+        return torch.empty_strided(shape, (N * H * D, D, H * D, 1), dtype=dtype, device=device)
     return torch.empty(shape, dtype=dtype, device=device)
 
 

@@ -13,6 +13,7 @@ Outputs and workspaces are allocated on the stream that the call runs on.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 
@@ -23,9 +24,12 @@ from .binding import (FA_MASK_ADDITIVE, FA_MASK_BOOL, FA_MASK_KEY_PADDING, FA_OK
 from .cache import (_BF16, _DTYPES, _F32, _PAIRINGS, _SIZE, RopeAxes, _bhnd, _exact, _given, _positions, _raise, _rope_new,
                     _run, _strided)
 
-# Six and eight fa_tensor structs side by side (pointer and three strides each).
-_Tensors6 = ctypes.c_longlong * 24
-_Tensors8 = ctypes.c_longlong * 32
+
+def _tensors(fields) -> tuple:
+    """fa_tensor structs side by side (pointer and three strides each), which live as long as the first result, and
+    their address."""
+    ts = array.array("q", fields)
+    return ts, ts.buffer_info()[0]
 
 
 def _norm(q, k, q_weight, k_weight, eps, device) -> FaNorm:
@@ -73,8 +77,7 @@ def _norm_rope(q, k, pos, axes, q_weight, k_weight, eps, q_out, k_out, new, toke
         Hk = _bhnd(k, "k")[1]
         more, k_out = _side((k, k_out), ("k", "k_out"), (B, Hk, N, D), dtype, device, new, token_major)
         fields += more
-    ts = _Tensors6(*fields)
-    at = ctypes.addressof(ts)
+    ts, at = _tensors(fields)
     rc = load_library().fa_norm_rope(axes.ref, ctypes.byref(norm), pos.data_ptr(), pos_b, at, at + _SIZE, Hq,
                                      at + 2 * _SIZE if k is not None else None,
                                      at + 3 * _SIZE if k is not None else None, Hk, B, N, D, _DTYPES[dtype],
@@ -137,8 +140,7 @@ def _norm_rope_bwd(dq_out, dk_out, q, k, pos, axes, q_weight, k_weight, eps, dq,
     at_w = [None if dw is None else _exact(dw, name, _F32, (D,), device)
             for dw, name in ((dwq, "dq_weight"), (dwk, "dk_weight"))]
     ws_ptr, ws_bytes = _workspace(workspace, device)
-    ts = _Tensors6(*fields)
-    at = ctypes.addressof(ts)
+    ts, at = _tensors(fields)
     kt = [at + i * _SIZE if k is not None else None for i in (3, 4, 5)]
     rc = lib.fa_norm_rope_bwd(axes.ref, ctypes.byref(norm), pos.data_ptr(), pos_b, at, at + _SIZE, at + 2 * _SIZE, Hq,
                               *kt, Hk, *at_w, B, N, D, _DTYPES[dtype], _PAIRINGS[pairing], ws_ptr, ws_bytes, handle)
@@ -227,8 +229,7 @@ def _bwd(dout, q, k, v, out, lse, dlse, key_mask, full_mask, causal, scale, dq, 
     lse_at = _exact(lse, "lse", _F32, (B, Hq, Nq), device)
     dlse_at = None if dlse is None else _exact(dlse, "dlse", _F32, (B, Hq, Nq), device)
     ws_ptr, ws_bytes = _workspace(workspace, device)
-    ts = _Tensors8(*fields)
-    at = ctypes.addressof(ts)
+    ts, at = _tensors(fields)
     rc = lib.fa_bwd(*(at + i * _SIZE for i in range(5)), lse_at, dlse_at,
                     _mask(key_mask, full_mask, B, Hq, Nq, Nk, device), causal,
                     *(at + i * _SIZE for i in range(5, 8)), B, Hq, Hk, Nq, Nk, D,
