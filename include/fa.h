@@ -393,8 +393,8 @@ FA_API size_t fa_norm_rope_workspace_bytes(int D);
  * start 16-byte aligned; no axis is broadcast (stride 0).  Results share no
  * element with the other tensors or each other (tensors of two lengths: no range).
  *
- * A row that sees no key (LSE = -inf) has no gradient: its dQ is 0 and it adds
- * nothing to dK and dV; keys that no row sees have dK = dV = 0.  P and dS are
+ * A row that sees no key (LSE = -inf) has no gradient, whatever its dLSE: its dQ is 0
+ * and it adds nothing to dK and dV; keys that no row sees have dK = dV = 0.  P and dS are
  * rounded to bf16 for the products that take them; everything else is fp32, in a
  * fixed order: results repeat bit for bit on one GPU.  Numbers in q, k, v, out or
  * dout that are not finite, in masked places too, may turn any gradient of
