@@ -32,6 +32,12 @@ def _tensors(fields) -> tuple:
     return ts, ts.buffer_info()[0]
 
 
+def _rope_strides(shape, token_major) -> tuple:
+    """The strides of a tensor that _rope_new allocates, but for the last."""
+    B, H, N, D = shape
+    return (N * H * D, D, H * D) if token_major else (H * N * D, N * D, D)
+
+
 def _norm(q, k, q_weight, k_weight, eps, device) -> FaNorm:
     D = q.shape[3]
     if k is None and k_weight is not None:
@@ -62,7 +68,7 @@ def _side(tensors, names, shape, dtype, device, new, token_major):
     out = tensors[-1]
     if new:
         out = _rope_new(shape, dtype, tensors[0].device, token_major)
-        return fields + (out.data_ptr(), *out.stride()[:3]), out
+        return fields + (out.data_ptr(), *_rope_strides(shape, token_major)), out
     return fields + _strided(out, names[-1], dtype, shape, device), out
 
 
@@ -217,12 +223,13 @@ def _bwd(dout, q, k, v, out, lse, dlse, key_mask, full_mask, causal, scale, dq, 
         fields += _strided(t, name, _BF16, shape, device)
     lib = load_library()
     if new:
-        dq, dk, dv = (_rope_new(shape, _BF16, q.device, token_major) for shape in (q_shape, k_shape, k_shape))
+        on = q.device
+        dq, dk, dv = (_rope_new(q_shape, _BF16, on, token_major), _rope_new(k_shape, _BF16, on, token_major),
+                      _rope_new(k_shape, _BF16, on, token_major))
         heads = 0 if full_mask is None or full_mask.dtype is _F32 or full_mask.dim() != 4 else full_mask.shape[1]
-        workspace = torch.empty(lib.fa_bwd_workspace_bytes(B, Hq, Hk, Nq, Nk, D, heads), dtype=torch.uint8,
-                                device=q.device)
-        for t in (dq, dk, dv):
-            fields += (t.data_ptr(), *t.stride()[:3])
+        workspace = torch.empty(lib.fa_bwd_workspace_bytes(B, Hq, Hk, Nq, Nk, D, heads), dtype=torch.uint8, device=on)
+        q_strides, k_strides = _rope_strides(q_shape, token_major), _rope_strides(k_shape, token_major)
+        fields += (dq.data_ptr(), *q_strides, dk.data_ptr(), *k_strides, dv.data_ptr(), *k_strides)
     else:
         for t, name, shape in ((dq, "dq", q_shape), (dk, "dk", k_shape), (dv, "dv", k_shape)):
             fields += _strided(t, name, _BF16, shape, device)
@@ -230,9 +237,9 @@ def _bwd(dout, q, k, v, out, lse, dlse, key_mask, full_mask, causal, scale, dq, 
     dlse_at = None if dlse is None else _exact(dlse, "dlse", _F32, (B, Hq, Nq), device)
     ws_ptr, ws_bytes = _workspace(workspace, device)
     ts, at = _tensors(fields)
-    rc = lib.fa_bwd(*(at + i * _SIZE for i in range(5)), lse_at, dlse_at,
-                    _mask(key_mask, full_mask, B, Hq, Nq, Nk, device), causal,
-                    *(at + i * _SIZE for i in range(5, 8)), B, Hq, Hk, Nq, Nk, D,
+    rc = lib.fa_bwd(at, at + _SIZE, at + 2 * _SIZE, at + 3 * _SIZE, at + 4 * _SIZE, lse_at, dlse_at,
+                    _mask(key_mask, full_mask, B, Hq, Nq, Nk, device), causal, at + 5 * _SIZE, at + 6 * _SIZE,
+                    at + 7 * _SIZE, B, Hq, Hk, Nq, Nk, D,
                     1.0 / math.sqrt(D) if scale is None else scale, ws_ptr, ws_bytes, handle)
     if rc != FA_OK:
         _raise("fa_bwd", rc)
