@@ -173,6 +173,47 @@ def test_two_masked_gradients_on_two_streams():
     assert all(torch.equal(u, w) for u, w in zip(got, want))
 
 
+def _packed(B, heads, Nq, Nk, cuts, seed):
+    """Sequences packed into one row (another offset for each head), some empty stretches."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    shift = torch.randint(0, 200, (B, heads, 1, 1), generator=g, device="cuda")
+    row = (torch.arange(Nq, device="cuda")[:, None] + shift) * cuts // (Nq + 200)
+    key = (torch.arange(Nk, device="cuda")[None] + shift) * cuts // (Nk + 200)
+    keep = row == key
+    keep[:, :, Nq // 3:Nq // 3 + 300] = False
+    return keep
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("B,Hq,Hk,Nq,Nk,per_head,causal", [
+    (1, 2, 2, 1500, 1500, False, False), (1, 2, 1, 2100, 900, True, False), (2, 4, 1, 700, 1300, True, True),
+    (1, 1, 1, 5000, 300, False, False), (1, 1, 1, 200, 4500, False, False), (1, 8, 8, 1300, 1300, True, True)])
+def test_tiles_without_a_kept_pair(D, B, Hq, Hk, Nq, Nk, per_head, causal):
+    """Tiles that a mask leaves empty are left out: at either end, in between, whole units, whole pieces of cut units."""
+    x = _inputs(B, Hq, Hk, Nq, Nk, D, full_mask=_packed(B, Hq if per_head else 1, Nq, Nk, 7, 3), causal=causal, dlse=True)
+    _check_bwd(fa.bwd(**x), x)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Nk,keys", [(5000, (3, 4100)), (4500, (4400, 4500)), (300, (0, 1)), (1000, (0, 0))])
+def test_key_tiles_without_a_key(D, Nk, keys):
+    m = torch.full((2, Nk), -math.inf, device="cuda")
+    m[:, keys[0]:keys[0] + 1] = 0.5
+    m[0, keys[1]:] = -0.25
+    m[1] = 0 if keys == (0, 0) else m[1]
+    x = _inputs(2, 2, 1, 333, Nk, D, key_mask=m, dlse=True)
+    _check_bwd(fa.bwd(**x), x)
+
+
+def test_one_pair_of_a_million():
+    keep = torch.zeros(1, 1, 1100, 1000, dtype=torch.bool, device="cuda")
+    keep[0, 0, 1027, 513] = True
+    x = _inputs(1, 2, 2, 1100, 1000, 64, full_mask=keep, dlse=True)
+    dq, dk, dv = got = fa.bwd(**x)
+    _check_bwd(got, x)
+    assert int((dv != 0).any(-1).sum()) == 2 and torch.equal(dv[:, :, 513], x["dout"][:, :, 1027])  # P = 1
+
+
 CHILD = r'''
 import sys, torch
 sys.path.insert(0, ROOT)

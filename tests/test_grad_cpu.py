@@ -201,11 +201,14 @@ def test_bwd_accepts(lib, kw):
 
 def test_bwd_workspace(lib):
     rows = 2 * 4 * 256  # whole tiles of queries
-    plain = 2 * rows * 4 + 2 * 192 * 3 * 128 * 128 * 4
+    plain = 2 * rows * 4 + 2 * 192 * 3 * 128 * 128 * 4 + 256  # (the last for the key tiles of a padding mask)
     assert fa.bwd_workspace_bytes(2, 4, 2, 200, 300, 128) == plain
     for heads in (1, 4):  # a boolean mask's bits, by rows of 3 key tiles and by keys of 2 query tiles
         bits = sum(-(-2 * heads * n // 256) * 256 for n in (200 * 3 * 16, 300 * 2 * 16))
-        assert fa.bwd_workspace_bytes(2, 4, 2, 200, 300, 128, heads) == plain + bits
+        # ... and the tiles with a kept pair: 4 bytes each, then as bits by either side
+        bits += sum(-(-2 * heads * n // 256) * 256 for n in (2 * 3 * 4, 3 * 4)) + 256 - 256
+        bits += -(-2 * heads * 2 * 4 // 256) * 256
+        assert fa.bwd_workspace_bytes(2, 4, 2, 200, 300, 128, heads) == plain - 256 + bits
     assert fa.bwd_workspace_bytes(2, 4, 2, 200, 300, 128, 3) == 0
     assert fa.bwd_workspace_bytes(2, 4, 2, 200, 300, 128, -1) == 0
     assert fa.bwd_workspace_bytes(2, 3, 2, 200, 300, 128) == 0

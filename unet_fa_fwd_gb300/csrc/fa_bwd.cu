@@ -18,8 +18,13 @@
 
 namespace fa {
 
-int launch_bwd_prep(const BwdPrepParams& p, int D, cudaStream_t s) {
-  const long long blocks = (p.rows + 256 / (D / 8) - 1) / (256 / (D / 8));
+int launch_bwd_prep(BwdPrepParams& p, int D, cudaStream_t s) {
+  p.row_blocks = (p.rows + 256 / (D / 8) - 1) / (256 / (D / 8));
+  const long long words = p.key_mask ? (long long)p.heads * p.tile_words_q
+                          : p.some   ? (long long)p.heads * ((long long)p.tiles_of_q * p.tile_words_q +
+                                                             (long long)p.tiles_of_k * p.tile_words_k)
+                                     : 0;
+  const long long blocks = p.row_blocks + (words + 7) / 8;
   if (blocks > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
   log_launch("fa_bwd_prep_kernel<D=%d> grid %lld x 256 threads, %lld rows", D, blocks, p.rows);
   switch (D) {
@@ -69,9 +74,10 @@ bool mask_ok(int B, int Hq, int Nq, int Nk, int heads) {
 
 // The workspace, in order (each part 256-byte aligned).  Partial sums are for
 // the most CTAs a plan has: it does not depend on the GPU.  bool_heads: heads of
-// a boolean mask (0: no such mask), whose bits are kept by rows and by keys.
+// a boolean mask (0: no such mask), whose bits are kept by rows and by keys, with
+// those of its tiles; without one, the key tiles' of a key-padding mask.
 struct Layout {
-  size_t nlse, ndelta, part_kv, part_q, bits_q, bits_k, total;
+  size_t nlse, ndelta, part_kv, part_q, bits_q, bits_k, some, tiles_q, tiles_k, total;
 };
 
 Layout layout(int B, int Hq, int Nq, int Nk, int D, int bool_heads) {
@@ -86,6 +92,9 @@ Layout layout(int B, int Hq, int Nq, int Nk, int D, int bool_heads) {
   l.part_q = off;   off += slots * tile;
   l.bits_q = off;   off += align256(masks * Nq * kt * 16);
   l.bits_k = off;   off += align256(masks * Nk * qt * 16);
+  l.some = off;     off += align256(masks * qt * kt * 4);
+  l.tiles_q = off;  off += align256((bool_heads ? masks * qt : B) * ((kt + 31) / 32) * 4);
+  l.tiles_k = off;  off += align256(masks * kt * ((qt + 31) / 32) * 4);
   l.total = off;
   return l;
 }
@@ -246,6 +255,10 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   p.bits_k = reinterpret_cast<uint32_t*>(ws + l.bits_k);
   p.words_q = kt * 4;
   p.words_k = qt * 4;
+  p.tiles_q = reinterpret_cast<uint32_t*>(ws + l.tiles_q);
+  p.tiles_k = reinterpret_cast<uint32_t*>(ws + l.tiles_k);
+  p.tile_words_q = (kt + 31) / 32;
+  p.tile_words_k = (qt + 31) / 32;
   p.dq = view(*dq);
   p.dk = view(*dk);
   p.dv = view(*dv);
@@ -277,6 +290,7 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
     bp.mask = static_cast<const uint8_t*>(mask_data);
     bp.bits_q = reinterpret_cast<uint32_t*>(ws + l.bits_q);
     bp.bits_k = reinterpret_cast<uint32_t*>(ws + l.bits_k);
+    bp.some = reinterpret_cast<uint8_t*>(ws + l.some);
     bp.Nq = Nq;
     bp.Nk = Nk;
     bp.words_q = p.words_q;
@@ -298,6 +312,16 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   pp.nqp = p.nqp;
   pp.rows = (long long)B * Hq * p.nqp;
   pp.div_h = fa::FastDiv::make((uint32_t)Hq);
+  if (kind == FA_MASK_BOOL) pp.some = reinterpret_cast<const uint32_t*>(ws + l.some);
+  if (kind == FA_MASK_KEY_PADDING) pp.key_mask = static_cast<const float*>(mask_data);
+  pp.tiles_q = reinterpret_cast<uint32_t*>(ws + l.tiles_q);
+  pp.tiles_k = reinterpret_cast<uint32_t*>(ws + l.tiles_k);
+  pp.heads = kind == FA_MASK_BOOL ? B * mask_heads : B;
+  pp.tiles_of_q = qt;
+  pp.tiles_of_k = kt;
+  pp.Nk = Nk;
+  pp.tile_words_q = p.tile_words_q;
+  pp.tile_words_k = p.tile_words_k;
   rc = fa::launch_bwd_prep(pp, D, s);
   if (rc != FA_OK) return rc;
   return launch(p, D, mk, st->device, s);

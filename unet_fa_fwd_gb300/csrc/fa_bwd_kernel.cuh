@@ -70,6 +70,10 @@ struct BwdParams {
   const uint32_t* bits_q;  // [B][mask_heads][Nq][words_q]
   const uint32_t* bits_k;  // [B][mask_heads][Nk][words_k]
   int words_q, words_k;
+  // Tiles with a pair that is kept, as bits.  Boolean masks: by query tiles
+  // [B][mask_heads][tiles][tile_words_q] and by key tiles; key padding: [B][tile_words_q].
+  const uint32_t *tiles_q, *tiles_k;
+  int tile_words_q, tile_words_k;
   BwdTensor dq, dk, dv;
   float* part[2];       // partial sums of cut units
   unsigned long long timeout_ns;
@@ -342,11 +346,16 @@ __device__ __forceinline__ void bwd_store_row(uint32_t t, float mul, bool zero, 
   }
 }
 template <int NC>
-__device__ __forceinline__ void bwd_store_part(uint32_t t, bool ok, float* dst, int row) {
+__device__ __forceinline__ void bwd_store_part(uint32_t t, bool zero, bool ok, float* dst, int row) {
 #pragma unroll
   for (int cb = 0; cb < NC; cb += 8) {
     uint32_t r[8];
-    ptx::tmem_ld32x32b_x8(t + cb, r);
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] = 0u;
+    } else {
+      ptx::tmem_ld32x32b_x8(t + cb, r);
+    }
     if (ok) {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
@@ -357,20 +366,72 @@ __device__ __forceinline__ void bwd_store_part(uint32_t t, bool ok, float* dst, 
 }
 
 // Where a piece's iterations lie: query head (of a group that shares the key
-// head) and tile of the other side.
+// head) and tile of the other side.  Tiles of which a boolean or key-padding mask
+// keeps nothing are left out (their P and dS are 0); `count` is how many are left.
+template <int MK, bool KV>
 struct BwdIter {
-  int g, tile;  // head in the group, tile
+  static constexpr bool SKIP = MK == kBwdMaskBool || (MK == kBwdMaskKey && !KV);
+  int g, tile;    // head in the group, tile
   int first, n;
-  __device__ __forceinline__ void start(const BwdUnits& u, int unit_tile, int it) {
-    u.range(unit_tile, first, n);
+  int it, end;    // as if none were left out
+  int count;
+  const uint32_t* words;  // tiles' bits, of the group's first head
+  int words_head;         // from one head of the group to the next
+
+  __device__ __forceinline__ void start(const BwdParams& p, const BwdUnits& u, const BwdPiece& pc, int b, int h) {
+    u.range(pc.tile, first, n);
+    it = pc.it0;
+    end = pc.it1;
     g = n > 0 && u.group > 1 ? it / n : 0;
     tile = first + it - g * n;
+    count = end - it;
+    if constexpr (MK == kBwdMaskKey) {
+      words = p.tiles_q + (size_t)b * p.tile_words_q;
+      words_head = 0;
+      if (KV && !((__ldcg(words + pc.tile / 32) >> (pc.tile % 32)) & 1u)) count = 0;
+    } else if constexpr (MK == kBwdMaskBool) {
+      const int head = p.mask_heads == 1 ? 0 : (KV ? h * p.group : h), per = KV ? p.tile_words_k : p.tile_words_q;
+      words = (KV ? p.tiles_k : p.tiles_q) + ((size_t)(b * p.mask_heads + head) * u.tiles + pc.tile) * per;
+      words_head = p.mask_heads == 1 ? 0 : u.tiles * per;
+    }
+    if constexpr (SKIP) {
+      count = 0;
+      BwdIter i = *this;
+      while (i.it < end) {
+        int span;
+        count += __popc(i.ahead(span));
+        i.move(span);
+      }
+      seek();
+    }
   }
-  __device__ __forceinline__ void next() {
-    if (++tile == first + n) {
+  // Bits of the next tiles that share a word, and how many these are.
+  __device__ __forceinline__ uint32_t ahead(int& span) const {
+    span = min(min(32 - tile % 32, first + n - tile), end - it);
+    return __ldcg(words + (size_t)g * words_head + tile / 32) >> (tile % 32) & (~0u >> (32 - span));
+  }
+  __device__ __forceinline__ void move(int by) {
+    it += by;
+    tile += by;
+    if (tile == first + n) {
       tile = first;
       ++g;
     }
+  }
+  __device__ __forceinline__ void seek() {
+    while (it < end) {
+      int span;
+      const uint32_t w = ahead(span);
+      if (w) {
+        move(__ffs(w) - 1);
+        return;
+      }
+      move(span);
+    }
+  }
+  __device__ __forceinline__ void next() {
+    move(1);
+    if constexpr (SKIP) seek();
   }
 };
 
@@ -434,11 +495,11 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
             ++n;
             return true;
           };
-          BwdIter at;
-          at.start(plan.units, pc.tile, pc.it0);
-          for (int it = pc.it0; ok && it < pc.it1; ++it, ++j, at.next()) {
+          BwdIter<MK, KV> at;
+          at.start(p, plan.units, pc, b, h);
+          for (int i = 0; ok && i < at.count; ++i, ++j, at.next()) {
             const int ho = h_other + (KV ? at.g : 0);
-            if (it == pc.it0) ok = load_unit(mA, sA, bars->a_full, bars->a_empty, na);
+            if (i == 0) ok = load_unit(mA, sA, bars->a_full, bars->a_empty, na);
             if (!ok) break;
             const uint32_t s0 = j % C::RING0, s1 = j % C::RING1;
             ok = bwd_wait(bars->r0_empty[s0], ((j / C::RING0) & 1) ^ 1, bars, p);
@@ -451,7 +512,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
             ptx::mbar_arrive_expect_tx(full, C::TILE);
             bwd_load_tile<D>(ptx::smem_u32(sR0 + s0 * C::TILE), m0, full, at.tile * 128, ho, b);
             ++n0;
-            if (it == pc.it0) ok = load_unit(mB, sB, bars->b_full, bars->b_empty, nb);
+            if (i == 0) ok = load_unit(mB, sB, bars->b_full, bars->b_empty, nb);
             if (!ok) break;
             if constexpr (KV) {
               const uint32_t ss = j & 1;
@@ -522,7 +583,11 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       BwdWalk walk;
       BwdPiece pc;
       while (ok && walk.next(plan, cta, pc)) {
-        const uint32_t n = (uint32_t)(pc.it1 - pc.it0);
+        if (!__all_sync(0xffffffffu, piece_ok(pc))) break;
+        const int b = (int)div_h.div((uint32_t)pc.head);
+        BwdIter<MK, KV> at;
+        at.start(p, plan.units, pc, b, pc.head - b * heads);
+        const uint32_t n = (uint32_t)at.count;
         if (n == 0) continue;
         ok = bwd_wait_warp(bars->a_full, nu & 1, bars, p) && scores(j);
         if (ok && n == 1) commit(bars->a_empty);
@@ -641,43 +706,44 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       float nlse = 0.f, ndelta = 0.f, key_add[4] = {};
       if constexpr (!KV) {
         const size_t at = (size_t)pc.head * p.nqp + my;
-        nlse = __ldg(p.nlse + at);
-        ndelta = __ldg(p.ndelta + at);
+        nlse = __ldcg(p.nlse + at);
+        ndelta = __ldcg(p.ndelta + at);
       } else if constexpr (MK == kBwdMaskKey) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           key_add[r] = __ldg(static_cast<const float*>(p.mask) + (size_t)b * p.Nk + min(my4 + 8 * r, p.Nk - 1)) * kLog2e;
       }
-      BwdIter at;
-      at.start(plan.units, pc.tile, pc.it0);
+      BwdIter<MK, KV> at;
+      at.start(p, plan.units, pc, b, h);
+      const int n = at.count;
       // The first mask values of the iteration at `i`, which are fetched an iteration ahead.
       uint32_t bits[ROWS] = {};
-      auto mask_head = [&](const BwdIter& i) {
+      auto mask_head = [&](const BwdIter<MK, KV>& i) {
         return (size_t)b * p.mask_heads + (p.mask_heads == 1 ? 0 : (KV ? h * p.group + i.g : h));
       };
-      auto stage = [&](const BwdIter& i, int c0) {
+      auto stage = [&](const BwdIter<MK, KV>& i, int c0) {
         Stage::copy(ptx::smem_u32(sMask), static_cast<const float*>(p.mask) + mask_head(i) * p.Nq * p.Nk,
                     pc.tile * 128 + (warp % 4) * 32, i.tile * 128 + wg * kBwdCols + c0, p.Nq, p.Nk, p.mask_vec,
                     (int)lane);
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      auto fetch = [&](const BwdIter& i) {
+      auto fetch = [&](const BwdIter<MK, KV>& i) {
         if constexpr (MK == kBwdMaskBool) {
           const int rows = KV ? p.Nk : p.Nq, words = KV ? p.words_k : p.words_q;
 #pragma unroll
           for (int r = 0; r < ROWS; ++r)
-            bits[r] = __ldg((KV ? p.bits_k : p.bits_q) + (mask_head(i) * rows + min(my4 + 8 * r, rows - 1)) * words +
+            bits[r] = __ldcg((KV ? p.bits_k : p.bits_q) + (mask_head(i) * rows + min(my4 + 8 * r, rows - 1)) * words +
                             i.tile * 4 + wg);
         } else if constexpr (MK == kBwdMaskAdd) {
           stage(i, 0);
         }
       };
-      if (pc.it0 < pc.it1) fetch(at);
-      for (int it = pc.it0; it < pc.it1; ++it, ++j) {
+      if (n > 0) fetch(at);
+      for (int it = 0; it < n; ++it, ++j) {
         const uint32_t sb = j % T::NS;
         const uint32_t tS = t0 + T::S + sb * 128 + wg * kBwdCols, tDP = t0 + T::DP + wg * kBwdCols;
         const int col0 = at.tile * 128 + wg * kBwdCols;  // this thread's first query or key of the tile
-        const BwdIter now = at;
+        const BwdIter<MK, KV> now = at;
         at.next();
         const float *lcol = nullptr, *dcol = nullptr;  // -L and -delta of this thread's columns
         if constexpr (KV) {
@@ -709,7 +775,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
             edge = edge || seen[r] != ~0u;
           }
           if constexpr (MK == kBwdMaskBool) {
-            if (it + 1 < pc.it1) fetch(at);
+            if (it + 1 < n) fetch(at);
           }
           edge = __any_sync(0xffffffffu, edge);
         }
@@ -736,7 +802,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
               __syncwarp();
               if (cb + 16 < kBwdCols)
                 stage(now, cb + 16);
-              else if (it + 1 < pc.it1)
+              else if (it + 1 < n)
                 fetch(at);
             }
           } else if constexpr (MK == kBwdMaskKey && !KV) {
@@ -833,7 +899,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       if (!ok) break;
 
       // The unit's gradients, a quarter of the accumulators' columns each.
-      const bool zero = pc.it0 == pc.it1;
+      const bool zero = n == 0;
       if (!zero) {
         ok = bwd_wait_warp(bars->acc_full, nu & 1, bars, p);
         if (!ok) break;
@@ -851,7 +917,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         bwd_store_row<NC>(tA, is_dv ? 1.f : p.scale, zero, in, o.p + b * o.b + h * o.h + (long long)my * o.n + col);
       } else {
         const bool in = bwd_check(p, bars, pc.slot < 2 * plan.ctas, kCheckGradSlot, pc.slot, pc.head);
-        bwd_store_part<NC>(tA, in, p.part[KV ? 0 : 1] + (size_t)pc.slot * (128 * T::ACC) + wg * NC * 128, row);
+        bwd_store_part<NC>(tA, zero, in, p.part[KV ? 0 : 1] + (size_t)pc.slot * (128 * T::ACC) + wg * NC * 128, row);
       }
       ptx::tc_fence_before_sync();
     }
@@ -919,12 +985,57 @@ struct BwdPrepParams {
   int Hq, Nq, nqp;
   long long rows;  // B Hq nqp
   FastDiv div_h;
+  // Tiles with a kept pair, as bits (BwdParams), by the blocks behind the rows':
+  // of a boolean mask from `some`, or of a key-padding mask.
+  long long row_blocks;
+  const uint32_t* some;    // [heads][query tiles][key tiles]
+  const float* key_mask;   // [heads][Nk]
+  uint32_t *tiles_q, *tiles_k;
+  int heads, tiles_of_q, tiles_of_k, Nk, tile_words_q, tile_words_k;
 };
+
+// A warp makes one word.
+static __device__ __forceinline__ void bwd_tile_bits(const BwdPrepParams& p, long long i) {
+  const int lane = threadIdx.x % 32;
+  if (p.key_mask) {
+    if (i >= (long long)p.heads * p.tile_words_q) return;
+    const int b = (int)(i / p.tile_words_q), w = (int)(i - (long long)b * p.tile_words_q);
+    uint32_t word = 0;
+    for (int t = 0; t < 32 && w * 32 + t < p.tiles_of_k; ++t) {
+      bool some = false;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int k = (w * 32 + t) * 128 + c * 32 + lane;
+        some = some || (k < p.Nk && p.key_mask[(size_t)b * p.Nk + k] != -INFINITY);
+      }
+      if (__any_sync(0xffffffffu, some)) word |= 1u << t;
+    }
+    if (lane == 0) p.tiles_q[i] = word;
+    return;
+  }
+  const long long by_q = (long long)p.heads * p.tiles_of_q * p.tile_words_q;
+  const long long by_k = (long long)p.heads * p.tiles_of_k * p.tile_words_k;
+  if (i >= by_q + by_k) return;
+  const bool q = i < by_q;
+  const long long at = q ? i : i - by_q;
+  const int words = q ? p.tile_words_q : p.tile_words_k, tiles = q ? p.tiles_of_q : p.tiles_of_k;
+  const long long row = at / words;
+  const int head = (int)(row / tiles), tile = (int)(row - (long long)head * tiles);
+  const int other = (int)(at - row * words) * 32 + lane, tq = q ? tile : other, tk = q ? other : tile;
+  const bool some = tq < p.tiles_of_q && tk < p.tiles_of_k &&
+                    p.some[((size_t)head * p.tiles_of_q + tq) * p.tiles_of_k + tk] != 0;
+  const uint32_t word = __ballot_sync(0xffffffffu, some);
+  if (lane == 0) (q ? p.tiles_q : p.tiles_k)[at] = word;
+}
 
 template <int D>
 __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant__ BwdPrepParams p) {
   constexpr int L = D / 8;  // lanes a row
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x >= p.row_blocks) {
+    bwd_tile_bits(p, (blockIdx.x - p.row_blocks) * 8 + threadIdx.x / 32);
+    return;
+  }
   const long long i = (long long)blockIdx.x * (256 / L) + threadIdx.x / L;
   const int piece = threadIdx.x % L;
   const bool live = i < p.rows;
@@ -968,6 +1079,7 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
 struct BwdBitsParams {
   const uint8_t* mask;  // [B mask_heads][Nq][Nk]
   uint32_t *bits_q, *bits_k;
+  uint8_t* some;                 // [B mask_heads][query tiles][key tiles][4]: 32 rows of a tile keep a pair
   int Nq, Nk, words_q, words_k;  // words of a row: 32-key and 32-row blocks of whole tiles
   long long blocks;              // 32 rows x 128 keys of every head
 };
@@ -983,7 +1095,7 @@ static __global__ void __launch_bounds__(256) fa_bwd_bits_kernel(const __grid_co
   const int rows = min(32, p.Nq - bq * 32), valid = min(max(p.Nk - k, 0), 4);
   const uint32_t keep = valid == 4 ? ~0u : (1u << (8 * valid)) - 1;
   const uint8_t* at = p.mask + (bh * p.Nq + bq * 32) * p.Nk + k;
-  uint32_t col[4] = {}, word = 0;
+  uint32_t col[4] = {}, word = 0, any = 0;
 #pragma unroll
   for (int y0 = 0; y0 < 32; y0 += 8) {
     uint32_t lo[8], hi[8];
@@ -1004,6 +1116,7 @@ static __global__ void __launch_bounds__(256) fa_bwd_bits_kernel(const __grid_co
       t |= t >> 2;
       t |= t >> 1;
       t &= 0x01010101u;
+      any |= t;
 #pragma unroll
       for (int c = 0; c < 4; ++c) col[c] |= ((t >> (8 * c)) & 1u) << (y0 + y);
       uint32_t r = (t * 0x01020408u) >> 24 << (4 * (lane % 8));  // the four bits together
@@ -1018,6 +1131,8 @@ static __global__ void __launch_bounds__(256) fa_bwd_bits_kernel(const __grid_co
 #pragma unroll
   for (int c = 0; c < 4; ++c)
     if (c < valid) p.bits_k[((size_t)bh * p.Nk + k + c) * p.words_k + bq] = col[c];
+  any = __any_sync(0xffffffffu, any != 0);
+  if (lane == 0) p.some[((bh * (p.words_k / 4) + bq / 4) * tiles_k + bk) * 4 + bq % 4] = (uint8_t)any;
 }
 
 // Joins the partial sums of cut units, in the order of their pieces.  Block
