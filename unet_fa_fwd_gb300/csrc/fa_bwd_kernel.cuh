@@ -21,8 +21,8 @@
 //   warps 0-15   four warpgroups, each with 32 of a tile's 128 columns; a warp
 //                has 32 rows of the unit (lanes of tensor memory)
 //   warp 16      TMA producer      warp 17  MMA issuer (owns tensor memory)
-// Four warps a sub-partition hide the latency of tensor memory and of the
-// exponentials, which two (64 columns a thread) did not.
+// Four warps a sub-partition: with two (64 columns a thread) heads of 64 take
+// 193 us for 179, heads of 128 the same.
 // L and delta are a query's: in query units a row's, so that a thread has one row
 // and 32 columns; in key units a column's, where a thread has 4 rows and 8 columns
 // (the 16 x 256 bit shape of tensor memory's accesses) and so a fourth of the reads
@@ -32,6 +32,14 @@
 // P and dS go back to tensor memory as bf16, the A operand of the products that
 // take them; both sides' rows are operands K-major for S and dP and MN-major for
 // the gradients, from one copy in shared memory.
+//
+// What bounds it.  D = 128: the tensor pipe, 83 % active with operands at the rate of
+// shared memory, and for long runs the GPU's power: 4608 tokens of 24 heads 495 to
+// 517 us, 16896 6.6 to 6.9 ms, 1.26 to 1.32 PFLOP/s of the five products that the
+// gradient needs, 1.8 of the seven taken.  D = 64: a thread's chain of waits, loads of
+// tensor memory, exponentials and roundings, whose phases all warps are in together
+// (issue slots 57 % used, tensor pipe 59, exponential units 34): 4096 tokens of 8
+// heads, batch 2, 179 us, 0.96 PFLOP/s.
 //
 // Waits are bounded: past the limit a CTA records FA_ERR_TIMEOUT in the device
 // status word, drains its copies and MMAs, frees tensor memory and returns.
@@ -976,8 +984,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_kernel(const __grid_con
 
 // -L and -delta of every query row, and of the rows that fill up the last tile:
 // L_i = log2(e) LSE_i (+inf for a row that sees nothing, so that its P is 0),
-// delta_i = dO_i . O_i - dLSE_i.  HBM bound (O and dO are read once); D / 8
-// neighbouring lanes share a row.
+// delta_i = dO_i . O_i - dLSE_i.  HBM bound (O and dO are read once: 4608 tokens of
+// 24 heads of 128 14 us, 4.1 TB/s cold); D / 8 neighbouring lanes share a row.
 struct BwdPrepParams {
   BwdTensor out, dout;
   const float *lse, *dlse;  // [B][Hq][Nq]; dlse may be nullptr
@@ -1137,7 +1145,8 @@ static __global__ void __launch_bounds__(256) fa_bwd_bits_kernel(const __grid_co
 
 // Joins the partial sums of cut units, in the order of their pieces.  Block
 // (c, y): the unit that starts in CTA c's range (key units' CTAs, then query
-// units'), 8 columns of its accumulators.
+// units'), 8 columns of its accumulators.  Latency bound (7 to 11 us cold); its
+// blocks start beside the last of the kernel before it.
 template <int D>
 __global__ void __launch_bounds__(128) fa_bwd_join_kernel(const __grid_constant__ BwdParams p) {
   const bool kv = blockIdx.x < (unsigned)p.plan[0].ctas;

@@ -9,12 +9,20 @@
 // HBM bound: x (and dy) are read once and y (dx) written once; r is computed
 // again in the gradient, so nothing is kept for it.  A thread owns one 16-byte
 // piece of a token's row (when the pairs are the row's halves two, half a row
-// apart, of 8 elements together in 16 bits) and walks heads with its pairs' sines and its weights in registers;
-// the threads of a row are neighbours in a warp and sum by shuffles.
+// apart, of 8 elements together in 16 bits: with 16, 219 registers left one block
+// an SM) and walks heads with its pairs' sines and its weights in registers; the
+// threads of a row are neighbours in a warp and sum by shuffles.  Four heads' loads
+// are in flight together: the gradient's 16 warps an SM need that to cover HBM's
+// latency (with two, 225 us for 200 below).
 //
 // dw: a thread adds up its elements over all its rows, a block's threads are
 // joined in a fixed order into one row of partial sums, and a second kernel adds
 // the blocks' rows in a fixed order: no atomics, results repeat bit for bit.
+//
+// Measured: forward of 119056 tokens of 24 + 24 heads of 128 in bf16 472 us (6.2
+// TB/s); gradient of 16896 tokens in fp32 200 us (6.2 TB/s), of 4608 in bf16 39 us
+// (4.4 TB/s: twice the arithmetic a byte, 55 % of the issue slots, and the second
+// kernel).
 #pragma once
 
 #include <cuda_bf16.h>
