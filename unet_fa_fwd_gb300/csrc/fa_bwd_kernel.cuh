@@ -246,47 +246,40 @@ struct BwdStage {
   static constexpr int PIECES = SC / 4;
   static __device__ __forceinline__ int swizzle(int r) { return SC == 32 ? (r & 7) : ((r >> 1) & 3); }
   static __device__ __forceinline__ int turned(int key, int c) { return (key + 8 * (c / 2)) & 31; }
+  // (Addresses go up by a constant from copy to copy: the mask's cost is
+  // instructions.  What lies outside copies no byte and is zero.)
   static __device__ __forceinline__ void copy(uint32_t buf, const float* base, int row0, int col0, int Nq, int Nk,
                                               int vec, int lane) {
     const int q0 = KV ? col0 : row0, k0 = KV ? row0 : col0;
-    if (vec) {
+    if (vec) {  // 16 bytes a lane (Nk is a multiple of 4)
+      constexpr int LANES = KV ? 8 : PIECES, STEP = 32 / LANES;  // of a mask row; mask rows a copy
+      const int r = lane / LANES, g = lane % LANES, k = k0 + 4 * g;
+      const float* src = base + (size_t)(q0 + r) * Nk + k;
+      const size_t step = (size_t)STEP * Nk;
+      const int rows = k < Nk ? Nq - q0 - r : 0;
+      // 16-byte piece of the row; other in every second copy by `flip`
+      const int piece = KV ? (g + 2 * (r / 2)) & 7 : g ^ swizzle(r);
+      constexpr int flip = KV || SC == 32 ? 4 : 0, ROW = KV ? 128 : SC * 4;
+      const uint32_t dst = buf + r * ROW;
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        int q, k;
-        uint32_t dst;
-        if constexpr (KV) {
-          const int c = 4 * i + lane / 8, g = lane % 8;
-          q = q0 + c;
-          k = k0 + 4 * g;
-          dst = buf + (c * 32 + turned(4 * g, c)) * 4;
-        } else {
-          const int r = i * (32 / PIECES) + lane / PIECES, g = lane % PIECES;
-          q = q0 + r;
-          k = k0 + 4 * g;
-          dst = buf + r * SC * 4 + ((g ^ swizzle(r)) << 4);
-        }
-        const bool in = q < Nq && k < Nk;  // (Nk is a multiple of 4)
-        const float* src = in ? base + (size_t)q * Nk + k : base;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-      }
-    } else {
+      for (int i = 0; i < PIECES; ++i, src += step)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * STEP * ROW +
+                                                                          ((piece ^ (i % 2 * flip)) << 4)),
+                     "l"(src), "r"(i * STEP < rows ? 16 : 0)
+                     : "memory");
+    } else {  // 4 bytes a lane
+      constexpr int LANES = KV ? 32 : SC, STEP = 32 / LANES;
+      const int r = lane / LANES, c = lane % LANES, k = k0 + c;
+      const float* src = base + (size_t)(q0 + r) * Nk + k;
+      const size_t step = (size_t)STEP * Nk;
+      const int rows = k < Nk ? Nq - q0 - r : 0;
 #pragma unroll 8
-      for (int i = 0; i < SC; ++i) {
-        int q, k;
-        uint32_t dst;
-        if constexpr (KV) {
-          q = q0 + i;
-          k = k0 + lane;
-          dst = buf + (i * 32 + turned(lane, i)) * 4;
-        } else {
-          const int r = i * (32 / SC) + lane / SC, c = lane % SC;
-          q = q0 + r;
-          k = k0 + c;
-          dst = buf + r * SC * 4 + (((c / 4) ^ swizzle(r)) << 4) + (c % 4) * 4;
-        }
-        const bool in = q < Nq && k < Nk;
-        const float* src = in ? base + (size_t)q * Nk + k : base;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+      for (int i = 0; i < SC; ++i, src += step) {
+        const int at = KV ? i * 32 + turned(c, i)
+                          : (i * STEP + r) * SC + (((c / 4) ^ swizzle(i * STEP + r)) << 2) + c % 4;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(buf + at * 4), "l"(src),
+                     "r"(i * STEP < rows ? 4 : 0)
+                     : "memory");
       }
     }
   }
@@ -298,17 +291,23 @@ struct BwdStage {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int c = c0 + 8 * (e / 8) + 2 * (lane % 4) + e % 2, key = lane / 4 + 8 * (e / 2 % 4);
-        m[e] = buf[c * 32 + turned(key, c)] * kLog2e;
+        m[e] = buf[c * 32 + turned(key, c)];
       }
     } else {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const float4 v = *reinterpret_cast<const float4*>(buf + lane * SC + (((c0 / 4 + g) ^ swizzle(lane)) << 2));
-        m[4 * g] = v.x * kLog2e;
-        m[4 * g + 1] = v.y * kLog2e;
-        m[4 * g + 2] = v.z * kLog2e;
-        m[4 * g + 3] = v.w * kLog2e;
+        m[4 * g] = v.x;
+        m[4 * g + 1] = v.y;
+        m[4 * g + 2] = v.z;
+        m[4 * g + 3] = v.w;
       }
+    }
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const float2 v = __fmul2_rn(make_float2(m[e], m[e + 1]), make_float2(kLog2e, kLog2e));
+      m[e] = v.x;
+      m[e + 1] = v.y;
     }
   }
 };
