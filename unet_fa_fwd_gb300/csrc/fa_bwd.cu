@@ -27,12 +27,22 @@ int launch_bwd_prep(BwdPrepParams& p, int D, cudaStream_t s) {
   const long long blocks = p.row_blocks + (words + 7) / 8;
   if (blocks > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
   log_launch("fa_bwd_prep_kernel<D=%d> grid %lld x 256 threads, %lld rows", D, blocks, p.rows);
-  switch (D) {
-    case 32: fa_bwd_prep_kernel<32><<<(unsigned)blocks, 256, 0, s>>>(p); break;
-    case 64: fa_bwd_prep_kernel<64><<<(unsigned)blocks, 256, 0, s>>>(p); break;
-    default: fa_bwd_prep_kernel<128><<<(unsigned)blocks, 256, 0, s>>>(p); break;
-  }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  // Behind the kernel of a boolean mask's bits its blocks may start beside that one's
+  // (the blocks that read its results wait themselves).
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = p.some ? 1 : 0;
+  const BwdPrepParams& prm = p;
+  const cudaError_t e = D == 32   ? cudaLaunchKernelEx(&cfg, fa_bwd_prep_kernel<32>, prm)
+                        : D == 64 ? cudaLaunchKernelEx(&cfg, fa_bwd_prep_kernel<64>, prm)
+                                  : cudaLaunchKernelEx(&cfg, fa_bwd_prep_kernel<128>, prm);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 int launch_bwd_bits(const BwdBitsParams& p, cudaStream_t s) {

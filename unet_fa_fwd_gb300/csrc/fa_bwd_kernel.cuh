@@ -1020,6 +1020,7 @@ static __device__ __forceinline__ void bwd_tile_bits(const BwdPrepParams& p, lon
     if (lane == 0) p.tiles_q[i] = word;
     return;
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // `some` is there
   const long long by_q = (long long)p.heads * p.tiles_of_q * p.tile_words_q;
   const long long by_k = (long long)p.heads * p.tiles_of_k * p.tile_words_k;
   if (i >= by_q + by_k) return;
@@ -1092,6 +1093,7 @@ struct BwdBitsParams {
 };
 
 static __global__ void __launch_bounds__(256) fa_bwd_bits_kernel(const __grid_constant__ BwdBitsParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long i = (long long)blockIdx.x * 8 + threadIdx.x / 32;
   if (i >= p.blocks) return;
   const int lane = threadIdx.x % 32, tiles_k = p.words_q / 4;
