@@ -395,7 +395,7 @@ struct BwdIter {
     if constexpr (MK == kBwdMaskKey) {
       words = p.tiles_q + (size_t)b * p.tile_words_q;
       words_head = 0;
-      if (KV && !((__ldcg(words + pc.tile / 32) >> (pc.tile % 32)) & 1u)) count = 0;
+      if (KV && !((words[pc.tile / 32] >> (pc.tile % 32)) & 1u)) count = 0;
     } else if constexpr (MK == kBwdMaskBool) {
       const int head = p.mask_heads == 1 ? 0 : (KV ? h * p.group : h), per = KV ? p.tile_words_k : p.tile_words_q;
       words = (KV ? p.tiles_k : p.tiles_q) + ((size_t)(b * p.mask_heads + head) * u.tiles + pc.tile) * per;
@@ -415,7 +415,7 @@ struct BwdIter {
   // Bits of the next tiles that share a word, and how many these are.
   __device__ __forceinline__ uint32_t ahead(int& span) const {
     span = min(min(32 - tile % 32, first + n - tile), end - it);
-    return __ldcg(words + (size_t)g * words_head + tile / 32) >> (tile % 32) & (~0u >> (32 - span));
+    return words[(size_t)g * words_head + tile / 32] >> (tile % 32) & (~0u >> (32 - span));
   }
   __device__ __forceinline__ void move(int by) {
     it += by;
@@ -705,17 +705,27 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
     bool ok = true;
     BwdWalk walk;
     BwdPiece pc;
-    while (ok && walk.next(plan, cta, pc)) {
+    // -L and -delta of a query unit's row, loaded a piece ahead.
+    float nlse_next = 0.f, ndelta_next = 0.f;
+    auto next_piece = [&](BwdPiece& next) {
+      if (!walk.next(plan, cta, next)) return false;
+      if (!KV && piece_ok(next)) {
+        const size_t at = (size_t)next.head * p.nqp + next.tile * 128 + row;
+        nlse_next = __ldcg(p.nlse + at);
+        ndelta_next = __ldcg(p.ndelta + at);
+      }
+      return true;
+    };
+    for (bool have = next_piece(pc); have;) {
       ok = __all_sync(0xffffffffu, piece_ok(pc));
       if (!ok) break;
       const int b = (int)div_h.div((uint32_t)pc.head), h = pc.head - b * heads;
       const int my = pc.tile * 128 + row, my4 = pc.tile * 128 + row4;  // this thread's key or query
-      float nlse = 0.f, ndelta = 0.f, key_add[4] = {};
-      if constexpr (!KV) {
-        const size_t at = (size_t)pc.head * p.nqp + my;
-        nlse = __ldcg(p.nlse + at);
-        ndelta = __ldcg(p.ndelta + at);
-      } else if constexpr (MK == kBwdMaskKey) {
+      const float nlse = nlse_next, ndelta = ndelta_next;
+      float key_add[4] = {};
+      BwdPiece following;
+      have = next_piece(following);
+      if constexpr (KV && MK == kBwdMaskKey) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           key_add[r] = __ldg(static_cast<const float*>(p.mask) + (size_t)b * p.Nk + min(my4 + 8 * r, p.Nk - 1)) * kLog2e;
@@ -927,6 +937,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         bwd_store_part<NC>(tA, zero, in, p.part[KV ? 0 : 1] + (size_t)pc.slot * (128 * T::ACC) + wg * NC * 128, row);
       }
       ptx::tc_fence_before_sync();
+      pc = following;
     }
     ptx::tc_fence_before_sync();
   }
