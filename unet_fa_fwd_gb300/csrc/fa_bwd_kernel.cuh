@@ -332,24 +332,52 @@ __device__ __forceinline__ float2 bwd_exp(float s0, float s1, float sl2, float2 
 }
 
 // NC columns of a thread's accumulator row at `t`, times `mul`, rounded to `dst`
-// (16-byte aligned), or as they are to a slot of partial sums (laid out
-// [columns / 4][128 rows][4]).
+// (16-byte aligned; neighbouring lanes' rows are `row_step` elements apart; `rows`:
+// how many from the lane's on are in the tensor).  Neighbouring lanes first exchange
+// 16-byte pieces so that up to four store 64 bytes of one row together: a store of
+// every lane to a row of its own takes a clock a row (units of one tile each at
+// D = 64: 1100 clocks of 4050).
 template <int NC>
-__device__ __forceinline__ void bwd_store_row(uint32_t t, float mul, bool zero, bool ok, __nv_bfloat16* dst) {
+__device__ __forceinline__ void bwd_store_row(uint32_t t, float mul, bool zero, bool ok, int rows, int lane,
+                                              __nv_bfloat16* dst, long long row_step) {
+  constexpr int CH = NC >= 32 ? 4 : NC / 8;  // lanes that share rows, and their pieces
+  const int l = lane % CH;
 #pragma unroll
-  for (int cb = 0; cb < NC; cb += 8) {
-    uint32_t r[8];
-    if (zero) {
+  for (int cb = 0; cb < NC; cb += 8 * CH) {
+    uint32_t v[CH][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = 0u;
-    } else {
-      ptx::tmem_ld32x32b_x8(t + cb, r);
+    for (int c = 0; c < CH; ++c) {
+      uint32_t r[8];
+      if (zero) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = 0u;
+      } else {
+        ptx::tmem_ld32x32b_x8(t + cb + 8 * c, r);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[c][i] = ptx::pack_bf16x2(__uint_as_float(r[2 * i]) * mul, __uint_as_float(r[2 * i + 1]) * mul);
     }
-    uint32_t w[4];
+    // v[c] of lane l becomes piece l of lane c's row.
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = ptx::pack_bf16x2(__uint_as_float(r[2 * i]) * mul, __uint_as_float(r[2 * i + 1]) * mul);
-    if (ok) *reinterpret_cast<uint4*>(dst + cb) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int m = 1; m < CH; m <<= 1)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if (c & m) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool upper = (l & m) != 0;
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? v[c][i] : v[c | m][i], m);
+          if (upper)
+            v[c][i] = got;
+          else
+            v[c | m][i] = got;
+        }
+      }
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (ok && c - l < rows)
+        *reinterpret_cast<uint4*>(dst + (c - l) * row_step + cb + 8 * l) = make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]);
   }
 }
 template <int NC>
@@ -941,9 +969,8 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         ptx::tc_fence_after_sync();
       }
       if (pc.slot < 0) {
-        const bool in = my < (KV ? p.Nk : p.Nq) && bwd_check(p, bars, pc.head < plan.units.heads && col + NC <= D,
-                                                            kCheckGradStore, pc.head, my);
-        bwd_store_row<NC>(tA, is_dv ? 1.f : p.scale, zero, in, dst);
+        const bool in = bwd_check(p, bars, pc.head < plan.units.heads && col + NC <= D, kCheckGradStore, pc.head, my);
+        bwd_store_row<NC>(tA, is_dv ? 1.f : p.scale, zero, in, (KV ? p.Nk : p.Nq) - my, (int)lane, dst, o.n);
       } else {
         const bool in = bwd_check(p, bars, pc.slot < 2 * plan.ctas, kCheckGradSlot, pc.slot, pc.head);
         bwd_store_part<NC>(tA, zero, in, p.part[KV ? 0 : 1] + (size_t)pc.slot * (128 * T::ACC) + wg * NC * 128, row);
