@@ -35,11 +35,11 @@
 //
 // What bounds it.  D = 128: the tensor pipe, 83 % active with operands at the rate of
 // shared memory, and for long runs the GPU's power: 4608 tokens of 24 heads 495 to
-// 517 us, 16896 6.6 to 6.9 ms, 1.26 to 1.32 PFLOP/s of the five products that the
+// 515 us, 16896 6.6 to 6.9 ms, 1.26 to 1.32 PFLOP/s of the five products that the
 // gradient needs, 1.8 of the seven taken.  D = 64: a thread's chain of waits, loads of
 // tensor memory, exponentials and roundings, whose phases all warps are in together
 // (issue slots 57 % used, tensor pipe 59, exponential units 34): 4096 tokens of 8
-// heads, batch 2, 179 us, 0.96 PFLOP/s.
+// heads, batch 2, 177 us, 0.97 PFLOP/s.
 //
 // Waits are bounded: past the limit a CTA records FA_ERR_TIMEOUT in the device
 // status word, drains its copies and MMAs, frees tensor memory and returns.
