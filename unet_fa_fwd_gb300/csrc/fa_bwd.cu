@@ -18,15 +18,17 @@
 
 namespace fa {
 
-int launch_bwd_prep(BwdPrepParams& p, int D, cudaStream_t s) {
-  p.row_blocks = (p.rows + 256 / (D / 8) - 1) / (256 / (D / 8));
+int launch_bwd_prep(BwdPrepParams& p, long long heads, int D, cudaStream_t s) {
+  p.head_blocks = p.nqp / (D == 32 ? kBwdPrepRows<32> : D == 64 ? kBwdPrepRows<64> : kBwdPrepRows<128>);
+  p.div_blocks = FastDiv::make((uint32_t)p.head_blocks);
+  p.row_blocks = heads * p.head_blocks;
   const long long words = p.key_mask ? (long long)p.heads * p.tile_words_q
                           : p.some   ? (long long)p.heads * ((long long)p.tiles_of_q * p.tile_words_q +
                                                              (long long)p.tiles_of_k * p.tile_words_k)
                                      : 0;
   const long long blocks = p.row_blocks + (words + 7) / 8;
   if (blocks > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
-  log_launch("fa_bwd_prep_kernel<D=%d> grid %lld x 256 threads, %lld rows", D, blocks, p.rows);
+  log_launch("fa_bwd_prep_kernel<D=%d> grid %lld x 256 threads, %lld rows", D, blocks, heads * p.nqp);
   // Behind the kernel of a boolean mask's bits its blocks may start beside that one's
   // (the blocks that read its results wait themselves).
   cudaLaunchAttribute at[1];
@@ -321,7 +323,6 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   pp.Hq = Hq;
   pp.Nq = Nq;
   pp.nqp = p.nqp;
-  pp.rows = (long long)B * Hq * p.nqp;
   pp.div_h = fa::FastDiv::make((uint32_t)Hq);
   if (kind == FA_MASK_BOOL) pp.some = reinterpret_cast<const uint32_t*>(ws + l.some);
   if (kind == FA_MASK_KEY_PADDING) pp.key_mask = static_cast<const float*>(mask_data);
@@ -333,7 +334,7 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   pp.Nk = Nk;
   pp.tile_words_q = p.tile_words_q;
   pp.tile_words_k = p.tile_words_k;
-  rc = fa::launch_bwd_prep(pp, D, s);
+  rc = fa::launch_bwd_prep(pp, (long long)B * Hq, D, s);
   if (rc != FA_OK) return rc;
   return launch(p, D, mk, st->device, s);
 }

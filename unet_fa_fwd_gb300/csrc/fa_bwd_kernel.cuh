@@ -1039,8 +1039,9 @@ struct BwdPrepParams {
   const float *lse, *dlse;  // [B][Hq][Nq]; dlse may be nullptr
   float *nlse, *ndelta;     // [B Hq][nqp]
   int Hq, Nq, nqp;
-  long long rows;  // B Hq nqp
   FastDiv div_h;
+  int head_blocks;     // blocks of a head's rows
+  FastDiv div_blocks;
   // Tiles with a kept pair, as bits (BwdParams), by the blocks behind the rows':
   // of a boolean mask from `some`, or of a key-padding mask.
   long long row_blocks;
@@ -1085,6 +1086,10 @@ static __device__ __forceinline__ void bwd_tile_bits(const BwdPrepParams& p, lon
   if (lane == 0) (q ? p.tiles_q : p.tiles_k)[at] = word;
 }
 
+// Rows of a block (they divide a tile's 128).
+template <int D>
+constexpr int kBwdPrepRows = D == 128 ? 64 : 128;
+
 template <int D>
 __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant__ BwdPrepParams p) {
   constexpr int L = D / 8;  // lanes a row
@@ -1093,39 +1098,46 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
     bwd_tile_bits(p, (blockIdx.x - p.row_blocks) * 8 + threadIdx.x / 32);
     return;
   }
-  const long long i = (long long)blockIdx.x * (256 / L) + threadIdx.x / L;
-  const int piece = threadIdx.x % L;
-  const bool live = i < p.rows;
-  const long long bh = (live ? i : 0) / p.nqp;
-  const int n = live ? (int)(i - bh * p.nqp) : 0;
-  const int b = (int)p.div_h.div((uint32_t)bh), h = (int)bh - b * p.Hq;
-  const bool in = live && n < p.Nq;
-  float sum = 0.f;
-  if (in) {
-    const uint4 o = *reinterpret_cast<const uint4*>(p.out.p + b * p.out.b + h * p.out.h + n * p.out.n + piece * 8);
-    const uint4 g = *reinterpret_cast<const uint4*>(p.dout.p + b * p.dout.b + h * p.dout.h + n * p.dout.n + piece * 8);
-    const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
+  // A block's rows are of one head.  All of a thread's loads go out together.
+  constexpr int STEP = 256 / L, U = kBwdPrepRows<D> / STEP;
+  const int bh = (int)p.div_blocks.div(blockIdx.x);
+  const int n0 = (int)(blockIdx.x - (unsigned)bh * p.head_blocks) * kBwdPrepRows<D> + threadIdx.x / L;
+  const int b = (int)p.div_h.div((uint32_t)bh), h = bh - b * p.Hq, piece = threadIdx.x % L;
+  const __nv_bfloat16 *out = p.out.p + b * p.out.b + h * p.out.h + piece * 8,
+                      *dout = p.dout.p + b * p.dout.b + h * p.dout.h + piece * 8;
+  uint4 o[U] = {}, g[U] = {};
+  float lse[U], sum[U];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {  // a bf16 is the upper half of its fp32
-      sum = fmaf(__uint_as_float(ow[k] << 16), __uint_as_float(gw[k] << 16), sum);
-      sum = fmaf(__uint_as_float(ow[k] & 0xffff0000u), __uint_as_float(gw[k] & 0xffff0000u), sum);
+  for (int u = 0; u < U; ++u) {
+    const int n = n0 + u * STEP;
+    sum[u] = 0.f;
+    lse[u] = -INFINITY;
+    if (n < p.Nq) {
+      o[u] = *reinterpret_cast<const uint4*>(out + n * p.out.n);
+      g[u] = *reinterpret_cast<const uint4*>(dout + n * p.dout.n);
+      if (piece == 0) {
+        lse[u] = p.lse[(size_t)bh * p.Nq + n];
+        if (p.dlse) sum[u] = -p.dlse[(size_t)bh * p.Nq + n];
+      }
     }
   }
 #pragma unroll
-  for (int m = 1; m < L; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  if (live && piece == 0) {
-    float nlse = -INFINITY;
-    if (in) {
-      const size_t at = (size_t)bh * p.Nq + n;
-      const float lse = p.lse[at];
-      if (p.dlse) sum -= p.dlse[at];
-      if (lse != -INFINITY)
-        nlse = -lse * 1.4426950408889634f;
-      else
-        sum = 0.f;  // (dLSE of a row that sees nothing may be anything)
+  for (int u = 0; u < U; ++u) {
+    const uint32_t ow[4] = {o[u].x, o[u].y, o[u].z, o[u].w}, gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+    float dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // a bf16 is the upper half of its fp32
+      dot = fmaf(__uint_as_float(ow[k] << 16), __uint_as_float(gw[k] << 16), dot);
+      dot = fmaf(__uint_as_float(ow[k] & 0xffff0000u), __uint_as_float(gw[k] & 0xffff0000u), dot);
     }
-    p.nlse[i] = nlse;
-    p.ndelta[i] = in ? -sum : 0.f;
+#pragma unroll
+    for (int m = 1; m < L; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+    if (piece == 0) {
+      const size_t at = (size_t)bh * p.nqp + n0 + u * STEP;
+      const bool sees = lse[u] != -INFINITY;  // (dLSE of a row that sees nothing may be anything)
+      p.nlse[at] = sees ? -lse[u] * 1.4426950408889634f : -INFINITY;
+      p.ndelta[at] = sees ? -(dot + sum[u]) : 0.f;
+    }
   }
 }
 
