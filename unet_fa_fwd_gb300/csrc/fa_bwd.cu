@@ -47,8 +47,8 @@ int launch_bwd_prep(BwdPrepParams& p, long long heads, int D, cudaStream_t s) {
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-int launch_bwd_bits(const BwdBitsParams& p, cudaStream_t s) {
-  const long long blocks = (p.blocks + 7) / 8;
+int launch_bwd_bits(const BwdBitsParams& p, long long heads, cudaStream_t s) {
+  const long long blocks = heads * p.tiles_q * p.tiles_k;
   if (blocks > INT_MAX) return FA_ERR_INVALID_ARGUMENT;
   log_launch("fa_bwd_bits_kernel grid %lld x 256 threads", blocks);
   fa_bwd_bits_kernel<<<(unsigned)blocks, 256, 0, s>>>(p);
@@ -303,13 +303,12 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
     bp.mask = static_cast<const uint8_t*>(mask_data);
     bp.bits_q = reinterpret_cast<uint32_t*>(ws + l.bits_q);
     bp.bits_k = reinterpret_cast<uint32_t*>(ws + l.bits_k);
-    bp.some = reinterpret_cast<uint8_t*>(ws + l.some);
+    bp.some = reinterpret_cast<uint32_t*>(ws + l.some);
     bp.Nq = Nq;
     bp.Nk = Nk;
-    bp.words_q = p.words_q;
-    bp.words_k = p.words_k;
-    bp.blocks = (long long)B * mask_heads * p.words_k * kt;
-    rc = fa::launch_bwd_bits(bp, s);
+    bp.tiles_q = qt;
+    bp.tiles_k = kt;
+    rc = fa::launch_bwd_bits(bp, (long long)B * mask_heads, s);
     if (rc != FA_OK) return rc;
   }
   fa::BwdPrepParams pp;

@@ -11,7 +11,7 @@ namespace fa {
 
 // -L, -delta and the bits of a mask's tiles; before it, a boolean mask's bits.
 int launch_bwd_prep(BwdPrepParams& p, long long heads, int D, cudaStream_t s);
-int launch_bwd_bits(const BwdBitsParams& p, cudaStream_t s);
+int launch_bwd_bits(const BwdBitsParams& p, long long heads, cudaStream_t s);
 
 // dQ, dK and dV of prm.plan, with the join where units are cut.  mask: kBwdMask*.
 // FA_OK, FA_ERR_UNSUPPORTED (a build whose register split does not fit) or
