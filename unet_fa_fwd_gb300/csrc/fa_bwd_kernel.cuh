@@ -34,12 +34,12 @@
 // the gradients, from one copy in shared memory.
 //
 // What bounds it.  D = 128: the tensor pipe, 83 % active with operands at the rate of
-// shared memory, and for long runs the GPU's power: 4608 tokens of 24 heads 495 to
-// 515 us, 16896 6.6 to 6.9 ms, 1.26 to 1.32 PFLOP/s of the five products that the
+// shared memory, and for long runs the GPU's power: 4608 tokens of 24 heads 486 to
+// 502 us, 16896 6.5 to 6.9 ms, 1.27 to 1.34 PFLOP/s of the five products that the
 // gradient needs, 1.8 of the seven taken.  D = 64: a thread's chain of waits, loads of
 // tensor memory, exponentials and roundings, whose phases all warps are in together
 // (issue slots 57 % used, tensor pipe 59, exponential units 34): 4096 tokens of 8
-// heads, batch 2, 177 us, 0.97 PFLOP/s.
+// heads, batch 2, 174 us, 0.99 PFLOP/s.
 //
 // Waits are bounded: past the limit a CTA records FA_ERR_TIMEOUT in the device
 // status word, drains its copies and MMAs, frees tensor memory and returns.
@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_kernel(const __grid_con
 // -L and -delta of every query row, and of the rows that fill up the last tile:
 // L_i = log2(e) LSE_i (+inf for a row that sees nothing, so that its P is 0),
 // delta_i = dO_i . O_i - dLSE_i.  HBM bound (O and dO are read once: 4608 tokens of
-// 24 heads of 128 14 us, 4.1 TB/s cold); D / 8 neighbouring lanes share a row.
+// 24 heads of 128 11 us, 5.1 TB/s cold; 14 with one row a thread); D / 8 neighbouring lanes share a row.
 struct BwdPrepParams {
   BwdTensor out, dout;
   const float *lse, *dlse;  // [B][Hq][Nq]; dlse may be nullptr
