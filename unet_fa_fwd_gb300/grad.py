@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import math
 
 import torch
@@ -116,6 +117,7 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, axes: 
                 pairing)
 
 
+@functools.lru_cache(maxsize=1024)  # (a call of its own into the library otherwise)
 def norm_rope_workspace_bytes(D: int) -> int:
     return int(load_library().fa_norm_rope_workspace_bytes(D))
 
@@ -138,7 +140,7 @@ def _norm_rope_bwd(dq_out, dk_out, q, k, pos, axes, q_weight, k_weight, eps, dq,
     if new:
         dwq, dwk = (None if w is None else torch.empty(D, dtype=_F32, device=q.device) for w in (q_weight, k_weight))
         if dwq is not None or dwk is not None:
-            workspace = torch.empty(lib.fa_norm_rope_workspace_bytes(D), dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(norm_rope_workspace_bytes(D), dtype=torch.uint8, device=q.device)
     else:
         for w, dw, name in ((q_weight, dwq, "dq_weight"), (k_weight, dwk, "dk_weight")):
             if (w is None) != (dw is None):
@@ -191,6 +193,7 @@ def norm_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Tensor, k:
                 None, True, token_major, pairing)
 
 
+@functools.lru_cache(maxsize=1024)
 def bwd_workspace_bytes(B: int, Hq: int, Hk: int, Nq: int, Nk: int, D: int, bool_mask_heads: int = 0) -> int:
     """``bool_mask_heads``: heads (1 or Hq) of a boolean mask, which is kept as bits; 0 for any other mask."""
     return int(load_library().fa_bwd_workspace_bytes(B, Hq, Hk, Nq, Nk, D, bool_mask_heads))
@@ -227,7 +230,7 @@ def _bwd(dout, q, k, v, out, lse, dlse, key_mask, full_mask, causal, scale, dq, 
         dq, dk, dv = (_rope_new(q_shape, _BF16, on, token_major), _rope_new(k_shape, _BF16, on, token_major),
                       _rope_new(k_shape, _BF16, on, token_major))
         heads = 0 if full_mask is None or full_mask.dtype is _F32 or full_mask.dim() != 4 else full_mask.shape[1]
-        workspace = torch.empty(lib.fa_bwd_workspace_bytes(B, Hq, Hk, Nq, Nk, D, heads), dtype=torch.uint8, device=on)
+        workspace = torch.empty(bwd_workspace_bytes(B, Hq, Hk, Nq, Nk, D, heads), dtype=torch.uint8, device=on)
         q_strides, k_strides = _rope_strides(q_shape, token_major), _rope_strides(k_shape, token_major)
         fields += (dq.data_ptr(), *q_strides, dk.data_ptr(), *k_strides, dv.data_ptr(), *k_strides)
     else:
