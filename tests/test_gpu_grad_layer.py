@@ -214,6 +214,54 @@ def test_one_pair_of_a_million():
     assert int((dv != 0).any(-1).sum()) == 2 and torch.equal(dv[:, :, 513], x["dout"][:, :, 1027])  # P = 1
 
 
+def _far(x, step):
+    """x [B, H, N, D] with its tokens `step` elements apart, in a buffer that passes 2^31 elements."""
+    B, H, N, D = x.shape
+    buf = torch.empty(B * N * step, dtype=x.dtype, device="cuda")
+    assert buf.numel() > 2 ** 31
+    y = buf.as_strided((B, H, N, D), (N * step, D, step, 1))
+    y.copy_(x)
+    return y
+
+
+def test_offsets_past_32_bits():
+    B, H, N, D = 2, 2, 140, 64
+    x = _inputs(B, H, H, N, N, D, causal=True, dlse=True)
+    want = fa.bwd(**x)
+    step = 2 ** 23
+    far = dict(x, **{n: _far(x[n], step) for n in ("q", "dout")})
+    dq = _far(torch.zeros_like(x["q"]), step)
+    dk, dv = torch.empty_like(x["k"]), _far(torch.zeros_like(x["v"]), step)
+    ws = torch.empty(fa.bwd_workspace_bytes(B, H, H, N, N, D), dtype=torch.uint8, device="cuda")
+    fa.fa_bwd(far["dout"], far["q"], x["k"], x["v"], x["out"], x["lse"], dq, dk, dv, ws, causal=True,
+              scale=x["scale"], dlse=x["dlse"])
+    assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), want))
+    axes, pos = fa.RopeAxes(DIMS[D]), torch.arange(3 * N, dtype=torch.int32, device="cuda").view(N, 3)
+    w = 1 + 0.3 * _rand((D,), 4, torch.float32)
+    far_out = _far(torch.zeros_like(x["q"]), step)
+    fa.fa_norm_rope(far["q"], None, pos, axes, w, None, far_out, None)
+    assert torch.equal(far_out, fa.norm_rope(x["q"], None, pos, axes, w)[0])
+    got = fa.norm_rope_bwd(far["dout"], None, far["q"], None, pos, axes, w)
+    assert all(torch.equal(a, b) for a, b in zip(got[::2], fa.norm_rope_bwd(x["dout"], None, x["q"], None, pos, axes,
+                                                                            w)[::2]))
+
+
+@pytest.mark.parametrize("kind,N", [("bool", 47000), ("add", 33100)])
+def test_masks_past_32_bits(kind, N):
+    """A mask that keeps everything (adds 0 everywhere) leaves the results as they are, bit for bit; one that leaves
+    the last rows out by its last bytes does not touch the others' dQ."""
+    q, k, v, do = (_rand((1, 1, N, 32), i) for i in range(4))
+    out, lse = fa.fwd(q, k, v)
+    want = fa.bwd(do, q, k, v, out, lse)
+    m = torch.ones(1, 1, N, N, dtype=torch.bool, device="cuda") if kind == "bool" else torch.zeros(1, 1, N, N, device="cuda")
+    assert m.numel() * m.element_size() > 2 ** 31
+    got = fa.bwd(do, q, k, v, out, lse, full_mask=m)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    m[:, :, -200:] = False if kind == "bool" else -math.inf
+    dq = fa.bwd(do, q, k, v, out, lse, full_mask=m)[0]
+    assert torch.equal(dq[:, :, :-200], want[0][:, :, :-200]) and bool((dq[:, :, -200:] == 0).all())
+
+
 CHILD = r'''
 import sys, torch
 sys.path.insert(0, ROOT)
