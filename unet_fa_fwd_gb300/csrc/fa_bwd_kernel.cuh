@@ -977,6 +977,8 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       }
       ptx::tc_fence_before_sync();
     }
+    // (after an abort a mask's copies may be on their way to this CTA's shared memory)
+    if constexpr (MK == kBwdMaskAdd) asm volatile("cp.async.wait_all;" ::: "memory");
     ptx::tc_fence_before_sync();
   }
   finish();
