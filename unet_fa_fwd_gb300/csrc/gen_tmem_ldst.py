@@ -35,7 +35,8 @@ __device__ __forceinline__ void tmem_st32x32b_x{n}(uint32_t taddr, const uint32_
 def ld2(n):
     """Two loads of 16 lanes by 256 bits: an element's place is 8 * (8-column block) + 2 * (row / 8) + its column."""
     at = [[8 * (k // 4) + 4 * h + k % 4 for k in range(4 * n)] for h in (0, 1)]
-    outs = ", ".join(f'"=r"(r[{i}])' for i in range(8 * n))
+    # (early-clobber: the first load's results must not take the register of the second one's address)
+    outs = ", ".join(f'"=&r"(r[{i}])' for i in range(8 * n))
     lines = "\n      ".join(f'"tcgen05.ld.sync.aligned.16x256b.x{n}.b32 {{{{{",".join(f"%{i}" for i in at[h])}}}}}, [%{8 * n + h}];\\n"'
                              for h in (0, 1)).replace("{{", "{").replace("}}", "}")
     return f'''// {8 * n} consecutive 32-bit TMEM columns of the warp's 32 lanes, waited for: r[8 i + 2 j + c]
