@@ -1,0 +1,139 @@
+"""Gradients of rows that masks leave in an unusual state: wholly under a large finite
+mask.
+
+A row's softmax does not change when a constant is taken off its scores, so the 64-bit
+definition takes each row's largest mask value off first; O and LSE are rounded from it
+as the forward's are.
+"""
+import math
+
+import pytest
+import torch
+
+import unet_fa_fwd_gb300 as fa
+
+from . import grad_ref as ref
+from .test_gpu_bwd import _full_mask, _inputs, _rand
+
+pytestmark = pytest.mark.gpu
+
+INF = math.inf
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    fa.load_library()
+    torch.cuda.set_device(0)
+    yield
+    torch.cuda.synchronize()
+    assert fa.read_device_status() == 0
+
+
+# ---- rows wholly under a large finite mask ----
+
+def _check_shifted(B, Hq, Hk, Nq, Nk, D, causal, seed=1, **mask):
+    """Tolerances as in the tests of ordinary masks, and 2^-9 of P (in its terms, and in the norm).  Rows of |LSE|
+    below 2^14: LSE is within 2^-11 (half its step), L = LSE log2(e) and mask log2(e) within 2^-10 each in the log2
+    domain, so P within 2^-11 + 2 ln(2) 2^-10 < 2^-9 of itself.  Rows past that are summed again, from scores to
+    which what the reference's rounding left is added: up to 2^14 for masks below 2^38, so scores and the sum are
+    within 2^-10 each, and P within 2 ln(2) 2^-10."""
+    m = mask["key_mask"][:, None, None].expand(B, 1, Nq, Nk) if "key_mask" in mask else mask["full_mask"]
+    seen = m > -INF
+    if causal:
+        seen = seen & torch.ones(Nq, Nk, dtype=torch.bool, device="cuda").tril()
+    top = m.double().masked_fill(~seen, -INF).amax(-1, keepdim=True)
+    shift = torch.where(top.isfinite(), top, 0.0)
+    even = (m.double() - shift).masked_fill(~seen, -INF)
+    q, k, v, do = (_rand((B, H, N, D), seed + i) for i, (H, N) in enumerate(((Hq, Nq), (Hk, Nk), (Hk, Nk), (Hq, Nq))))
+    scale = 1 / math.sqrt(D)
+    o, lse = ref.attend(q, k, v, scale, full_mask=even)
+    x = dict(dout=do, q=q, k=k, v=v, out=o.to(torch.bfloat16), scale=scale)
+    got = fa.bwd(**x, lse=(lse + shift[..., 0]).float(), causal=causal, **mask)
+    torch.cuda.synchronize()
+    assert fa.read_device_status() == 0
+    want, size, fine = ref.attend_bwd(**x, lse=lse, full_mask=even)
+    for name, y, w, s, f in zip(("dq", "dk", "dv"), got, want, size, fine):
+        err = (y.double() - w).abs()
+        tol = 2.0 ** -8 * w.abs() + (2.0 ** -8 + 2.0 ** -13 + 2.0 ** -9) * s + 2.0 ** -16 * f
+        assert bool((err <= tol).all()), (name, float((err - tol).max()), float(err.max()))
+        assert float(err.norm()) <= (5e-3 + 2.0 ** -9) * float(w.norm()), (name, float(err.norm() / w.norm()))
+
+
+LARGE = [-1e4, -65504.0, -1e6, -1e9, -2.7e11, 1e9]
+LOST = [-2.8e11, -1e30, -2e38]  # (past 2.3e38 a mask leaves fp32's range in the log2 domain)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("c", LARGE)
+@pytest.mark.parametrize("size", [(2, 2, 2, 130, 77), (3, 4, 2, 300, 400), (2, 1, 1, 1, 33)])
+def test_entries_wholly_under_a_large_key_mask(D, c, size):
+    B, Nk = size[0], size[4]
+    m = torch.zeros(B, Nk, device="cuda")
+    m[0, Nk // 2:] = -abs(c)            # ordinary padding
+    m[1] = c                            # a whole entry
+    m[1, Nk // 3] = -INF
+    if B > 2:
+        m[2, 5:] = c                    # five ordinary keys, or all but five above the others
+    _check_shifted(*size, D, False, key_mask=m)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("c", LARGE[1:5])
+@pytest.mark.parametrize("size,pad", [((2, 2, 2, 260, 260), 100), ((1, 4, 1, 700, 700), 300), ((1, 1, 1, 2100, 2100), 140)])
+def test_padding_ahead_of_a_causal_sequence(D, c, size, pad):
+    """The first rows see padding only; those behind see both."""
+    m = torch.zeros(size[0], size[4], device="cuda")
+    m[0, :pad] = c
+    _check_shifted(*size, D, True, key_mask=m)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("c", LARGE)
+@pytest.mark.parametrize("size,heads,causal", [((2, 2, 2, 130, 77), 1, False), ((1, 4, 2, 257, 400), 4, True),
+                                               ((2, 2, 1, 3, 33), 2, False), ((1, 1, 1, 1500, 1100), 1, False)])
+def test_rows_wholly_under_a_large_additive_mask(D, c, size, heads, causal):
+    B, Hq, Hk, Nq, Nk = size
+    m = _full_mask("add", B, heads, Nq, Nk, 4)
+    m[:, :, Nq // 2:Nq // 2 + 20] = c   # whole rows, and one of two heights
+    m[:, :, -1] = c
+    m[:, :, -1, Nk // 2:] = -abs(c) * 1.5
+    m[..., 0, :, 3] = -INF
+    m[0, 0, :, Nk // 4] = -abs(c)       # a column that ordinary rows do not see
+    _check_shifted(*size, D, causal, full_mask=m)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("c", LOST)
+def test_rows_past_the_last_bound_see_nothing(D, c):
+    """Rows wholly under such masks have no gradient, as under -inf; ordinary rows do not see keys under them."""
+    B, Hq, Hk, Nq, Nk = 2, 4, 2, 260, 300
+    m = _full_mask("add", B, 1, Nq, Nk, 4)
+    m[:, :, 100:140] = c
+    m[:, :, 150, ::2] = c
+    key = torch.zeros(B, Nk, device="cuda")
+    key[0, 200:], key[1] = c, c
+    for mask in (dict(full_mask=m), dict(key_mask=key)):
+        (name, large), = mask.items()
+        cut = large.masked_fill(large == c, -INF)
+        x = _inputs(B, Hq, Hk, Nq, Nk, D, **{name: cut}, dlse=True)
+        want = fa.bwd(**x)
+        x["lse"] = torch.where(x["lse"] == -INF, torch.tensor(c, device="cuda"), x["lse"])
+        x[name] = large
+        assert all(torch.equal(a, b) for a, b in zip(fa.bwd(**x), want))
+
+
+def test_large_masks_repeat_and_agree_with_none():
+    """All rows at one large value: the gradients of no mask, but for the rows' own normaliser; twice the same."""
+    B, H, N, D = 1, 3, 500, 64
+    x = _inputs(B, H, H, N, N, D)
+    x["lse"] = x["lse"] - 1e9
+    m = torch.full((B, 1, N, N), -1e9, device="cuda")
+    one, two = fa.bwd(**x, full_mask=m), fa.bwd(**x, key_mask=m[:, 0, 0].contiguous())
+    plain = fa.bwd(**dict(x, lse=x["lse"] * 0 + _inputs(B, H, H, N, N, D)["lse"]))
+    again = fa.bwd(**x, full_mask=m)
+    assert all(torch.equal(a, b) for a, b in zip(one, again))
+    for a, b, c in zip(one, two, plain):
+        # P within 2^-13 of itself either way; both results, P and dS rounded to bf16 alike or one step apart
+        for y in (a, b):
+            assert float((y.double() - c.double()).norm()) <= 5e-3 * float(c.double().norm())

@@ -41,9 +41,10 @@ int launch_bwd_prep(BwdPrepParams& p, long long heads, int D, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = p.some ? 1 : 0;
   const BwdPrepParams& prm = p;
-  const cudaError_t e = D == 32   ? cudaLaunchKernelEx(&cfg, fa_bwd_prep_kernel<32>, prm)
-                        : D == 64 ? cudaLaunchKernelEx(&cfg, fa_bwd_prep_kernel<64>, prm)
-                                  : cudaLaunchKernelEx(&cfg, fa_bwd_prep_kernel<128>, prm);
+  auto go = [&](auto* with, auto* without) { return cudaLaunchKernelEx(&cfg, p.mask ? with : without, prm); };
+  const cudaError_t e = D == 32   ? go(fa_bwd_prep_kernel<32, true>, fa_bwd_prep_kernel<32, false>)
+                        : D == 64 ? go(fa_bwd_prep_kernel<64, true>, fa_bwd_prep_kernel<64, false>)
+                                  : go(fa_bwd_prep_kernel<128, true>, fa_bwd_prep_kernel<128, false>);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -86,24 +87,29 @@ bool mask_ok(int B, int Hq, int Nq, int Nk, int heads) {
   return (heads == 1 || heads == Hq) && (__int128)B * heads * Nq * Nk <= ((__int128)1 << 58);
 }
 
+constexpr int kSlotCtas = 160;  // CTAs (one per SM) that partial sums are kept for
+
 // The workspace, in order (each part 256-byte aligned).  Partial sums are for
 // the most CTAs a plan has: it does not depend on the GPU.  bool_heads: heads of
 // a boolean mask (0: no such mask), whose bits are kept by rows and by keys, with
-// those of its tiles; without one, the key tiles' of a key-padding mask.
+// those of its tiles; without one, the key tiles' of a key-padding mask.  The
+// total is at least kBwdMaxCtas' partial sums and two floats a row, in which the
+// statistics fit up to 5900 tiles of queries (D = 32; 23800 for D = 128).
 struct Layout {
-  size_t nlse, ndelta, part_kv, part_q, bits_q, bits_k, some, tiles_q, tiles_k, total;
+  size_t stat, part_kv, part_q, bits_q, bits_k, some, tiles_q, tiles_k, total;
 };
 
 Layout layout(int B, int Hq, int Nq, int Nk, int D, int bool_heads) {
-  const size_t qt = ((size_t)Nq + 127) / 128, kt = ((size_t)Nk + 127) / 128, rows = (size_t)B * Hq * qt * 128;
-  const size_t slots = 2 * (size_t)fa::kBwdMaxCtas, tile = 128 * (size_t)D * sizeof(float);
+  const size_t qt = ((size_t)Nq + 127) / 128, kt = ((size_t)Nk + 127) / 128, tiles = (size_t)B * Hq * qt;
+  const size_t slots = 2 * (size_t)kSlotCtas, tile = 128 * (size_t)D * sizeof(float);
   const size_t masks = (size_t)B * bool_heads;
   Layout l{};
   size_t off = 0;
-  l.nlse = off;     off += align256(rows * sizeof(float));
-  l.ndelta = off;    off += align256(rows * sizeof(float));
+  l.stat = off;     off += align256(tiles * fa::kStatTile * sizeof(float));
   l.part_kv = off;  off += slots * 2 * tile;
   l.part_q = off;   off += slots * tile;
+  const size_t least = tiles * 2 * 128 * sizeof(float) + 2 * (size_t)fa::kBwdMaxCtas * 3 * tile;
+  off = off < least ? least : off;
   l.bits_q = off;   off += align256(masks * Nq * kt * 16);
   l.bits_k = off;   off += align256(masks * Nk * qt * 16);
   l.some = off;     off += align256(masks * qt * kt * 4);
@@ -250,8 +256,7 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   p.causal = causal ? 1 : 0;
   p.scale = scale;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  p.nlse = reinterpret_cast<float*>(ws + l.nlse);
-  p.ndelta = reinterpret_cast<float*>(ws + l.ndelta);
+  p.stat = reinterpret_cast<float*>(ws + l.stat);
   p.mask = mask_data;
   p.mask_heads = mask_heads;
   p.div_group = fa::FastDiv::make((uint32_t)group);
@@ -296,7 +301,7 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
     u.spread = p.causal && u.tiles < st->sm_count ? 1 : 0;
     u.div_heads = fa::FastDiv::make((uint32_t)u.heads);
     u.div_tiles = fa::FastDiv::make((uint32_t)u.tiles);
-    p.plan[kv ? 0 : 1] = fa::bwd_plan(u, st->sm_count, kJoinCost);
+    p.plan[kv ? 0 : 1] = fa::bwd_plan(u, st->sm_count < kSlotCtas ? st->sm_count : kSlotCtas, kJoinCost);
   }
 
   if (kind == FA_MASK_BOOL) {
@@ -318,8 +323,15 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   pp.dout = view(*dout);
   pp.lse = lse;
   pp.dlse = dlse;
-  pp.nlse = reinterpret_cast<float*>(ws + l.nlse);
-  pp.ndelta = reinterpret_cast<float*>(ws + l.ndelta);
+  pp.q = view(*q);
+  pp.k = view(*k);
+  pp.stat = reinterpret_cast<float*>(ws + l.stat);
+  if (kind == FA_MASK_KEY_PADDING || kind == FA_MASK_ADDITIVE) pp.mask = static_cast<const float*>(mask_data);
+  pp.mask_heads = mask_heads;
+  pp.mask_rows = kind == FA_MASK_ADDITIVE;
+  pp.causal = p.causal;
+  pp.group = group;
+  pp.scale_log2 = p.scale_log2;
   pp.Hq = Hq;
   pp.Nq = Nq;
   pp.nqp = p.nqp;

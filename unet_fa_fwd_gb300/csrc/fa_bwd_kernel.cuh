@@ -6,6 +6,9 @@
 //   dV_j = sum_i P_ij dO_i,  dK_j = scale sum_i dS_ij Q_i,  dQ_i = scale sum_j dS_ij K_j.
 // P is recomputed from L (no running maximum), so a tile's work is two products
 // into tensor memory, one pass of the threads, and the products of its results.
+// A row all of whose keys lie under a large finite mask has an LSE whose fp32 step
+// hides the sum; there L is summed again, of scores less the row's largest mask
+// value (bwd_resum), and t_ij is taken less that value too.
 //
 // Two kinds of unit, of 128 rows: keys (dK, dV; products S^T, dP^T, dV, dK) and
 // queries (dQ; S, dP, dQ).  Seven products for the five that one kind would need:
@@ -64,13 +67,28 @@ struct BwdTensor {
   long long b, h, n;
 };
 
+// The statistics of 128 queries (a tile), in the workspace: -L (-inf for rows that see
+// nothing and rows past Nq), -delta, flags (a word for each half of the rows: some have
+// references; two words to 16 bytes), which key units copy to shared memory together;
+// then the negated references (0 where L is LSE's).
+constexpr int kStatDelta = 128, kStatFlags = 256, kStatCopy = 260, kStatRef = 260, kStatTile = 388;  // floats
+
+// Under a finite mask LSE may be far from the scores.  Below the first bound its half
+// step is 2^-11, those of L and of the mask in the log2 domain 2^-10 each, so P is within
+// 2^-9 of itself (bf16, which P is rounded to, has 2^-8); a step further each doubles.
+// From there on rows get a reference: ref = the largest mask log2(e) that they see,
+// rounded, and mask log2(e) - ref in one rounding.  That leaves what the product's
+// rounding left, up to 2^14 below the second bound, in t and in L alike: again 2^-10
+// each.  Rows past it count as rows that see nothing.
+constexpr float kWeakLse = 16384.f, kLostLse = 274877906944.f;
+__device__ __forceinline__ bool bwd_weak(float lse) { return fabsf(lse) >= kWeakLse && fabsf(lse) < kLostLse; }
+
 struct BwdParams {
   BwdPlan plan[2];  // key units, query units
   int Hq, Hk, group, Nq, Nk, nqp;  // nqp: queries rounded up to whole tiles
   int causal;
   float scale, scale_log2;
-  const float* nlse;    // [B Hq][nqp]: -L, -inf for rows that see nothing and rows past Nq
-  const float* ndelta;  // [B Hq][nqp]: -delta
+  const float* stat;    // [B Hq][nqp / 128][kStatTile]
   const void* mask;     // fp32 [B][Nk] or [B][mask_heads][Nq][Nk]
   int mask_heads;
   int mask_vec;         // its rows are 16-byte aligned
@@ -108,7 +126,7 @@ struct BwdCfg {
   // later, and dO; query units: K and V).  At D = 128 the slots that fit.
   static constexpr int RING0 = D == 128 ? (MK == kBwdMaskAdd ? 2 : 3) : 4;
   static constexpr int RING1 = D == 128 ? 2 : 4;
-  static constexpr int STAT_BYTES = 2 * 1024;  // key units: two slots of -L and -delta of 128 queries
+  static constexpr int STAT_BYTES = 2 * kStatCopy * 4;  // key units: two slots of a tile's -L, -delta and flags
   static constexpr int SMEM_BAR = 512;
   static constexpr int SMEM_USED = (2 + RING0 + RING1) * TILE + STAT_BYTES + MASK_BYTES + SMEM_BAR;
   // (more than half of the SM's, so that one CTA has its tensor memory alone)
@@ -284,8 +302,8 @@ struct BwdStage {
     }
   }
   // The lane's 16 values of the columns c0 .. c0 + 15 (key units: of 4 rows and 4
-  // columns, in the order of bwd_elements), times log2(e).
-  static __device__ __forceinline__ void read(const float* buf, int c0, int lane, float (&m)[16]) {
+  // columns, in the order of bwd_elements), times log2(e), less the row's reference.
+  static __device__ __forceinline__ void read(const float* buf, int c0, int lane, float nref, float (&m)[16]) {
     constexpr float kLog2e = 1.4426950408889634f;
     if constexpr (KV) {
 #pragma unroll
@@ -305,7 +323,7 @@ struct BwdStage {
     }
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
-      const float2 v = __fmul2_rn(make_float2(m[e], m[e + 1]), make_float2(kLog2e, kLog2e));
+      const float2 v = __ffma2_rn(make_float2(m[e], m[e + 1]), make_float2(kLog2e, kLog2e), make_float2(nref, nref));
       m[e] = v.x;
       m[e + 1] = v.y;
     }
@@ -322,6 +340,8 @@ __device__ __forceinline__ void bwd_load_elements(uint32_t t, uint32_t (&r)[32])
   else
     ptx::tmem_ld32x32b_x32(t, r);
 }
+// Of a key unit the elements of the 8 columns at `t` (i = 0).
+__device__ __forceinline__ void bwd_load_elements(uint32_t t, uint32_t (&r)[8]) { ptx::tmem_ld2x16x256b_x1(t, r); }
 // Pairs of a key unit's elements in that order, as the 16 columns at `t`.
 __device__ __forceinline__ void bwd_store_pairs(uint32_t t, const uint32_t (&w)[16]) { ptx::tmem_st2x16x128b_x4(t, w); }
 
@@ -500,6 +520,10 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
   };
   const int heads = KV ? p.Hk : p.Hq;
   const FastDiv& div_h = KV ? p.div_hk : p.div_hq;
+  // A query tile's statistics.
+  auto stat_of = [&](int b, int hq, int tile) {
+    return (((size_t)b * p.Hq + hq) * (p.nqp / 128) + tile) * kStatTile;
+  };
 
   if (warp >= kBwdWarps) {
     ptx::setmaxnreg_dec<C::REGS_OTHER>();
@@ -554,10 +578,8 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
               ok = bwd_wait(bars->st_empty[ss], ((j / 2) & 1) ^ 1, bars, p);
               if (!ok) break;
               full = ptx::smem_u32(&bars->st_full[ss]);
-              ptx::mbar_arrive_expect_tx(full, 1024);
-              const size_t row = ((size_t)b * p.Hq + ho) * p.nqp + (size_t)at.tile * 128;
-              bulk_load(ptx::smem_u32(sStat + ss * 256), p.nlse + row, 512, full);
-              bulk_load(ptx::smem_u32(sStat + ss * 256 + 128), p.ndelta + row, 512, full);
+              ptx::mbar_arrive_expect_tx(full, kStatCopy * 4);
+              bulk_load(ptx::smem_u32(sStat + ss * kStatCopy), p.stat + stat_of(b, ho, at.tile), kStatCopy * 4, full);
               ++nst;
             }
             ok = bwd_wait(bars->r1_empty[s1], ((j / C::RING1) & 1) ^ 1, bars, p);
@@ -729,6 +751,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
     };
     using Stage = BwdStage<KV, MK == kBwdMaskAdd ? C::MASK_COLS : 32>;
     float* sMask = sStat + C::STAT_BYTES / 4 + warp * 32 * C::MASK_COLS;
+    constexpr bool REFS = MK == kBwdMaskKey || MK == kBwdMaskAdd;  // rows may have references
     uint32_t j = 0, nu = 0;
     bool ok = true;
     // A piece, and what follows from it.  The next one is made out while the last
@@ -738,7 +761,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       BwdPiece pc;
       int b, h;
       BwdIter<MK, KV> at;
-      float nlse, ndelta;  // of a query unit's row
+      float nlse, ndelta, nref;  // of a query unit's row
     };
     BwdWalk walk;
     auto next_work = [&](Work& w) {
@@ -749,11 +772,12 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       }
       w.b = (int)div_h.div((uint32_t)w.pc.head);
       w.h = w.pc.head - w.b * heads;
-      w.nlse = w.ndelta = 0.f;
+      w.nlse = w.ndelta = w.nref = 0.f;
       if constexpr (!KV) {
-        const size_t at = (size_t)w.pc.head * p.nqp + w.pc.tile * 128 + row;
-        w.nlse = __ldcg(p.nlse + at);
-        w.ndelta = __ldcg(p.ndelta + at);
+        const float* at = p.stat + stat_of(w.b, w.h, w.pc.tile) + row;
+        w.nlse = __ldcg(at);
+        w.ndelta = __ldcg(at + kStatDelta);
+        if constexpr (REFS) w.nref = __ldcg(at + kStatRef);
       }
       w.at.start(p, plan.units, w.pc, w.b, w.h);
       return true;
@@ -763,7 +787,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       const BwdPiece pc = work.pc;
       const int b = work.b, h = work.h;
       const int my = pc.tile * 128 + row, my4 = pc.tile * 128 + row4;  // this thread's key or query
-      const float nlse = work.nlse, ndelta = work.ndelta;
+      const float nlse = work.nlse, ndelta = work.ndelta, nref = work.nref;
       float key_add[4] = {};
       if constexpr (KV && MK == kBwdMaskKey) {
 #pragma unroll
@@ -803,8 +827,8 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         at.next();
         const float *lcol = nullptr, *dcol = nullptr;  // -L and -delta of this thread's columns
         if constexpr (KV) {
-          lcol = sStat + (j & 1) * 256 + wg * kBwdCols + col2;
-          dcol = lcol + 128;
+          lcol = sStat + (j & 1) * kStatCopy + wg * kBwdCols + col2;
+          dcol = lcol + kStatDelta;
         }
         // Pairs that the row does not see: above the diagonal, and keys past Nk
         // (as columns; as rows their gradients are not stored).
@@ -838,6 +862,11 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         ok = bwd_wait_warp(KV ? &bars->st_full[j & 1] : nullptr, (j / 2) & 1, bars->s_full[sb], (j / T::NS) & 1, bars, p);
         if (!ok) break;
         ptx::tc_fence_after_sync();
+        bool weak = false;  // (read ahead of the scores, whose wait hides it)
+        if constexpr (REFS && KV) {
+          const uint2 f = *reinterpret_cast<const uint2*>(sStat + (j & 1) * kStatCopy + kStatFlags);
+          weak = (f.x | f.y) != 0;
+        }
         float pr[kBwdCols];  // in the order of bwd_elements
         {
           uint32_t r[kBwdCols];
@@ -853,7 +882,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
               asm volatile("cp.async.wait_all;" ::: "memory");
               __syncwarp();
             }
-            Stage::read(sMask, cb % C::MASK_COLS, (int)lane, m);
+            Stage::read(sMask, cb % C::MASK_COLS, (int)lane, nref, m);
             if ((cb + 16) % C::MASK_COLS == 0) {  // the buffer has been read
               __syncwarp();
               if (cb + 16 < kBwdCols)
@@ -864,7 +893,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
           } else if constexpr (MK == kBwdMaskKey && !KV) {
             const float* mrow = static_cast<const float*>(p.mask) + (size_t)b * p.Nk;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) m[c] = __ldg(mrow + min(col0 + cb + c, p.Nk - 1)) * kLog2e;
+            for (int c = 0; c < 16; ++c) m[c] = fmaf(__ldg(mrow + min(col0 + cb + c, p.Nk - 1)), kLog2e, nref);
           }
 #pragma unroll
           for (int c = cb; c < cb + 16; c += 2) {
@@ -878,6 +907,33 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
             const float2 e = bwd_exp(pr[c], pr[c + 1], sl2, a);
             pr[c] = e.x;
             pr[c + 1] = e.y;
+          }
+        }
+        if constexpr (REFS && KV) {
+          // Queries with a reference: their columns again, S is still there.  (The block in
+          // the loop takes 2 % of a masked call that has none; two loops, or the threads'
+          // part out of line, took 4 to 13 % in spills and missed instructions.)
+          if (weak) {
+            const int hq = h * p.group + now.g;
+            const float* ref = p.stat + stat_of(b, hq, now.tile) + kStatRef + wg * kBwdCols + col2;
+            const float* mrow = static_cast<const float*>(p.mask) +
+                                (MK == kBwdMaskAdd ? mask_head(now) * p.Nq * p.Nk : (size_t)b * p.Nk);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 rf = __ldcg(reinterpret_cast<const float2*>(ref + 8 * i));
+              if (!__any_sync(0xffffffffu, rf.x != 0.f || rf.y != 0.f)) continue;
+              uint32_t t[8];
+              bwd_load_elements(tS + 8 * i, t);
+              const float2 l = *reinterpret_cast<const float2*>(lcol + 8 * i);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float nr = e % 2 ? rf.y : rf.x;
+                if (nr == 0.f) continue;
+                const int key = my4 + 8 * (e / 2), query = col0 + col2 + 8 * i + e % 2;  // (the query is below Nq)
+                const float m = key < p.Nk ? __ldg(mrow + (MK == kBwdMaskAdd ? (size_t)query * p.Nk : 0) + key) : -INFINITY;
+                pr[8 * i + e] = ptx::ex2(fmaf(__uint_as_float(t[e]), sl2, fmaf(m, kLog2e, nr) + (e % 2 ? l.y : l.x)));
+              }
+            }
           }
         }
         if (edge) {
@@ -1032,15 +1088,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_kernel(const __grid_con
     bwd_units<D, MK, false>(p, cta - keys, smem, bars, tmem);
 }
 
-// -L and -delta of every query row, and of the rows that fill up the last tile:
+// The statistics of every query row, and of the rows that fill up the last tile:
 // L_i = log2(e) LSE_i (+inf for a row that sees nothing, so that its P is 0),
 // delta_i = dO_i . O_i - dLSE_i.  HBM bound (O and dO are read once: 4608 tokens of
 // 24 heads of 128 11 us, 5.1 TB/s cold; 14 with one row a thread); D / 8 neighbouring lanes share a row.
 struct BwdPrepParams {
-  BwdTensor out, dout;
+  BwdTensor out, dout, q, k;
   const float *lse, *dlse;  // [B][Hq][Nq]; dlse may be nullptr
-  float *nlse, *ndelta;     // [B Hq][nqp]
+  float* stat;              // [B Hq][nqp / 128][kStatTile]
   int Hq, Nq, nqp;
+  const float* mask;        // of references: key padding ([B][Nk], mask_rows 0) or additive
+  int mask_heads, mask_rows, causal, group;
+  float scale_log2;
   FastDiv div_h;
   int head_blocks;     // blocks of a head's rows
   FastDiv div_blocks;
@@ -1092,7 +1151,93 @@ static __device__ __forceinline__ void bwd_tile_bits(const BwdPrepParams& p, lon
 template <int D>
 constexpr int kBwdPrepRows = D == 128 ? 64 : 128;
 
+// Joins two running (maximum, sum of 2^(x - maximum)).
+static __device__ __forceinline__ void bwd_join_sums(float& mx, float& sum, float mx2, float sum2) {
+  const float m = fmaxf(mx, mx2);
+  if (m == -INFINITY) return;
+  sum = sum * ptx::ex2(mx - m) + sum2 * ptx::ex2(mx2 - m);
+  mx = m;
+}
+
+// The reference of the rows among `rows` from row0 on whose LSE is too large to give P,
+// and L anew: log2 of the sum of 2^(scale s + (mask - ref)).  By 16 rows, whose keys the
+// block's 8 warps share.  Such rows are padding and few, so the products are a warp's
+// (mma.sync, 16 x 8 x 16) and their operands come from global memory.  Out of line: in
+// the blocks without such rows it takes no registers.
 template <int D>
+__device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int row0, int rows) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  __shared__ float s_ref[16], s_max[8][16], s_sum[8][16];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int b = (int)p.div_h.div((uint32_t)bh), h = bh - b * p.Hq;
+  const __nv_bfloat16* q = p.q.p + b * p.q.b + h * p.q.h + 2 * (lane % 4);
+  const __nv_bfloat16* k = p.k.p + b * p.k.b + (long long)(h / p.group) * p.k.h + 2 * (lane % 4);
+  const float* mask = p.mask + (p.mask_rows ? ((size_t)b * p.mask_heads + (p.mask_heads == 1 ? 0 : h)) * p.Nq * p.Nk
+                                            : (size_t)b * p.Nk);
+  auto mask_at = [&](int n, int j) { return mask[(p.mask_rows ? (size_t)n * p.Nk : 0) + j]; };
+  auto sees = [&](int n, int j) { return n < p.Nq && j < p.Nk && (!p.causal || j <= n); };
+  for (int r0 = row0; r0 < row0 + rows && r0 < p.Nq; r0 += 16) {
+    const int mine = r0 + lane % 16;
+    const uint32_t weak =
+        __ballot_sync(0xffffffffu, lane < 16 && mine < p.Nq && bwd_weak(p.lse[(size_t)bh * p.Nq + mine]));
+    if (weak == 0) continue;  // (in all warps alike)
+    {
+      const int n = r0 + threadIdx.x / 16;
+      float m = -INFINITY;
+      for (int j = threadIdx.x % 16; sees(n, j); j += 16) m = fmaxf(m, mask_at(n, j));
+#pragma unroll
+      for (int x = 1; x < 16; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+      if (threadIdx.x % 16 == 0) s_ref[threadIdx.x / 16] = m == -INFINITY ? 0.f : m * kLog2e;
+    }
+    __syncthreads();
+    const __nv_bfloat16 *q0 = q + min(r0 + lane / 4, p.Nq - 1) * p.q.n, *q1 = q + min(r0 + lane / 4 + 8, p.Nq - 1) * p.q.n;
+    float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {};
+    const int keys = p.causal ? min(p.Nk, r0 + 16) : p.Nk;
+    for (int j0 = warp * 16; j0 < keys; j0 += 128) {
+      float c[2][4] = {};
+      const __nv_bfloat16 *k0 = k + min(j0 + lane / 4, p.Nk - 1) * p.k.n, *k1 = k + min(j0 + 8 + lane / 4, p.Nk - 1) * p.k.n;
+#pragma unroll 2
+      for (int d = 0; d < D; d += 16) {
+        auto two = [&](const __nv_bfloat16* at, int e) { return *reinterpret_cast<const uint32_t*>(at + d + e); };
+        const uint32_t a[4] = {two(q0, 0), two(q1, 0), two(q0, 8), two(q1, 8)};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+              : "+f"(c[i][0]), "+f"(c[i][1]), "+f"(c[i][2]), "+f"(c[i][3])
+              : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(two(i ? k1 : k0, 0)), "r"(two(i ? k1 : k0, 8)));
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {  // row lane / 4 + 8 i, column 2 (lane % 4) + e % 2 of either eight
+        const int i = e / 2 % 2, r = lane / 4 + 8 * i, j = j0 + 8 * (e / 4) + 2 * (lane % 4) + e % 2;
+        if (!sees(r0 + r, j)) continue;
+        bwd_join_sums(mx[i], sum[i], fmaf(c[e / 4][e % 4], p.scale_log2, fmaf(mask_at(r0 + r, j), kLog2e, -s_ref[r])), 1.f);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int x = 1; x < 4; x <<= 1)
+        bwd_join_sums(mx[i], sum[i], __shfl_xor_sync(0xffffffffu, mx[i], x), __shfl_xor_sync(0xffffffffu, sum[i], x));
+      if (lane % 4 == 0) {
+        s_max[warp][lane / 4 + 8 * i] = mx[i];
+        s_sum[warp][lane / 4 + 8 * i] = sum[i];
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < 16 && (weak >> threadIdx.x & 1)) {
+      float m = s_max[0][threadIdx.x], l = s_sum[0][threadIdx.x];
+      for (int w = 1; w < 8; ++w) bwd_join_sums(m, l, s_max[w][threadIdx.x], s_sum[w][threadIdx.x]);
+      const int n = r0 + threadIdx.x;
+      float* at = p.stat + ((size_t)bh * (p.nqp / 128) + n / 128) * kStatTile + n % 128;
+      at[0] = l > 0.f ? -(m + log2f(l)) : -INFINITY;
+      at[kStatRef] = -s_ref[threadIdx.x];
+    }
+    __syncthreads();  // (the next rows' sums go to the same places)
+  }
+}
+
+// REFS: an additive or key-padding mask, under which rows may need references.
+template <int D, bool REFS>
 __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant__ BwdPrepParams p) {
   constexpr int L = D / 8;  // lanes a row
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1103,12 +1248,16 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
   // A block's rows are of one head.  All of a thread's loads go out together.
   constexpr int STEP = 256 / L, U = kBwdPrepRows<D> / STEP;
   const int bh = (int)p.div_blocks.div(blockIdx.x);
-  const int n0 = (int)(blockIdx.x - (unsigned)bh * p.head_blocks) * kBwdPrepRows<D> + threadIdx.x / L;
   const int b = (int)p.div_h.div((uint32_t)bh), h = bh - b * p.Hq, piece = threadIdx.x % L;
   const __nv_bfloat16 *out = p.out.p + b * p.out.b + h * p.out.h + piece * 8,
                       *dout = p.dout.p + b * p.dout.b + h * p.dout.h + piece * 8;
   uint4 o[U] = {}, g[U] = {};
   float lse[U], sum[U];
+  const int block_row = (int)(blockIdx.x - (unsigned)bh * p.head_blocks) * kBwdPrepRows<D>;
+  float* tile = p.stat + ((size_t)bh * (p.nqp / 128) + block_row / 128) * kStatTile;
+  float* stat = tile + block_row % 128 + threadIdx.x / L;
+  const int n0 = block_row + threadIdx.x / L;
+  bool weak = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int n = n0 + u * STEP;
@@ -1135,12 +1284,27 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
 #pragma unroll
     for (int m = 1; m < L; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
     if (piece == 0) {
-      const size_t at = (size_t)bh * p.nqp + n0 + u * STEP;
-      const bool sees = lse[u] != -INFINITY;  // (dLSE of a row that sees nothing may be anything)
-      p.nlse[at] = sees ? -lse[u] * 1.4426950408889634f : -INFINITY;
-      p.ndelta[at] = sees ? -(dot + sum[u]) : 0.f;
+      float* at = stat + u * STEP;
+      const bool sees = REFS ? !(fabsf(lse[u]) >= kLostLse) : lse[u] != -INFINITY;  // (else dLSE may be anything)
+      at[0] = sees ? -lse[u] * 1.4426950408889634f : -INFINITY;
+      at[kStatDelta] = sees ? -(dot + sum[u]) : 0.f;
+      if constexpr (REFS) {
+        at[kStatRef] = 0.f;
+        weak = weak || bwd_weak(lse[u]);
+      }
     }
   }
+  uint32_t flags = 0;
+  if constexpr (REFS) {
+    if (__syncthreads_or(weak)) {
+      flags = 1;
+      bwd_resum<D>(p, bh, block_row, kBwdPrepRows<D>);
+    }
+  }
+  // A word for each of a tile's blocks.
+  if (threadIdx.x < 128 / kBwdPrepRows<128>)
+    if (kBwdPrepRows<D> == 128 || (int)threadIdx.x == block_row % 128 / kBwdPrepRows<128>)
+      reinterpret_cast<uint32_t*>(tile)[kStatFlags + threadIdx.x] = flags;
 }
 
 // A boolean mask as bits, by query rows and by key rows: a block turns a tile, a warp

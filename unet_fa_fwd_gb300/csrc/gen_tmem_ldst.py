@@ -73,6 +73,7 @@ for n in (8, 16, 32, 64, 128):
     out.append(ld(n))
 for n in (8, 16, 32):
     out.append(st(n))
+out.append(ld2(1))
 out.append(ld2(4))
 out.append(st2(4))
 open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "tmem_ldst.inc"), "w").write(
