@@ -302,9 +302,8 @@ struct BwdStage {
     }
   }
   // The lane's 16 values of the columns c0 .. c0 + 15 (key units: of 4 rows and 4
-  // columns, in the order of bwd_elements), times log2(e), less the row's reference.
-  static __device__ __forceinline__ void read(const float* buf, int c0, int lane, float nref, float (&m)[16]) {
-    constexpr float kLog2e = 1.4426950408889634f;
+  // columns, in the order of bwd_elements).
+  static __device__ __forceinline__ void read(const float* buf, int c0, int lane, float (&m)[16]) {
     if constexpr (KV) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -320,12 +319,6 @@ struct BwdStage {
         m[4 * g + 2] = v.z;
         m[4 * g + 3] = v.w;
       }
-    }
-#pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      const float2 v = __ffma2_rn(make_float2(m[e], m[e + 1]), make_float2(kLog2e, kLog2e), make_float2(nref, nref));
-      m[e] = v.x;
-      m[e + 1] = v.y;
     }
   }
 };
@@ -344,12 +337,6 @@ __device__ __forceinline__ void bwd_load_elements(uint32_t t, uint32_t (&r)[32])
 __device__ __forceinline__ void bwd_load_elements(uint32_t t, uint32_t (&r)[8]) { ptx::tmem_ld2x16x256b_x1(t, r); }
 // Pairs of a key unit's elements in that order, as the 16 columns at `t`.
 __device__ __forceinline__ void bwd_store_pairs(uint32_t t, const uint32_t (&w)[16]) { ptx::tmem_st2x16x128b_x4(t, w); }
-
-// 2^(s sl2 + add) of a pair.
-__device__ __forceinline__ float2 bwd_exp(float s0, float s1, float sl2, float2 add) {
-  const float2 x = __ffma2_rn(make_float2(s0, s1), make_float2(sl2, sl2), add);
-  return make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-}
 
 // NC columns of a thread's accumulator row at `t`, times `mul`, rounded to `dst`
 // (16-byte aligned; neighbouring lanes' rows are `row_step` elements apart; `rows`:
@@ -788,6 +775,9 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       const int b = work.b, h = work.h;
       const int my = pc.tile * 128 + row, my4 = pc.tile * 128 + row4;  // this thread's key or query
       const float nlse = work.nlse, ndelta = work.ndelta, nref = work.nref;
+      // An additive mask's products are rounded together with -L, or the reference (and -L added behind the scores).
+      const bool has_ref = MK == kBwdMaskAdd && nref != 0.f;
+      const float first = has_ref ? nref : nlse, second = has_ref ? nlse : 0.f;
       float key_add[4] = {};
       if constexpr (KV && MK == kBwdMaskKey) {
 #pragma unroll
@@ -882,7 +872,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
               asm volatile("cp.async.wait_all;" ::: "memory");
               __syncwarp();
             }
-            Stage::read(sMask, cb % C::MASK_COLS, (int)lane, nref, m);
+            Stage::read(sMask, cb % C::MASK_COLS, (int)lane, m);
             if ((cb + 16) % C::MASK_COLS == 0) {  // the buffer has been read
               __syncwarp();
               if (cb + 16 < kBwdCols)
@@ -897,14 +887,18 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
           }
 #pragma unroll
           for (int c = cb; c < cb + 16; c += 2) {
-            float2 a = make_float2(nlse, nlse);
+            float2 a = make_float2(first, first);
             if constexpr (KV) {
               a = *reinterpret_cast<const float2*>(lcol + c / 8 * 8);
               if constexpr (MK == kBwdMaskKey) a = __fadd2_rn(a, make_float2(key_add[c / 2 % 4], key_add[c / 2 % 4]));
             }
-            if constexpr (MK == kBwdMaskAdd || (MK == kBwdMaskKey && !KV))
+            if constexpr (MK == kBwdMaskAdd)
+              a = __ffma2_rn(make_float2(m[c - cb], m[c - cb + 1]), make_float2(kLog2e, kLog2e), a);
+            else if constexpr (MK == kBwdMaskKey && !KV)
               a = __fadd2_rn(a, make_float2(m[c - cb], m[c - cb + 1]));
-            const float2 e = bwd_exp(pr[c], pr[c + 1], sl2, a);
+            float2 x = __ffma2_rn(make_float2(pr[c], pr[c + 1]), make_float2(sl2, sl2), a);
+            if constexpr (MK == kBwdMaskAdd && !KV) x = __fadd2_rn(x, make_float2(second, second));
+            const float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
             pr[c] = e.x;
             pr[c + 1] = e.y;
           }
