@@ -396,11 +396,9 @@ FA_API size_t fa_norm_rope_workspace_bytes(int D);
  * A row that sees no key (LSE = -inf) has no gradient, whatever its dLSE: its dQ is 0
  * and it adds nothing to dK and dV; keys that no row sees have dK = dV = 0.  Under an
  * additive or key-padding mask a row of |LSE| >= 2^14 (all that it sees lies under a large
- * finite mask, whose size hides the row's sum in LSE) has its sum taken again, and P is
- * within 2^-9 of itself; a row of |LSE| >= 2^38 counts as one that sees no key, as under
- * masks that leave fp32's range in the log2 domain.  P and dS are
- * rounded to bf16 for the products that take them; everything else is fp32, in a
- * fixed order: results repeat bit for bit on one GPU.  Numbers in q, k, v, out or
+ * finite mask, whose size hides the row's sum in LSE) has its sum taken again; below, P
+ * is within 2^-9 of itself.  P and dS are rounded to bf16 for the products that take
+ * them; everything else is fp32, in a fixed order: results repeat bit for bit on one GPU.  Numbers in q, k, v, out or
  * dout that are not finite, in masked places too, may turn any gradient of
  * their heads into NaN.
  *

@@ -33,11 +33,10 @@ def _device():
 # ---- rows wholly under a large finite mask ----
 
 def _check_shifted(B, Hq, Hk, Nq, Nk, D, causal, seed=1, **mask):
-    """Tolerances as in the tests of ordinary masks, and 2^-9 of P (in its terms, and in the norm).  Rows of |LSE|
-    below 2^14: LSE is within 2^-11 (half its step), L = LSE log2(e) and mask log2(e) within 2^-10 each in the log2
-    domain, so P within 2^-11 + 2 ln(2) 2^-10 < 2^-9 of itself.  Rows past that are summed again, from scores to
-    which what the reference's rounding left is added: up to 2^14 for masks below 2^38, so scores and the sum are
-    within 2^-10 each, and P within 2 ln(2) 2^-10."""
+    """Tolerances as in the tests of ordinary masks, and 2^-9 of P (in its terms, and in the norm) for rows of
+    |LSE| below 2^14: LSE is within 2^-11 (half its step), L = LSE log2(e) and mask log2(e) within 2^-10 each in
+    the log2 domain, so P within 2^-11 + 2 ln(2) 2^-10 < 2^-9 of itself.  Rows past that are summed again from
+    scores whole, whose errors are those of ordinary rows."""
     m = mask["key_mask"][:, None, None].expand(B, 1, Nq, Nk) if "key_mask" in mask else mask["full_mask"]
     seen = m > -INF
     if causal:
@@ -60,8 +59,7 @@ def _check_shifted(B, Hq, Hk, Nq, Nk, D, causal, seed=1, **mask):
         assert float(err.norm()) <= (5e-3 + 2.0 ** -9) * float(w.norm()), (name, float(err.norm() / w.norm()))
 
 
-LARGE = [-1e4, -65504.0, -1e6, -1e9, -2.7e11, 1e9]
-LOST = [-2.8e11, -1e30, -2e38]  # (past 2.3e38 a mask leaves fp32's range in the log2 domain)
+LARGE = [-1e4, -65504.0, -1e6, -1e9, -1e30, -2e38, 1e9]  # (past 2.3e38 they leave fp32's range in the log2 domain)
 
 
 @pytest.mark.parametrize("D", [32, 64, 128])
@@ -97,30 +95,10 @@ def test_rows_wholly_under_a_large_additive_mask(D, c, size, heads, causal):
     m = _full_mask("add", B, heads, Nq, Nk, 4)
     m[:, :, Nq // 2:Nq // 2 + 20] = c   # whole rows, and one of two heights
     m[:, :, -1] = c
-    m[:, :, -1, Nk // 2:] = -abs(c) * 1.5
+    m[:, :, -1, Nk // 2:] = -abs(c) * 1.1
     m[..., 0, :, 3] = -INF
     m[0, 0, :, Nk // 4] = -abs(c)       # a column that ordinary rows do not see
     _check_shifted(*size, D, causal, full_mask=m)
-
-
-@pytest.mark.parametrize("D", [32, 64, 128])
-@pytest.mark.parametrize("c", LOST)
-def test_rows_past_the_last_bound_see_nothing(D, c):
-    """Rows wholly under such masks have no gradient, as under -inf; ordinary rows do not see keys under them."""
-    B, Hq, Hk, Nq, Nk = 2, 4, 2, 260, 300
-    m = _full_mask("add", B, 1, Nq, Nk, 4)
-    m[:, :, 100:140] = c
-    m[:, :, 150, ::2] = c
-    key = torch.zeros(B, Nk, device="cuda")
-    key[0, 200:], key[1] = c, c
-    for mask in (dict(full_mask=m), dict(key_mask=key)):
-        (name, large), = mask.items()
-        cut = large.masked_fill(large == c, -INF)
-        x = _inputs(B, Hq, Hk, Nq, Nk, D, **{name: cut}, dlse=True)
-        want = fa.bwd(**x)
-        x["lse"] = torch.where(x["lse"] == -INF, torch.tensor(c, device="cuda"), x["lse"])
-        x[name] = large
-        assert all(torch.equal(a, b) for a, b in zip(fa.bwd(**x), want))
 
 
 def test_large_masks_repeat_and_agree_with_none():

@@ -41,7 +41,7 @@ int launch_bwd_prep(BwdPrepParams& p, long long heads, int D, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = p.some ? 1 : 0;
   const BwdPrepParams& prm = p;
-  auto go = [&](auto* with, auto* without) { return cudaLaunchKernelEx(&cfg, p.mask ? with : without, prm); };
+  auto go = [&](auto* refs, auto* plain) { return cudaLaunchKernelEx(&cfg, p.mask ? refs : plain, prm); };
   const cudaError_t e = D == 32   ? go(fa_bwd_prep_kernel<32, true>, fa_bwd_prep_kernel<32, false>)
                         : D == 64 ? go(fa_bwd_prep_kernel<64, true>, fa_bwd_prep_kernel<64, false>)
                                   : go(fa_bwd_prep_kernel<128, true>, fa_bwd_prep_kernel<128, false>);
@@ -93,10 +93,10 @@ constexpr int kSlotCtas = 160;  // CTAs (one per SM) that partial sums are kept 
 // the most CTAs a plan has: it does not depend on the GPU.  bool_heads: heads of
 // a boolean mask (0: no such mask), whose bits are kept by rows and by keys, with
 // those of its tiles; without one, the key tiles' of a key-padding mask.  The
-// total is at least kBwdMaxCtas' partial sums and two floats a row, in which the
-// statistics fit up to 5900 tiles of queries (D = 32; 23800 for D = 128).
+// total is at least kBwdMaxCtas' partial sums and two floats a row, in which flags
+// and references fit up to 5900 tiles of queries (D = 32; 23800 for D = 128).
 struct Layout {
-  size_t stat, part_kv, part_q, bits_q, bits_k, some, tiles_q, tiles_k, total;
+  size_t stat, flags, ref, part_kv, part_q, bits_q, bits_k, some, tiles_q, tiles_k, total;
 };
 
 Layout layout(int B, int Hq, int Nq, int Nk, int D, int bool_heads) {
@@ -105,10 +105,12 @@ Layout layout(int B, int Hq, int Nq, int Nk, int D, int bool_heads) {
   const size_t masks = (size_t)B * bool_heads;
   Layout l{};
   size_t off = 0;
-  l.stat = off;     off += align256(tiles * fa::kStatTile * sizeof(float));
+  l.stat = off;     off += tiles * fa::kStatTile * sizeof(float);
+  l.flags = off;    off += align256(tiles * fa::kFlagTile * sizeof(uint32_t));
+  l.ref = off;      off += align256(tiles * 128 * sizeof(float));
   l.part_kv = off;  off += slots * 2 * tile;
   l.part_q = off;   off += slots * tile;
-  const size_t least = tiles * 2 * 128 * sizeof(float) + 2 * (size_t)fa::kBwdMaxCtas * 3 * tile;
+  const size_t least = tiles * fa::kStatTile * sizeof(float) + 2 * (size_t)fa::kBwdMaxCtas * 3 * tile;
   off = off < least ? least : off;
   l.bits_q = off;   off += align256(masks * Nq * kt * 16);
   l.bits_k = off;   off += align256(masks * Nk * qt * 16);
@@ -257,6 +259,8 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   p.scale = scale;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.stat = reinterpret_cast<float*>(ws + l.stat);
+  p.flags = reinterpret_cast<uint32_t*>(ws + l.flags);
+  p.ref = reinterpret_cast<float*>(ws + l.ref);
   p.mask = mask_data;
   p.mask_heads = mask_heads;
   p.div_group = fa::FastDiv::make((uint32_t)group);
@@ -326,6 +330,8 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   pp.q = view(*q);
   pp.k = view(*k);
   pp.stat = reinterpret_cast<float*>(ws + l.stat);
+  pp.flags = reinterpret_cast<uint8_t*>(ws + l.flags);
+  pp.ref = reinterpret_cast<float*>(ws + l.ref);
   if (kind == FA_MASK_KEY_PADDING || kind == FA_MASK_ADDITIVE) pp.mask = static_cast<const float*>(mask_data);
   pp.mask_heads = mask_heads;
   pp.mask_rows = kind == FA_MASK_ADDITIVE;

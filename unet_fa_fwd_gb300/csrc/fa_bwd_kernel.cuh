@@ -67,28 +67,30 @@ struct BwdTensor {
   long long b, h, n;
 };
 
-// The statistics of 128 queries (a tile), in the workspace: -L (-inf for rows that see
-// nothing and rows past Nq), -delta, flags (a word for each half of the rows: some have
-// references; two words to 16 bytes), which key units copy to shared memory together;
-// then the negated references (0 where L is LSE's).
-constexpr int kStatDelta = 128, kStatFlags = 256, kStatCopy = 260, kStatRef = 260, kStatTile = 388;  // floats
+// Of 128 queries (a tile), in the workspace: -L (-inf for rows that see nothing and rows
+// past Nq) and -delta; under fp32 masks also flags, a byte for each warp that made them
+// (16), and negated references (0 where L is LSE's).
+constexpr int kStatDelta = 128, kStatTile = 256, kFlagTile = 4;  // words
+enum : uint32_t {  // (of the four bytes of a word)
+  kFlagRefs = 0x01010101  // some rows have references
+};
 
-// Under a finite mask LSE may be far from the scores.  Below the first bound its half
-// step is 2^-11, those of L and of the mask in the log2 domain 2^-10 each, so P is within
-// 2^-9 of itself (bf16, which P is rounded to, has 2^-8); a step further each doubles.
-// From there on rows get a reference: ref = the largest mask log2(e) that they see,
-// rounded, and mask log2(e) - ref in one rounding.  That leaves what the product's
-// rounding left, up to 2^14 below the second bound, in t and in L alike: again 2^-10
-// each.  Rows past it count as rows that see nothing.
-constexpr float kWeakLse = 16384.f, kLostLse = 274877906944.f;
-__device__ __forceinline__ bool bwd_weak(float lse) { return fabsf(lse) >= kWeakLse && fabsf(lse) < kLostLse; }
+// Under a finite mask LSE may be far from the scores.  Below this bound its half step is
+// 2^-11, those of L and of the mask in the log2 domain 2^-10 each, so P is within 2^-9 of
+// itself (bf16, which P is rounded to, has 2^-8); a step further each doubles.  From there
+// on a row has a reference, the largest mask value that it sees: its mask is taken less
+// that value, and L is the sum's own.
+constexpr float kWeakLse = 16384.f;
+__device__ __forceinline__ bool bwd_weak(float lse) { return fabsf(lse) >= kWeakLse && fabsf(lse) < INFINITY; }
 
 struct BwdParams {
   BwdPlan plan[2];  // key units, query units
   int Hq, Hk, group, Nq, Nk, nqp;  // nqp: queries rounded up to whole tiles
   int causal;
   float scale, scale_log2;
-  const float* stat;    // [B Hq][nqp / 128][kStatTile]
+  const float* stat;      // [B Hq][nqp / 128][kStatTile]
+  const uint32_t* flags;  // [B Hq][nqp / 128][kFlagTile]
+  const float* ref;       // [B Hq][nqp]; fp32 masks
   const void* mask;     // fp32 [B][Nk] or [B][mask_heads][Nq][Nk]
   int mask_heads;
   int mask_vec;         // its rows are 16-byte aligned
@@ -126,7 +128,7 @@ struct BwdCfg {
   // later, and dO; query units: K and V).  At D = 128 the slots that fit.
   static constexpr int RING0 = D == 128 ? (MK == kBwdMaskAdd ? 2 : 3) : 4;
   static constexpr int RING1 = D == 128 ? 2 : 4;
-  static constexpr int STAT_BYTES = 2 * kStatCopy * 4;  // key units: two slots of a tile's -L, -delta and flags
+  static constexpr int STAT_BYTES = 2 * (kStatTile + kFlagTile) * 4;  // key units: two slots of -L, -delta; of flags
   static constexpr int SMEM_BAR = 512;
   static constexpr int SMEM_USED = (2 + RING0 + RING1) * TILE + STAT_BYTES + MASK_BYTES + SMEM_BAR;
   // (more than half of the SM's, so that one CTA has its tensor memory alone)
@@ -300,6 +302,13 @@ struct BwdStage {
                      : "memory");
       }
     }
+  }
+  // Adds the negated references (key units: of the SC queries from ref[0] on; query units:
+  // of the lane's row) to what has been staged.
+  static __device__ __forceinline__ void refer(float* buf, const float* ref, int lane) {
+#pragma unroll 1
+    for (int c = 0; c < SC; ++c) buf[KV ? c * 32 + lane : lane * SC + c] += KV ? __ldcg(ref + c) : *ref;
+    __syncwarp();
   }
   // The lane's 16 values of the columns c0 .. c0 + 15 (key units: of 4 rows and 4
   // columns, in the order of bwd_elements).
@@ -507,10 +516,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
   };
   const int heads = KV ? p.Hk : p.Hq;
   const FastDiv& div_h = KV ? p.div_hk : p.div_hq;
-  // A query tile's statistics.
-  auto stat_of = [&](int b, int hq, int tile) {
-    return (((size_t)b * p.Hq + hq) * (p.nqp / 128) + tile) * kStatTile;
-  };
+  auto query_tile = [&](int b, int hq, int tile) { return ((size_t)b * p.Hq + hq) * (p.nqp / 128) + tile; };
 
   if (warp >= kBwdWarps) {
     ptx::setmaxnreg_dec<C::REGS_OTHER>();
@@ -565,8 +571,12 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
               ok = bwd_wait(bars->st_empty[ss], ((j / 2) & 1) ^ 1, bars, p);
               if (!ok) break;
               full = ptx::smem_u32(&bars->st_full[ss]);
-              ptx::mbar_arrive_expect_tx(full, kStatCopy * 4);
-              bulk_load(ptx::smem_u32(sStat + ss * kStatCopy), p.stat + stat_of(b, ho, at.tile), kStatCopy * 4, full);
+              constexpr bool FLAGS = MK == kBwdMaskKey || MK == kBwdMaskAdd;
+              const size_t qt = query_tile(b, ho, at.tile);
+              ptx::mbar_arrive_expect_tx(full, (kStatTile + (FLAGS ? kFlagTile : 0)) * 4);
+              bulk_load(ptx::smem_u32(sStat + ss * kStatTile), p.stat + qt * kStatTile, kStatTile * 4, full);
+              if constexpr (FLAGS)
+                bulk_load(ptx::smem_u32(sStat + 2 * kStatTile + ss * kFlagTile), p.flags + qt * kFlagTile, kFlagTile * 4, full);
               ++nst;
             }
             ok = bwd_wait(bars->r1_empty[s1], ((j / C::RING1) & 1) ^ 1, bars, p);
@@ -761,10 +771,10 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       w.h = w.pc.head - w.b * heads;
       w.nlse = w.ndelta = w.nref = 0.f;
       if constexpr (!KV) {
-        const float* at = p.stat + stat_of(w.b, w.h, w.pc.tile) + row;
-        w.nlse = __ldcg(at);
-        w.ndelta = __ldcg(at + kStatDelta);
-        if constexpr (REFS) w.nref = __ldcg(at + kStatRef);
+        const size_t qt = query_tile(w.b, w.h, w.pc.tile);
+        w.nlse = __ldcg(p.stat + qt * kStatTile + row);
+        w.ndelta = __ldcg(p.stat + qt * kStatTile + kStatDelta + row);
+        if constexpr (REFS) w.nref = __ldcg(p.ref + qt * 128 + row);
       }
       w.at.start(p, plan.units, w.pc, w.b, w.h);
       return true;
@@ -775,9 +785,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       const int b = work.b, h = work.h;
       const int my = pc.tile * 128 + row, my4 = pc.tile * 128 + row4;  // this thread's key or query
       const float nlse = work.nlse, ndelta = work.ndelta, nref = work.nref;
-      // An additive mask's products are rounded together with -L, or the reference (and -L added behind the scores).
-      const bool has_ref = MK == kBwdMaskAdd && nref != 0.f;
-      const float first = has_ref ? nref : nlse, second = has_ref ? nlse : 0.f;
+      const bool refs = MK == kBwdMaskAdd && !KV && __any_sync(0xffffffffu, nref != 0.f);
       float key_add[4] = {};
       if constexpr (KV && MK == kBwdMaskKey) {
 #pragma unroll
@@ -817,7 +825,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         at.next();
         const float *lcol = nullptr, *dcol = nullptr;  // -L and -delta of this thread's columns
         if constexpr (KV) {
-          lcol = sStat + (j & 1) * kStatCopy + wg * kBwdCols + col2;
+          lcol = sStat + (j & 1) * kStatTile + wg * kBwdCols + col2;
           dcol = lcol + kStatDelta;
         }
         // Pairs that the row does not see: above the diagonal, and keys past Nk
@@ -852,10 +860,10 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         ok = bwd_wait_warp(KV ? &bars->st_full[j & 1] : nullptr, (j / 2) & 1, bars->s_full[sb], (j / T::NS) & 1, bars, p);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        bool weak = false;  // (read ahead of the scores, whose wait hides it)
-        if constexpr (REFS && KV) {
-          const uint2 f = *reinterpret_cast<const uint2*>(sStat + (j & 1) * kStatCopy + kStatFlags);
-          weak = (f.x | f.y) != 0;
+        uint32_t flags = 0;  // (read ahead of the scores, whose wait hides it)
+        if constexpr (KV && REFS) {
+          const uint4 f = *reinterpret_cast<const uint4*>(sStat + 2 * kStatTile + (j & 1) * kFlagTile);
+          flags = f.x | f.y | f.z | f.w;
         }
         float pr[kBwdCols];  // in the order of bwd_elements
         {
@@ -871,6 +879,9 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
             if (cb % C::MASK_COLS == 0) {
               asm volatile("cp.async.wait_all;" ::: "memory");
               __syncwarp();
+              if (KV ? flags & kFlagRefs : refs)
+                Stage::refer(sMask, KV ? p.ref + query_tile(b, h * p.group + now.g, now.tile) * 128 + wg * kBwdCols + cb : &nref,
+                             (int)lane);
             }
             Stage::read(sMask, cb % C::MASK_COLS, (int)lane, m);
             if ((cb + 16) % C::MASK_COLS == 0) {  // the buffer has been read
@@ -883,11 +894,11 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
           } else if constexpr (MK == kBwdMaskKey && !KV) {
             const float* mrow = static_cast<const float*>(p.mask) + (size_t)b * p.Nk;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) m[c] = fmaf(__ldg(mrow + min(col0 + cb + c, p.Nk - 1)), kLog2e, nref);
+            for (int c = 0; c < 16; ++c) m[c] = (__ldg(mrow + min(col0 + cb + c, p.Nk - 1)) + nref) * kLog2e;
           }
 #pragma unroll
           for (int c = cb; c < cb + 16; c += 2) {
-            float2 a = make_float2(first, first);
+            float2 a = make_float2(nlse, nlse);
             if constexpr (KV) {
               a = *reinterpret_cast<const float2*>(lcol + c / 8 * 8);
               if constexpr (MK == kBwdMaskKey) a = __fadd2_rn(a, make_float2(key_add[c / 2 % 4], key_add[c / 2 % 4]));
@@ -896,36 +907,28 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
               a = __ffma2_rn(make_float2(m[c - cb], m[c - cb + 1]), make_float2(kLog2e, kLog2e), a);
             else if constexpr (MK == kBwdMaskKey && !KV)
               a = __fadd2_rn(a, make_float2(m[c - cb], m[c - cb + 1]));
-            float2 x = __ffma2_rn(make_float2(pr[c], pr[c + 1]), make_float2(sl2, sl2), a);
-            if constexpr (MK == kBwdMaskAdd && !KV) x = __fadd2_rn(x, make_float2(second, second));
+            const float2 x = __ffma2_rn(make_float2(pr[c], pr[c + 1]), make_float2(sl2, sl2), a);
             const float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
             pr[c] = e.x;
             pr[c + 1] = e.y;
           }
         }
-        if constexpr (REFS && KV) {
-          // Queries with a reference: their columns again, S is still there.  (The block in
-          // the loop takes 2 % of a masked call that has none; two loops, or the threads'
-          // part out of line, took 4 to 13 % in spills and missed instructions.)
-          if (weak) {
-            const int hq = h * p.group + now.g;
-            const float* ref = p.stat + stat_of(b, hq, now.tile) + kStatRef + wg * kBwdCols + col2;
-            const float* mrow = static_cast<const float*>(p.mask) +
-                                (MK == kBwdMaskAdd ? mask_head(now) * p.Nq * p.Nk : (size_t)b * p.Nk);
+        if constexpr (MK == kBwdMaskKey && KV) {
+          // Queries with a reference: their columns again, S is still there.
+          if (flags & kFlagRefs) {
+            const float* ref = p.ref + query_tile(b, h * p.group + now.g, now.tile) * 128 + wg * kBwdCols + col2;
+            const float* mrow = static_cast<const float*>(p.mask) + (size_t)b * p.Nk;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float2 rf = __ldcg(reinterpret_cast<const float2*>(ref + 8 * i));
-              if (!__any_sync(0xffffffffu, rf.x != 0.f || rf.y != 0.f)) continue;
               uint32_t t[8];
               bwd_load_elements(tS + 8 * i, t);
-              const float2 l = *reinterpret_cast<const float2*>(lcol + 8 * i);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float nr = e % 2 ? rf.y : rf.x;
+                const int c = 8 * i + e % 2;
+                const float nr = __ldcg(ref + c);
                 if (nr == 0.f) continue;
-                const int key = my4 + 8 * (e / 2), query = col0 + col2 + 8 * i + e % 2;  // (the query is below Nq)
-                const float m = key < p.Nk ? __ldg(mrow + (MK == kBwdMaskAdd ? (size_t)query * p.Nk : 0) + key) : -INFINITY;
-                pr[8 * i + e] = ptx::ex2(fmaf(__uint_as_float(t[e]), sl2, fmaf(m, kLog2e, nr) + (e % 2 ? l.y : l.x)));
+                const float m = (__ldg(mrow + min(my4 + 8 * (e / 2), p.Nk - 1)) + nr) * kLog2e;
+                pr[8 * i + e] = ptx::ex2(fmaf(__uint_as_float(t[e]), sl2, m + lcol[c]));
               }
             }
           }
@@ -1089,7 +1092,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_kernel(const __grid_con
 struct BwdPrepParams {
   BwdTensor out, dout, q, k;
   const float *lse, *dlse;  // [B][Hq][Nq]; dlse may be nullptr
-  float* stat;              // [B Hq][nqp / 128][kStatTile]
+  float *stat, *ref;        // as BwdParams
+  uint8_t* flags;
   int Hq, Nq, nqp;
   const float* mask;        // of references: key padding ([B][Nk], mask_rows 0) or additive
   int mask_heads, mask_rows, causal, group;
@@ -1153,86 +1157,85 @@ static __device__ __forceinline__ void bwd_join_sums(float& mx, float& sum, floa
   mx = m;
 }
 
-// The reference of the rows among `rows` from row0 on whose LSE is too large to give P,
-// and L anew: log2 of the sum of 2^(scale s + (mask - ref)).  By 16 rows, whose keys the
-// block's 8 warps share.  Such rows are padding and few, so the products are a warp's
-// (mma.sync, 16 x 8 x 16) and their operands come from global memory.  Out of line: in
-// the blocks without such rows it takes no registers.
-template <int D>
-__device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int row0, int rows) {
+// The references of a warp's 16 rows whose LSE is too large to give P, and L anew: log2 of
+// the sum of 2^(scale s + mask - ref).  Row i of them is n0 + i / RUN * STEP + i % RUN (`weak`:
+// bit i).  Such rows are padding and few, so the products are a warp's (mma.sync,
+// 16 x 8 x 16) and their operands come from global memory.  Out of line: warps without
+// such rows take no registers for it.
+template <int D, int RUN, int STEP>
+__device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, uint32_t weak) {
   constexpr float kLog2e = 1.4426950408889634f;
-  __shared__ float s_ref[16], s_max[8][16], s_sum[8][16];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  constexpr int KEYS = 4;  // eights of keys whose products are under way together
+  const int lane = threadIdx.x % 32;
   const int b = (int)p.div_h.div((uint32_t)bh), h = bh - b * p.Hq;
   const __nv_bfloat16* q = p.q.p + b * p.q.b + h * p.q.h + 2 * (lane % 4);
   const __nv_bfloat16* k = p.k.p + b * p.k.b + (long long)(h / p.group) * p.k.h + 2 * (lane % 4);
   const float* mask = p.mask + (p.mask_rows ? ((size_t)b * p.mask_heads + (p.mask_heads == 1 ? 0 : h)) * p.Nq * p.Nk
                                             : (size_t)b * p.Nk);
-  auto mask_at = [&](int n, int j) { return mask[(p.mask_rows ? (size_t)n * p.Nk : 0) + j]; };
-  auto sees = [&](int n, int j) { return n < p.Nq && j < p.Nk && (!p.causal || j <= n); };
-  for (int r0 = row0; r0 < row0 + rows && r0 < p.Nq; r0 += 16) {
-    const int mine = r0 + lane % 16;
-    const uint32_t weak =
-        __ballot_sync(0xffffffffu, lane < 16 && mine < p.Nq && bwd_weak(p.lse[(size_t)bh * p.Nq + mine]));
-    if (weak == 0) continue;  // (in all warps alike)
-    {
-      const int n = r0 + threadIdx.x / 16;
-      float m = -INFINITY;
-      for (int j = threadIdx.x % 16; sees(n, j); j += 16) m = fmaxf(m, mask_at(n, j));
+  auto row = [&](int i) { return n0 + i / RUN * STEP + i % RUN; };
+  auto mask_row = [&](int n) { return mask + (p.mask_rows ? (size_t)n * p.Nk : 0); };
+  auto keys = [&](int n) { return n >= p.Nq ? 0 : p.causal ? min(p.Nk, n + 1) : p.Nk; };  // (it sees, by the triangle)
+  // The largest mask value of each row (lane i: of row i).
+  float ref = 0.f;
+  for (int i = 0; i < 16; ++i) {
+    if (!(weak >> i & 1)) continue;
+    const float* m = mask_row(row(i));
+    float top = -INFINITY;
+    for (int j = lane; j < keys(row(i)); j += 32) top = fmaxf(top, m[j]);
 #pragma unroll
-      for (int x = 1; x < 16; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-      if (threadIdx.x % 16 == 0) s_ref[threadIdx.x / 16] = m == -INFINITY ? 0.f : m * kLog2e;
-    }
-    __syncthreads();
-    const __nv_bfloat16 *q0 = q + min(r0 + lane / 4, p.Nq - 1) * p.q.n, *q1 = q + min(r0 + lane / 4 + 8, p.Nq - 1) * p.q.n;
-    float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {};
-    const int keys = p.causal ? min(p.Nk, r0 + 16) : p.Nk;
-    for (int j0 = warp * 16; j0 < keys; j0 += 128) {
-      float c[2][4] = {};
-      const __nv_bfloat16 *k0 = k + min(j0 + lane / 4, p.Nk - 1) * p.k.n, *k1 = k + min(j0 + 8 + lane / 4, p.Nk - 1) * p.k.n;
+    for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    if (lane % 16 == i && top > -INFINITY) ref = top;
+  }
+  // This lane's rows of a product: lane / 4 and lane / 4 + 8.
+  const int n[2] = {row(lane / 4), row(lane / 4 + 8)};
+  const float r[2] = {__shfl_sync(0xffffffffu, ref, lane / 4), __shfl_sync(0xffffffffu, ref, lane / 4 + 8)};
+  const float* m[2] = {mask_row(n[0]), mask_row(n[1])};
+  const int end[2] = {weak >> (lane / 4) & 1 ? keys(n[0]) : 0, weak >> (lane / 4 + 8) & 1 ? keys(n[1]) : 0};
+  const __nv_bfloat16 *q0 = q + min(n[0], p.Nq - 1) * p.q.n, *q1 = q + min(n[1], p.Nq - 1) * p.q.n;
+  int most = max(end[0], end[1]);
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
+  float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {};
+  for (int j0 = 0; j0 < most; j0 += 8 * KEYS) {
+    float c[KEYS][4] = {};
+    const __nv_bfloat16* at[KEYS];
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) at[i] = k + min(j0 + 8 * i + lane / 4, p.Nk - 1) * p.k.n;
 #pragma unroll 2
-      for (int d = 0; d < D; d += 16) {
-        auto two = [&](const __nv_bfloat16* at, int e) { return *reinterpret_cast<const uint32_t*>(at + d + e); };
-        const uint32_t a[4] = {two(q0, 0), two(q1, 0), two(q0, 8), two(q1, 8)};
+    for (int d = 0; d < D; d += 16) {
+      auto two = [&](const __nv_bfloat16* x, int e) { return *reinterpret_cast<const uint32_t*>(x + d + e); };
+      const uint32_t a[4] = {two(q0, 0), two(q1, 0), two(q0, 8), two(q1, 8)};
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-              : "+f"(c[i][0]), "+f"(c[i][1]), "+f"(c[i][2]), "+f"(c[i][3])
-              : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(two(i ? k1 : k0, 0)), "r"(two(i ? k1 : k0, 8)));
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {  // row lane / 4 + 8 i, column 2 (lane % 4) + e % 2 of either eight
-        const int i = e / 2 % 2, r = lane / 4 + 8 * i, j = j0 + 8 * (e / 4) + 2 * (lane % 4) + e % 2;
-        if (!sees(r0 + r, j)) continue;
-        bwd_join_sums(mx[i], sum[i], fmaf(c[e / 4][e % 4], p.scale_log2, fmaf(mask_at(r0 + r, j), kLog2e, -s_ref[r])), 1.f);
-      }
+      for (int i = 0; i < KEYS; ++i)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[i][0]), "+f"(c[i][1]), "+f"(c[i][2]), "+f"(c[i][3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(two(at[i], 0)), "r"(two(at[i], 8)));
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < KEYS; ++i)
 #pragma unroll
-      for (int x = 1; x < 4; x <<= 1)
-        bwd_join_sums(mx[i], sum[i], __shfl_xor_sync(0xffffffffu, mx[i], x), __shfl_xor_sync(0xffffffffu, sum[i], x));
-      if (lane % 4 == 0) {
-        s_max[warp][lane / 4 + 8 * i] = mx[i];
-        s_sum[warp][lane / 4 + 8 * i] = sum[i];
+      for (int e = 0; e < 4; ++e) {  // row e / 2 of the lane's, column 2 (lane % 4) + e % 2
+        const int j = j0 + 8 * i + 2 * (lane % 4) + e % 2;
+        if (j < end[e / 2])
+          bwd_join_sums(mx[e / 2], sum[e / 2], fmaf(c[i][e], p.scale_log2, (m[e / 2][j] - r[e / 2]) * kLog2e), 1.f);
       }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1)
+      bwd_join_sums(mx[i], sum[i], __shfl_xor_sync(0xffffffffu, mx[i], x), __shfl_xor_sync(0xffffffffu, sum[i], x));
+    if (lane % 4 == 0 && (weak >> (lane / 4 + 8 * i) & 1)) {
+      p.stat[((size_t)bh * (p.nqp / 128) + n[i] / 128) * kStatTile + n[i] % 128] =
+          sum[i] > 0.f ? -(mx[i] + log2f(sum[i])) : -INFINITY;
+      p.ref[(size_t)bh * p.nqp + n[i]] = -r[i];
     }
-    __syncthreads();
-    if (threadIdx.x < 16 && (weak >> threadIdx.x & 1)) {
-      float m = s_max[0][threadIdx.x], l = s_sum[0][threadIdx.x];
-      for (int w = 1; w < 8; ++w) bwd_join_sums(m, l, s_max[w][threadIdx.x], s_sum[w][threadIdx.x]);
-      const int n = r0 + threadIdx.x;
-      float* at = p.stat + ((size_t)bh * (p.nqp / 128) + n / 128) * kStatTile + n % 128;
-      at[0] = l > 0.f ? -(m + log2f(l)) : -INFINITY;
-      at[kStatRef] = -s_ref[threadIdx.x];
-    }
-    __syncthreads();  // (the next rows' sums go to the same places)
   }
 }
 
-// REFS: an additive or key-padding mask, under which rows may need references.
+// REFS (an additive or key-padding mask): rows may need references.
 template <int D, bool REFS>
-__global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant__ BwdPrepParams p) {
+__global__ void __launch_bounds__(256, 4) fa_bwd_prep_kernel(const __grid_constant__ BwdPrepParams p) {
   constexpr int L = D / 8;  // lanes a row
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x >= p.row_blocks) {
@@ -1248,10 +1251,9 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
   uint4 o[U] = {}, g[U] = {};
   float lse[U], sum[U];
   const int block_row = (int)(blockIdx.x - (unsigned)bh * p.head_blocks) * kBwdPrepRows<D>;
-  float* tile = p.stat + ((size_t)bh * (p.nqp / 128) + block_row / 128) * kStatTile;
-  float* stat = tile + block_row % 128 + threadIdx.x / L;
+  const size_t tile = (size_t)bh * (p.nqp / 128) + block_row / 128;
+  float* stat = p.stat + tile * kStatTile + block_row % 128 + threadIdx.x / L;
   const int n0 = block_row + threadIdx.x / L;
-  bool weak = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int n = n0 + u * STEP;
@@ -1279,26 +1281,35 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
     for (int m = 1; m < L; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
     if (piece == 0) {
       float* at = stat + u * STEP;
-      const bool sees = REFS ? !(fabsf(lse[u]) >= kLostLse) : lse[u] != -INFINITY;  // (else dLSE may be anything)
+      const bool sees = lse[u] != -INFINITY;  // (dLSE of a row that sees nothing may be anything)
       at[0] = sees ? -lse[u] * 1.4426950408889634f : -INFINITY;
       at[kStatDelta] = sees ? -(dot + sum[u]) : 0.f;
-      if constexpr (REFS) {
-        at[kStatRef] = 0.f;
-        weak = weak || bwd_weak(lse[u]);
-      }
+      if constexpr (REFS) p.ref[tile * 128 + block_row % 128 + threadIdx.x / L + u * STEP] = 0.f;
     }
   }
-  uint32_t flags = 0;
-  if constexpr (REFS) {
-    if (__syncthreads_or(weak)) {
-      flags = 1;
-      bwd_resum<D>(p, bh, block_row, kBwdPrepRows<D>);
+  if constexpr (REFS) {  // the flags of the warp's rows
+    uint32_t weak = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) weak |= bwd_weak(lse[u]) ? 1u << u : 0u;
+    uint32_t flags = 0;
+    if (__any_sync(0xffffffffu, weak)) {
+      flags = kFlagRefs & 0xff;
+      constexpr int RUN = 32 / L;  // rows of a warp at a time
+      uint32_t bits = 0;
+#pragma unroll
+      for (int i = 0; i < U * RUN; ++i)
+        bits |= (__shfl_sync(0xffffffffu, weak, i % RUN * L) >> (i / RUN) & 1u) << i;
+      __syncwarp();  // (-L of these rows is written again)
+      bwd_resum<D, RUN, STEP>(p, bh, n0 - threadIdx.x % 32 / L, bits);
+    }
+    if (threadIdx.x % 32 == 0) {  // (tiles of one block: 2 bytes a warp)
+      const int warp = block_row % 128 / 8 + threadIdx.x / 32;
+      if (kBwdPrepRows<D> == 128)
+        reinterpret_cast<uint16_t*>(p.flags + tile * kFlagTile * 4)[warp] = flags;
+      else
+        p.flags[tile * kFlagTile * 4 + warp] = flags;
     }
   }
-  // A word for each of a tile's blocks.
-  if (threadIdx.x < 128 / kBwdPrepRows<128>)
-    if (kBwdPrepRows<D> == 128 || (int)threadIdx.x == block_row % 128 / kBwdPrepRows<128>)
-      reinterpret_cast<uint32_t*>(tile)[kStatFlags + threadIdx.x] = flags;
 }
 
 // A boolean mask as bits, by query rows and by key rows: a block turns a tile, a warp
