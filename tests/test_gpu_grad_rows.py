@@ -1,5 +1,5 @@
 """Gradients of rows that masks leave in an unusual state: wholly under a large finite
-mask.
+mask, or without a key while they hold numbers that are not finite.
 
 A row's softmax does not change when a constant is taken off its scores, so the 64-bit
 definition takes each row's largest mask value off first; O and LSE are rounded from it
@@ -115,3 +115,54 @@ def test_large_masks_repeat_and_agree_with_none():
         # P within 2^-13 of itself either way; both results, P and dS rounded to bf16 alike or one step apart
         for y in (a, b):
             assert float((y.double() - c.double()).norm()) <= 5e-3 * float(c.double().norm())
+
+
+# ---- rows without a key ----
+
+def _bad_rows(x, rows, value):
+    """What padding rows hold: anything, in all of their tensors."""
+    y = dict(x)
+    for n in ("q", "dout", "out"):
+        y[n] = x[n].clone()
+        y[n][:, :, rows] = value
+        y[n][:, :, rows, ::3] = -value
+    if x.get("dlse") is not None:
+        y["dlse"] = x["dlse"].clone()
+        y["dlse"][:, :, rows] = value
+    return y
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("kind", ["bool", "u8", "add", "lowest"])
+@pytest.mark.parametrize("size,heads,causal", [((2, 2, 2, 130, 77), 1, False), ((1, 4, 2, 400, 257), 4, True),
+                                               ((1, 2, 1, 900, 700), 1, False), ((2, 1, 1, 3, 200), 1, False)])
+@pytest.mark.parametrize("value", [math.nan, INF, 3e38])
+def test_rows_without_a_key_may_hold_anything(D, kind, size, heads, causal, value):
+    B, Hq, Hk, Nq, Nk = size
+    m = _full_mask(kind, B, heads, Nq, Nk, 4)
+    rows = sorted({Nq // 3, *range(Nq // 2, Nq // 2 + Nq // 10), Nq - 1})
+    m[:, :, rows] = {"add": -INF, "lowest": torch.finfo(torch.float32).min}.get(kind, 0)
+    plain = m.masked_fill(m < -1e38, -INF) if kind == "lowest" else m
+    x = dict(_inputs(*size, D, full_mask=plain, causal=causal, dlse=True), full_mask=m)
+    assert bool((x["lse"][:, :, rows] == -INF).all())
+    want = fa.bwd(**x)
+    got = fa.bwd(**_bad_rows(x, rows, value))
+    assert all(bool(y.isfinite().all()) for y in want)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert bool((got[0][:, :, rows] == 0).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_an_entry_without_a_key_may_hold_anything(D):
+    """A whole entry of a padded batch; ordinary keys of the other one are padding too."""
+    B, H, Nq, Nk = 2, 2, 300, 500
+    for low in (-INF, torch.finfo(torch.float32).min):
+        m = torch.zeros(B, Nk, device="cuda")
+        m[0, 200:], m[1] = -INF, -INF
+        x = _inputs(B, H, H, Nq, Nk, D, key_mask=m, dlse=True)
+        x["key_mask"] = m.masked_fill(m == -INF, low)
+        want = fa.bwd(**x)
+        bad = _bad_rows(x, list(range(Nq)), math.nan)
+        for n in ("q", "dout", "out", "dlse"):
+            bad[n][0] = x[n][0]
+        assert all(torch.equal(a, b) for a, b in zip(fa.bwd(**bad), want))

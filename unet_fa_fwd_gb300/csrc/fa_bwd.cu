@@ -41,10 +41,13 @@ int launch_bwd_prep(BwdPrepParams& p, long long heads, int D, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = p.some ? 1 : 0;
   const BwdPrepParams& prm = p;
-  auto go = [&](auto* refs, auto* plain) { return cudaLaunchKernelEx(&cfg, p.mask ? refs : plain, prm); };
-  const cudaError_t e = D == 32   ? go(fa_bwd_prep_kernel<32, true>, fa_bwd_prep_kernel<32, false>)
-                        : D == 64 ? go(fa_bwd_prep_kernel<64, true>, fa_bwd_prep_kernel<64, false>)
-                                  : go(fa_bwd_prep_kernel<128, true>, fa_bwd_prep_kernel<128, false>);
+  auto go = [&](auto* refs, auto* masked, auto* plain) {
+    return cudaLaunchKernelEx(&cfg, p.mask ? refs : p.some ? masked : plain, prm);
+  };
+  const cudaError_t e =
+      D == 32   ? go(fa_bwd_prep_kernel<32, true, true>, fa_bwd_prep_kernel<32, true, false>, fa_bwd_prep_kernel<32, false, false>)
+      : D == 64 ? go(fa_bwd_prep_kernel<64, true, true>, fa_bwd_prep_kernel<64, true, false>, fa_bwd_prep_kernel<64, false, false>)
+                : go(fa_bwd_prep_kernel<128, true, true>, fa_bwd_prep_kernel<128, true, false>, fa_bwd_prep_kernel<128, false, false>);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

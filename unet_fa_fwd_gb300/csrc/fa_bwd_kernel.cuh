@@ -68,11 +68,12 @@ struct BwdTensor {
 };
 
 // Of 128 queries (a tile), in the workspace: -L (-inf for rows that see nothing and rows
-// past Nq) and -delta; under fp32 masks also flags, a byte for each warp that made them
-// (16), and negated references (0 where L is LSE's).
+// past Nq) and -delta; under masks also flags, a byte for each warp that made them (16),
+// and under fp32 masks negated references (0 where L is LSE's).
 constexpr int kStatDelta = 128, kStatTile = 256, kFlagTile = 4;  // words
 enum : uint32_t {  // (of the four bytes of a word)
-  kFlagRefs = 0x01010101  // some rows have references
+  kFlagRefs = 0x01010101,  // some rows have references
+  kFlagBare = 0x02020202   // some rows that see nothing hold numbers that are not finite, or past 2^60
 };
 
 // Under a finite mask LSE may be far from the scores.  Below this bound its half step is
@@ -353,8 +354,9 @@ __device__ __forceinline__ void bwd_store_pairs(uint32_t t, const uint32_t (&w)[
 // 16-byte pieces so that up to four store 64 bytes of one row together: a store of
 // every lane to a row of its own takes a clock a row (units of one tile each at
 // D = 64: 1100 clocks of 4050).
+// `keep` false: the lane's own row is zeros (`zero`: every row of the warp).
 template <int NC>
-__device__ __forceinline__ void bwd_store_row(uint32_t t, float mul, bool zero, bool ok, int rows, int lane,
+__device__ __forceinline__ void bwd_store_row(uint32_t t, float mul, bool zero, bool keep, bool ok, int rows, int lane,
                                               __nv_bfloat16* dst, long long row_step) {
   constexpr int CH = NC >= 32 ? 4 : NC / 8;  // lanes that share rows, and their pieces
   const int l = lane % CH;
@@ -372,7 +374,7 @@ __device__ __forceinline__ void bwd_store_row(uint32_t t, float mul, bool zero, 
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        v[c][i] = ptx::pack_bf16x2(__uint_as_float(r[2 * i]) * mul, __uint_as_float(r[2 * i + 1]) * mul);
+        v[c][i] = keep ? ptx::pack_bf16x2(__uint_as_float(r[2 * i]) * mul, __uint_as_float(r[2 * i + 1]) * mul) : 0u;
     }
     // v[c] of lane l becomes piece l of lane c's row.
 #pragma unroll
@@ -397,7 +399,7 @@ __device__ __forceinline__ void bwd_store_row(uint32_t t, float mul, bool zero, 
   }
 }
 template <int NC>
-__device__ __forceinline__ void bwd_store_part(uint32_t t, bool zero, bool ok, float* dst, int row) {
+__device__ __forceinline__ void bwd_store_part(uint32_t t, bool zero, bool keep, bool ok, float* dst, int row) {
 #pragma unroll
   for (int cb = 0; cb < NC; cb += 8) {
     uint32_t r[8];
@@ -406,6 +408,10 @@ __device__ __forceinline__ void bwd_store_part(uint32_t t, bool zero, bool ok, f
       for (int i = 0; i < 8; ++i) r[i] = 0u;
     } else {
       ptx::tmem_ld32x32b_x8(t + cb, r);
+      if (!keep) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = 0u;
+      }
     }
     if (ok) {
 #pragma unroll
@@ -485,6 +491,43 @@ struct BwdIter {
     if constexpr (SKIP) seek();
   }
 };
+
+// Key units: what a tile's queries that see nothing hold goes nowhere.  Their P and dS
+// are 0, but 0 times what is not finite is not: their rows of Q and dO become zeros before
+// the products that sum over queries, and their columns of S and dP too (S may be inf
+// where q is merely large).  By all rows' warps, ahead of their P, each for 8 rows and its
+// own part of tensor memory; false: a wait ran out.
+template <int D>
+__device__ __noinline__ bool bwd_scrub(const BwdParams& p, BwdBars* bars, const float* nlse, uint32_t tS, uint32_t tDP,
+                                       uint8_t* q, uint8_t* dout, uint32_t dp_parity) {
+  using F = Cfg<D>;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, col0 = warp / 4 * kBwdCols;
+  if (!bwd_wait_warp(bars->dp_full, dp_parity, bars, p)) return false;  // (dP reads dO until then)
+  ptx::tc_fence_after_sync();
+  for (int i = 0; i < kBwdCols; i += 8) {
+    uint32_t s[8], d[8];
+    ptx::tmem_ld32x32b_x8(tS + i, s);
+    ptx::tmem_ld32x32b_x8(tDP + i, d);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (nlse[col0 + i + c] == -INFINITY) s[c] = d[c] = 0u;
+    ptx::tmem_st32x32b_x8(tS + i, s);
+    ptx::tmem_st32x32b_x8(tDP + i, d);
+  }
+  ptx::tmem_wait_st();
+  // A row is D / (64 or 32) spans of the swizzle, which moves 16-byte pieces within one.
+  constexpr int BYTES = D / 2;  // of a lane, a quarter of a row
+  const int row = warp * 8 + lane / 4, at = lane % 4 * BYTES;
+  if (nlse[row] == -INFINITY) {
+    const int off = at / F::SW * F::CHUNK_BYTES + row * F::SW + at % F::SW;
+#pragma unroll
+    for (int i = 0; i < BYTES; i += 16)
+      *reinterpret_cast<uint4*>(q + off + i) = *reinterpret_cast<uint4*>(dout + off + i) = make_uint4(0, 0, 0, 0);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the products that follow see the zeros
+  __syncwarp();
+  return true;
+}
 
 // A CTA's units of one kind: dK and dV of 128 keys (KV), or dQ of 128 queries.
 template <int D, int MK, bool KV>
@@ -571,7 +614,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
               ok = bwd_wait(bars->st_empty[ss], ((j / 2) & 1) ^ 1, bars, p);
               if (!ok) break;
               full = ptx::smem_u32(&bars->st_full[ss]);
-              constexpr bool FLAGS = MK == kBwdMaskKey || MK == kBwdMaskAdd;
+              constexpr bool FLAGS = MK != kBwdMaskNone;
               const size_t qt = query_tile(b, ho, at.tile);
               ptx::mbar_arrive_expect_tx(full, (kStatTile + (FLAGS ? kFlagTile : 0)) * 4);
               bulk_load(ptx::smem_u32(sStat + ss * kStatTile), p.stat + qt * kStatTile, kStatTile * 4, full);
@@ -861,7 +904,7 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         if (!ok) break;
         ptx::tc_fence_after_sync();
         uint32_t flags = 0;  // (read ahead of the scores, whose wait hides it)
-        if constexpr (KV && REFS) {
+        if constexpr (KV && MK != kBwdMaskNone) {
           const uint4 f = *reinterpret_cast<const uint4*>(sStat + 2 * kStatTile + (j & 1) * kFlagTile);
           flags = f.x | f.y | f.z | f.w;
         }
@@ -869,6 +912,14 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         {
           uint32_t r[kBwdCols];
           bwd_load_elements<KV>(tS, r);
+          if constexpr (KV && MK != kBwdMaskNone) {
+            if (flags & kFlagBare) {
+              ok = bwd_scrub<D>(p, bars, sStat + (j & 1) * kStatTile, tS, tDP, sR0 + j % C::RING0 * C::TILE,
+                                sR1 + j % C::RING1 * C::TILE, j & 1);
+              if (!ok) break;
+              bwd_load_elements<KV>(tS, r);
+            }
+          }
 #pragma unroll
           for (int c = 0; c < kBwdCols; ++c) pr[c] = __uint_as_float(r[c]);
         }
@@ -1011,6 +1062,8 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       constexpr int NC = T::ACC / kBwdGroups;
       const uint32_t tA = t0 + wg * NC;
       const bool is_dv = KV && wg < kBwdGroups / 2, zero = n == 0;
+      // (the products of a query that sees nothing may be no numbers)
+      const bool keep = KV || MK == kBwdMaskNone || nlse != -INFINITY;
       const BwdTensor& o = KV ? (is_dv ? p.dv : p.dk) : p.dq;
       const int col = KV ? (wg % (kBwdGroups / 2)) * NC : wg * NC;
       __nv_bfloat16* dst = o.p + b * o.b + h * o.h + (long long)my * o.n + col;
@@ -1023,10 +1076,10 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
       }
       if (pc.slot < 0) {
         const bool in = bwd_check(p, bars, pc.head < plan.units.heads && col + NC <= D, kCheckGradStore, pc.head, my);
-        bwd_store_row<NC>(tA, is_dv ? 1.f : p.scale, zero, in, (KV ? p.Nk : p.Nq) - my, (int)lane, dst, o.n);
+        bwd_store_row<NC>(tA, is_dv ? 1.f : p.scale, zero, keep, in, (KV ? p.Nk : p.Nq) - my, (int)lane, dst, o.n);
       } else {
         const bool in = bwd_check(p, bars, pc.slot < 2 * plan.ctas, kCheckGradSlot, pc.slot, pc.head);
-        bwd_store_part<NC>(tA, zero, in, p.part[KV ? 0 : 1] + (size_t)pc.slot * (128 * T::ACC) + wg * NC * 128, row);
+        bwd_store_part<NC>(tA, zero, keep, in, p.part[KV ? 0 : 1] + (size_t)pc.slot * (128 * T::ACC) + wg * NC * 128, row);
       }
       ptx::tc_fence_before_sync();
     }
@@ -1233,8 +1286,21 @@ __device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, u
   }
 }
 
-// REFS (an additive or key-padding mask): rows may need references.
-template <int D, bool REFS>
+// Whether a number is not finite or past 2^60, under which products of 128 such numbers
+// are finite (their own and with keys like them).
+__device__ __forceinline__ bool bwd_large(const uint4& v) {
+  bool large = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    large = large || (w & 0x7fffu) >= 0x5d80u || (w >> 16 & 0x7fffu) >= 0x5d80u;
+  }
+  return large;
+}
+
+// MASKED: rows may see nothing; REFS (an additive or key-padding mask): they may need
+// references.
+template <int D, bool MASKED, bool REFS>
 __global__ void __launch_bounds__(256, 4) fa_bwd_prep_kernel(const __grid_constant__ BwdPrepParams p) {
   constexpr int L = D / 8;  // lanes a row
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1262,10 +1328,8 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_prep_kernel(const __grid_consta
     if (n < p.Nq) {
       o[u] = *reinterpret_cast<const uint4*>(out + n * p.out.n);
       g[u] = *reinterpret_cast<const uint4*>(dout + n * p.dout.n);
-      if (piece == 0) {
-        lse[u] = p.lse[(size_t)bh * p.Nq + n];
-        if (p.dlse) sum[u] = -p.dlse[(size_t)bh * p.Nq + n];
-      }
+      if (MASKED || piece == 0) lse[u] = p.lse[(size_t)bh * p.Nq + n];
+      if (piece == 0 && p.dlse) sum[u] = -p.dlse[(size_t)bh * p.Nq + n];
     }
   }
 #pragma unroll
@@ -1287,20 +1351,29 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_prep_kernel(const __grid_consta
       if constexpr (REFS) p.ref[tile * 128 + block_row % 128 + threadIdx.x / L + u * STEP] = 0.f;
     }
   }
-  if constexpr (REFS) {  // the flags of the warp's rows
+  if constexpr (MASKED) {  // the flags of the warp's rows
+    bool bare = false;
     uint32_t weak = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) weak |= bwd_weak(lse[u]) ? 1u << u : 0u;
-    uint32_t flags = 0;
-    if (__any_sync(0xffffffffu, weak)) {
-      flags = kFlagRefs & 0xff;
-      constexpr int RUN = 32 / L;  // rows of a warp at a time
-      uint32_t bits = 0;
+    for (int u = 0; u < U; ++u) {
+      const int n = n0 + u * STEP;
+      if (n < p.Nq && lse[u] == -INFINITY)
+        bare = bare || bwd_large(g[u]) ||
+               bwd_large(*reinterpret_cast<const uint4*>(p.q.p + b * p.q.b + h * p.q.h + n * p.q.n + piece * 8));
+      if constexpr (REFS) weak |= bwd_weak(lse[u]) ? 1u << u : 0u;
+    }
+    uint32_t flags = __any_sync(0xffffffffu, bare) ? kFlagBare & 0xff : 0;
+    if constexpr (REFS) {
+      if (__any_sync(0xffffffffu, weak)) {
+        flags |= kFlagRefs & 0xff;
+        constexpr int RUN = 32 / L;  // rows of a warp at a time
+        uint32_t bits = 0;
 #pragma unroll
-      for (int i = 0; i < U * RUN; ++i)
-        bits |= (__shfl_sync(0xffffffffu, weak, i % RUN * L) >> (i / RUN) & 1u) << i;
-      __syncwarp();  // (-L of these rows is written again)
-      bwd_resum<D, RUN, STEP>(p, bh, n0 - threadIdx.x % 32 / L, bits);
+        for (int i = 0; i < U * RUN; ++i)
+          bits |= (__shfl_sync(0xffffffffu, weak, i % RUN * L) >> (i / RUN) & 1u) << i;
+        __syncwarp();  // (-L of these rows is written again)
+        bwd_resum<D, RUN, STEP>(p, bh, n0 - threadIdx.x % 32 / L, bits);
+      }
     }
     if (threadIdx.x % 32 == 0) {  // (tiles of one block: 2 bytes a warp)
       const int warp = block_row % 128 / 8 + threadIdx.x / 32;
