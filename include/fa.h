@@ -358,9 +358,10 @@ FA_API int fa_norm_rope(const fa_rope_axes* axes, const fa_norm* norm, const int
  *                   fa_norm_rope_workspace_bytes(D) bytes where a weight is given, not
  *                   shared with a concurrent call
  *
- * Sums are fp32, in a fixed order: results repeat bit for bit on one GPU.  One
- * kernel is enqueued on `stream`, with weights a second that joins their partial
- * sums.  Errors as fa_norm_rope.
+ * Sums are fp32, in a fixed order: results repeat bit for bit on one GPU.  Those of dw
+ * keep what they round off, so that it is within about 1e-7 of its norm however many
+ * rows there are.  One kernel is enqueued on `stream`, with weights a second that joins
+ * their partial sums.  Errors as fa_norm_rope.
  */
 FA_API int fa_norm_rope_bwd(const fa_rope_axes* axes, const fa_norm* norm, const int* pos, long long pos_stride_b,
                             const fa_tensor* dq_out, const fa_tensor* q, const fa_tensor* dq, int Hq,
