@@ -358,6 +358,9 @@ FA_API int fa_norm_rope(const fa_rope_axes* axes, const fa_norm* norm, const int
  *                   fa_norm_rope_workspace_bytes(D) bytes where a weight is given, not
  *                   shared with a concurrent call
  *
+ * Rows whose squares sum past fp32's range, of which the forward makes zeros, have dx = 0
+ * and add nothing to dw.
+ *
  * Sums are fp32, in a fixed order: results repeat bit for bit on one GPU.  Those of dw
  * keep what they round off, so that it is within about 1e-7 of its norm however many
  * rows there are.  One kernel is enqueued on `stream`, with weights a second that joins

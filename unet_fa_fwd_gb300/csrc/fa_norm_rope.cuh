@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kNormThreads, VEC && !BACK ? 3 : 2)
           sq = norm_row_sum<CHUNKS>(sq);
           const float r = rsqrtf(fmaf(sq, 1.f / D, p.eps));
           if constexpr (BACK) {
-            const float mean = along * r * (1.f / D);
+            const float mean = r > 0.f ? along * r * (1.f / D) : 0.f;  // (r = 0: a row of zeros; `along` may be inf)
             const bool count = live && h + u < hi;
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
