@@ -67,7 +67,6 @@ using fa::aligned16;
 using fa::apart;
 using fa::extent;
 using fa::ranges_overlap;
-using fa::same;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 

@@ -142,6 +142,40 @@ FA_HD bool bwd_join(const BwdPlan& p, int c, int& unit, int& last, int& first_sl
 
 // ---- host ----
 
+// Weights of units dealt to CTAs in snake order, from unit 0 on.  Runs of units of one
+// weight count by rounds, in which each CTA has one unit: a plan takes the time of its
+// levels, not of its units, where these are many (short sequences of many heads).
+struct BwdDeal {
+  int ctas;
+  long long unit = 0, all = 0;          // next unit; what full rounds gave every CTA
+  long long extra[kBwdMaxCtas] = {};    // what a CTA has besides
+  long long most = 0;                   // the largest `extra`
+
+  explicit BwdDeal(int c) : ctas(c) {}
+  long long longest() const { return all + most; }
+  long long of(int c) const { return all + extra[c]; }
+  void one(long long w) {
+    const int r = (int)(unit / ctas), at = (int)(unit - (long long)r * ctas), c = (r & 1) ? ctas - 1 - at : at;
+    extra[c] += w;
+    most = extra[c] > most ? extra[c] : most;
+    ++unit;
+  }
+  // Units up to `end`, each of weight w.
+  void run(long long end, long long w) {
+    while (unit < end && unit % ctas) one(w);
+    const long long rounds = end > unit ? (end - unit) / ctas : 0;
+    all += rounds * w;
+    unit += rounds * ctas;
+    while (unit < end) one(w);
+  }
+};
+
+// Units from u on that are known to have u's weight: the end of the run.
+inline int bwd_run_end(const BwdUnits& units, int u) {
+  if (!units.causal) return units.count();
+  return units.spread ? (u / units.heads + 1) * units.heads : u + 1;
+}
+
 // Deals the units out to at most `sms` CTAs.  `join_cost`: iterations that a
 // partial result and its join cost; units are cut only where that makes the
 // longest CTA shorter by more.
@@ -152,25 +186,21 @@ inline BwdPlan bwd_plan(const BwdUnits& units, int sms, int join_cost) {
   if (sms > kBwdMaxCtas) sms = kBwdMaxCtas;
   // All units whole.
   const int few = n < sms ? n : sms;
-  long long total = 0, longest = 0;
-  if (!units.causal) {  // (units of one weight)
-    const long long w = units.weight(0);
-    total = w * n;
-    longest = w * ((n + few - 1LL) / few);
-  } else {
-    long long load[kBwdMaxCtas] = {};
-    for (int u = 0; u < n; ++u) {
-      const int r = u / few, at = u - r * few, c = (r & 1) ? few - 1 - at : at, w = units.weight(u);
-      total += w;
-      load[c] += w;
-      longest = load[c] > longest ? load[c] : longest;
-    }
+  long long total = 0;
+  BwdDeal whole_deal(few);
+  for (int u = 0; u < n;) {
+    const int end = bwd_run_end(units, u);
+    const long long w = units.weight(u);
+    total += w * (end - u);
+    whole_deal.run(end, w);
+    u = end;
   }
+  const long long longest = whole_deal.longest();
   // Cut: no CTA gets less than join_cost iterations.
   long long ctas = total / join_cost;
   ctas = ctas < 1 ? 1 : (ctas > sms ? sms : ctas);
   const long long target = (total + ctas - 1) / ctas;
-  if (longest <= target + join_cost || n > (1 << 30)) {
+  if (longest <= target + join_cost) {
     p.ctas = few;
     p.whole = n;
     for (int c = 0; c <= few; ++c) p.cut[c] = BwdCut{n, 0};
@@ -178,25 +208,33 @@ inline BwdPlan bwd_plan(const BwdUnits& units, int sms, int join_cost) {
   }
   p.ctas = (int)ctas;
   // Full rounds of whole units as long as no CTA passes the target.
-  long long have[kBwdMaxCtas] = {};
+  BwdDeal deal(p.ctas);
   int whole = 0;
-  if (!units.causal) {
-    whole = (int)(n / ctas * ctas);
-    for (int c = 0; c < p.ctas; ++c) have[c] = (long long)units.weight(0) * (n / ctas);
-  }
-  while (units.causal && (long long)whole + ctas <= n) {
-    const int r = whole / p.ctas;
-    bool fits = true;
-    for (int c = 0; c < p.ctas; ++c) fits = fits && have[c] + units.weight((int)bwd_snake(r, c, p.ctas)) <= target;
-    if (!fits) break;
-    for (int c = 0; c < p.ctas; ++c) have[c] += units.weight((int)bwd_snake(r, c, p.ctas));
-    whole += p.ctas;
+  while ((long long)whole + ctas <= n) {
+    const int end = bwd_run_end(units, whole);
+    const long long w = units.weight(whole);
+    long long rounds = (end - whole) / ctas;
+    if (rounds > 0) {  // of one weight
+      const long long fit = (target - deal.longest()) / w;
+      if (target < deal.longest() || fit == 0) break;
+      rounds = rounds < fit ? rounds : fit;
+      deal.run(whole + rounds * ctas, w);
+    } else {
+      const int r = whole / p.ctas;
+      bool fits = true;
+      for (int c = 0; c < p.ctas; ++c)
+        fits = fits && deal.of(c) + units.weight((int)bwd_snake(r, c, p.ctas)) <= target;
+      if (!fits) break;
+      for (int i = 0; i < p.ctas; ++i) deal.one(units.weight(whole + i));
+      rounds = 1;
+    }
+    whole += (int)(rounds * ctas);
   }
   p.whole = whole;
   int u = whole, it = 0;
   for (int c = 0; c < p.ctas; ++c) {
     p.cut[c] = BwdCut{u, it};
-    long long left = target - have[c];
+    long long left = target - deal.of(c);
     while (left > 0 && u < n) {
       const int w = units.weight(u) - it;
       if (w <= left) {
