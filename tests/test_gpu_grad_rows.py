@@ -6,6 +6,9 @@ definition takes each row's largest mask value off first; O and LSE are rounded 
 as the forward's are.
 """
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -18,6 +21,7 @@ from .test_gpu_bwd import _full_mask, _inputs, _rand
 pytestmark = pytest.mark.gpu
 
 INF = math.inf
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -166,3 +170,72 @@ def test_an_entry_without_a_key_may_hold_anything(D):
         for n in ("q", "dout", "out", "dlse"):
             bad[n][0] = x[n][0]
         assert all(torch.equal(a, b) for a, b in zip(fa.bwd(**bad), want))
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("kind", ["add", "key", "bool"])
+def test_strided_tensors_streams_and_graphs(D, kind):
+    """Both kinds of row in tensors of other strides, on another stream and captured: bit for bit the same."""
+    B, Hq, Hk, N = 2, 4, 2, 330
+    if kind == "key":
+        masks = dict(key_mask=torch.zeros(B, N, device="cuda"), causal=True)
+        masks["key_mask"][0, :40], masks["key_mask"][1, :140] = -INF, -1e9
+        odd = list(range(40))
+    else:
+        m = _full_mask(kind, B, 1, N, N, 4)
+        if kind == "add":
+            m[:, :, 200:230] = -1e9
+        m[:, :, 280:300] = -INF if kind == "add" else False
+        masks, odd = dict(full_mask=m), list(range(280, 300))
+    x = _inputs(B, Hq, Hk, N, N, D, **masks, dlse=True)
+    x["dlse"] = torch.where(x["lse"] == -INF, math.nan, x["dlse"])
+    for n in ("q", "dout", "out"):
+        x[n][0, :, odd] = math.nan
+    want = fa.bwd(**x)
+    assert all(bool(y.isfinite().all()) for y in want)
+    y = dict(x)
+    for n in ("dout", "q", "k", "v", "out"):  # token-major, every other head of wider rows
+        b, h, t, d = x[n].shape
+        wide = torch.full((b, t, 2 * h, d + 8), math.nan, dtype=torch.bfloat16, device="cuda")
+        y[n] = wide[:, :, ::2, 8:].transpose(1, 2)
+        y[n].copy_(x[n])
+    assert all(torch.equal(a, b) for a, b in zip(fa.bwd(**y, token_major=True), want))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = fa.bwd(**y, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fa.bwd(**y)
+    for g in got:
+        g.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+CHILD = r'''
+import sys, torch
+sys.path.insert(0, ROOT)
+import unet_fa_fwd_gb300 as fa
+from tests.test_gpu_grad_rows import _check_shifted, test_rows_without_a_key_may_hold_anything
+assert fa.debug_build(), "the debug library was not loaded"
+torch.cuda.set_device(0)
+for D in (32, 64, 128):
+    m = torch.zeros(2, 300, device="cuda")
+    m[0, 200:], m[1] = -1e9, -1e6
+    _check_shifted(2, 4, 2, 260, 300, D, False, key_mask=m)
+    test_rows_without_a_key_may_hold_anything(D, "add", (1, 4, 2, 400, 257), 4, True, float("nan"))
+    torch.cuda.synchronize()
+    st, rec = fa.read_device_status(), fa.debug_report()
+    assert st == 0 and rec == [0] * 8, (D, st, rec)
+print("debug build: no violation")
+'''
+
+
+def test_debug_build_reports_no_violation():
+    r = subprocess.run([sys.executable, "-c", CHILD.replace("ROOT", repr(ROOT))], cwd=ROOT,
+                       env=dict(os.environ, FA_DEBUG="1"), capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
+    assert "no violation" in r.stdout

@@ -307,8 +307,10 @@ struct BwdStage {
   // Adds the negated references (key units: of the SC queries from ref[0] on; query units:
   // of the lane's row) to what has been staged.
   static __device__ __forceinline__ void refer(float* buf, const float* ref, int lane) {
+    const float own = KV ? (lane < SC ? __ldcg(ref + lane) : 0.f) : *ref;
 #pragma unroll 1
-    for (int c = 0; c < SC; ++c) buf[KV ? c * 32 + lane : lane * SC + c] += KV ? __ldcg(ref + c) : *ref;
+    for (int c = 0; c < SC; ++c)
+      buf[KV ? c * 32 + lane : lane * SC + c] += KV ? __shfl_sync(0xffffffffu, own, c) : own;
     __syncwarp();
   }
   // The lane's 16 values of the columns c0 .. c0 + 15 (key units: of 4 rows and 4
@@ -1202,86 +1204,123 @@ static __device__ __forceinline__ void bwd_tile_bits(const BwdPrepParams& p, lon
 template <int D>
 constexpr int kBwdPrepRows = D == 128 ? 64 : 128;
 
-// Joins two running (maximum, sum of 2^(x - maximum)).
-static __device__ __forceinline__ void bwd_join_sums(float& mx, float& sum, float mx2, float sum2) {
-  const float m = fmaxf(mx, mx2);
-  if (m == -INFINITY) return;
-  sum = sum * ptx::ex2(mx - m) + sum2 * ptx::ex2(mx2 - m);
-  mx = m;
-}
+// A row's sum so far: of 2^(x + (mask - ref) log2(e) - most) over its keys, `ref` the
+// largest mask and `most` the largest exponent that it has met.
+struct BwdRowSum {
+  float ref = -INFINITY, most = -INFINITY, sum = 0.f;
+  // Takes the sum to another, larger reference.
+  __device__ __forceinline__ void refer(float to) {
+    if (to > ref) {
+      most += (ref - to) * 1.4426950408889634f;
+      ref = to;
+    }
+  }
+  __device__ __forceinline__ void raise(float to) {
+    if (to > most) {
+      sum *= ptx::ex2(most - to);
+      most = to;
+    }
+  }
+  __device__ __forceinline__ void join(BwdRowSum o) {
+    refer(o.ref);
+    o.refer(ref);
+    raise(o.most);
+    if (o.most > -INFINITY) sum += o.sum * ptx::ex2(o.most - most);
+  }
+};
 
 // The references of a warp's 16 rows whose LSE is too large to give P, and L anew: log2 of
 // the sum of 2^(scale s + mask - ref).  Row i of them is n0 + i / RUN * STEP + i % RUN (`weak`:
 // bit i).  Such rows are padding and few, so the products are a warp's (mma.sync,
-// 16 x 8 x 16) and their operands come from global memory.  Out of line: warps without
-// such rows take no registers for it.
+// 16 x 8 x 16) and their operands come from global memory, 16 bytes a lane: of every 32
+// elements lane l has those from 8 (l % 4) on, in rows and keys alike, which is an order of
+// the sum over the head dimension.  Out of line: warps without such rows take no registers.
 template <int D, int RUN, int STEP>
 __device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, uint32_t weak) {
   constexpr float kLog2e = 1.4426950408889634f;
   constexpr int KEYS = 4;  // eights of keys whose products are under way together
   const int lane = threadIdx.x % 32;
   const int b = (int)p.div_h.div((uint32_t)bh), h = bh - b * p.Hq;
-  const __nv_bfloat16* q = p.q.p + b * p.q.b + h * p.q.h + 2 * (lane % 4);
-  const __nv_bfloat16* k = p.k.p + b * p.k.b + (long long)(h / p.group) * p.k.h + 2 * (lane % 4);
+  const __nv_bfloat16* q = p.q.p + b * p.q.b + h * p.q.h + 8 * (lane % 4);
+  const __nv_bfloat16* k = p.k.p + b * p.k.b + (long long)(h / p.group) * p.k.h + 8 * (lane % 4);
   const float* mask = p.mask + (p.mask_rows ? ((size_t)b * p.mask_heads + (p.mask_heads == 1 ? 0 : h)) * p.Nq * p.Nk
                                             : (size_t)b * p.Nk);
-  auto row = [&](int i) { return n0 + i / RUN * STEP + i % RUN; };
-  auto mask_row = [&](int n) { return mask + (p.mask_rows ? (size_t)n * p.Nk : 0); };
-  auto keys = [&](int n) { return n >= p.Nq ? 0 : p.causal ? min(p.Nk, n + 1) : p.Nk; };  // (it sees, by the triangle)
-  // The largest mask value of each row (lane i: of row i).
-  float ref = 0.f;
-  for (int i = 0; i < 16; ++i) {
-    if (!(weak >> i & 1)) continue;
-    const float* m = mask_row(row(i));
-    float top = -INFINITY;
-    for (int j = lane; j < keys(row(i)); j += 32) top = fmaxf(top, m[j]);
+  const int Nk = p.Nk;
+  const float scale = p.scale_log2;
+  // This lane's rows of a product, lane / 4 and lane / 4 + 8, and how many keys they see (by the triangle).
+  int n[2], end[2];
+  const float* m[2];
+  const __nv_bfloat16* row[2];
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (lane % 16 == i && top > -INFINITY) ref = top;
+  for (int e = 0; e < 2; ++e) {
+    const int i = lane / 4 + 8 * e;
+    n[e] = n0 + i / RUN * STEP + i % RUN;
+    end[e] = !(weak >> i & 1) ? 0 : p.causal ? min(Nk, n[e] + 1) : Nk;
+    const int at = min(n[e], p.Nq - 1);
+    m[e] = mask + (p.mask_rows ? (size_t)at * Nk : 0) + 2 * (lane % 4);
+    row[e] = q + at * p.q.n;
   }
-  // This lane's rows of a product: lane / 4 and lane / 4 + 8.
-  const int n[2] = {row(lane / 4), row(lane / 4 + 8)};
-  const float r[2] = {__shfl_sync(0xffffffffu, ref, lane / 4), __shfl_sync(0xffffffffu, ref, lane / 4 + 8)};
-  const float* m[2] = {mask_row(n[0]), mask_row(n[1])};
-  const int end[2] = {weak >> (lane / 4) & 1 ? keys(n[0]) : 0, weak >> (lane / 4 + 8) & 1 ? keys(n[1]) : 0};
-  const __nv_bfloat16 *q0 = q + min(n[0], p.Nq - 1) * p.q.n, *q1 = q + min(n[1], p.Nq - 1) * p.q.n;
-  int most = max(end[0], end[1]);
-#pragma unroll
-  for (int x = 1; x < 32; x <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
-  float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {};
+  const int most = __reduce_max_sync(0xffffffffu, max(end[0], end[1]));
+  BwdRowSum of[2];
   for (int j0 = 0; j0 < most; j0 += 8 * KEYS) {
     float c[KEYS][4] = {};
-    const __nv_bfloat16* at[KEYS];
+#pragma unroll 1
+    for (int d = 0; d < D; d += 32) {
+      uint4 a[2], x[KEYS];
 #pragma unroll
-    for (int i = 0; i < KEYS; ++i) at[i] = k + min(j0 + 8 * i + lane / 4, p.Nk - 1) * p.k.n;
-#pragma unroll 2
-    for (int d = 0; d < D; d += 16) {
-      auto two = [&](const __nv_bfloat16* x, int e) { return *reinterpret_cast<const uint32_t*>(x + d + e); };
-      const uint32_t a[4] = {two(q0, 0), two(q1, 0), two(q0, 8), two(q1, 8)};
+      for (int e = 0; e < 2; ++e) a[e] = *reinterpret_cast<const uint4*>(row[e] + d);
 #pragma unroll
       for (int i = 0; i < KEYS; ++i)
+        x[i] = *reinterpret_cast<const uint4*>(k + min(j0 + 8 * i + lane / 4, Nk - 1) * p.k.n + d);
+      auto mma = [](float (&y)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[i][0]), "+f"(c[i][1]), "+f"(c[i][2]), "+f"(c[i][3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(two(at[i], 0)), "r"(two(at[i], 8)));
+            : "+f"(y[0]), "+f"(y[1]), "+f"(y[2]), "+f"(y[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      };
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) {
+        mma(c[i], a[0].x, a[1].x, a[0].y, a[1].y, x[i].x, x[i].y);
+        mma(c[i], a[0].z, a[1].z, a[0].w, a[1].w, x[i].z, x[i].w);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < KEYS; ++i)
+    for (int e = 0; e < 2; ++e) {  // the lane's rows; columns 2 (lane % 4), + 1 of each eight
+      float add[2 * KEYS], ref = of[e].ref;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {  // row e / 2 of the lane's, column 2 (lane % 4) + e % 2
-        const int j = j0 + 8 * i + 2 * (lane % 4) + e % 2;
-        if (j < end[e / 2])
-          bwd_join_sums(mx[e / 2], sum[e / 2], fmaf(c[i][e], p.scale_log2, (m[e / 2][j] - r[e / 2]) * kLog2e), 1.f);
+      for (int i = 0; i < 2 * KEYS; ++i) {  // (all loads at once, the last key's again behind it)
+        const int j = j0 + 8 * (i / 2) + i % 2, at = min(j, Nk - 1 - 2 * (lane % 4));
+        add[i] = m[e][at];
+        if (j + 2 * (lane % 4) >= end[e]) add[i] = -INFINITY;
+        ref = fmaxf(ref, add[i]);
       }
+      if (ref == -INFINITY) continue;
+      of[e].refer(ref);
+      float top = of[e].most;
+#pragma unroll
+      for (int i = 0; i < 2 * KEYS; ++i) {
+        float& x = c[i / 2][2 * e + i % 2];
+        x = fmaf(x, scale, (add[i] - ref) * kLog2e);
+        top = fmaxf(top, x);
+      }
+      of[e].raise(top);
+#pragma unroll
+      for (int i = 0; i < 2 * KEYS; ++i) of[e].sum += ptx::ex2(c[i / 2][2 * e + i % 2] - of[e].most);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int e = 0; e < 2; ++e) {
 #pragma unroll
-    for (int x = 1; x < 4; x <<= 1)
-      bwd_join_sums(mx[i], sum[i], __shfl_xor_sync(0xffffffffu, mx[i], x), __shfl_xor_sync(0xffffffffu, sum[i], x));
-    if (lane % 4 == 0 && (weak >> (lane / 4 + 8 * i) & 1)) {
-      p.stat[((size_t)bh * (p.nqp / 128) + n[i] / 128) * kStatTile + n[i] % 128] =
-          sum[i] > 0.f ? -(mx[i] + log2f(sum[i])) : -INFINITY;
-      p.ref[(size_t)bh * p.nqp + n[i]] = -r[i];
+    for (int x = 1; x < 4; x <<= 1) {
+      BwdRowSum o;
+      o.ref = __shfl_xor_sync(0xffffffffu, of[e].ref, x);
+      o.most = __shfl_xor_sync(0xffffffffu, of[e].most, x);
+      o.sum = __shfl_xor_sync(0xffffffffu, of[e].sum, x);
+      of[e].join(o);
+    }
+    if (lane % 4 == 0 && (weak >> (lane / 4 + 8 * e) & 1)) {
+      p.stat[((size_t)bh * (p.nqp / 128) + n[e] / 128) * kStatTile + n[e] % 128] =
+          of[e].sum > 0.f ? -(of[e].most + log2f(of[e].sum)) : -INFINITY;
+      p.ref[(size_t)bh * p.nqp + n[e]] = of[e].ref > -INFINITY ? -of[e].ref : 0.f;
     }
   }
 }
