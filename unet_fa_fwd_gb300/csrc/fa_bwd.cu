@@ -70,9 +70,10 @@ using fa::ranges_overlap;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Iterations that a partial result and its join cost (fa_bwd_geom.h): the writing
-// of 64 KB (32 KB of dQ) by a CTA and the join's launch, 4 to 5 us.  (With 2 or 7 every
-// case measured takes the same time within 1 %.)
+// Iterations that a partial result and its join count for (fa_bwd_geom.h), so that no
+// range is shorter than its join: the writing of 64 KB (32 KB of dQ) by a CTA and the
+// join's launch take 4 to 5 us.  (A bound, not a setting: with 2 or 7 every case measured
+// takes the same time within 1 %.)
 constexpr int kJoinCost = 4;
 
 // Sizes that the entry points take.

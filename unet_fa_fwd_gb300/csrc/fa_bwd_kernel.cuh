@@ -25,7 +25,7 @@
 //                has 32 rows of the unit (lanes of tensor memory)
 //   warp 16      TMA producer      warp 17  MMA issuer (owns tensor memory)
 // Four warps a sub-partition: with two (64 columns a thread) heads of 64 take
-// 193 us for 179, heads of 128 the same.
+// 8 % longer (measured on an earlier form of the loop), heads of 128 the same.
 // L and delta are a query's: in query units a row's, so that a thread has one row
 // and 32 columns; in key units a column's, where a thread has 4 rows and 8 columns
 // (the 16 x 256 bit shape of tensor memory's accesses) and so a fourth of the reads

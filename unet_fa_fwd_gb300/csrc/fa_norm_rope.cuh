@@ -37,7 +37,8 @@
 namespace fa {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormBackPerSm = 2;     // blocks of the gradient that are resident
+constexpr int kNormBackPerSm = 2;     // blocks of the gradient that are resident (128 registers: with the pairs as
+                                      // halves in fp32, and off 16 bytes in 16 bits, they spill 36 to 52 bytes a thread)
 constexpr int kNormMaxBlocks = 1024;  // blocks of the gradient (rows of partial sums)
 constexpr int kNormReduceRows = 32;   // rows of threads of the second kernel
 
