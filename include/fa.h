@@ -400,12 +400,12 @@ FA_API size_t fa_norm_rope_workspace_bytes(int D);
  * A row that sees no key (LSE = -inf) has no gradient, whatever its dLSE: its dQ is 0
  * and it adds nothing to dK and dV; keys that no row sees have dK = dV = 0.  Under an
  * additive or key-padding mask a row of |LSE| >= 2^14 (all that it sees lies under a large
- * finite mask, whose size hides the row's sum in LSE) has its sum taken again; below, P
- * is within 2^-9 of itself.  P and dS are rounded to bf16 for the products that take
- * them; everything else is fp32, in a fixed order: results repeat bit for bit on one GPU.  Rows
- * of q, dout, out and dlse that see no key may hold anything.  Numbers in k and v that are
- * not finite, in masked places too, and such numbers in other rows may turn any gradient
- * of their heads into NaN.
+ * finite mask, whose fp32 step hides the row's sum in LSE and its scores in O) has its sum
+ * and delta taken again from whole scores; below, P is within 2^-9 of itself.  P and dS
+ * are rounded to bf16 for the products that take them; everything else is fp32, in a fixed
+ * order: results repeat bit for bit on one GPU.  Rows of q, dout, out and dlse that see no
+ * key may hold anything.  Numbers in k and v that are not finite, in masked places too, and
+ * such numbers in other rows may turn any gradient of their heads into NaN.
  *
  * Two kernels are enqueued on `stream`, one ahead of them for a boolean mask and one
  * after them where units were cut to fill the GPU.  Errors as fa_fwd_ex, waits that ran out

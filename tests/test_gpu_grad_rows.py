@@ -52,7 +52,10 @@ def _check_shifted(B, Hq, Hk, Nq, Nk, D, causal, seed=1, **mask):
     scale = 1 / math.sqrt(D)
     o, lse = ref.attend(q, k, v, scale, full_mask=even)
     x = dict(dout=do, q=q, k=k, v=v, out=o.to(torch.bfloat16), scale=scale)
-    got = fa.bwd(**x, lse=(lse + shift[..., 0]).float(), causal=causal, **mask)
+    low = (lse + shift[..., 0]).float()
+    again = ((low.abs() >= 2 ** 14) & low.isfinite())[..., None]  # rows whose O is not used: delta is that of the definition
+    got = fa.bwd(**dict(x, out=x["out"].masked_fill(again, math.nan)), lse=low, causal=causal, **mask)
+    x["out"] = torch.where(again, o, x["out"].double())
     torch.cuda.synchronize()
     assert fa.read_device_status() == 0
     want, size, fine = ref.attend_bwd(**x, lse=lse, full_mask=even)
@@ -103,6 +106,23 @@ def test_rows_wholly_under_a_large_additive_mask(D, c, size, heads, causal):
     m[..., 0, :, 3] = -INF
     m[0, 0, :, Nk // 4] = -abs(c)       # a column that ordinary rows do not see
     _check_shifted(*size, D, causal, full_mask=m)
+
+
+@pytest.mark.parametrize("c", [-1e4, -1e6, -1e9, -1e30])
+@pytest.mark.parametrize("kind", ["key", "add"])
+def test_with_the_forwards_own_results(c, kind):
+    """Rows wholly at one value: the gradients are those of no mask, although the forward's O is of scores that the
+    mask's step has rounded.  Both are within P's 2^-9 (the rows at -1e4), its rounding and the results'."""
+    B, H, N, D = 2, 2, 300, 64
+    q, k, v, do = (_rand((B, H, N, D), i) for i in range(4))
+    mask = dict(key_mask=torch.full((B, N), c, device="cuda")) if kind == "key" else dict(
+        full_mask=torch.full((B, 1, N, N), c, device="cuda"))
+    out, lse = fa.fwd_ex(q, k, v, **mask)
+    got = fa.bwd(do, q, k, v, out, lse, **mask)
+    o, lse = ref.attend(q, k, v, 1 / math.sqrt(D))
+    want = ref.attend_bwd(do, q, k, v, o, lse, 1 / math.sqrt(D))[0]
+    for a, b in zip(got, want):
+        assert float((a.double() - b).norm()) <= (5e-3 + 2.0 ** -9) * float(b.norm())
 
 
 def test_large_masks_repeat_and_agree_with_none():

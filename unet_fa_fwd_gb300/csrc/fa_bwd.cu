@@ -332,6 +332,7 @@ int fa_bwd(const fa_tensor* dout, const fa_tensor* q, const fa_tensor* k, const 
   pp.dlse = dlse;
   pp.q = view(*q);
   pp.k = view(*k);
+  pp.v = view(*v);
   pp.stat = reinterpret_cast<float*>(ws + l.stat);
   pp.flags = reinterpret_cast<uint8_t*>(ws + l.flags);
   pp.ref = reinterpret_cast<float*>(ws + l.ref);

@@ -1145,7 +1145,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_bwd_kernel(const __grid_con
 // delta_i = dO_i . O_i - dLSE_i.  HBM bound (O and dO are read once: 4608 tokens of
 // 24 heads of 128 11 us, 5.1 TB/s cold; 14 with one row a thread); D / 8 neighbouring lanes share a row.
 struct BwdPrepParams {
-  BwdTensor out, dout, q, k;
+  BwdTensor out, dout, q, k, v;
   const float *lse, *dlse;  // [B][Hq][Nq]; dlse may be nullptr
   float *stat, *ref;        // as BwdParams
   uint8_t* flags;
@@ -1204,10 +1204,10 @@ static __device__ __forceinline__ void bwd_tile_bits(const BwdPrepParams& p, lon
 template <int D>
 constexpr int kBwdPrepRows = D == 128 ? 64 : 128;
 
-// A row's sum so far: of 2^(x + (mask - ref) log2(e) - most) over its keys, `ref` the
-// largest mask and `most` the largest exponent that it has met.
+// A row's sums so far: of 2^(x + (mask - ref) log2(e) - most) over its keys, and of that
+// times dP; `ref` the largest mask and `most` the largest exponent that it has met.
 struct BwdRowSum {
-  float ref = -INFINITY, most = -INFINITY, sum = 0.f;
+  float ref = -INFINITY, most = -INFINITY, sum = 0.f, along = 0.f;
   // Takes the sum to another, larger reference.
   __device__ __forceinline__ void refer(float to) {
     if (to > ref) {
@@ -1217,7 +1217,9 @@ struct BwdRowSum {
   }
   __device__ __forceinline__ void raise(float to) {
     if (to > most) {
-      sum *= ptx::ex2(most - to);
+      const float by = ptx::ex2(most - to);
+      sum *= by;
+      along *= by;
       most = to;
     }
   }
@@ -1225,12 +1227,16 @@ struct BwdRowSum {
     refer(o.ref);
     o.refer(ref);
     raise(o.most);
-    if (o.most > -INFINITY) sum += o.sum * ptx::ex2(o.most - most);
+    if (o.most == -INFINITY) return;
+    const float by = ptx::ex2(o.most - most);
+    sum += o.sum * by;
+    along += o.along * by;
   }
 };
 
-// The references of a warp's 16 rows whose LSE is too large to give P, and L anew: log2 of
-// the sum of 2^(scale s + mask - ref).  Row i of them is n0 + i / RUN * STEP + i % RUN (`weak`:
+// The references of a warp's 16 rows whose LSE is too large to give P, and L and delta
+// anew: log2 of the sum of 2^(scale s + mask - ref), and the sum of P dP less dLSE (such a
+// row's O is of scores that the forward has rounded with the mask).  Row i of them is n0 + i / RUN * STEP + i % RUN (`weak`:
 // bit i).  Such rows are padding and few, so the products are a warp's (mma.sync,
 // 16 x 8 x 16) and their operands come from global memory, 16 bytes a lane: of every 32
 // elements lane l has those from 8 (l % 4) on, in rows and keys alike, which is an order of
@@ -1238,11 +1244,12 @@ struct BwdRowSum {
 template <int D, int RUN, int STEP>
 __device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, uint32_t weak) {
   constexpr float kLog2e = 1.4426950408889634f;
-  constexpr int KEYS = 4;  // eights of keys whose products are under way together
+  constexpr int KEYS = 2;  // eights of keys whose products are under way together
   const int lane = threadIdx.x % 32;
   const int b = (int)p.div_h.div((uint32_t)bh), h = bh - b * p.Hq;
   const __nv_bfloat16* q = p.q.p + b * p.q.b + h * p.q.h + 8 * (lane % 4);
   const __nv_bfloat16* k = p.k.p + b * p.k.b + (long long)(h / p.group) * p.k.h + 8 * (lane % 4);
+  const __nv_bfloat16* v = p.v.p + b * p.v.b + (long long)(h / p.group) * p.v.h + 8 * (lane % 4);
   const float* mask = p.mask + (p.mask_rows ? ((size_t)b * p.mask_heads + (p.mask_heads == 1 ? 0 : h)) * p.Nq * p.Nk
                                             : (size_t)b * p.Nk);
   const int Nk = p.Nk;
@@ -1250,7 +1257,7 @@ __device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, u
   // This lane's rows of a product, lane / 4 and lane / 4 + 8, and how many keys they see (by the triangle).
   int n[2], end[2];
   const float* m[2];
-  const __nv_bfloat16* row[2];
+  const __nv_bfloat16 *row[2], *grad[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int i = lane / 4 + 8 * e;
@@ -1259,19 +1266,17 @@ __device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, u
     const int at = min(n[e], p.Nq - 1);
     m[e] = mask + (p.mask_rows ? (size_t)at * Nk : 0) + 2 * (lane % 4);
     row[e] = q + at * p.q.n;
+    grad[e] = p.dout.p + b * p.dout.b + h * p.dout.h + 8 * (lane % 4) + at * p.dout.n;
   }
-  const int most = __reduce_max_sync(0xffffffffu, max(end[0], end[1]));
-  BwdRowSum of[2];
-  for (int j0 = 0; j0 < most; j0 += 8 * KEYS) {
-    float c[KEYS][4] = {};
+  // Products of the lane's rows of `a` and of keys j0 .. j0 + 8 KEYS - 1 of `x`.
+  auto product = [&](float (&c)[KEYS][4], const __nv_bfloat16* const (&a)[2], const __nv_bfloat16* x, long long x_n, int j0) {
 #pragma unroll 1
     for (int d = 0; d < D; d += 32) {
-      uint4 a[2], x[KEYS];
+      uint4 ra[2], rx[KEYS];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) a[e] = *reinterpret_cast<const uint4*>(row[e] + d);
+      for (int e = 0; e < 2; ++e) ra[e] = *reinterpret_cast<const uint4*>(a[e] + d);
 #pragma unroll
-      for (int i = 0; i < KEYS; ++i)
-        x[i] = *reinterpret_cast<const uint4*>(k + min(j0 + 8 * i + lane / 4, Nk - 1) * p.k.n + d);
+      for (int i = 0; i < KEYS; ++i) rx[i] = *reinterpret_cast<const uint4*>(x + min(j0 + 8 * i + lane / 4, Nk - 1) * x_n + d);
       auto mma = [](float (&y)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(y[0]), "+f"(y[1]), "+f"(y[2]), "+f"(y[3])
@@ -1279,10 +1284,17 @@ __device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, u
       };
 #pragma unroll
       for (int i = 0; i < KEYS; ++i) {
-        mma(c[i], a[0].x, a[1].x, a[0].y, a[1].y, x[i].x, x[i].y);
-        mma(c[i], a[0].z, a[1].z, a[0].w, a[1].w, x[i].z, x[i].w);
+        mma(c[i], ra[0].x, ra[1].x, ra[0].y, ra[1].y, rx[i].x, rx[i].y);
+        mma(c[i], ra[0].z, ra[1].z, ra[0].w, ra[1].w, rx[i].z, rx[i].w);
       }
     }
+  };
+  const int most = __reduce_max_sync(0xffffffffu, max(end[0], end[1]));
+  BwdRowSum of[2];
+  for (int j0 = 0; j0 < most; j0 += 8 * KEYS) {
+    float c[KEYS][4] = {}, dp[KEYS][4] = {};
+    product(c, row, k, p.k.n, j0);
+    product(dp, grad, v, p.v.n, j0);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {  // the lane's rows; columns 2 (lane % 4), + 1 of each eight
       float add[2 * KEYS], ref = of[e].ref;
@@ -1304,7 +1316,11 @@ __device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, u
       }
       of[e].raise(top);
 #pragma unroll
-      for (int i = 0; i < 2 * KEYS; ++i) of[e].sum += ptx::ex2(c[i / 2][2 * e + i % 2] - of[e].most);
+      for (int i = 0; i < 2 * KEYS; ++i) {
+        const float w = ptx::ex2(c[i / 2][2 * e + i % 2] - of[e].most);
+        of[e].sum += w;
+        if (w > 0.f) of[e].along = fmaf(w, dp[i / 2][2 * e + i % 2], of[e].along);
+      }
     }
   }
 #pragma unroll
@@ -1315,11 +1331,14 @@ __device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, u
       o.ref = __shfl_xor_sync(0xffffffffu, of[e].ref, x);
       o.most = __shfl_xor_sync(0xffffffffu, of[e].most, x);
       o.sum = __shfl_xor_sync(0xffffffffu, of[e].sum, x);
+      o.along = __shfl_xor_sync(0xffffffffu, of[e].along, x);
       of[e].join(o);
     }
     if (lane % 4 == 0 && (weak >> (lane / 4 + 8 * e) & 1)) {
-      p.stat[((size_t)bh * (p.nqp / 128) + n[e] / 128) * kStatTile + n[e] % 128] =
-          of[e].sum > 0.f ? -(of[e].most + log2f(of[e].sum)) : -INFINITY;
+      float* stat = p.stat + ((size_t)bh * (p.nqp / 128) + n[e] / 128) * kStatTile + n[e] % 128;
+      const bool sees = of[e].sum > 0.f;
+      stat[0] = sees ? -(of[e].most + log2f(of[e].sum)) : -INFINITY;
+      stat[kStatDelta] = sees ? (p.dlse ? p.dlse[(size_t)bh * p.Nq + n[e]] : 0.f) - of[e].along / of[e].sum : 0.f;
       p.ref[(size_t)bh * p.nqp + n[e]] = of[e].ref > -INFINITY ? -of[e].ref : 0.f;
     }
   }
@@ -1410,7 +1429,7 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_prep_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < U * RUN; ++i)
           bits |= (__shfl_sync(0xffffffffu, weak, i % RUN * L) >> (i / RUN) & 1u) << i;
-        __syncwarp();  // (-L of these rows is written again)
+        __syncwarp();  // (-L and -delta of these rows are written again)
         bwd_resum<D, RUN, STEP>(p, bh, n0 - threadIdx.x % 32 / L, bits);
       }
     }
