@@ -399,8 +399,8 @@ FA_API size_t fa_norm_rope_workspace_bytes(int D);
  *
  * A row that sees no key (LSE = -inf) has no gradient, whatever its dLSE: its dQ is 0
  * and it adds nothing to dK and dV; keys that no row sees have dK = dV = 0.  Under an
- * additive or key-padding mask a row of |LSE| >= 2^14 (all that it sees lies under a large
- * finite mask, whose fp32 step hides the row's sum in LSE and its scores in O) has its sum
+ * additive or key-padding mask a row of |LSE| >= 2^14 all of whose keys lie under a large
+ * finite mask (whose fp32 step hides the row's sum in LSE and its scores in O) has its sum
  * and delta taken again from whole scores; below, P is within 2^-9 of itself.  P and dS
  * are rounded to bf16 for the products that take them; everything else is fp32, in a fixed
  * order: results repeat bit for bit on one GPU.  Rows of q, dout, out and dlse that see no

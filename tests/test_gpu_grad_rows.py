@@ -125,6 +125,18 @@ def test_with_the_forwards_own_results(c, kind):
         assert float((a.double() - b).norm()) <= (5e-3 + 2.0 ** -9) * float(b.norm())
 
 
+@pytest.mark.parametrize("D", [32, 128])
+def test_rows_that_their_scores_make_large(D):
+    """|LSE| past 2^14 from scores, under masks that add nothing: bit for bit what no mask gives."""
+    B, H, N = 1, 2, 200
+    x = _inputs(B, H, H, N, N, D, scale=4000.0)
+    assert float(x["lse"].abs().median()) > 2 ** 14
+    want = fa.bwd(**x)
+    assert all(bool(y.isfinite().all()) for y in want)
+    for mask in (dict(key_mask=torch.zeros(B, N, device="cuda")), dict(full_mask=torch.zeros(B, 1, N, N, device="cuda"))):
+        assert all(torch.equal(a, b) for a, b in zip(fa.bwd(**x, **mask), want))
+
+
 def test_large_masks_repeat_and_agree_with_none():
     """All rows at one large value: the gradients of no mask, but for the rows' own normaliser; twice the same."""
     B, H, N, D = 1, 3, 500, 64

@@ -1236,11 +1236,13 @@ struct BwdRowSum {
 
 // The references of a warp's 16 rows whose LSE is too large to give P, and L and delta
 // anew: log2 of the sum of 2^(scale s + mask - ref), and the sum of P dP less dLSE (such a
-// row's O is of scores that the forward has rounded with the mask).  Row i of them is n0 + i / RUN * STEP + i % RUN (`weak`:
-// bit i).  Such rows are padding and few, so the products are a warp's (mma.sync,
-// 16 x 8 x 16) and their operands come from global memory, 16 bytes a lane: of every 32
-// elements lane l has those from 8 (l % 4) on, in rows and keys alike, which is an order of
-// the sum over the head dimension.  Out of line: warps without such rows take no registers.
+// row's O is of scores that the forward has rounded with the mask).  Rows whose scores
+// make LSE large, not their mask, stay as they are: LSE and O come from those scores.
+// Row i of the 16 is n0 + i / RUN * STEP + i % RUN (`weak`: bit i).  Such rows are padding
+// and few, so the products are a warp's (mma.sync, 16 x 8 x 16) and their operands come
+// from global memory, 16 bytes a lane: of every 32 elements lane l has those from
+// 8 (l % 4) on, in rows and keys alike, which is an order of the sum over the head
+// dimension.  Out of line: warps without such rows take no registers.
 template <int D, int RUN, int STEP>
 __device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, uint32_t weak) {
   constexpr float kLog2e = 1.4426950408889634f;
@@ -1334,12 +1336,12 @@ __device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, u
       o.along = __shfl_xor_sync(0xffffffffu, of[e].along, x);
       of[e].join(o);
     }
-    if (lane % 4 == 0 && (weak >> (lane / 4 + 8 * e) & 1)) {
+    if (lane % 4 == 0 && (weak >> (lane / 4 + 8 * e) & 1) && fabsf(of[e].ref) >= kWeakLse / 4) {
       float* stat = p.stat + ((size_t)bh * (p.nqp / 128) + n[e] / 128) * kStatTile + n[e] % 128;
       const bool sees = of[e].sum > 0.f;
       stat[0] = sees ? -(of[e].most + log2f(of[e].sum)) : -INFINITY;
       stat[kStatDelta] = sees ? (p.dlse ? p.dlse[(size_t)bh * p.Nq + n[e]] : 0.f) - of[e].along / of[e].sum : 0.f;
-      p.ref[(size_t)bh * p.nqp + n[e]] = of[e].ref > -INFINITY ? -of[e].ref : 0.f;
+      p.ref[(size_t)bh * p.nqp + n[e]] = sees ? -of[e].ref : 0.f;
     }
   }
 }
