@@ -53,7 +53,7 @@ def _check_shifted(B, Hq, Hk, Nq, Nk, D, causal, seed=1, **mask):
     o, lse = ref.attend(q, k, v, scale, full_mask=even)
     x = dict(dout=do, q=q, k=k, v=v, out=o.to(torch.bfloat16), scale=scale)
     low = (lse + shift[..., 0]).float()
-    again = ((low.abs() >= 2 ** 14) & low.isfinite())[..., None]  # rows whose O is not used: delta is that of the definition
+    again = ((low.abs() >= 2 ** 14) & low.isfinite())[..., None]  # (O is not used: delta is the definition's)
     got = fa.bwd(**dict(x, out=x["out"].masked_fill(again, math.nan)), lse=low, causal=causal, **mask)
     x["out"] = torch.where(again, o, x["out"].double())
     torch.cuda.synchronize()

@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <type_traits>
 
 #include "fa.h"
 #include "fa_bwd_launch.h"
@@ -41,13 +42,17 @@ int launch_bwd_prep(BwdPrepParams& p, long long heads, int D, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = p.some ? 1 : 0;
   const BwdPrepParams& prm = p;
-  auto go = [&](auto* refs, auto* masked, auto* plain) {
-    return cudaLaunchKernelEx(&cfg, p.mask ? refs : p.some ? masked : plain, prm);
+  auto go = [&](auto d) {
+    constexpr int W = decltype(d)::value;
+    return cudaLaunchKernelEx(&cfg,
+                              p.mask   ? fa_bwd_prep_kernel<W, true, true>
+                              : p.some ? fa_bwd_prep_kernel<W, true, false>
+                                       : fa_bwd_prep_kernel<W, false, false>,
+                              prm);
   };
-  const cudaError_t e =
-      D == 32   ? go(fa_bwd_prep_kernel<32, true, true>, fa_bwd_prep_kernel<32, true, false>, fa_bwd_prep_kernel<32, false, false>)
-      : D == 64 ? go(fa_bwd_prep_kernel<64, true, true>, fa_bwd_prep_kernel<64, true, false>, fa_bwd_prep_kernel<64, false, false>)
-                : go(fa_bwd_prep_kernel<128, true, true>, fa_bwd_prep_kernel<128, true, false>, fa_bwd_prep_kernel<128, false, false>);
+  const cudaError_t e = D == 32   ? go(std::integral_constant<int, 32>{})
+                        : D == 64 ? go(std::integral_constant<int, 64>{})
+                                  : go(std::integral_constant<int, 128>{});
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -621,7 +621,8 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
               ptx::mbar_arrive_expect_tx(full, (kStatTile + (FLAGS ? kFlagTile : 0)) * 4);
               bulk_load(ptx::smem_u32(sStat + ss * kStatTile), p.stat + qt * kStatTile, kStatTile * 4, full);
               if constexpr (FLAGS)
-                bulk_load(ptx::smem_u32(sStat + 2 * kStatTile + ss * kFlagTile), p.flags + qt * kFlagTile, kFlagTile * 4, full);
+                bulk_load(ptx::smem_u32(sStat + 2 * kStatTile + ss * kFlagTile), p.flags + qt * kFlagTile,
+                          kFlagTile * 4, full);
               ++nst;
             }
             ok = bwd_wait(bars->r1_empty[s1], ((j / C::RING1) & 1) ^ 1, bars, p);
@@ -933,7 +934,8 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
               asm volatile("cp.async.wait_all;" ::: "memory");
               __syncwarp();
               if (KV ? flags & kFlagRefs : refs)
-                Stage::refer(sMask, KV ? p.ref + query_tile(b, h * p.group + now.g, now.tile) * 128 + wg * kBwdCols + cb : &nref,
+                Stage::refer(sMask,
+                             KV ? p.ref + query_tile(b, h * p.group + now.g, now.tile) * 128 + wg * kBwdCols + cb : &nref,
                              (int)lane);
             }
             Stage::read(sMask, cb % C::MASK_COLS, (int)lane, m);
@@ -1081,7 +1083,8 @@ __device__ __forceinline__ void bwd_units(const BwdParams& p, int cta, uint8_t* 
         bwd_store_row<NC>(tA, is_dv ? 1.f : p.scale, zero, keep, in, (KV ? p.Nk : p.Nq) - my, (int)lane, dst, o.n);
       } else {
         const bool in = bwd_check(p, bars, pc.slot < 2 * plan.ctas, kCheckGradSlot, pc.slot, pc.head);
-        bwd_store_part<NC>(tA, zero, keep, in, p.part[KV ? 0 : 1] + (size_t)pc.slot * (128 * T::ACC) + wg * NC * 128, row);
+        float* part = p.part[KV ? 0 : 1] + (size_t)pc.slot * (128 * T::ACC) + wg * NC * 128;
+        bwd_store_part<NC>(tA, zero, keep, in, part, row);
       }
       ptx::tc_fence_before_sync();
     }
@@ -1271,14 +1274,16 @@ __device__ __noinline__ void bwd_resum(const BwdPrepParams& p, int bh, int n0, u
     grad[e] = p.dout.p + b * p.dout.b + h * p.dout.h + 8 * (lane % 4) + at * p.dout.n;
   }
   // Products of the lane's rows of `a` and of keys j0 .. j0 + 8 KEYS - 1 of `x`.
-  auto product = [&](float (&c)[KEYS][4], const __nv_bfloat16* const (&a)[2], const __nv_bfloat16* x, long long x_n, int j0) {
+  auto product = [&](float (&c)[KEYS][4], const __nv_bfloat16* const (&a)[2], const __nv_bfloat16* x, long long x_n,
+                     int j0) {
 #pragma unroll 1
     for (int d = 0; d < D; d += 32) {
       uint4 ra[2], rx[KEYS];
 #pragma unroll
       for (int e = 0; e < 2; ++e) ra[e] = *reinterpret_cast<const uint4*>(a[e] + d);
 #pragma unroll
-      for (int i = 0; i < KEYS; ++i) rx[i] = *reinterpret_cast<const uint4*>(x + min(j0 + 8 * i + lane / 4, Nk - 1) * x_n + d);
+      for (int i = 0; i < KEYS; ++i)
+        rx[i] = *reinterpret_cast<const uint4*>(x + min(j0 + 8 * i + lane / 4, Nk - 1) * x_n + d);
       auto mma = [](float (&y)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(y[0]), "+f"(y[1]), "+f"(y[2]), "+f"(y[3])

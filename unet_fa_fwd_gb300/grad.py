@@ -268,8 +268,8 @@ def bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o
     :func:`~unet_fa_fwd_gb300.fwd_ex` from what they were given and returned: ``dout`` (and ``dlse``) are the
     gradients of O (and LSE).  bf16 [B, H, N, D] tensors of any strides whose rows start 16-byte aligned; k and v
     may have fewer heads than q (shared by neighbouring query heads, whose gradients add up).  Masks as
-    fwd_ex's, of any finite size; rows that see no key may hold anything.  Returns (dq, dk, dv), contiguous or with ``token_major`` views of contiguous [B, N, H, D] tensors.
-    Autograd does not record the call."""
+    fwd_ex's, of any finite size; rows that see no key may hold anything.  Returns (dq, dk, dv), contiguous or
+    with ``token_major`` views of contiguous [B, N, H, D] tensors.  Autograd does not record the call."""
     _bhnd(q, "q")
     return _run(q, stream, _bwd, dout, q, k, v, out, lse, dlse, key_mask, full_mask, bool(causal), scale, None, None,
                 None, None, True, token_major)
